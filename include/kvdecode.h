@@ -419,6 +419,193 @@ kvd_status kvd_decode_ex(const kvd_cache* cache, const void* q, const int32_t* s
                          int32_t* status_word, kvd_stream_t stream);
 
 /*
+ * Rotary positions. Pair i of a head's first rotary_dim columns, i < rotary_dim
+ * / 2, is turned by the angle position * w_i:
+ *   (a, b) -> factor * (a cos - b sin, b cos + a sin)
+ * Columns from rotary_dim on are copied. The pair is columns (2i, 2i + 1) when
+ * `interleaved`, else columns (i, i + rotary_dim / 2).
+ *   turns       : device uint64 [rotary_dim / 2], 8-byte aligned: w_i / (2 pi), the
+ *                 turns of pair i per position, in units of 2^-64 turn. The phase
+ *                 of position p is p * turns[i] modulo 2^64 in integers, so it is
+ *                 as exact at position 2^31 - 1 as at 1 (a float32 angle is off by
+ *                 0.06 radians at position 10^6). Negative positions turn back.
+ *   factor      : multiplies cosine and sine (1, or a long-context scaling's own)
+ *   rotary_dim  : a multiple of 16 in [16, 256], at most the head dimension
+ * kvd_rope_table fills a HOST array of rotary_dim / 2 entries, to be copied to
+ * the device once, and the factor, from the base and the scaling of the
+ * frequencies w_i = base^(-2i / rotary_dim):
+ *   NONE        as they are
+ *   LINEAR      w_i / scale
+ *   BASE        with base * scale^(rotary_dim / (rotary_dim - 2)) for base
+ *               (rotary_dim 16 and up, so the exponent is finite)
+ *   WAVELENGTH  with n_i = original_len * w_i / (2 pi) turns in the original
+ *               context: w_i where n_i >= fast, w_i / scale where n_i <= slow, and
+ *               between them w_i k + w_i / scale (1 - k), k = (n_i - slow) / (fast - slow)
+ *   PARTS       the same mix with k falling linearly in the pair's index from 1 at
+ *               the pair of `fast` turns (rounded down, at least 0) to 0 at the pair
+ *               of `slow` turns (rounded up, at most rotary_dim - 1), the index of n turns being
+ *               rotary_dim ln(original_len / (2 pi n)) / (2 ln base)
+ * and factor = attn_factor if that is > 0, else 0.1 ln(scale) + 1 for PARTS and 1 otherwise.
+ * Errors: KVD_ERR_INVALID_ARG for null pointers, rotary_dim out of range, base
+ * <= 1 or non-finite, and where the scaling uses them: scale < 1, original_len
+ * <= 0, slow <= 0 or fast <= slow (all finite), an unknown scaling, or an
+ * attn_factor that is negative or not finite.
+ */
+typedef enum kvd_rope_scaling {
+    KVD_ROPE_NONE = 0,
+    KVD_ROPE_LINEAR = 1,
+    KVD_ROPE_BASE = 2,
+    KVD_ROPE_PARTS = 3,
+    KVD_ROPE_WAVELENGTH = 4
+} kvd_rope_scaling;
+
+typedef struct kvd_rope {
+    const uint64_t* turns;
+    float factor;
+    int rotary_dim;
+    int interleaved;
+} kvd_rope;
+
+kvd_status kvd_rope_table(int rotary_dim, double base, kvd_rope_scaling scaling, double scale, double original_len,
+                          double slow, double fast, double attn_factor, uint64_t* turns_host, float* factor_out);
+
+/*
+ * kvd_rope_apply: rows turned by their positions.
+ *   x, y      : [rows, n_heads, head_dim], bf16 or fp32 each (in_dtype,
+ *               out_dtype), 16-byte aligned; the heads of a row are contiguous
+ *               and rows lie x_stride, y_stride elements apart (a slice of a fused
+ *               projection, say): at least n_heads * head_dim, and a multiple
+ *               of 8 for bf16, 4 for fp32. y may be x itself (same dtype and
+ *               stride); any other overlap of the two is refused.
+ *   positions : device int32 [rows], any values
+ * The angles' cosines and sines and the products are float32; the result is
+ * rounded once. head_dim: a multiple of 8 up to 1024. rows = 0 is a no-op.
+ * Errors: KVD_ERR_INVALID_ARG for a bad rope description, null or misaligned
+ * pointers, sizes, strides or dtypes out of range, or an overlap;
+ * KVD_ERR_UNSUPPORTED for head_dim past 1024; KVD_ERR_CUDA.
+ */
+kvd_status kvd_rope_apply(const kvd_rope* rope, const void* x, long long x_stride, kvd_out_dtype in_dtype, void* y,
+                          long long y_stride, kvd_out_dtype out_dtype, const int32_t* positions, long long rows,
+                          int n_heads, int head_dim, kvd_stream_t stream);
+
+/*
+ * kvd_kv_append_rope: new rows appended to a cache of kvd_decode_ex's
+ * description (bf16, int8 or fp8; contiguous or paged), keys turned by their
+ * positions on the way, and the new tokens' queries with them: exactly
+ * kvd_rope_apply of k_new (to bf16) and the append of the result and v_new,
+ * and kvd_rope_apply of q into q_out.
+ *   k_new, v_new : bf16 [n_rows, n_heads_kv, head_dim], rows k_stride, v_stride
+ *                  elements apart (multiples of 8, at least n_heads_kv *
+ *                  head_dim), 16-byte aligned
+ *   q, q_out     : bf16 [n_rows, n_heads_q, head_dim] with q_stride, q_out_stride
+ *                  likewise; both NULL to leave the queries out. q_out may be q
+ *                  itself (same stride), and overlaps nothing else of the call.
+ *   pos          : device int32 [batch], the position of each sequence's first new row
+ *   row_offsets  : NULL: n_rows = batch * T, T rows to a sequence, row b * T + i at
+ *                  position pos[b] + i. Else device int32 [batch + 1], not
+ *                  decreasing: the rows of sequence b are row_offsets[b] ..
+ *                  row_offsets[b + 1] - 1 (prompts of any length packed end to
+ *                  end), row_offsets[b] + i at position pos[b] + i. Rows before the first
+ *                  offset or from the last one on belong to no sequence and are left as they are, in q_out too.
+ * A row at a position outside [0, s_max) or on a block that names no page is
+ * not appended and sets KVD_STATUS_POS_OUT_OF_RANGE or KVD_STATUS_BAD_PAGE; its
+ * query is turned all the same.
+ * Errors: as the appends and kvd_rope_apply; KVD_ERR_INVALID_ARG also for n_rows
+ * not a multiple of batch (row_offsets NULL), only one of q and q_out, n_rows
+ * past 2^31 - 1 or written and read ranges that overlap; KVD_ERR_UNSUPPORTED for
+ * head_dim outside {64, 128, 256} with an 8-bit cache, or past 1024.
+ */
+kvd_status kvd_kv_append_rope(const kvd_cache* cache, const kvd_rope* rope, const void* q, long long q_stride,
+                              void* q_out, long long q_out_stride, const void* k_new, long long k_stride,
+                              const void* v_new, long long v_stride, const int32_t* pos, const int32_t* row_offsets,
+                              int batch, long long n_rows, int n_heads_q, int n_heads_kv, int head_dim,
+                              int32_t* status_word, kvd_stream_t stream);
+
+/*
+ * fp4 KV cache: 4-bit E2M1 codes (1 sign, 2 exponent, 1 mantissa bit: 0, 0.5,
+ * 1, 1.5, 2, 3, 4, 6) with an E4M3 scale per 16 columns and a power of two per
+ * row, (D / 2 + D / 16 + 1) bytes a row (4.56 bits a value at head_dim 128):
+ *   a = max_d |x_d|; e = the smallest integer >= -126 with a <= 2688 * 2^e
+ *   (2688 = 448 * 6, the largest scale times the largest code);
+ *   y_d = x_d * 2^-e; per 16 columns s = E4M3(max |y_d| * fl(1/6)), and
+ *   code_d = E2M1(y_d * fl(1 / s)), all float32, round to nearest even and
+ *   saturating, a zero result stored as +0, codes 0 where s = 0 (a = 0: e = -127).
+ *   The row reads back as code_d * s * 2^e, which bf16 holds exactly
+ *   (inside bf16's range). Inputs must be finite.
+ * The rows of 16 consecutive tokens of one KV head form a block of 9 * head_dim
+ * + 16 bytes, so that a kernel reads a head's tokens as one stream:
+ *   [0, 8 D)        codes, min(D, 128) columns at a time: for column group c, 16
+ *                   tokens x min(D, 128) / 2 bytes; byte j of a token holds columns
+ *                   128 c + 2j (low half) and 128 c + 2j + 1 (high half)
+ *   [8 D, 9 D)      scales, E4M3 [16 tokens][D / 16]
+ *   [9 D, 9 D + 16) row exponents e + 127, one byte [16 tokens] (E8M0)
+ *   contiguous : uint8 [batch, n_heads_kv, s_max / 16, 9 D + 16], s_max a multiple of 16
+ *   paged      : uint8 pool [num_pages, n_heads_kv, page_size / 16, 9 D + 16],
+ *                with the block table and page sizes of the other paged calls
+ * 16-byte aligned; head_dim 64, 128 or 256. Rows past a sequence's length may
+ * hold anything.
+ */
+typedef struct kvd_cache_fp4 {
+    void* k;                       /* blocks of the cache or page pool */
+    void* v;
+    const int32_t* block_table;    /* paged: int32 [batch, max_blocks]; NULL for contiguous */
+    int s_max;                     /* contiguous: capacity of each sequence, a multiple of 16 */
+    int max_blocks, page_size, num_pages;  /* paged */
+} kvd_cache_fp4;
+
+/* Bytes of one block of 16 tokens (9 * head_dim + 16), or 0 for an unsupported head_dim. */
+size_t kvd_fp4_block_bytes(int head_dim);
+
+/*
+ * kvd_kv_quantize_fp4: rows t < seq_lens[b] (clamped to max_seq_len) of a
+ * contiguous bf16 cache [batch, s_max, n_heads_kv, head_dim] (K or V) into the
+ * blocks of a contiguous fp4 cache of s_max_blocks >= max_seq_len tokens (a
+ * multiple of 16); other rows are left as they are. kvd_kv_read_fp4: rows t < seq_lens[b] (clamped) of
+ * the K or V blocks of an fp4 cache (contiguous, or paged with block_table) back
+ * to bf16 [batch, s_out, n_heads_kv, head_dim], s_out >= max_seq_len, other rows left as
+ * they are; a block that names no page reads as zero rows and sets
+ * KVD_STATUS_BAD_PAGE. Errors as kvd_kv_quantize_q8; max_seq_len is at most each capacity.
+ */
+kvd_status kvd_kv_quantize_fp4(const void* cache, void* blocks, const int32_t* seq_lens, int batch, int s_max,
+                               int s_max_blocks, int max_seq_len, int n_heads_kv, int head_dim, kvd_stream_t stream);
+kvd_status kvd_kv_read_fp4(const void* blocks, const int32_t* block_table, int s_max_blocks, int max_blocks,
+                           int page_size, int num_pages, void* out, int s_out, const int32_t* seq_lens, int batch,
+                           int max_seq_len, int n_heads_kv, int head_dim, int32_t* status_word, kvd_stream_t stream);
+
+/*
+ * kvd_kv_append_fp4: kvd_kv_append_rope for an fp4 cache; rope NULL appends
+ * k_new as it is (q and q_out are then NULL too). Other arguments, status and errors as there.
+ */
+kvd_status kvd_kv_append_fp4(const kvd_cache_fp4* cache, const kvd_rope* rope, const void* q, long long q_stride,
+                             void* q_out, long long q_out_stride, const void* k_new, long long k_stride,
+                             const void* v_new, long long v_stride, const int32_t* pos, const int32_t* row_offsets,
+                             int batch, long long n_rows, int n_heads_q, int n_heads_kv, int head_dim,
+                             int32_t* status_word, kvd_stream_t stream);
+
+/*
+ * kvd_decode_fp4: kvd_decode_ex over an fp4 cache: attention of n_tokens new
+ * tokens per sequence (q, out [batch, n_tokens, n_heads_q, head_dim]; token i
+ * attends to the first seq_lens[b] - n_tokens + 1 + i tokens) over the rows read
+ * back, contiguous or paged, groups up to KVD_MAX_GROUP, with the step's append
+ * (k_new, v_new [batch, n_tokens, n_heads_kv, head_dim] and pos, no rotation) or
+ * without it (all three NULL). The cache rows enter the products exactly (a
+ * code times its scale fits f16), q is taken to f16 relative to its row's
+ * largest element, the softmax weights are rounded to f16 (fp32 output: carried
+ * to ~2^-22 as two f16 values), sums and statistics are fp32.
+ * kvd_decode_plan_fp4 gives the split count and the workspace, as
+ * kvd_decode_plan_multi does for the other caches (the fp4 kernel has its own
+ * launch shape, so the two are not interchangeable).
+ * Arguments, results, status and errors otherwise as kvd_decode_ex.
+ */
+kvd_status kvd_decode_plan_fp4(int batch, int n_tokens, int n_heads_q, int n_heads_kv, int head_dim, int max_seq_len,
+                               int num_sms, int n_split_request, int* n_split_out, size_t* workspace_bytes_out);
+kvd_status kvd_decode_fp4(const kvd_cache_fp4* cache, const void* q, const int32_t* seq_lens, int batch, int n_tokens,
+                          int max_seq_len, int n_heads_q, int n_heads_kv, int head_dim, float scale, int n_split,
+                          void* workspace, size_t workspace_bytes, void* out, kvd_out_dtype out_dtype,
+                          float* lse_out, const void* k_new, const void* v_new, const int32_t* pos,
+                          int32_t* status_word, kvd_stream_t stream);
+
+/*
  * The two launches of kvd_decode_attention, exposed separately so that each
  * can be timed on its own. Arguments and errors are those of
  * kvd_decode_attention; calling kvd_split_kv_chunk then kvd_split_kv_merge on

@@ -24,6 +24,7 @@ OK, ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_WORKSPACE_TOO_SMALL, ERR_CUDA = range(
 OUT_BF16, OUT_F32 = 0, 1
 STATUS_SEQ_LEN_CLAMPED = 0x1
 STATUS_POS_OUT_OF_RANGE = 0x2
+STATUS_BAD_PAGE = 0x8
 STATUS_UMAX_FALLBACK = 0x10
 
 # Every symbol include/kvdecode.h declares.
@@ -36,7 +37,8 @@ EXPORTED = (
     "kvd_decode_attention_multi", "kvd_decode_step_multi", "kvd_decode_ex", "kvd_kv_append_q8_paged",
     "kvd_decode_attention_umax", "kvd_decode_step_umax", "kvd_step_staging_bytes", "kvd_decode_step_host",
     "kvd_kv_quantize_fp8", "kvd_kv_append_fp8", "kvd_kv_append_fp8_paged", "kvd_merge_attention",
-    "kvd_probe_read",
+    "kvd_probe_read", "kvd_rope_table", "kvd_rope_apply", "kvd_kv_append_rope", "kvd_fp4_block_bytes",
+    "kvd_kv_quantize_fp4", "kvd_kv_read_fp4", "kvd_kv_append_fp4", "kvd_decode_plan_fp4", "kvd_decode_fp4",
 )
 STATIC_WORKSPACE_BYTES = 16 << 20  # KVD_STATIC_WORKSPACE_BYTES
 
@@ -73,6 +75,19 @@ class _CCache(ctypes.Structure):
                 ("v_scales", ctypes.c_void_p), ("block_table", ctypes.c_void_p), ("s_max", ctypes.c_int),
                 ("max_blocks", ctypes.c_int), ("page_size", ctypes.c_int), ("num_pages", ctypes.c_int),
                 ("fp8", ctypes.c_int)]
+
+
+class _CRope(ctypes.Structure):
+    """struct kvd_rope of kvdecode.h."""
+    _fields_ = [("turns", ctypes.c_void_p), ("factor", ctypes.c_float), ("rotary_dim", ctypes.c_int),
+                ("interleaved", ctypes.c_int)]
+
+
+class _CCacheFp4(ctypes.Structure):
+    """struct kvd_cache_fp4 of kvdecode.h."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("block_table", ctypes.c_void_p),
+                ("s_max", ctypes.c_int), ("max_blocks", ctypes.c_int), ("page_size", ctypes.c_int),
+                ("num_pages", ctypes.c_int)]
 
 
 def _declare(lib):
@@ -139,6 +154,22 @@ def _declare(lib):
     lib.kvd_decode_ex.argtypes = [ctypes.POINTER(_CCache), P, P, I, I, I, I, I, I, F, I, P, SZ, P, I, P, P, P, P,
                                   P, P]
     lib.kvd_decode_ex.restype = I
+    # rotary positions, rotating appends, fp4 cache
+    LL, DBL, PROPE = ctypes.c_longlong, ctypes.c_double, ctypes.POINTER(_CRope)
+    lib.kvd_rope_table.argtypes = [I, DBL, I, DBL, DBL, DBL, DBL, DBL, P, ctypes.POINTER(F)]
+    lib.kvd_rope_apply.argtypes = [PROPE, P, LL, I, P, LL, I, P, LL, I, I, P]
+    app = [PROPE, P, LL, P, LL, P, LL, P, LL, P, P, I, LL, I, I, I, P, P]
+    lib.kvd_kv_append_rope.argtypes = [ctypes.POINTER(_CCache)] + app
+    lib.kvd_kv_append_fp4.argtypes = [ctypes.POINTER(_CCacheFp4)] + app
+    lib.kvd_fp4_block_bytes.argtypes = [I]
+    lib.kvd_fp4_block_bytes.restype = SZ
+    lib.kvd_kv_quantize_fp4.argtypes = [P, P, P, I, I, I, I, I, I, P]
+    lib.kvd_kv_read_fp4.argtypes = [P, P, I, I, I, I, P, I, P, I, I, I, I, P, P]
+    lib.kvd_decode_plan_fp4.argtypes = [I, I, I, I, I, I, I, I, PI, PSZ]
+    lib.kvd_decode_fp4.argtypes = [ctypes.POINTER(_CCacheFp4)] + lib.kvd_decode_ex.argtypes[1:]
+    for name in ("kvd_rope_table", "kvd_rope_apply", "kvd_kv_append_rope", "kvd_kv_append_fp4",
+                 "kvd_kv_quantize_fp4", "kvd_kv_read_fp4", "kvd_decode_plan_fp4", "kvd_decode_fp4"):
+        getattr(lib, name).restype = I
     lib.kvd_schedule_describe.argtypes = [P, I, I, I, I, I, I, I, I, P, I, PI, PI]
     lib.kvd_kernel_info.argtypes = [I, I, I, I, PI, PI, PI, PI, PI, PI]
     lib.kvd_status_string.argtypes = [I]
@@ -868,3 +899,328 @@ def split_kv_merge(q, k_cache, v_cache, seq_lens, max_seq_len: int, scale: float
     args = _decode_args(q, k_cache, v_cache, seq_lens, max_seq_len, scale, n_split, workspace,
                         out, lse, status, stream)
     _check(load().kvd_split_kv_merge(*args), "kvd_split_kv_merge")
+
+
+# ---------------------------------------------------------------------------
+# Rotary positions, appends that apply them, and the fp4 cache
+# ---------------------------------------------------------------------------
+
+ROPE_SCALINGS = {"none": 0, "linear": 1, "base": 2, "parts": 3, "wavelength": 4}
+#: Default (slow, fast) turns in the original context between which a scaling mixes.
+_ROPE_TURNS = {"parts": (1.0, 32.0), "wavelength": (1.0, 4.0)}
+
+
+def rope_table(rotary_dim: int, base: float = 10000.0, scaling: str = "none", factor: float = 1.0,
+               original_len: float = 0.0, slow: Optional[float] = None, fast: Optional[float] = None,
+               attn_factor: float = 0.0):
+    """(turns, factor): the pairs' frequencies as uint64 fractions of a turn per
+    position [rotary_dim / 2] (numpy, on the host) and what multiplies cosine
+    and sine (kvd_rope_table)."""
+    if scaling not in ROPE_SCALINGS:
+        raise ValueError(f"scaling must be one of {sorted(ROPE_SCALINGS)}, got {scaling!r}")
+    dslow, dfast = _ROPE_TURNS.get(scaling, (0.0, 0.0))
+    turns = np.zeros(max(int(rotary_dim) // 2, 1), np.uint64)
+    out = ctypes.c_float(0.0)
+    _check(load().kvd_rope_table(int(rotary_dim), float(base), ROPE_SCALINGS[scaling], float(factor),
+                                 float(original_len), float(dslow if slow is None else slow),
+                                 float(dfast if fast is None else fast), float(attn_factor),
+                                 turns.ctypes.data_as(ctypes.c_void_p), ctypes.byref(out)), "kvd_rope_table")
+    return turns, out.value
+
+
+class RopeTable:
+    """Rotary positions of one model, made once: the frequencies of rope_table
+    (same arguments) on `device`, adjacent pairs when `interleaved`, else halves."""
+
+    def __init__(self, rotary_dim: int, base: float = 10000.0, scaling: str = "none", factor: float = 1.0,
+                 original_len: float = 0.0, slow: Optional[float] = None, fast: Optional[float] = None,
+                 attn_factor: float = 0.0, interleaved: bool = False, device="cuda"):
+        import torch
+        turns, self.factor = rope_table(rotary_dim, base, scaling, factor, original_len, slow, fast, attn_factor)
+        self.rotary_dim, self.interleaved = int(rotary_dim), bool(interleaved)
+        self.turns = torch.from_numpy(turns.view(np.int64)).to(device)
+
+    def _c(self):
+        return _CRope(self.turns.data_ptr(), self.factor, self.rotary_dim, 1 if self.interleaved else 0)
+
+
+def _same_device(what, first, *others):
+    for t in others:
+        if t is not None and t.device != first.device:
+            raise ValueError(f"{what}: tensors on {first.device} and {t.device}")
+
+
+def _launch(fn, args, what, t, stream):
+    """Calls fn(*args, stream handle) with t's device current; without a stream, on that device's current one."""
+    import torch
+    with torch.cuda.device(t.device):
+        _check(fn(*args, _stream_handle(stream)), what)
+
+
+def _status_arg(status, what):
+    import torch
+    if status is not None:
+        _require(status, f"{what}: status", torch.int32)
+    return _ptr(status)
+
+
+def _rows(t, name, dtypes, what):
+    """[N, H, D] rows, or [B, T, H, D] as B * T of them, whose heads are contiguous:
+    (rows, heads, head_dim, elements between rows)."""
+    import torch
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be on a CUDA device")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} must be {dtypes}, got {t.dtype}")
+    if t.dim() not in (3, 4):
+        raise ValueError(f"{what}: {name} must be [N, H, D] or [B, T, H, D]")
+    H, D = t.shape[-2], t.shape[-1]
+    N = t.shape[0] if t.dim() == 3 else t.shape[0] * t.shape[1]
+    if t.numel() == 0:
+        return N, H, D, H * D
+    if t.stride(-1) != 1 or (H > 1 and t.stride(-2) != D):
+        raise ValueError(f"{what}: {name}'s heads must be contiguous")
+    step = t.stride(-3) if t.shape[-3] > 1 else (t.stride(0) if t.dim() == 4 and t.shape[0] > 1 else H * D)
+    if t.dim() == 4 and t.shape[0] > 1 and t.shape[1] > 1 and t.stride(0) != t.shape[1] * step:
+        raise ValueError(f"{what}: {name}'s rows must be evenly spaced")
+    return N, H, D, step
+
+
+def rope_apply(rope: RopeTable, x, positions, out, stream=None):
+    """out = x's rows turned by their positions: x, out [N, H, D] or [B, T, H, D],
+    bf16 or fp32 each, rows evenly spaced (slices of a fused projection may be
+    passed as they are); positions int32, one a row. out may be x."""
+    import torch
+    what, dts = "rope_apply", (torch.bfloat16, torch.float32)
+    N, H, D, xs = _rows(x, "x", dts, what)
+    No, Ho, Do, ys = _rows(out, "out", dts, what)
+    _require(positions, "positions", torch.int32)
+    if (No, Ho, Do) != (N, H, D) or positions.numel() != N:
+        raise ValueError(f"{what}: inconsistent shapes")
+    _same_device(what, x, out, positions, rope.turns)
+    if N == 0:
+        return
+    code = lambda t: OUT_BF16 if t.dtype == torch.bfloat16 else OUT_F32
+    _launch(load().kvd_rope_apply, [ctypes.byref(rope._c()), x.data_ptr(), xs, code(x), out.data_ptr(), ys, code(out),
+                                    positions.data_ptr(), N, H, D], "kvd_rope_apply", x, stream)
+
+
+def _new_rows_args(what, rope, q, q_out, k_new, v_new, pos, row_offsets, cache, others):
+    """(the arguments of kvd_kv_append_rope after the cache but for status and stream, [the rope struct kept alive])."""
+    import torch
+    bf = (torch.bfloat16,)
+    N, Hkv, D, ks = _rows(k_new, "k_new", bf, what)
+    Nv, Hv, Dv, vs = _rows(v_new, "v_new", bf, what)
+    _require(pos, "pos", torch.int32, 1)
+    B = pos.shape[0]
+    if (Nv, Hv, Dv) != (N, Hkv, D):
+        raise ValueError(f"{what}: inconsistent shapes")
+    if row_offsets is not None:
+        _require(row_offsets, "row_offsets", torch.int32, 1)
+        if row_offsets.shape[0] != B + 1:
+            raise ValueError(f"{what}: row_offsets must be [batch + 1]")
+    elif (N % B if B else N):
+        raise ValueError(f"{what}: {N} new rows for {B} sequences")
+    if (q is None) != (q_out is None):
+        raise ValueError(f"{what}: q and q_out go together")
+    if q is not None and rope is None:
+        raise ValueError(f"{what}: q needs a rope")
+    Hq, qs, qos = 0, 0, 0
+    if q is not None:
+        Nq, Hq, Dq, qs = _rows(q, "q", bf, what)
+        No, Ho, Do, qos = _rows(q_out, "q_out", bf, what)
+        if (Nq, Dq) != (N, D) or (No, Ho, Do) != (Nq, Hq, Dq):
+            raise ValueError(f"{what}: inconsistent shapes")
+    _same_device(what, cache, k_new, v_new, pos, row_offsets, q, q_out, None if rope is None else rope.turns, *others)
+    c = None if rope is None else rope._c()
+    return (N, Hkv, D), [None if c is None else ctypes.byref(c), _ptr(q), qs, _ptr(q_out), qos, k_new.data_ptr(), ks,
+                         v_new.data_ptr(), vs, pos.data_ptr(), _ptr(row_offsets), B, N, Hq, Hkv, D], c
+
+
+def kv_append_rope(rope: RopeTable, k, v, k_new, v_new, pos, *, q=None, q_out=None, k_scales=None, v_scales=None,
+                   block_table=None, row_offsets=None, status=None, stream=None):
+    """New rows into a cache as decode_ex takes it (k, v contiguous [B, S_max, Hkv,
+    D], or pools with block_table; bf16, or 8-bit codes with scales), keys
+    turned by their positions, and q turned into q_out (kvd_kv_append_rope).
+    k_new, v_new, q: [B, Hkv, D] or [B, T, H, D] at pos[b] + i, or with row_offsets
+    int32 [B + 1] the packed rows [N, H, D] of prompts of any lengths; rows evenly
+    spaced, so slices of a fused projection may be passed as they are."""
+    import torch
+    what = "kv_append_rope"
+    quant = k_scales is not None
+    dts = (torch.int8, torch.uint8, torch.float8_e4m3fn) if quant else (torch.bfloat16,)
+    for t, n in ((k, "k"), (v, "v")):
+        _require(t, n, dts, 4)
+    (N, Hkv, D), args, keep = _new_rows_args(what, rope, q, q_out, k_new, v_new, pos, row_offsets, k,
+                                             (v, k_scales, v_scales, block_table, status))
+    if v.shape != k.shape or v.dtype != k.dtype or k.shape[2:] != (Hkv, D):
+        raise ValueError(f"{what}: inconsistent shapes")
+    if quant:
+        _q8_args(k, v, k_scales, v_scales, "fp8" if _is_fp8(k) else "int8")
+    elif v_scales is not None:
+        raise ValueError(f"{what}: k_scales and v_scales go together")
+    c = _CCache()
+    c.k, c.v, c.k_scales, c.v_scales = k.data_ptr(), v.data_ptr(), _ptr(k_scales), _ptr(v_scales)
+    c.fp8 = 1 if quant and _is_fp8(k) else 0
+    if block_table is not None:
+        _require(block_table, "block_table", torch.int32, 2)
+        if block_table.shape[0] != pos.shape[0]:
+            raise ValueError(f"{what}: inconsistent shapes")
+        c.block_table, c.max_blocks = block_table.data_ptr(), block_table.shape[1]
+        c.page_size, c.num_pages = k.shape[1], k.shape[0]
+    else:
+        if k.shape[0] != pos.shape[0]:
+            raise ValueError(f"{what}: inconsistent shapes")
+        c.s_max = k.shape[1]
+    if N == 0:
+        return
+    _launch(load().kvd_kv_append_rope, [ctypes.byref(c), *args, _status_arg(status, what)], "kvd_kv_append_rope", k, stream)
+
+
+def fp4_block_bytes(head_dim: int) -> int:
+    """Bytes of an fp4 cache's block of 16 tokens of one KV head: 9 * head_dim + 16."""
+    n = int(load().kvd_fp4_block_bytes(int(head_dim)))
+    if n == 0:
+        raise ValueError(f"fp4 cache: head_dim must be 64, 128 or 256, got {head_dim}")
+    return n
+
+
+def alloc_cache_fp4(batch_or_pages: int, n_heads_kv: int, head_dim: int, tokens: int, device="cuda"):
+    """One fp4 tensor (K or V), zeroed: a contiguous cache of `tokens` (a multiple
+    of 16) per sequence, or a pool of pages of `tokens` each."""
+    import torch
+    if tokens < 16 or tokens % 16:
+        raise ValueError("fp4 cache: tokens must be a multiple of 16")
+    return torch.zeros(batch_or_pages, n_heads_kv, tokens // 16, fp4_block_bytes(head_dim), dtype=torch.uint8,
+                       device=device)
+
+
+def _fp4_cache(what, k, v, D, B, block_table):
+    """(struct kvd_cache_fp4, KV heads) of the blocks k and v (v may be None)."""
+    import torch
+    for t, n in ((k, "k"),) if v is None else ((k, "k"), (v, "v")):
+        _require(t, n, torch.uint8, 4)
+    if (v is not None and v.shape != k.shape) or k.shape[3] != fp4_block_bytes(D):
+        raise ValueError(f"{what}: inconsistent shapes")
+    c = _CCacheFp4()
+    c.k, c.v = k.data_ptr(), _ptr(v)
+    if block_table is not None:
+        _require(block_table, "block_table", torch.int32, 2)
+        if block_table.shape[0] != B:
+            raise ValueError(f"{what}: inconsistent shapes")
+        c.block_table, c.max_blocks = block_table.data_ptr(), block_table.shape[1]
+        c.page_size, c.num_pages = 16 * k.shape[2], k.shape[0]
+    else:
+        if k.shape[0] != B:
+            raise ValueError(f"{what}: inconsistent shapes")
+        c.s_max = 16 * k.shape[2]
+    return c, k.shape[1]
+
+
+def kv_append_fp4(k, v, k_new, v_new, pos, *, rope: Optional[RopeTable] = None, q=None, q_out=None, block_table=None,
+                  row_offsets=None, status=None, stream=None):
+    """kv_append_rope for an fp4 cache (k, v uint8 [B, Hkv, S_max / 16, 9 D + 16], or
+    pools [pages, Hkv, page / 16, 9 D + 16] with block_table); rope None appends
+    the rows as they are (kvd_kv_append_fp4)."""
+    what = "kv_append_fp4"
+    (N, Hkv, D), args, keep = _new_rows_args(what, rope, q, q_out, k_new, v_new, pos, row_offsets, k,
+                                             (v, block_table, status))
+    c, heads = _fp4_cache(what, k, v, D, pos.shape[0], block_table)
+    if heads != Hkv:
+        raise ValueError(f"{what}: inconsistent shapes")
+    if N == 0:
+        return
+    _launch(load().kvd_kv_append_fp4, [ctypes.byref(c), *args, _status_arg(status, what)], "kvd_kv_append_fp4", k, stream)
+
+
+def kv_quantize_fp4(cache, blocks, seq_lens, max_seq_len: int, stream=None):
+    """Rows t < seq_lens[b] of a bf16 cache [B, S_max, Hkv, D] (K or V) into the blocks
+    of a contiguous fp4 cache (kvd_kv_quantize_fp4)."""
+    import torch
+    what = "kv_quantize_fp4"
+    _require(cache, "cache", torch.bfloat16, 4)
+    _require(seq_lens, "seq_lens", torch.int32, 1)
+    B, S, Hkv, D = cache.shape
+    c, heads = _fp4_cache(what, blocks, None, D, B, None)
+    if heads != Hkv or seq_lens.shape != (B,):
+        raise ValueError(f"{what}: inconsistent shapes")
+    _same_device(what, cache, blocks, seq_lens)
+    if B == 0:
+        return
+    _launch(load().kvd_kv_quantize_fp4, [cache.data_ptr(), blocks.data_ptr(), seq_lens.data_ptr(), B, S, c.s_max,
+                                         int(max_seq_len), Hkv, D], "kvd_kv_quantize_fp4", cache, stream)
+
+
+def kv_read_fp4(blocks, out, seq_lens, max_seq_len: int, block_table=None, status=None, stream=None):
+    """Rows t < seq_lens[b] of an fp4 cache's K or V blocks (contiguous, or a pool
+    with block_table) back to bf16 out [B, S, Hkv, D], exactly (kvd_kv_read_fp4)."""
+    import torch
+    what = "kv_read_fp4"
+    _require(out, "out", torch.bfloat16, 4)
+    _require(seq_lens, "seq_lens", torch.int32, 1)
+    B, S, Hkv, D = out.shape
+    c, heads = _fp4_cache(what, blocks, None, D, B, block_table)
+    if heads != Hkv or seq_lens.shape != (B,):
+        raise ValueError(f"{what}: inconsistent shapes")
+    _same_device(what, out, blocks, seq_lens, block_table, status)
+    if B == 0:
+        return
+    _launch(load().kvd_kv_read_fp4, [blocks.data_ptr(), _ptr(block_table), c.s_max, c.max_blocks, c.page_size,
+                                     c.num_pages, out.data_ptr(), S, seq_lens.data_ptr(), B, int(max_seq_len), Hkv, D,
+                                     _status_arg(status, what)], "kvd_kv_read_fp4", out, stream)
+
+
+def decode_plan_fp4(batch: int, n_tokens: int, n_heads_q: int, n_heads_kv: int, head_dim: int, max_seq_len: int,
+                    num_sms: int = 0, n_split: int = 0) -> Tuple[int, int]:
+    """(n_split, workspace_bytes) for a decode_fp4 call of this shape."""
+    n = ctypes.c_int(0)
+    ws = ctypes.c_size_t(0)
+    _check(load().kvd_decode_plan_fp4(batch, n_tokens, n_heads_q, n_heads_kv, head_dim, max_seq_len, num_sms, n_split,
+                                      ctypes.byref(n), ctypes.byref(ws)), "kvd_decode_plan_fp4")
+    return n.value, ws.value
+
+
+def decode_fp4(q, k, v, seq_lens, max_seq_len: int, scale: float, out, *, block_table=None, k_new=None, v_new=None,
+               pos=None, workspace=None, n_split: int = 0, lse=None, status=None, stream=None):
+    """decode_ex over an fp4 cache (kvd_decode_fp4): q, out [B, Hq, D] or [B, T, Hq, D];
+    k, v uint8 [B, Hkv, S_max / 16, 9 D + 16], or pools [pages, Hkv, page / 16, 9 D + 16] with
+    block_table [B, max_blocks]; k_new, v_new ([B, Hkv, D] or [B, T, Hkv, D]) and
+    pos to append first. Workspace: decode_plan_fp4."""
+    import torch
+    what = "decode_fp4"
+    _require(q, "q", torch.bfloat16)
+    _require(out, "out", (torch.bfloat16, torch.float32))
+    _require(seq_lens, "seq_lens", torch.int32, 1)
+    if q.dim() not in (3, 4) or out.shape != q.shape:
+        raise ValueError(f"{what}: inconsistent shapes")
+    T = q.shape[1] if q.dim() == 4 else 1
+    B, Hq, D = q.shape[0], q.shape[-2], q.shape[-1]
+    c, Hkv = _fp4_cache(what, k, v, D, B, block_table)
+    if v is None or seq_lens.shape != (B,):
+        raise ValueError(f"{what}: inconsistent shapes")
+    if lse is not None:
+        _require(lse, "lse", torch.float32)
+        if lse.shape != q.shape[:-1]:
+            raise ValueError(f"{what}: lse must be shaped like q without its last dimension")
+    new = (k_new, v_new, pos)
+    if any(t is not None for t in new):
+        if any(t is None for t in new):
+            raise ValueError(f"{what}: k_new, v_new and pos go together")
+        _require(pos, "pos", torch.int32, 1)
+        for t, n in ((k_new, "k_new"), (v_new, "v_new")):
+            _require(t, n, torch.bfloat16, q.dim())
+            if t.shape != q.shape[:-2] + (Hkv, D):
+                raise ValueError(f"{what}: inconsistent shapes")
+        if pos.shape != (B,):
+            raise ValueError(f"{what}: inconsistent shapes")
+    _same_device(what, q, k, v, out, seq_lens, block_table, workspace, lse, status, *new)
+    ws_ptr, ws_bytes = (None, 0) if workspace is None else (workspace.data_ptr(),
+                                                           workspace.numel() * workspace.element_size())
+    if B == 0:
+        return
+    _launch(load().kvd_decode_fp4,
+            [ctypes.byref(c), q.data_ptr(), seq_lens.data_ptr(), B, T, int(max_seq_len), Hq, Hkv, D, float(scale),
+             int(n_split), ws_ptr, ws_bytes, out.data_ptr(), OUT_F32 if out.dtype == torch.float32 else OUT_BF16,
+             _ptr(lse), _ptr(k_new), _ptr(v_new), _ptr(pos), _status_arg(status, what)], "kvd_decode_fp4", q, stream)

@@ -5,6 +5,7 @@
 #include <cstring>
 
 #include "../../include/kvdecode.h"
+#include "api_common.h"
 #include "params.h"
 #include "schedule.cuh"
 
@@ -40,25 +41,12 @@ const ChunkKernel* find_chunk_kernel(int head_dim, int group, bool f32_out, bool
 
 namespace {
 
-constexpr int kMaxDevices = 64;
 std::atomic<int> g_num_sms[kMaxDevices];
 // Bit i % 64 of g_smem_ready[dev][i / 64] is set once kernel variant i may
 // use its dynamic shared memory size on device dev.
 std::atomic<uint64_t> g_smem_ready[kMaxDevices][2];
 
-bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
-
-// A byte range [p, p + n) of device memory; empty when n == 0.
-struct ByteRange {
-    const void* p;
-    size_t n;
-    bool overlaps(const ByteRange& o) const {
-        if (n == 0 || o.n == 0) return false;
-        const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(o.p);
-        return a < b + o.n && b < a + n;
-    }
-};
+}  // namespace
 
 kvd_status check_shape(int batch, int Hq, int Hkv, int D, kvd_out_dtype dt) {
     if (batch < 0 || Hq <= 0 || Hkv <= 0 || D <= 0) return KVD_ERR_INVALID_ARG;
@@ -68,6 +56,8 @@ kvd_status check_shape(int batch, int Hq, int Hkv, int D, kvd_out_dtype dt) {
     if (Hq / Hkv > KVD_MAX_GROUP) return KVD_ERR_UNSUPPORTED;
     return KVD_OK;
 }
+
+namespace {
 
 // Both forms of a variant share their launch shape and schedule geometry, so
 // planning and the host replica use the contiguous one. The split count is
@@ -85,8 +75,8 @@ struct QuantCache {
     bool fp8 = false;  // E4M3 codes rather than int8
 };
 
-// Paged cache arguments, checked; s_max of the contiguous calls becomes
-// max_blocks * page_size.
+}  // namespace
+
 kvd_status check_paged(const int32_t* block_table, int max_blocks, int page_size, int num_pages,
                        PagedCache* pg, int* s_max) {
     if (!block_table || !aligned(block_table, 4)) return KVD_ERR_INVALID_ARG;
@@ -116,6 +106,8 @@ kvd_status device_sms(int* sms) {
     return KVD_OK;
 }
 
+namespace {
+
 // Split count: one CTA per resident slot, but no fewer than two pipeline tiles
 // of work per CTA for short or small batches.
 int heuristic_split(const ChunkKernel* k, int batch, int Hkv, int max_len, int num_sms) {
@@ -126,12 +118,16 @@ int heuristic_split(const ChunkKernel* k, int batch, int Hkv, int max_len, int n
     return (int)std::max(1LL, std::min(slots, by_work));
 }
 
+}  // namespace
+
 size_t workspace_for(int n_split, int batch, int Hq, int Hkv, int D) {
     if (n_split <= 1 || batch == 0) return 0;
     const size_t P = (size_t)batch * Hkv, G = (size_t)(Hq / Hkv);
     const size_t slots = (size_t)n_split + P - 1;
     return align256(slots * G * D * sizeof(float)) + align256(slots * G * sizeof(float2));
 }
+
+namespace {
 
 kvd_status plan(int batch, int Hq, int Hkv, int D, int max_len, int num_sms, int n_split_req,
                 kvd_out_dtype dt, int* n_split, size_t* ws, const ChunkKernel** kern, int T = 1) {
@@ -172,6 +168,8 @@ struct AppendArgs {
     size_t copy_bytes = 0;
 };
 
+}  // namespace
+
 kvd_status check_append(void* k_cache, void* v_cache, const void* k_new, const void* v_new,
                         const int32_t* pos, int batch, int s_max, int Hkv, int D, const int32_t* status) {
     if (batch < 0 || s_max < 0 || Hkv <= 0 || D <= 0 || D % 8 != 0) return KVD_ERR_INVALID_ARG;
@@ -181,6 +179,8 @@ kvd_status check_append(void* k_cache, void* v_cache, const void* k_new, const v
         return KVD_ERR_INVALID_ARG;
     return KVD_OK;
 }
+
+namespace {
 
 kvd_status decode(int phase, const void* q, const void* k_cache, const void* v_cache,
                   const int32_t* seq_lens, int batch, int s_max, int max_seq_len, int Hq, int Hkv,

@@ -576,6 +576,113 @@ def decode_attention_multi(q, k_cache, v_cache, seq_lens, scale, n_threads: int 
     return out, lse
 
 
+# ---------------------------------------------------------------------------
+# Rotary positions and the fp4 cache (numpy, from their definitions)
+# ---------------------------------------------------------------------------
+
+def rope_phases(positions, turns):
+    """Angles in radians [N, R / 2], float64: the exact fraction of a turn
+    position * turns mod 2^64 (Python integers) times 2 pi."""
+    p = np.asarray(positions).reshape(-1)
+    out = np.empty((p.size, len(turns)))
+    for n, t in enumerate(p.tolist()):
+        out[n] = [((t * int(w)) % (1 << 64)) / 2.0 ** 64 for w in turns]
+    return out * (2.0 * np.pi)
+
+
+def rope(x, phases, factor, interleaved: bool):
+    """Rows x [N, H, D] (float64) turned by phases [N, R / 2]; columns past R copied."""
+    x = np.asarray(x, np.float64)
+    R = 2 * phases.shape[1]
+    c, s = factor * np.cos(phases)[:, None, :], factor * np.sin(phases)[:, None, :]
+    y = x.copy()
+    ia, ib = (np.arange(0, R, 2), np.arange(1, R, 2)) if interleaved else (np.arange(R // 2), np.arange(R // 2, R))
+    a, b = x[..., ia], x[..., ib]
+    y[..., ia] = a * c - b * s
+    y[..., ib] = b * c + a * s
+    return y
+
+
+E2M1 = np.array([0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0])
+
+
+def _nearest_even(grid, x):
+    """Index of the nearest value of an ascending grid, ties to the even index, saturating."""
+    hi = np.clip(np.searchsorted(grid, x), 1, len(grid) - 1)
+    lo = hi - 1
+    d, u = x - grid[lo], grid[hi] - x
+    return np.where((d < u) | ((d == u) & (lo % 2 == 0)), lo, hi)
+
+
+def quantize_fp4(bits):
+    """bf16 rows [..., D] (bit patterns) -> (codes uint8 [..., D] 0..15, scale bytes
+    uint8 [..., D / 16], exponent bytes uint8 [...]), with the definition's float32 steps."""
+    from workloads import bf16_bits_to_f32
+    x = bf16_bits_to_f32(bits).astype(np.float32)
+    D = x.shape[-1]
+    a = np.abs(x).max(-1).astype(np.float64)
+    e = np.full(a.shape, -126, np.int64)
+    for _ in range(2 ** 8):  # the smallest e with a <= 2688 * 2^e, by its definition
+        grow = a > 2688.0 * np.exp2(e.astype(np.float64))
+        if not grow.any():
+            break
+        e = e + grow
+    y = (x * np.exp2(-e).astype(np.float32)[..., None]).reshape(x.shape[:-1] + (D // 16, 16))
+    m = np.abs(y).max(-1) * np.float32(1.0 / 6.0)
+    grid = np.array([e4m3_value(c) for c in range(127)])
+    sb = _nearest_even(grid, m.astype(np.float64)).astype(np.uint8)
+    sv = grid[sb].astype(np.float32)
+    inv = np.where(sv > 0, np.float32(1.0) / np.where(sv > 0, sv, np.float32(1.0)), np.float32(0.0)).astype(np.float32)
+    z = (y * inv[..., None]).astype(np.float32)
+    mag = _nearest_even(E2M1, np.abs(z).astype(np.float64))
+    codes = (mag + 8 * ((z < 0) & (mag > 0))).astype(np.uint8).reshape(x.shape)
+    exps = np.where(a > 0, e + 127, 0).astype(np.uint8)
+    return codes, sb, exps
+
+
+def dequantize_fp4(codes, sb, exps):
+    """float64 rows code * scale * 2^(exponent byte - 127)."""
+    grid = np.array([e4m3_value(c) for c in range(127)] + [np.nan])
+    val = np.where(codes & 8, -1.0, 1.0) * E2M1[codes & 7]
+    s = grid[sb & 127] * np.where(sb & 128, -1.0, 1.0)
+    return val * np.repeat(s, 16, axis=-1) * np.exp2(exps.astype(np.float64) - 127.0)[..., None]
+
+
+def pack_fp4(codes, sb, exps):
+    """Blocks uint8 [..., S / 16, 9 D + 16] of rows [..., S, D]."""
+    S, D = codes.shape[-2:]
+    out = np.zeros(codes.shape[:-2] + (S // 16, 9 * D + 16), np.uint8)
+    W = min(D, 128)
+    for t in range(S):
+        blk, r = out[..., t // 16, :], t % 16
+        for c in range(0, D, W):
+            part = codes[..., t, c:c + W]
+            at = (c // W) * 16 * (W // 2) + r * (W // 2)
+            blk[..., at:at + W // 2] = part[..., 0::2] | (part[..., 1::2] << 4)
+        blk[..., 8 * D + r * (D // 16):8 * D + (r + 1) * (D // 16)] = sb[..., t, :]
+        blk[..., 9 * D + r] = exps[..., t]
+    return out
+
+
+def unpack_fp4(blocks, D):
+    """(codes, scale bytes, exponent bytes) of blocks [..., S / 16, 9 D + 16]."""
+    n = blocks.shape[-2]
+    S, W = 16 * n, min(D, 128)
+    codes = np.zeros(blocks.shape[:-2] + (S, D), np.uint8)
+    sb = np.zeros(blocks.shape[:-2] + (S, D // 16), np.uint8)
+    exps = np.zeros(blocks.shape[:-2] + (S,), np.uint8)
+    for t in range(S):
+        blk, r = blocks[..., t // 16, :], t % 16
+        for c in range(0, D, W):
+            at = (c // W) * 16 * (W // 2) + r * (W // 2)
+            part = blk[..., at:at + W // 2]
+            codes[..., t, c:c + W:2] = part & 15
+            codes[..., t, c + 1:c + W:2] = part >> 4
+        sb[..., t, :] = blk[..., 8 * D + r * (D // 16):8 * D + (r + 1) * (D // 16)]
+        exps[..., t] = blk[..., 9 * D + r]
+    return codes, sb, exps
+
+
 def max_threads(lib=None) -> int:
     lib = lib or _load()
     return int(lib.kvo_max_threads())

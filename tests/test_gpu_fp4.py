@@ -1,0 +1,398 @@
+"""The fp4 KV cache on the GPU: quantizer and reader bit for bit against the
+oracle, attention over the rows read back against float64.
+
+Tolerances (assert_close's): fp32 output 1e-4, bf16 output 1e-2 or half a step
+plus the weights' rounding. The kernel's weights carry f16's 2^-11 (half a step,
+bf16 output), the fp32 output's 2^-22, so both lie inside them; scores are fp32
+sums of at most 256 products of |q| <= ~5 with |k| <= ~5, times scale
+<= 1/8: within 256 * 25 / 8 * 2^-24 < 5e-5 absolute, a relative weight error of the same
+size, spread over outputs of size 1."""
+import math
+
+import numpy as np
+import pytest
+
+import oracle
+from gpu_helpers import assert_close, bf16_tensor_bits, cuda_or_skip, guarded, guards_intact, to_dev_bf16
+from workloads import bf16_bits_to_f32, f32_to_bf16_bits
+
+pytestmark = pytest.mark.gpu
+
+
+def _rows(r, shape, spread=0.0):
+    x = r.standard_normal(shape).astype(np.float32)
+    if spread:
+        x *= np.exp2(r.uniform(-spread, spread, shape[:-1] + (1,))).astype(np.float32)
+    return f32_to_bf16_bits(x)
+
+
+def _blocks(bits):
+    """(blocks [B, Hkv, S / 16, ...], float64 rows [B, S, Hkv, D]) of bf16 rows [B, S, Hkv, D]."""
+    c = oracle.quantize_fp4(np.ascontiguousarray(bits.transpose(0, 2, 1, 3)))
+    return oracle.pack_fp4(*c), np.ascontiguousarray(oracle.dequantize_fp4(*c).transpose(0, 2, 1, 3))
+
+
+def _poison(blocks, lens, D):
+    """Rows past each length get codes, scales and exponents of all ones (NaN scales)."""
+    codes, sb, exps = oracle.unpack_fp4(blocks, D)
+    for b, L in enumerate(lens):
+        codes[b, :, L:], sb[b, :, L:], exps[b, :, L:] = 15, 255, 255
+    return oracle.pack_fp4(codes, sb, exps)
+
+
+class Case:
+    def __init__(self, seed, Hq, Hkv, D, lens, T=1, page=0, spread=0.0, dev=None):
+        import torch
+        r = np.random.default_rng(seed)
+        self.T, self.D, self.Hq, self.Hkv, self.page = T, D, Hq, Hkv, page
+        B, step = len(lens), page or 16
+        self.lens = np.asarray(lens, np.int32)
+        S = max(step, -(-max(max(lens), 1) // step) * step)
+        self.S, self.B = S, B
+        self.scale = float(np.float32(D ** -0.5))
+        self.q = _rows(r, (B, T, Hq, D))
+        kb, self.kd = _blocks(_rows(r, (B, S, Hkv, D), spread))
+        vb, self.vd = _blocks(_rows(r, (B, S, Hkv, D), spread))
+        kb, vb = _poison(kb, self.lens, D), _poison(vb, self.lens, D)
+        self.bt = None
+        if page:
+            nb = S // page
+            table = r.permutation(B * nb + 3)[:B * nb].reshape(B, nb).astype(np.int32)
+            pool = [np.full((B * nb + 3, Hkv, page // 16, 9 * D + 16), 255, np.uint8) for _ in range(2)]
+            for b in range(B):
+                for j in range(nb):
+                    for p, x in zip(pool, (kb, vb)):
+                        p[table[b, j]] = x[b, :, j * (page // 16):(j + 1) * (page // 16)]
+            for b in range(B):  # entries of blocks past the length name nothing
+                table[b, -(-int(self.lens[b]) // page):] = -7
+            kb, vb = pool
+            self.bt = torch.from_numpy(table).to(dev)
+        self.k, self.v = torch.from_numpy(kb).to(dev), torch.from_numpy(vb).to(dev)
+        self.qd = to_dev_bf16(self.q, dev)
+        self.lens_d = torch.from_numpy(self.lens).to(dev)
+
+    def run(self, kvd, torch, dev, dtype, n_split=0, max_len=None, q=None):
+        B, T, Hq, D = self.q.shape
+        mx = self.S if max_len is None else max_len
+        full, out = guarded((B, T, Hq, D), torch.bfloat16 if dtype == "bf16" else torch.float32, dev)
+        lfull, lse = guarded((B, T, Hq), torch.float32, dev)
+        _, n = kvd.decode_plan_fp4(B, T, Hq, self.Hkv, D, mx, 0, n_split)
+        ws = torch.full((n + 512,), 0xa5, dtype=torch.uint8, device=dev)
+        self.status = torch.zeros(1, dtype=torch.int32, device=dev)
+        kvd.decode_fp4(self.qd if q is None else q, self.k, self.v, self.lens_d, mx, self.scale, out, block_table=self.bt,
+                       workspace=ws[:n] if n else None, n_split=n_split, lse=lse, status=self.status)
+        torch.cuda.synchronize()
+        assert guards_intact(full) and guards_intact(lfull) and bool((ws[n:] == 0xa5).all())
+        got = bf16_bits_to_f32(bf16_tensor_bits(out)) if dtype == "bf16" else out.cpu().numpy()
+        return got.astype(np.float64), lse.cpu().numpy().astype(np.float64)
+
+    def want(self):
+        outs, lses = [], []
+        for i in range(self.T):
+            L = np.clip(self.lens - self.T + 1 + i, 0, None).astype(np.int32)
+            o, l = oracle.decode_attention_f64kv(self.q[:, i], self.kd, self.vd, L, self.scale)
+            outs.append(o)
+            lses.append(l)
+        return np.stack(outs, 1), np.stack(lses, 1)
+
+    def check(self, kvd, torch, dev, dtype, **kw):
+        got, lse = self.run(kvd, torch, dev, dtype, **kw)
+        want, wl = self.want()
+        assert int(self.status.item()) == 0
+        assert_close(got, want, dtype, "fp4")
+        none = np.isneginf(wl)
+        assert np.array_equal(np.isneginf(lse), none) and np.abs(lse[~none] - wl[~none]).max(initial=0.0) < 1e-4
+        assert (got[none] == 0).all()
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_quantize_and_read(D):
+    import torch
+    import kv_cache_decode_gb300 as kvd
+    dev = cuda_or_skip()
+    r = np.random.default_rng(D)
+    B, S, Hkv = 5, 48, 3
+    bits = _rows(r, (B, S, Hkv, D), 12.0)
+    bits[0, 3] = 0
+    bits[1, 2, 0, :16] = 0
+    lens = np.array([48, 17, 0, 33, 60], np.int32)  # the last is clamped
+    blocks = torch.full((B, Hkv, 4, 9 * D + 16), 0x5a, dtype=torch.uint8, device=dev)  # a longer cache
+    kvd.kv_quantize_fp4(to_dev_bf16(bits, dev), blocks, torch.from_numpy(lens).to(dev), S)
+    torch.cuda.synchronize()
+    want, rows = _blocks(bits)
+    want = np.concatenate([want, np.full((B, Hkv, 1, 9 * D + 16), 0x5a, np.uint8)], 2)
+    old = [a.copy() for a in oracle.unpack_fp4(np.full_like(want, 0x5a), D)]
+    new = oracle.unpack_fp4(want, D)
+    for b in range(B):
+        for o, n in zip(old, new):
+            o[b, :, :min(lens[b], S)] = n[b, :, :min(lens[b], S)]
+    assert np.array_equal(blocks.cpu().numpy(), oracle.pack_fp4(*old))
+    # back: contiguous, then the same rows in pages
+    out = torch.full((B, S + 7, Hkv, D), 3.0, dtype=torch.bfloat16, device=dev)
+    ld = torch.from_numpy(lens).to(dev)
+    kvd.kv_read_fp4(blocks, out, ld, S)
+    torch.cuda.synchronize()
+    exp = np.full((B, S + 7, Hkv, D), 3.0)
+    for b in range(B):
+        exp[b, :min(lens[b], S)] = rows[b, :min(lens[b], S)]
+    assert np.array_equal(out.double().cpu().numpy(), exp)
+    table = torch.randperm(B * 4 + 2, device=dev)[:B * 4].view(B, 4).int()
+    pool = torch.zeros(B * 4 + 2, Hkv, 1, 9 * D + 16, dtype=torch.uint8, device=dev)
+    pool[table.long()] = blocks.transpose(1, 2).unsqueeze(3)
+    table[2] = -1  # an empty sequence's entries are not looked at
+    table[3, 1] = 1 << 20
+    exp[3, 16:32] = 0
+    out.fill_(3.0)
+    status = torch.zeros(1, dtype=torch.int32, device=dev)
+    kvd.kv_read_fp4(pool, out, ld, S, block_table=table, status=status)
+    torch.cuda.synchronize()
+    assert int(status.item()) == kvd.STATUS_BAD_PAGE
+    assert np.array_equal(out.double().cpu().numpy(), exp)
+
+
+LENS = [0, 1, 2, 15, 16, 17, 31, 32, 33, 63, 64, 65, 200, 257, 300]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("Hq,Hkv,D", [(8, 1, 128), (32, 8, 128), (3, 3, 64), (9, 1, 64), (48, 1, 256), (5, 1, 256), (16, 1, 128),
+                                      (64, 1, 128), (40, 2, 64)])
+def test_attention(Hq, Hkv, D, dtype):
+    import torch
+    import kv_cache_decode_gb300 as kvd
+    dev = cuda_or_skip()
+    c = Case(Hq * D, Hq, Hkv, D, LENS, dev=dev)
+    c.check(kvd, torch, dev, dtype)
+    for n in (1, 2, 7, 600):  # every cut of the line gives the same answer
+        c.check(kvd, torch, dev, dtype, n_split=n)
+
+
+@pytest.mark.parametrize("page", [16, 32, 128])
+@pytest.mark.parametrize("Hq,Hkv,D,T", [(8, 2, 128, 1), (24, 1, 64, 1), (6, 1, 256, 1), (8, 2, 128, 3), (12, 3, 64, 7), (4, 1, 256, 64)])
+def test_attention_paged_multi(page, Hq, Hkv, D, T):
+    import torch
+    import kv_cache_decode_gb300 as kvd
+    dev = cuda_or_skip()
+    c = Case(page + T, Hq, Hkv, D, [300, 0, 1, T, 16, 47, 129], T=T, page=page, dev=dev)
+    c.check(kvd, torch, dev, "f32")
+    c.check(kvd, torch, dev, "bf16", n_split=5)
+
+
+@pytest.mark.parametrize("Hq,Hkv,D,lens", [(8, 1, 128, [70001]), (4, 4, 64, [5000, 1, 12345]), (48, 1, 256, [9000, 4097]),
+                                           (8, 8, 128, [3] * 200)])
+def test_attention_long_and_many(Hq, Hkv, D, lens):
+    import torch
+    import kv_cache_decode_gb300 as kvd
+    dev = cuda_or_skip()
+    r = np.random.default_rng(1)
+    c = Case(7, Hq, Hkv, D, lens, page=16, dev=dev)
+    c.check(kvd, torch, dev, "f32")
+    c.check(kvd, torch, dev, "bf16")
+
+
+def test_magnitudes():
+    """Rows whose sizes lie up to 2^60 apart, queries far below and above f16's range: the f16 weights
+    keep their precision, checked relative to the terms that make up each output."""
+    import torch
+    import kv_cache_decode_gb300 as kvd
+    dev = cuda_or_skip()
+    c = Case(31, 8, 2, 128, [200, 333, 40], dev=dev, spread=0.0)
+    r = np.random.default_rng(5)
+    # value rows spread over 2^+-30
+    vb, c.vd = _blocks(_rows(r, (c.B, c.S, 2, 128), 30.0))
+    c.v = torch.from_numpy(_poison(vb, c.lens, 128)).to(dev)
+    # queries times 2^-40, keys times 2^40
+    kb, c.kd = _blocks(f32_to_bf16_bits(bf16_bits_to_f32(_rows(r, (c.B, c.S, 2, 128))) * np.float32(2.0 ** 40)))
+    c.k = torch.from_numpy(_poison(kb, c.lens, 128)).to(dev)
+    c.q = f32_to_bf16_bits(bf16_bits_to_f32(c.q) * np.float32(2.0 ** -40))
+    c.qd = to_dev_bf16(c.q, dev)
+    got, lse = c.run(kvd, torch, dev, "f32")
+    want, wl = c.want()
+    mag, _ = oracle.decode_attention_f64kv(c.q[:, 0], c.kd, np.abs(c.vd), c.lens, c.scale)
+    # weights to 2^-22 and scores to 5e-5, relative to sum_t w_t |v_t|
+    assert (np.abs(got[:, 0] - want[:, 0]) <= 1e-4 * mag).all()
+    assert np.abs(lse - wl).max() < 1e-4
+    got, _ = c.run(kvd, torch, dev, "bf16")
+    # bf16 output: f16 weights 2^-11 and half a bf16 step besides
+    assert (np.abs(got[:, 0] - want[:, 0]) <= (1e-4 + 2.0 ** -10) * mag + np.abs(want[:, 0]) * 2.0 ** -8).all()
+
+
+def test_rising_scores():
+    """Scores that keep rising along the sequence raise the running maxima again and again."""
+    import torch
+    import kv_cache_decode_gb300 as kvd
+    dev = cuda_or_skip()
+    c = Case(3, 8, 1, 64, [700], dev=dev)
+    q = np.zeros((1, 1, 8, 64), np.float32)
+    q[..., 0] = 8.0
+    k = np.random.default_rng(0).standard_normal((1, c.S, 1, 64)).astype(np.float32) * 0.1
+    k[0, :, 0, 0] = np.arange(c.S) * 0.5
+    kb, c.kd = _blocks(f32_to_bf16_bits(k))
+    c.k = torch.from_numpy(_poison(kb, c.lens, 64)).to(dev)
+    c.q = f32_to_bf16_bits(q)
+    c.qd = to_dev_bf16(c.q, dev)
+    got, lse = c.run(kvd, torch, dev, "f32", n_split=3)
+    want, wl = c.want()
+    # scores up to 350: fp32 sums of that size are off by 2^-24 * 350 * a few
+    assert np.abs(got - want).max() < 1e-3 and np.abs(lse - wl).max() < 1e-3
+
+
+def test_status_and_clamp():
+    import torch
+    import kv_cache_decode_gb300 as kvd
+    dev = cuda_or_skip()
+    c = Case(9, 8, 2, 128, [100, 64, 90], page=16, dev=dev)
+    # one block of sequence 1 names no page: zero rows
+    c.bt[1, 2] = 99999
+    c.kd[1, 32:48] = c.vd[1, 32:48] = 0
+    got, _ = c.run(kvd, torch, dev, "f32")
+    assert int(c.status.item()) == kvd.STATUS_BAD_PAGE
+    assert_close(got, c.want()[0], "f32", "bad page")
+    # lengths past max_seq_len and below zero are clamped
+    c = Case(9, 8, 2, 128, [100, 64, 90], dev=dev)
+    c.lens = np.array([80, 64, 0], np.int32)
+    c.lens_d = torch.tensor([2 ** 31 - 1, 64, -5], dtype=torch.int32, device=dev)
+    got, _ = c.run(kvd, torch, dev, "f32", max_len=80)
+    assert int(c.status.item()) == kvd.STATUS_SEQ_LEN_CLAMPED
+    assert_close(got, c.want()[0], "f32", "clamped")
+
+
+def test_step_equals_append_then_attention():
+    import torch
+    import kv_cache_decode_gb300 as kvd
+    dev = cuda_or_skip()
+    for T, page in ((1, 0), (1, 16), (4, 64)):
+        c = Case(12 + T, 16, 4, 128, [300, 17, 100], T=T, page=page, dev=dev)
+        r = np.random.default_rng(2)
+        kn, vn = (to_dev_bf16(_rows(r, (c.B, T, 4, 128)), dev) for _ in range(2))
+        pos = c.lens_d - T
+        if c.T == 1:
+            kn, vn = kn[:, 0], vn[:, 0]
+        _, n = kvd.decode_plan_fp4(c.B, T, 16, 4, 128, c.S)
+        ws = torch.empty(max(n, 1), dtype=torch.uint8, device=dev)
+        q = c.qd if T > 1 else c.qd[:, 0]
+        k1, v1, k2, v2 = c.k.clone(), c.v.clone(), c.k.clone(), c.v.clone()
+        a, b = torch.empty_like(q), torch.empty_like(q)
+        kvd.kv_append_fp4(k1, v1, kn, vn, pos, block_table=c.bt)
+        kvd.decode_fp4(q, k1, v1, c.lens_d, c.S, c.scale, a, block_table=c.bt, workspace=ws)
+        kvd.decode_fp4(q, k2, v2, c.lens_d, c.S, c.scale, b, block_table=c.bt, workspace=ws, k_new=kn, v_new=vn, pos=pos)
+        torch.cuda.synchronize()
+        assert torch.equal(k1, k2) and torch.equal(v1, v2) and torch.equal(a, b)
+
+
+def test_empty_batch():
+    import torch
+    import kv_cache_decode_gb300 as kvd
+    dev = cuda_or_skip()
+    q = torch.empty(0, 8, 128, dtype=torch.bfloat16, device=dev)
+    k = kvd.alloc_cache_fp4(0, 2, 128, 64, device=dev)
+    lens = torch.empty(0, dtype=torch.int32, device=dev)
+    kvd.decode_fp4(q, k, k.clone(), lens, 64, 0.1, torch.empty_like(q))
+    kvd.kv_quantize_fp4(torch.empty(0, 64, 2, 128, dtype=torch.bfloat16, device=dev), k, lens, 64)
+    kvd.kv_append_fp4(k, k.clone(), q[:, :2], q[:, :2], lens)
+
+
+def test_layers_together_in_a_graph():
+    """A few layers' steps as a serving loop runs them: queries and keys turned and appended into a paged fp4
+    cache, attention over it, several steps, captured once and replayed; against the oracle."""
+    import torch
+    import kv_cache_decode_gb300 as kvd
+    dev = cuda_or_skip()
+    B, Hq, Hkv, D, page, layers, steps = 3, 8, 2, 128, 16, 2, 20
+    S, scale = 96, float(np.float32(128 ** -0.5))
+    g = torch.Generator(device=dev).manual_seed(1)
+    rope = kvd.RopeTable(64, scaling="linear", factor=2.0, device=dev)
+    start = torch.tensor([40, 3, 11], dtype=torch.int32, device=dev)
+    off = torch.tensor([0, 40, 43, 54], dtype=torch.int32, device=dev)
+    nb = S // page
+    bt = torch.randperm(B * nb, generator=g, device=dev).view(B, nb).int()
+    k = [kvd.alloc_cache_fp4(B * nb, Hkv, D, page, device=dev) for _ in range(layers)]
+    v = [kvd.alloc_cache_fp4(B * nb, Hkv, D, page, device=dev) for _ in range(layers)]
+    zero = torch.zeros(B, dtype=torch.int32, device=dev)
+    width = (Hq + 2 * Hkv) * D
+    seen = [[[], []] for _ in range(layers)]  # rotated keys and values, [rows of the prompt] then steps
+
+    def split(x):
+        return (x[:, :Hq * D].view(-1, Hq, D), x[:, Hq * D:(Hq + Hkv) * D].view(-1, Hkv, D), x[:, (Hq + Hkv) * D:].view(-1, Hkv, D))
+    prompt_pos = torch.cat([torch.arange(int(n), device=dev) for n in start]).int()
+    for i in range(layers):  # the prompts, packed
+        fused = torch.randn(54, width, generator=g, device=dev).bfloat16()
+        _, kn, vn = split(fused)
+        kvd.kv_append_fp4(k[i], v[i], kn, vn, zero, rope=rope, block_table=bt, row_offsets=off)
+        kr = torch.empty_like(kn, memory_format=torch.contiguous_format)
+        kvd.rope_apply(rope, kn, prompt_pos, kr)
+        seen[i][0].append(kr.cpu())
+        seen[i][1].append(vn.cpu())
+    pos, lens = start.clone(), start + 1
+    fused = [torch.zeros(B, width, device=dev, dtype=torch.bfloat16) for _ in range(layers)]
+    q_rot = [torch.empty(B, Hq, D, device=dev, dtype=torch.bfloat16) for _ in range(layers)]
+    out = [torch.empty(B, Hq, D, device=dev) for _ in range(layers)]
+    ws = [torch.empty(max(kvd.decode_plan_fp4(B, 1, Hq, Hkv, D, S)[1], 1), device=dev, dtype=torch.uint8) for _ in range(layers)]
+
+    def step():
+        for i in range(layers):
+            q, kn, vn = split(fused[i])
+            kvd.kv_append_fp4(k[i], v[i], kn, vn, pos, rope=rope, q=q, q_out=q_rot[i], block_table=bt)
+            kvd.decode_fp4(q_rot[i], k[i], v[i], lens, S, scale, out[i], block_table=bt, workspace=ws[i])
+        pos.add_(1)
+        lens.add_(1)
+    draws = [[torch.randn(B, width, generator=g, device=dev).bfloat16() for _ in range(layers)] for _ in range(steps)]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    for s in range(steps):
+        for i in range(layers):
+            fused[i].copy_(draws[s][i])
+        at = pos.clone()
+        if s == 0:
+            with torch.cuda.stream(side):
+                side.wait_stream(torch.cuda.default_stream())
+                step()
+            torch.cuda.current_stream().wait_stream(side)
+            torch.cuda.synchronize()
+            with torch.cuda.graph(graph):
+                step()
+        else:
+            graph.replay()
+        torch.cuda.synchronize()
+        for i in range(layers):
+            q, kn, vn = split(draws[s][i])
+            kr, qr = torch.empty(B, Hkv, D, device=dev, dtype=torch.bfloat16), torch.empty(B, Hq, D, device=dev, dtype=torch.bfloat16)
+            kvd.rope_apply(rope, kn, at, kr)
+            kvd.rope_apply(rope, q, at, qr)
+            seen[i][0].append(kr.cpu())
+            seen[i][1].append(vn.cpu())
+            if s not in (0, 1, steps - 1):
+                continue
+            kd, vd = np.zeros((B, S, Hkv, D)), np.zeros((B, S, Hkv, D))
+            L = (at + 1).cpu().numpy().astype(np.int32)
+            for which, dst in ((0, kd), (1, vd)):
+                for b in range(B):
+                    lo, hi = int(off[b]), int(off[b + 1])
+                    rows = torch.cat([seen[i][which][0][lo:hi]] + [x[b:b + 1] for x in seen[i][which][1:]])
+                    assert rows.shape[0] == L[b]
+                    dst[b, :L[b]] = oracle.dequantize_fp4(*oracle.quantize_fp4(bf16_tensor_bits(rows)))
+            want, _ = oracle.decode_attention_f64kv(bf16_tensor_bits(qr), kd, vd, L, scale)
+            assert_close(out[i].cpu().numpy().astype(np.float64), want, "f32", f"layer {i} step {s}")
+
+
+def test_two_streams():
+    """Two steps at once on two streams, each with its own workspace, give what they give alone."""
+    import torch
+    import kv_cache_decode_gb300 as kvd
+    dev = cuda_or_skip()
+    cs = [Case(20 + i, 32, 8, 128, [2000, 1500, 999], dev=dev) for i in range(2)]
+    ws = [torch.empty(kvd.decode_plan_fp4(c.B, 1, 32, 8, 128, c.S)[1] + 1, dtype=torch.uint8, device=dev) for c in cs]
+    alone = []
+    for c, w in zip(cs, ws):
+        out = torch.empty_like(c.qd)
+        kvd.decode_fp4(c.qd, c.k, c.v, c.lens_d, c.S, c.scale, out, workspace=w)
+        torch.cuda.synchronize()
+        alone.append(out)
+    streams = [torch.cuda.Stream() for _ in cs]
+    outs = [torch.zeros_like(c.qd) for c in cs]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for c, w, o, s in zip(cs, ws, outs, streams):
+            kvd.decode_fp4(c.qd, c.k, c.v, c.lens_d, c.S, c.scale, o, workspace=w, stream=s)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, o) for a, o in zip(alone, outs))

@@ -1,0 +1,303 @@
+"""Rotary positions and the rotating appends on the GPU: rope_apply against
+float64 (phases in exact integers), the appends bit for bit against rope_apply
+followed by the oracle's placement and quantizers.
+
+Tolerance of rope_apply, per element, for the pair (a, b) and factor f: the
+phase's 24 bits move the angle by at most 2^-25 pi, sincospif is within 2 units in
+the last place (2^-23 of a value up to 1), the factor's product, the inner product
+and the fused sum round once each (2^-24): |f| (|a| + |b|) (2^-25 pi + 2^-23 +
+3 * 2^-24) < 4.0e-7 |f| (|a| + |b|), and a bf16 result half a step of itself more."""
+import numpy as np
+import pytest
+
+import oracle
+from gpu_helpers import bf16_tensor_bits, cuda_or_skip
+from workloads import bf16_bits_to_f32
+
+pytestmark = pytest.mark.gpu
+
+
+def _check(got, x, ph, factor, inter, dtype):
+    import torch
+    want = oracle.rope(x, ph, factor, inter)
+    R = 2 * ph.shape[1]
+    pair = np.zeros_like(x)
+    ia, ib = (np.arange(0, R, 2), np.arange(1, R, 2)) if inter else (np.arange(R // 2), np.arange(R // 2, R))
+    pair[..., ia] = pair[..., ib] = np.abs(x[..., ia]) + np.abs(x[..., ib])
+    tol = 4.0e-7 * factor * pair
+    if dtype == torch.bfloat16:
+        tol = tol + np.abs(want) * (torch.finfo(dtype).eps / 2) * (1 + 1e-6) + 1e-40
+    bad = np.abs(got - want) > tol
+    assert not bad.any(), (int(bad.sum()), float(np.abs(got - want)[bad].max()))
+
+
+@pytest.mark.parametrize("D,R,H,N,inter", [
+    (128, 128, 32, 64, False), (128, 64, 40, 7, True), (64, 64, 1, 1, False), (256, 256, 48, 3, True), (80, 16, 5, 33, False),
+    (80, 80, 2, 9, True), (72, 48, 3, 11, False), (128, 16, 8, 650, False), (1024, 256, 1, 5, False), (192, 112, 7, 5000, True),
+])
+def test_rope_apply(D, R, H, N, inter):
+    import torch
+    import kv_cache_decode_gb300 as kvd
+    dev = cuda_or_skip()
+    rope = kvd.RopeTable(R, scaling="parts", factor=16.0, original_len=4096, interleaved=inter, device=dev)
+    turns = rope.turns.cpu().numpy().view(np.uint64)
+    g = torch.Generator(device=dev).manual_seed(D + N)
+    pos = torch.randint(-5, 1 << 20, (N,), generator=g, device=dev).int()
+    edge = torch.tensor([0, -1, 2 ** 31 - 1, -2 ** 31, 1], dtype=torch.int32, device=dev)[:N]
+    pos[:edge.numel()] = edge
+    ph = oracle.rope_phases(pos.cpu().numpy(), turns)
+    for idt in (torch.bfloat16, torch.float32):
+        x = torch.randn(N, H, D, generator=g, device=dev).to(idt)
+        x[0, 0, :4] = 0
+        for odt in (torch.bfloat16, torch.float32):
+            out = torch.full_like(x, float("nan"), dtype=odt)
+            kvd.rope_apply(rope, x, pos, out)
+            torch.cuda.synchronize()
+            _check(out.double().cpu().numpy(), x.double().cpu().numpy(), ph, rope.factor, inter, odt)
+            if R < D and odt == idt:  # the other columns are copied
+                assert torch.equal(out[..., R:], x[..., R:])
+        y = x.clone()  # in place: the same bits
+        out = torch.empty_like(x)
+        kvd.rope_apply(rope, x, pos, out)
+        kvd.rope_apply(rope, y, pos, y)
+        torch.cuda.synchronize()
+        assert torch.equal(y, out)
+
+
+def test_rope_apply_strided_and_turned_back():
+    import torch
+    import kv_cache_decode_gb300 as kvd
+    dev = cuda_or_skip()
+    rope = kvd.RopeTable(64, device=dev)
+    N, H, D = 37, 6, 128
+    g = torch.Generator(device=dev).manual_seed(5)
+    wide = torch.randn(N, 10 * D, generator=g, device=dev)
+    x = wide[:, 2 * D:8 * D].view(N, H, D)
+    pos = torch.randint(0, 1 << 17, (N,), generator=g, device=dev).int()
+    keep = wide.clone()
+    ref = torch.empty(N, H, D, device=dev)
+    kvd.rope_apply(rope, x.contiguous(), pos, ref)
+    outw = torch.full((N, 9 * D), 7.0, device=dev)
+    out = outw[:, D:7 * D].view(N, H, D)
+    kvd.rope_apply(rope, x, pos, out)
+    torch.cuda.synchronize()
+    assert torch.equal(out, ref) and torch.equal(wide, keep)
+    assert (outw[:, :D] == 7).all() and (outw[:, 7 * D:] == 7).all()
+    kvd.rope_apply(rope, x, pos, x)  # a slice in place: its neighbours stay
+    torch.cuda.synchronize()
+    assert torch.equal(x, ref) and torch.equal(wide[:, :2 * D], keep[:, :2 * D]) and torch.equal(wide[:, 8 * D:], keep[:, 8 * D:])
+    # [B, T, H, D] is B * T rows; negative positions turn back
+    back = torch.empty(1, N, H, D, device=dev)
+    kvd.rope_apply(rope, ref.view(1, N, H, D), -pos.view(1, N), back)
+    torch.cuda.synchronize()
+    # two turns, each within 4.0e-7 (|a| + |b|) with |a|, |b| <= 6
+    assert (back[0] - keep[:, 2 * D:8 * D].view(N, H, D)).abs().max() < 2 * 4.0e-7 * 12
+
+
+def test_rope_apply_refuses_views():
+    import torch
+    import kv_cache_decode_gb300 as kvd
+    dev = cuda_or_skip()
+    rope = kvd.RopeTable(64, device=dev)
+    x = torch.zeros(4, 8, 128, device=dev, dtype=torch.bfloat16)
+    pos = torch.zeros(4, device=dev, dtype=torch.int32)
+    bad = [lambda: kvd.rope_apply(rope, x.transpose(0, 1), pos, x), lambda: kvd.rope_apply(rope, x.half(), pos, x),
+           lambda: kvd.rope_apply(rope, x, pos[:3], x), lambda: kvd.rope_apply(rope, x, pos.long(), x),
+           lambda: kvd.rope_apply(rope, x, pos.cpu(), x), lambda: kvd.rope_apply(rope, x[..., :120], pos, x[..., :120]),
+           lambda: kvd.rope_apply(rope, x[:, :, :32].contiguous(), pos, x[:, :, :32].contiguous()),
+           lambda: kvd.rope_apply(kvd.RopeTable(64, device="cpu"), x, pos, x),
+           lambda: kvd.rope_apply(rope, x, pos, x[:2])]
+    for fn in bad:
+        with pytest.raises((ValueError, TypeError, kvd.KvdError)):
+            fn()
+
+
+# ---------------------------------------------------------------------------
+# the rotating appends
+# ---------------------------------------------------------------------------
+
+def _cache(kvd, torch, form, B, S, Hkv, D, page, dev, g):
+    """(tensors by name, block table or None, bytes before): caches filled with a recognisable pattern."""
+    lead = (B, S) if not page else (B * (S // page) + 2, page)
+    bt = None
+    if page:
+        bt = torch.randperm(lead[0], generator=g, device=dev)[:B * (S // page)].view(B, S // page).int()
+    t = {}
+    for n in ("k", "v"):
+        if form == "fp4":
+            t[n] = torch.full((lead[0], Hkv, lead[1] // 16, 9 * D + 16), 0x5a, dtype=torch.uint8, device=dev)
+        elif form == "bf16":
+            t[n] = torch.full(lead + (Hkv, D), -3.0, dtype=torch.bfloat16, device=dev)
+        else:
+            t[n] = torch.full(lead + (Hkv, D), 85, dtype=torch.int8 if form == "int8" else torch.uint8, device=dev)
+            t[n + "_scales"] = torch.full(lead + (Hkv,), -1.0, device=dev)
+    return t, bt
+
+
+def _expected(form, t, bt, S, page, k_bits, v_bits, seq, at):
+    """numpy images of the cache tensors after rows (k_bits[n], v_bits[n]) go to position at[n] of sequence seq[n]."""
+    e = {n: (bf16_tensor_bits(x) if x.dtype.is_floating_point and x.element_size() == 2 else x.cpu().numpy()).copy()
+         for n, x in t.items()}
+    table = None if bt is None else bt.cpu().numpy()
+    for n, (b, p) in enumerate(zip(seq, at)):
+        if p < 0 or p >= S:
+            continue
+        i, r = (b, p) if table is None else (table[b, p // page], p % page)
+        for name, bits in (("k", k_bits[n]), ("v", v_bits[n])):
+            if form == "bf16":
+                e[name][i, r] = bits
+            elif form == "fp4":
+                codes, sb, exps = oracle.quantize_fp4(bits)
+                H, D = codes.shape
+                blk = e[name][i, :, r // 16]
+                pad = lambda a: np.zeros((H, 16) + a.shape[1:], a.dtype)  # noqa: E731
+                c16, s16, e16 = pad(codes), pad(sb), pad(exps)
+                c16[:, r % 16], s16[:, r % 16], e16[:, r % 16] = codes, sb, exps
+                new = oracle.pack_fp4(c16, s16, e16)[:, 0]
+                m16 = [pad(a) for a in (codes, sb, exps)]
+                m16[0][:, r % 16], m16[1][:, r % 16], m16[2][:, r % 16] = 15, 255, 255
+                mask = oracle.pack_fp4(*m16)[:, 0]
+                e[name][i, :, r // 16] = (blk & ~mask) | (new & mask)
+            else:
+                q = oracle.quantize_q8(bits) if form == "int8" else oracle.quantize_fp8(bits)
+                e[name][i, r] = np.asarray(q[0]).view(e[name].dtype)
+                e[name + "_scales"][i, r] = q[1]
+    return e
+
+
+def _same(t, e):
+    import torch
+    for n, x in t.items():
+        got = bf16_tensor_bits(x) if x.dtype == torch.bfloat16 else x.cpu().numpy()
+        bad = got != e[n]
+        assert not bad.any(), (n, int(bad.sum()), np.argwhere(bad)[:5].tolist())
+
+
+def _call(kvd, form, rope, t, *args, **kw):
+    if form == "fp4":
+        kvd.kv_append_fp4(t["k"], t["v"], *args, rope=rope, **kw)
+    else:
+        kvd.kv_append_rope(rope, t["k"], t["v"], *args, k_scales=t.get("k_scales"), v_scales=t.get("v_scales"), **kw)
+
+
+@pytest.mark.parametrize("form", ["bf16", "int8", "fp8", "fp4"])
+@pytest.mark.parametrize("D,R,inter,Hq,Hkv,page,T", [
+    (128, 128, False, 32, 8, 0, 1), (128, 64, True, 8, 8, 16, 3), (64, 16, False, 6, 2, 32, 1), (64, 48, False, 5, 5, 16, 2),
+    (256, 256, True, 48, 1, 64, 2), (256, 112, False, 3, 1, 0, 5),
+])
+def test_append_rope_uniform(form, D, R, inter, Hq, Hkv, page, T):
+    import torch
+    import kv_cache_decode_gb300 as kvd
+    dev = cuda_or_skip()
+    g = torch.Generator(device=dev).manual_seed(D + R + T)
+    B, S = 5, 128
+    rope = kvd.RopeTable(R, scaling="wavelength", factor=8.0, original_len=64, interleaved=inter, device=dev)
+    t, bt = _cache(kvd, torch, form, B, S, Hkv, D, page, dev, g)
+    fused = torch.randn(B, T, (Hq + 2 * Hkv) * D, generator=g, device=dev).bfloat16()
+    q = fused[..., :Hq * D].view(B, T, Hq, D)
+    k = fused[..., Hq * D:(Hq + Hkv) * D].view(B, T, Hkv, D)
+    v = fused[..., (Hq + Hkv) * D:].view(B, T, Hkv, D)
+    k[1, 0, 0] = 0  # an all-zero head
+    k[0, 0, 0] *= 1e-3
+    pos = torch.tensor([0, 15, 61, S - T, 31], dtype=torch.int32, device=dev)
+    positions = (pos[:, None] + torch.arange(T, device=dev, dtype=torch.int32)).contiguous()
+    kr, qr = torch.empty(B, T, Hkv, D, device=dev, dtype=torch.bfloat16), torch.empty(B, T, Hq, D, device=dev, dtype=torch.bfloat16)
+    kvd.rope_apply(rope, k, positions, kr)
+    kvd.rope_apply(rope, q, positions, qr)
+    torch.cuda.synchronize()
+    seq = np.repeat(np.arange(B), T)
+    want = _expected(form, t, bt, S, page, bf16_tensor_bits(kr).reshape(B * T, Hkv, D), bf16_tensor_bits(v).reshape(B * T, Hkv, D),
+                     seq, positions.cpu().numpy().reshape(-1))
+    q_out = torch.zeros_like(qr)
+    status = torch.zeros(1, dtype=torch.int32, device=dev)
+    before = fused.clone()
+    _call(kvd, form, rope, t, k, v, pos, q=q, q_out=q_out, block_table=bt, status=status)
+    torch.cuda.synchronize()
+    assert int(status.item()) == 0 and torch.equal(fused, before)
+    assert torch.equal(q_out, qr)
+    _same(t, want)
+    # queries turned in place in the fused rows, the cache as before
+    _call(kvd, form, rope, t, k, v, pos, q=q, q_out=q, block_table=bt, status=status)
+    torch.cuda.synchronize()
+    assert torch.equal(q, qr) and torch.equal(k, before[..., Hq * D:(Hq + Hkv) * D].view(B, T, Hkv, D))
+    _same(t, want)
+
+
+@pytest.mark.parametrize("form,page", [("bf16", 32), ("int8", 0), ("fp8", 16), ("fp4", 16), ("fp4", 0)])
+def test_append_rope_ragged(form, page):
+    import torch
+    import kv_cache_decode_gb300 as kvd
+    dev = cuda_or_skip()
+    D, R, Hq, Hkv, S = 128, 64, 4, 2, 96
+    lens = [0, 1, 17, 0, 40, 96, 3]
+    B = len(lens)
+    first = 2                       # rows before the first offset belong to nobody
+    off = np.concatenate([[0], np.cumsum(lens)]) + first
+    N = int(off[-1]) + 5            # nor do those behind the last
+    g = torch.Generator(device=dev).manual_seed(11)
+    rope = kvd.RopeTable(R, device=dev)
+    t, bt = _cache(kvd, torch, form, B, S, Hkv, D, page, dev, g)
+    q, k, v = (torch.randn(N, h, D, generator=g, device=dev).bfloat16() for h in (Hq, Hkv, Hkv))
+    start = np.array([5, 7, 60, 3, 50, 0, S - 1])  # the last sequence runs over its end
+    pos = torch.tensor(start, dtype=torch.int32, device=dev)
+    seq = np.full(N, -1)
+    at = np.full(N, -1)
+    for b in range(B):
+        seq[off[b]:off[b + 1]] = b
+        at[off[b]:off[b + 1]] = start[b] + np.arange(lens[b])
+    live = seq >= 0
+    positions = torch.tensor(np.where(live, at, 0), dtype=torch.int32, device=dev)
+    kr, qr = torch.empty_like(k), torch.empty_like(q)
+    kvd.rope_apply(rope, k, positions, kr)
+    kvd.rope_apply(rope, q, positions, qr)
+    torch.cuda.synchronize()
+    want = _expected(form, t, bt, S, page, bf16_tensor_bits(kr)[live], bf16_tensor_bits(v)[live], seq[live], at[live])
+    q_out = torch.full_like(q, 9.0)
+    status = torch.zeros(1, dtype=torch.int32, device=dev)
+    _call(kvd, form, rope, t, k, v, pos, q=q, q_out=q_out, block_table=bt, status=status,
+          row_offsets=torch.tensor(off, dtype=torch.int32, device=dev))
+    torch.cuda.synchronize()
+    assert int(status.item()) == kvd.STATUS_POS_OUT_OF_RANGE
+    lt = torch.tensor(live, device=dev)
+    assert torch.equal(q_out[lt], qr[lt]) and (q_out[~lt] == 9).all()
+    _same(t, want)
+
+
+@pytest.mark.parametrize("form", ["bf16", "fp4"])
+def test_append_rope_bad_pages_and_positions(form):
+    import torch
+    import kv_cache_decode_gb300 as kvd
+    dev = cuda_or_skip()
+    D, Hkv, S, page, B = 64, 3, 64, 16, 5
+    g = torch.Generator(device=dev).manual_seed(4)
+    rope = kvd.RopeTable(64, device=dev)
+    t, bt = _cache(kvd, torch, form, B, S, Hkv, D, page, dev, g)
+    bt[0, 1], bt[2, 0], bt[3, 3] = -1, t["k"].shape[0], 2 ** 30
+    k, v = (torch.randn(B, Hkv, D, generator=g, device=dev).bfloat16() for _ in range(2))
+    pos = torch.tensor([20, 63, 0, -1, 64], dtype=torch.int32, device=dev)
+    kr = torch.empty_like(k)
+    kvd.rope_apply(rope, k, pos, kr)
+    torch.cuda.synchronize()
+    want = _expected(form, t, bt, S, page, bf16_tensor_bits(kr)[1:2], bf16_tensor_bits(v)[1:2], [1], [63])
+    status = torch.zeros(1, dtype=torch.int32, device=dev)
+    _call(kvd, form, rope, t, k, v, pos, block_table=bt, status=status)
+    torch.cuda.synchronize()
+    assert int(status.item()) == kvd.STATUS_POS_OUT_OF_RANGE | kvd.STATUS_BAD_PAGE
+    _same(t, want)
+
+
+def test_append_fp4_plain_and_many_rows():
+    """No rotation, and enough rows for several tokens to a block."""
+    import torch
+    import kv_cache_decode_gb300 as kvd
+    dev = cuda_or_skip()
+    B, T, Hkv, D, S = 50, 64, 2, 64, 64
+    g = torch.Generator(device=dev).manual_seed(8)
+    t, _ = _cache(kvd, torch, "fp4", B, S, Hkv, D, 0, dev, g)
+    k, v = (torch.randn(B, T, Hkv, D, generator=g, device=dev).bfloat16() for _ in range(2))
+    pos = torch.zeros(B, dtype=torch.int32, device=dev)
+    kvd.kv_append_fp4(t["k"], t["v"], k, v, pos)
+    torch.cuda.synchronize()
+    for n, x in (("k", k), ("v", v)):
+        want = oracle.pack_fp4(*oracle.quantize_fp4(bf16_tensor_bits(x).transpose(0, 2, 1, 3)))
+        assert np.array_equal(t[n].cpu().numpy(), want)
