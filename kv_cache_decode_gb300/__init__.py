@@ -939,53 +939,92 @@ class RopeTable:
         turns, self.factor = rope_table(rotary_dim, base, scaling, factor, original_len, slow, fast, attn_factor)
         self.rotary_dim, self.interleaved = int(rotary_dim), bool(interleaved)
         self.turns = torch.from_numpy(turns.view(np.int64)).to(device)
-
-    def _c(self):
-        return _CRope(self.turns.data_ptr(), self.factor, self.rotary_dim, 1 if self.interleaved else 0)
-
-
-def _same_device(what, first, *others):
-    for t in others:
-        if t is not None and t.device != first.device:
-            raise ValueError(f"{what}: tensors on {first.device} and {t.device}")
+        self._device = self.turns.get_device()  # -1 on the CPU
+        self._struct = _CRope(self.turns.data_ptr(), self.factor, self.rotary_dim, 1 if self.interleaved else 0)
+        self._ref = ctypes.byref(self._struct)
 
 
-def _launch(fn, args, what, t, stream):
-    """Calls fn(*args, stream handle) with t's device current; without a stream, on that device's current one."""
+# The calls below are made once a layer and step, so their checks are written to
+# cost a few microseconds: metadata is read once per tensor, and the device is
+# only switched to when it is not the current one.
+
+def _device_of(what, *named):
+    """The CUDA device all the given tensors lie on: (tensor, name, dtypes or None, dims or None), tensor None passed over."""
     import torch
-    with torch.cuda.device(t.device):
-        _check(fn(*args, _stream_handle(stream)), what)
+    Tensor = torch.Tensor
+    dev = None
+    for t, name, dtypes, ndim in named:
+        if t is None:
+            continue
+        if not isinstance(t, Tensor):
+            raise TypeError(f"{what}: {name} must be a torch.Tensor")
+        i = t.get_device()
+        if i != dev:
+            if i < 0:
+                raise ValueError(f"{what}: {name} must be on a CUDA device")
+            if dev is not None:
+                raise ValueError(f"{what}: {name} is on cuda:{i}, other tensors on cuda:{dev}")
+            dev = i
+        if dtypes is not None and t.dtype not in dtypes:
+            raise TypeError(f"{what}: {name} must be {dtypes}, got {t.dtype}")
+        if ndim is not None:
+            if t.dim() != ndim:
+                raise ValueError(f"{what}: {name} must have {ndim} dims, got {t.dim()}")
+            if not t.is_contiguous():
+                raise ValueError(f"{what}: {name} must be contiguous")
+    return dev
 
 
-def _status_arg(status, what):
-    import torch
-    if status is not None:
-        _require(status, f"{what}: status", torch.int32)
-    return _ptr(status)
+def _rope_on(rope, dev, what):
+    if not isinstance(rope, RopeTable):
+        raise TypeError(f"{what}: rope must be a RopeTable")
+    if rope._device != dev:
+        raise ValueError(f"{what}: the rope table is on {rope.turns.device}, the tensors on cuda:{dev}")
+    return rope._ref
 
 
-def _rows(t, name, dtypes, what):
+def _launch(fn, what, dev, stream, *args):
+    """Calls fn(*args, stream handle) with device `dev` current; without a stream, on that device's current one."""
+    from torch import _C
+    if stream is None:
+        h = _C._cuda_getCurrentRawStream(dev)
+    elif hasattr(stream, "cuda_stream"):
+        if stream.device_index != dev:
+            raise ValueError(f"{what}: a stream of cuda:{stream.device_index}, tensors on cuda:{dev}")
+        h = stream.cuda_stream
+    else:
+        h = int(stream)
+    if _C._cuda_getDevice() == dev:
+        rc = fn(*args, h)
+    else:
+        import torch
+        with torch.cuda.device(dev):
+            rc = fn(*args, h)
+    if rc != OK:
+        raise KvdError(rc, what)
+
+
+def _rows(t, name, what):
     """[N, H, D] rows, or [B, T, H, D] as B * T of them, whose heads are contiguous:
     (rows, heads, head_dim, elements between rows)."""
-    import torch
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be on a CUDA device")
-    if t.dtype not in dtypes:
-        raise TypeError(f"{name} must be {dtypes}, got {t.dtype}")
-    if t.dim() not in (3, 4):
+    s, st = t.shape, t.stride()
+    if len(s) == 3:
+        N, H, D = s
+        step, even = st[0], True
+    elif len(s) == 4:
+        B, T, H, D = s
+        N = B * T
+        step = st[1] if T > 1 else st[0]
+        even = B <= 1 or T <= 1 or st[0] == T * step
+    else:
         raise ValueError(f"{what}: {name} must be [N, H, D] or [B, T, H, D]")
-    H, D = t.shape[-2], t.shape[-1]
-    N = t.shape[0] if t.dim() == 3 else t.shape[0] * t.shape[1]
-    if t.numel() == 0:
+    if N == 0 or H == 0 or D == 0:
         return N, H, D, H * D
-    if t.stride(-1) != 1 or (H > 1 and t.stride(-2) != D):
+    if (st[-1] != 1 and D > 1) or (st[-2] != D and H > 1):
         raise ValueError(f"{what}: {name}'s heads must be contiguous")
-    step = t.stride(-3) if t.shape[-3] > 1 else (t.stride(0) if t.dim() == 4 and t.shape[0] > 1 else H * D)
-    if t.dim() == 4 and t.shape[0] > 1 and t.shape[1] > 1 and t.stride(0) != t.shape[1] * step:
+    if not even:
         raise ValueError(f"{what}: {name}'s rows must be evenly spaced")
-    return N, H, D, step
+    return N, H, D, step if N > 1 else H * D
 
 
 def rope_apply(rope: RopeTable, x, positions, out, stream=None):
@@ -993,50 +1032,56 @@ def rope_apply(rope: RopeTable, x, positions, out, stream=None):
     bf16 or fp32 each, rows evenly spaced (slices of a fused projection may be
     passed as they are); positions int32, one a row. out may be x."""
     import torch
-    what, dts = "rope_apply", (torch.bfloat16, torch.float32)
-    N, H, D, xs = _rows(x, "x", dts, what)
-    No, Ho, Do, ys = _rows(out, "out", dts, what)
-    _require(positions, "positions", torch.int32)
-    if (No, Ho, Do) != (N, H, D) or positions.numel() != N:
+    what, bf, f32 = "rope_apply", torch.bfloat16, torch.float32
+    dev = _device_of(what, (x, "x", (bf, f32), None), (out, "out", (bf, f32), None),
+                     (positions, "positions", (torch.int32,), None))
+    N, H, D, xs = _rows(x, "x", what)
+    No, Ho, Do, ys = _rows(out, "out", what)
+    if No != N or Ho != H or Do != D or positions.numel() != N:
         raise ValueError(f"{what}: inconsistent shapes")
-    _same_device(what, x, out, positions, rope.turns)
+    if not positions.is_contiguous():
+        raise ValueError(f"{what}: positions must be contiguous")
+    ref = _rope_on(rope, dev, what)
     if N == 0:
         return
-    code = lambda t: OUT_BF16 if t.dtype == torch.bfloat16 else OUT_F32
-    _launch(load().kvd_rope_apply, [ctypes.byref(rope._c()), x.data_ptr(), xs, code(x), out.data_ptr(), ys, code(out),
-                                    positions.data_ptr(), N, H, D], "kvd_rope_apply", x, stream)
+    _launch((_lib or load()).kvd_rope_apply, "kvd_rope_apply", dev, stream, ref, x.data_ptr(), xs,
+            OUT_F32 if x.dtype is f32 else OUT_BF16, out.data_ptr(), ys, OUT_F32 if out.dtype is f32 else OUT_BF16,
+            positions.data_ptr(), N, H, D)
 
 
-def _new_rows_args(what, rope, q, q_out, k_new, v_new, pos, row_offsets, cache, others):
-    """(the arguments of kvd_kv_append_rope after the cache but for status and stream, [the rope struct kept alive])."""
-    import torch
-    bf = (torch.bfloat16,)
-    N, Hkv, D, ks = _rows(k_new, "k_new", bf, what)
-    Nv, Hv, Dv, vs = _rows(v_new, "v_new", bf, what)
-    _require(pos, "pos", torch.int32, 1)
+def _append_rows(what, rope, q, q_out, k_new, v_new, pos, row_offsets, dev):
+    """(batch, rows, KV heads, head_dim, the arguments of kvd_kv_append_rope between the cache and the status word)."""
+    N, Hkv, D, ks = _rows(k_new, "k_new", what)
+    Nv, Hv, Dv, vs = _rows(v_new, "v_new", what)
     B = pos.shape[0]
-    if (Nv, Hv, Dv) != (N, Hkv, D):
+    if Nv != N or Hv != Hkv or Dv != D:
         raise ValueError(f"{what}: inconsistent shapes")
     if row_offsets is not None:
-        _require(row_offsets, "row_offsets", torch.int32, 1)
         if row_offsets.shape[0] != B + 1:
             raise ValueError(f"{what}: row_offsets must be [batch + 1]")
-    elif (N % B if B else N):
-        raise ValueError(f"{what}: {N} new rows for {B} sequences")
-    if (q is None) != (q_out is None):
-        raise ValueError(f"{what}: q and q_out go together")
-    if q is not None and rope is None:
-        raise ValueError(f"{what}: q needs a rope")
-    Hq, qs, qos = 0, 0, 0
-    if q is not None:
-        Nq, Hq, Dq, qs = _rows(q, "q", bf, what)
-        No, Ho, Do, qos = _rows(q_out, "q_out", bf, what)
-        if (Nq, Dq) != (N, D) or (No, Ho, Do) != (Nq, Hq, Dq):
+        off = row_offsets.data_ptr()
+    else:
+        if (N % B if B else N):
+            raise ValueError(f"{what}: {N} new rows for {B} sequences")
+        off = None
+    ref = None if rope is None else _rope_on(rope, dev, what)
+    if q is None:
+        if q_out is not None:
+            raise ValueError(f"{what}: q and q_out go together")
+        qp = op = None
+        Hq = qs = os_ = 0
+    else:
+        if q_out is None:
+            raise ValueError(f"{what}: q and q_out go together")
+        if rope is None:
+            raise ValueError(f"{what}: q needs a rope")
+        Nq, Hq, Dq, qs = _rows(q, "q", what)
+        No, Ho, Do, os_ = _rows(q_out, "q_out", what)
+        if Nq != N or Dq != D or No != N or Ho != Hq or Do != D:
             raise ValueError(f"{what}: inconsistent shapes")
-    _same_device(what, cache, k_new, v_new, pos, row_offsets, q, q_out, None if rope is None else rope.turns, *others)
-    c = None if rope is None else rope._c()
-    return (N, Hkv, D), [None if c is None else ctypes.byref(c), _ptr(q), qs, _ptr(q_out), qos, k_new.data_ptr(), ks,
-                         v_new.data_ptr(), vs, pos.data_ptr(), _ptr(row_offsets), B, N, Hq, Hkv, D], c
+        qp, op = q.data_ptr(), q_out.data_ptr()
+    return B, N, Hkv, D, (ref, qp, qs, op, os_, k_new.data_ptr(), ks, v_new.data_ptr(), vs, pos.data_ptr(), off, B, N, Hq,
+                          Hkv, D)
 
 
 def kv_append_rope(rope: RopeTable, k, v, k_new, v_new, pos, *, q=None, q_out=None, k_scales=None, v_scales=None,
@@ -1048,35 +1093,38 @@ def kv_append_rope(rope: RopeTable, k, v, k_new, v_new, pos, *, q=None, q_out=No
     int32 [B + 1] the packed rows [N, H, D] of prompts of any lengths; rows evenly
     spaced, so slices of a fused projection may be passed as they are."""
     import torch
-    what = "kv_append_rope"
-    quant = k_scales is not None
-    dts = (torch.int8, torch.uint8, torch.float8_e4m3fn) if quant else (torch.bfloat16,)
-    for t, n in ((k, "k"), (v, "v")):
-        _require(t, n, dts, 4)
-    (N, Hkv, D), args, keep = _new_rows_args(what, rope, q, q_out, k_new, v_new, pos, row_offsets, k,
-                                             (v, k_scales, v_scales, block_table, status))
-    if v.shape != k.shape or v.dtype != k.dtype or k.shape[2:] != (Hkv, D):
-        raise ValueError(f"{what}: inconsistent shapes")
-    if quant:
-        _q8_args(k, v, k_scales, v_scales, "fp8" if _is_fp8(k) else "int8")
-    elif v_scales is not None:
+    what, bf, i32, f32 = "kv_append_rope", (torch.bfloat16,), (torch.int32,), (torch.float32,)
+    if rope is None:
+        raise TypeError(f"{what}: rope must be a RopeTable")
+    if (k_scales is None) != (v_scales is None):
         raise ValueError(f"{what}: k_scales and v_scales go together")
-    c = _CCache()
-    c.k, c.v, c.k_scales, c.v_scales = k.data_ptr(), v.data_ptr(), _ptr(k_scales), _ptr(v_scales)
-    c.fp8 = 1 if quant and _is_fp8(k) else 0
+    quant = k_scales is not None
+    dts = (torch.int8, torch.uint8, torch.float8_e4m3fn) if quant else bf
+    dev = _device_of(what, (k, "k", dts, 4), (v, "v", dts, 4), (k_new, "k_new", bf, None), (v_new, "v_new", bf, None),
+                     (pos, "pos", i32, 1), (q, "q", bf, None), (q_out, "q_out", bf, None),
+                     (block_table, "block_table", i32, 2), (row_offsets, "row_offsets", i32, 1),
+                     (k_scales, "k_scales", f32, 3), (v_scales, "v_scales", f32, 3), (status, "status", i32, None))
+    B, N, Hkv, D, args = _append_rows(what, rope, q, q_out, k_new, v_new, pos, row_offsets, dev)
+    shape = k.shape
+    if v.shape != shape or shape[2] != Hkv or shape[3] != D:
+        raise ValueError(f"{what}: inconsistent shapes")
+    c = _CCache(k.data_ptr(), v.data_ptr())
+    if quant:
+        if v.dtype != k.dtype or k_scales.shape != shape[:3] or v_scales.shape != shape[:3]:
+            raise ValueError(f"{what}: codes [B, S_max, Hkv, D] and scales [B, S_max, Hkv] disagree")
+        c.k_scales, c.v_scales, c.fp8 = k_scales.data_ptr(), v_scales.data_ptr(), 1 if _is_fp8(k) else 0
     if block_table is not None:
-        _require(block_table, "block_table", torch.int32, 2)
-        if block_table.shape[0] != pos.shape[0]:
+        if block_table.shape[0] != B:
             raise ValueError(f"{what}: inconsistent shapes")
         c.block_table, c.max_blocks = block_table.data_ptr(), block_table.shape[1]
-        c.page_size, c.num_pages = k.shape[1], k.shape[0]
+        c.page_size, c.num_pages = shape[1], shape[0]
     else:
-        if k.shape[0] != pos.shape[0]:
+        if shape[0] != B:
             raise ValueError(f"{what}: inconsistent shapes")
-        c.s_max = k.shape[1]
+        c.s_max = shape[1]
     if N == 0:
         return
-    _launch(load().kvd_kv_append_rope, [ctypes.byref(c), *args, _status_arg(status, what)], "kvd_kv_append_rope", k, stream)
+    _launch((_lib or load()).kvd_kv_append_rope, "kvd_kv_append_rope", dev, stream, ctypes.byref(c), *args, _ptr(status))
 
 
 def fp4_block_bytes(head_dim: int) -> int:
@@ -1099,24 +1147,21 @@ def alloc_cache_fp4(batch_or_pages: int, n_heads_kv: int, head_dim: int, tokens:
 
 def _fp4_cache(what, k, v, D, B, block_table):
     """(struct kvd_cache_fp4, KV heads) of the blocks k and v (v may be None)."""
-    import torch
-    for t, n in ((k, "k"),) if v is None else ((k, "k"), (v, "v")):
-        _require(t, n, torch.uint8, 4)
-    if (v is not None and v.shape != k.shape) or k.shape[3] != fp4_block_bytes(D):
+    shape = k.shape
+    if shape[3] != 9 * D + 16 or D not in (64, 128, 256):
+        raise ValueError(f"{what}: blocks of {shape[3]} bytes at head_dim {D}")
+    if v is not None and v.shape != shape:
         raise ValueError(f"{what}: inconsistent shapes")
-    c = _CCacheFp4()
-    c.k, c.v = k.data_ptr(), _ptr(v)
+    vp = None if v is None else v.data_ptr()
     if block_table is not None:
-        _require(block_table, "block_table", torch.int32, 2)
         if block_table.shape[0] != B:
             raise ValueError(f"{what}: inconsistent shapes")
-        c.block_table, c.max_blocks = block_table.data_ptr(), block_table.shape[1]
-        c.page_size, c.num_pages = 16 * k.shape[2], k.shape[0]
+        c = _CCacheFp4(k.data_ptr(), vp, block_table.data_ptr(), 0, block_table.shape[1], 16 * shape[2], shape[0])
     else:
-        if k.shape[0] != B:
+        if shape[0] != B:
             raise ValueError(f"{what}: inconsistent shapes")
-        c.s_max = 16 * k.shape[2]
-    return c, k.shape[1]
+        c = _CCacheFp4(k.data_ptr(), vp, None, 16 * shape[2])
+    return c, shape[1]
 
 
 def kv_append_fp4(k, v, k_new, v_new, pos, *, rope: Optional[RopeTable] = None, q=None, q_out=None, block_table=None,
@@ -1124,15 +1169,19 @@ def kv_append_fp4(k, v, k_new, v_new, pos, *, rope: Optional[RopeTable] = None, 
     """kv_append_rope for an fp4 cache (k, v uint8 [B, Hkv, S_max / 16, 9 D + 16], or
     pools [pages, Hkv, page / 16, 9 D + 16] with block_table); rope None appends
     the rows as they are (kvd_kv_append_fp4)."""
-    what = "kv_append_fp4"
-    (N, Hkv, D), args, keep = _new_rows_args(what, rope, q, q_out, k_new, v_new, pos, row_offsets, k,
-                                             (v, block_table, status))
-    c, heads = _fp4_cache(what, k, v, D, pos.shape[0], block_table)
+    import torch
+    what, bf, u8, i32 = "kv_append_fp4", (torch.bfloat16,), (torch.uint8,), (torch.int32,)
+    dev = _device_of(what, (k, "k", u8, 4), (v, "v", u8, 4), (k_new, "k_new", bf, None), (v_new, "v_new", bf, None),
+                     (pos, "pos", i32, 1), (q, "q", bf, None), (q_out, "q_out", bf, None),
+                     (block_table, "block_table", i32, 2), (row_offsets, "row_offsets", i32, 1),
+                     (status, "status", i32, None))
+    B, N, Hkv, D, args = _append_rows(what, rope, q, q_out, k_new, v_new, pos, row_offsets, dev)
+    c, heads = _fp4_cache(what, k, v, D, B, block_table)
     if heads != Hkv:
         raise ValueError(f"{what}: inconsistent shapes")
     if N == 0:
         return
-    _launch(load().kvd_kv_append_fp4, [ctypes.byref(c), *args, _status_arg(status, what)], "kvd_kv_append_fp4", k, stream)
+    _launch((_lib or load()).kvd_kv_append_fp4, "kvd_kv_append_fp4", dev, stream, ctypes.byref(c), *args, _ptr(status))
 
 
 def kv_quantize_fp4(cache, blocks, seq_lens, max_seq_len: int, stream=None):
@@ -1140,36 +1189,33 @@ def kv_quantize_fp4(cache, blocks, seq_lens, max_seq_len: int, stream=None):
     of a contiguous fp4 cache (kvd_kv_quantize_fp4)."""
     import torch
     what = "kv_quantize_fp4"
-    _require(cache, "cache", torch.bfloat16, 4)
-    _require(seq_lens, "seq_lens", torch.int32, 1)
+    dev = _device_of(what, (cache, "cache", (torch.bfloat16,), 4), (blocks, "blocks", (torch.uint8,), 4),
+                     (seq_lens, "seq_lens", (torch.int32,), 1))
     B, S, Hkv, D = cache.shape
     c, heads = _fp4_cache(what, blocks, None, D, B, None)
-    if heads != Hkv or seq_lens.shape != (B,):
+    if heads != Hkv or seq_lens.shape[0] != B:
         raise ValueError(f"{what}: inconsistent shapes")
-    _same_device(what, cache, blocks, seq_lens)
     if B == 0:
         return
-    _launch(load().kvd_kv_quantize_fp4, [cache.data_ptr(), blocks.data_ptr(), seq_lens.data_ptr(), B, S, c.s_max,
-                                         int(max_seq_len), Hkv, D], "kvd_kv_quantize_fp4", cache, stream)
+    _launch((_lib or load()).kvd_kv_quantize_fp4, "kvd_kv_quantize_fp4", dev, stream, cache.data_ptr(), c.k,
+            seq_lens.data_ptr(), B, S, c.s_max, int(max_seq_len), Hkv, D)
 
 
 def kv_read_fp4(blocks, out, seq_lens, max_seq_len: int, block_table=None, status=None, stream=None):
     """Rows t < seq_lens[b] of an fp4 cache's K or V blocks (contiguous, or a pool
     with block_table) back to bf16 out [B, S, Hkv, D], exactly (kvd_kv_read_fp4)."""
     import torch
-    what = "kv_read_fp4"
-    _require(out, "out", torch.bfloat16, 4)
-    _require(seq_lens, "seq_lens", torch.int32, 1)
+    what, i32 = "kv_read_fp4", (torch.int32,)
+    dev = _device_of(what, (out, "out", (torch.bfloat16,), 4), (blocks, "blocks", (torch.uint8,), 4),
+                     (seq_lens, "seq_lens", i32, 1), (block_table, "block_table", i32, 2), (status, "status", i32, None))
     B, S, Hkv, D = out.shape
     c, heads = _fp4_cache(what, blocks, None, D, B, block_table)
-    if heads != Hkv or seq_lens.shape != (B,):
+    if heads != Hkv or seq_lens.shape[0] != B:
         raise ValueError(f"{what}: inconsistent shapes")
-    _same_device(what, out, blocks, seq_lens, block_table, status)
     if B == 0:
         return
-    _launch(load().kvd_kv_read_fp4, [blocks.data_ptr(), _ptr(block_table), c.s_max, c.max_blocks, c.page_size,
-                                     c.num_pages, out.data_ptr(), S, seq_lens.data_ptr(), B, int(max_seq_len), Hkv, D,
-                                     _status_arg(status, what)], "kvd_kv_read_fp4", out, stream)
+    _launch((_lib or load()).kvd_kv_read_fp4, "kvd_kv_read_fp4", dev, stream, c.k, c.block_table, c.s_max, c.max_blocks,
+            c.page_size, c.num_pages, out.data_ptr(), S, seq_lens.data_ptr(), B, int(max_seq_len), Hkv, D, _ptr(status))
 
 
 def decode_plan_fp4(batch: int, n_tokens: int, n_heads_q: int, n_heads_kv: int, head_dim: int, max_seq_len: int,
@@ -1189,38 +1235,40 @@ def decode_fp4(q, k, v, seq_lens, max_seq_len: int, scale: float, out, *, block_
     block_table [B, max_blocks]; k_new, v_new ([B, Hkv, D] or [B, T, Hkv, D]) and
     pos to append first. Workspace: decode_plan_fp4."""
     import torch
-    what = "decode_fp4"
-    _require(q, "q", torch.bfloat16)
-    _require(out, "out", (torch.bfloat16, torch.float32))
-    _require(seq_lens, "seq_lens", torch.int32, 1)
-    if q.dim() not in (3, 4) or out.shape != q.shape:
-        raise ValueError(f"{what}: inconsistent shapes")
-    T = q.shape[1] if q.dim() == 4 else 1
-    B, Hq, D = q.shape[0], q.shape[-2], q.shape[-1]
+    what, bf, u8, i32, f32 = "decode_fp4", (torch.bfloat16,), (torch.uint8,), (torch.int32,), torch.float32
+    dev = _device_of(what, (q, "q", bf, None), (k, "k", u8, 4), (v, "v", u8, 4), (seq_lens, "seq_lens", i32, 1),
+                     (out, "out", (torch.bfloat16, f32), None), (block_table, "block_table", i32, 2),
+                     (workspace, "workspace", None, None), (lse, "lse", (f32,), None), (status, "status", i32, None),
+                     (k_new, "k_new", bf, None), (v_new, "v_new", bf, None), (pos, "pos", i32, 1))
+    shape = q.shape
+    if len(shape) == 3:
+        (B, Hq, D), T = shape, 1
+    elif len(shape) == 4:
+        B, T, Hq, D = shape
+    else:
+        raise ValueError(f"{what}: q must be [B, Hq, D] or [B, T, Hq, D]")
+    if out.shape != shape or seq_lens.shape[0] != B or not (q.is_contiguous() and out.is_contiguous()):
+        raise ValueError(f"{what}: q, out and seq_lens disagree, or q or out is not contiguous")
     c, Hkv = _fp4_cache(what, k, v, D, B, block_table)
-    if v is None or seq_lens.shape != (B,):
-        raise ValueError(f"{what}: inconsistent shapes")
-    if lse is not None:
-        _require(lse, "lse", torch.float32)
-        if lse.shape != q.shape[:-1]:
-            raise ValueError(f"{what}: lse must be shaped like q without its last dimension")
-    new = (k_new, v_new, pos)
-    if any(t is not None for t in new):
-        if any(t is None for t in new):
+    if lse is not None and (lse.shape != shape[:-1] or not lse.is_contiguous()):
+        raise ValueError(f"{what}: lse must be contiguous, shaped like q without its last dimension")
+    kp = vp = pp = None
+    if k_new is not None or v_new is not None or pos is not None:
+        if k_new is None or v_new is None or pos is None:
             raise ValueError(f"{what}: k_new, v_new and pos go together")
-        _require(pos, "pos", torch.int32, 1)
-        for t, n in ((k_new, "k_new"), (v_new, "v_new")):
-            _require(t, n, torch.bfloat16, q.dim())
-            if t.shape != q.shape[:-2] + (Hkv, D):
-                raise ValueError(f"{what}: inconsistent shapes")
-        if pos.shape != (B,):
+        for t in (k_new, v_new):
+            if t.shape != shape[:-2] + (Hkv, D) or not t.is_contiguous():
+                raise ValueError(f"{what}: k_new and v_new must be contiguous, with a head for each KV head and token")
+        if pos.shape[0] != B:
             raise ValueError(f"{what}: inconsistent shapes")
-    _same_device(what, q, k, v, out, seq_lens, block_table, workspace, lse, status, *new)
-    ws_ptr, ws_bytes = (None, 0) if workspace is None else (workspace.data_ptr(),
-                                                           workspace.numel() * workspace.element_size())
+        kp, vp, pp = k_new.data_ptr(), v_new.data_ptr(), pos.data_ptr()
+    wp, wb = None, 0
+    if workspace is not None:
+        if not workspace.is_contiguous():
+            raise ValueError(f"{what}: workspace must be contiguous")
+        wp, wb = workspace.data_ptr(), workspace.numel() * workspace.element_size()
     if B == 0:
         return
-    _launch(load().kvd_decode_fp4,
-            [ctypes.byref(c), q.data_ptr(), seq_lens.data_ptr(), B, T, int(max_seq_len), Hq, Hkv, D, float(scale),
-             int(n_split), ws_ptr, ws_bytes, out.data_ptr(), OUT_F32 if out.dtype == torch.float32 else OUT_BF16,
-             _ptr(lse), _ptr(k_new), _ptr(v_new), _ptr(pos), _status_arg(status, what)], "kvd_decode_fp4", q, stream)
+    _launch((_lib or load()).kvd_decode_fp4, "kvd_decode_fp4", dev, stream, ctypes.byref(c), q.data_ptr(),
+            seq_lens.data_ptr(), B, T, int(max_seq_len), Hq, Hkv, D, float(scale), int(n_split), wp, wb, out.data_ptr(),
+            OUT_F32 if out.dtype is f32 else OUT_BF16, _ptr(lse), kp, vp, pp, _ptr(status))
