@@ -13,10 +13,12 @@ const ChunkKernel* fp4_table_d64(int nt, bool f32);
 const ChunkKernel* fp4_table_d128(int nt, bool f32);
 const ChunkKernel* fp4_table_d256(int nt, bool f32);
 
-// Query rows of a pair are the columns of the kernel's MMAs, 8 at a time: up
-// to 8 rows take one column tile, more take two per CTA (blocks of 16 rows).
+// The query rows of a pair are the columns of the kernel's MMAs, 8 to a tile; a
+// CTA takes up to 6 tiles (48 rows), so that a cached row is converted once for
+// all of them. More rows are dealt evenly to blocks of at most 48, a CTA each.
 const ChunkKernel* fp4_chunk_kernel(int head_dim, bool f32_out, int rows) {
-    const int nt = rows <= 8 ? 1 : 2;
+    const int blocks = (rows + 47) / 48;
+    const int nt = ((rows + blocks - 1) / blocks + 7) / 8;  // 5 tiles run as 6
     switch (head_dim) {
         case 64: return fp4_table_d64(nt, f32_out);
         case 128: return fp4_table_d128(nt, f32_out);
@@ -27,7 +29,7 @@ const ChunkKernel* fp4_chunk_kernel(int head_dim, bool f32_out, int rows) {
 
 namespace {
 
-std::atomic<uint64_t> g_fp4_ready[kMaxDevices];  // bit 4 * (head_dim index) + kernel index: shared memory allowed
+std::atomic<uint64_t> g_fp4_ready[kMaxDevices];  // bit 10 * (head_dim index) + kernel index: shared memory allowed
 
 kvd_status check_rope(const kvd_rope* rope, int head_dim, RopeTable* out) {
     if (!rope || !rope->turns || !aligned(rope->turns, 8)) return KVD_ERR_INVALID_ARG;
@@ -136,7 +138,7 @@ kvd_status check_fp4(const kvd_cache_fp4* c, int batch, int head_dim, PagedCache
 }
 
 // Split count: one CTA per resident slot, shared among the row blocks of a
-// token run, but no fewer than a tile for each of a CTA's 8 warps (256 tokens).
+// token run, but no fewer tokens than a tile for each of a CTA's 8 warps (256).
 kvd_status plan_fp4(int batch, int T, int Hq, int Hkv, int D, int max_len, int num_sms, int request, int* n_split,
                     size_t* ws) {
     kvd_status st = check_shape(batch, Hq, Hkv, D, KVD_OUT_BF16);
@@ -415,7 +417,7 @@ kvd_status kvd_decode_fp4(const kvd_cache_fp4* cache, const void* q, const int32
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     int dev = 0, sms = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return KVD_ERR_CUDA;
-    const uint64_t bit = 1ull << (k->index + (head_dim == 64 ? 0 : head_dim == 128 ? 4 : 8));
+    const uint64_t bit = 1ull << (k->index + (head_dim == 64 ? 0 : head_dim == 128 ? 10 : 20));
     if (!(g_fp4_ready[dev].load(std::memory_order_acquire) & bit)) {
         if (cudaFuncSetAttribute(k->fn, cudaFuncAttributeMaxDynamicSharedMemorySize, k->smem_bytes) != cudaSuccess)
             return KVD_ERR_CUDA;
