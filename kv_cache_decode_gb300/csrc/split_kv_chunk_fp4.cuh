@@ -37,7 +37,7 @@
 // again while V is still in use. Waits are bounded: one that gives up flags
 // KVD_STATUS_TIMEOUT, and since a segment fixes its tiles, the working warps go on to its end
 // together, on whatever the tiles hold, and stop there. The running maxima are only raised, after a vote, when a
-// score passes them by 2^8. At a segment's end the warps' states are merged through shared memory.
+// score passes them by 2^15. At a segment's end the warps' states are merged through shared memory.
 #pragma once
 
 #include "fp4.cuh"
@@ -57,8 +57,8 @@ struct Fp4Shape {
     static constexpr int DW = D / WD;            // columns of the output a warp holds
     static constexpr int ACC = KS / WD * NT * 4;
     // Blocks of 16 tokens of a warp per tile: two share each load of q's fragments; one where
-    // two would leave room for a single CTA per SM (shared memory, or the scores' registers).
-    static constexpr int TB = ((D == 256 && NT <= 3) || NT == 3) ? 1 : 2;
+    // two would leave room for a single CTA per SM.
+    static constexpr int TB = (D == 256 && NT <= 3) ? 1 : 2;
     static constexpr int GB = TB * WD;           // blocks of a group's part of a tile
     static constexpr int CB = TB * NW;           // blocks of a tile: at most 16, a lane for each
     static constexpr int TILE = 16 * CB;
@@ -75,7 +75,7 @@ struct Fp4Shape {
     static constexpr int QBYTES = QREG ? 0 : KS * NT * 32 * 8;
     static constexpr int SMEM = RING + SHARED + QBYTES;
     static constexpr int STATIC = 4096 + 2 * NW * ROWS * 4 + 24 * ROWS;  // an upper bound of the static arrays
-    static constexpr int MINB = (ACC <= 48 && 2 * (SMEM + STATIC + 1024) <= 228 * 1024) ? 2 : 1;
+    static constexpr int MINB = (ACC <= 32 && 2 * (SMEM + STATIC + 1024) <= 228 * 1024) ? 2 : 1;
     // The loading warp is a ninth; a CTA alone on its SM launches a warpgroup for it, whose
     // registers the working warps then take (168 a thread at launch, 232 and 40 after: 2 * 232 + 40 = 3 * 168).
     static constexpr bool SPLIT = MINB == 1;
@@ -129,7 +129,17 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
     return r;
 }
 
+// The low halves of a's bytes and the high halves of b's: (a & 0x0f..) | (b & 0xf0..) in one operation.
+__device__ __forceinline__ uint32_t nib(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("lop3.b32 %0, %1, %2, %3, 0xe4;" : "=r"(r) : "r"(a), "r"(b), "r"(0x0f0f0f0fu));
+    return r;
+}
+
 constexpr float kNoMax = -3e38f;  // running maximum before any score
+// How far (in powers of two) a score may pass its running maximum: a weight of 2^15 is still an f16 (the largest is
+// 65504), and one of 2^-14 of the maximum a normal one. Raising costs up to a fifth of a tile's time.
+constexpr float kRoom = 15.f;
 // Integers ordered as the floats they stand for.
 __device__ __forceinline__ int float_order(float f) {
     const int i = __float_as_int(f);
@@ -625,8 +635,8 @@ __global__ void __launch_bounds__(Fp4Shape<D, NT, F32OUT>::THREADS, Fp4Shape<D, 
                 for (int z = 0; z < 2; ++z)
 #pragma unroll
                     for (int x = 0; x < TB; ++x)
-                        raise |= fmaxf(s[x][j][z], s[x][j][2 + z]) > ms[j][z] + 8.f ||
-                                 fmaxf(s[x][j][z] + ev[x][0], s[x][j][2 + z] + ev[x][1]) > mo[j][z] + 8.f;
+                        raise |= fmaxf(s[x][j][z], s[x][j][2 + z]) > ms[j][z] + kRoom ||
+                                 fmaxf(s[x][j][z] + ev[x][0], s[x][j][2 + z] + ev[x][1]) > mo[j][z] + kRoom;
             if constexpr (WD > 1) {
                 raise = group_any(1 + group, 32 * WD, raise);  // also: the group is done with the previous tile's weights
             } else {
@@ -735,10 +745,10 @@ __global__ void __launch_bounds__(Fp4Shape<D, NT, F32OUT>::THREADS, Fp4Shape<D, 
 #pragma unroll
                     for (int v = 0; v < VW; ++v) {
                         uint32_t ev0[4], od0[4], ev1[4], od1[4];  // even and odd columns, token pairs 0 and 8 further
-                        e2m1x8_to_f16((w[0][v] & 0x0f0f0f0fu) | ((w[1][v] << 4) & 0xf0f0f0f0u), ev0);
-                        e2m1x8_to_f16(((w[0][v] >> 4) & 0x0f0f0f0fu) | (w[1][v] & 0xf0f0f0f0u), od0);
-                        e2m1x8_to_f16((w[2][v] & 0x0f0f0f0fu) | ((w[3][v] << 4) & 0xf0f0f0f0u), ev1);
-                        e2m1x8_to_f16(((w[2][v] >> 4) & 0x0f0f0f0fu) | (w[3][v] & 0xf0f0f0f0u), od1);
+                        e2m1x8_to_f16(nib(w[0][v], w[1][v] << 4), ev0);
+                        e2m1x8_to_f16(nib(w[0][v] >> 4, w[1][v]), od0);
+                        e2m1x8_to_f16(nib(w[2][v], w[3][v] << 4), ev1);
+                        e2m1x8_to_f16(nib(w[2][v] >> 4, w[3][v]), od1);
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
                             const uint32_t a[4] = {hmul2(ev0[i], sc[0]), hmul2(od0[i], sc[0]), hmul2(ev1[i], sc[1]),
@@ -753,14 +763,15 @@ __global__ void __launch_bounds__(Fp4Shape<D, NT, F32OUT>::THREADS, Fp4Shape<D, 
                 }
             };
             if constexpr (WD == 1) {
-#pragma unroll 1
-                for (int x = 0; x < min(blocks, TB); ++x) {  // one copy of the code: instruction fetch counts in short runs
+#pragma unroll
+                for (int x = 0; x < TB; ++x) {
+                    if (x >= blocks) break;
                     uint2 wx[NT][PL];
 #pragma unroll
                     for (int j = 0; j < NT; ++j)
 #pragma unroll
                         for (int k = 0; k < PL; ++k)
-                            wx[j][k] = make_uint2(x ? wf[TB - 1][j][k].x : wf[0][j][k].x, x ? wf[TB - 1][j][k].y : wf[0][j][k].y);
+                            wx[j][k] = wf[x][j][k];
                     block_pv(x, wx);
                 }
             } else {
