@@ -292,10 +292,8 @@ kvd_status kvd_kv_quantize_fp4(const void* cache, void* blocks, const int32_t* s
         rl{seq_lens, (size_t)batch * 4};
     if (rb.overlaps(rc) || rb.overlaps(rl)) return KVD_ERR_INVALID_ARG;
     if (batch == 0 || max_seq_len == 0) return KVD_OK;
-    int sms = 0;
-    const kvd_status st = device_sms(&sms);
-    if (st != KVD_OK) return st;
-    return launch_quantize_fp4(cache, blocks, seq_lens, batch, s_max, s_max_blocks, max_seq_len, n_heads_kv, head_dim, sms,
+    if ((long long)batch * ((max_seq_len + 15) / 16) > 0x7fffffffLL) return KVD_ERR_INVALID_ARG;
+    return launch_quantize_fp4(cache, blocks, seq_lens, batch, s_max, s_max_blocks, max_seq_len, n_heads_kv, head_dim,
                                static_cast<cudaStream_t>(stream)) == cudaSuccess
                ? KVD_OK
                : KVD_ERR_CUDA;
@@ -319,10 +317,9 @@ kvd_status kvd_kv_read_fp4(const void* blocks, const int32_t* block_table, int s
         rb{blocks, (size_t)(rows / 16) * n_heads_kv * kvd_fp4_block_bytes(head_dim)}, rl{seq_lens, (size_t)batch * 4};
     if (ro.overlaps(rb) || ro.overlaps(rl)) return KVD_ERR_INVALID_ARG;
     if (batch == 0 || max_seq_len == 0) return KVD_OK;
-    int sms = 0;
-    if ((st = device_sms(&sms)) != KVD_OK) return st;
+    if ((long long)batch * ((max_seq_len + 15) / 16) > 0x7fffffffLL) return KVD_ERR_INVALID_ARG;
     return launch_read_fp4(blocks, pg, s_max, out, s_out, seq_lens, batch, max_seq_len, n_heads_kv, head_dim, status_word,
-                           sms, static_cast<cudaStream_t>(stream)) == cudaSuccess
+                           static_cast<cudaStream_t>(stream)) == cudaSuccess
                ? KVD_OK
                : KVD_ERR_CUDA;
 }

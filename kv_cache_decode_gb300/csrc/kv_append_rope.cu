@@ -5,11 +5,10 @@
 // each; a separate rotation would read and write q and k once more. Bound by
 // memory for prompts and by latency for single tokens.
 //
-// A block takes a few tokens (fewer blocks per token for many tokens, several
-// blocks per token for few): each token's sequence, position and place in the
-// cache, then the rotary_dim / 2 cosines and sines, are worked out once in
-// shared memory for all its heads. A head is dealt to D / 16 threads as in
-// rope.cuh; where the cache is quantized these threads find the row's (and,
+// A warp takes a token (a share of its heads where there are few tokens): its
+// sequence, position and place in the cache and its cosines and sines, then the heads, two steps'
+// loads at a time; warps wait for nothing but their own loads. A head is dealt to D / 16
+// threads as in rope.cuh; where the cache is quantized these threads find the row's (and,
 // fp4, the 16 columns') largest magnitude by shuffles, so a row goes from its
 // load to its codes in registers.
 #include <algorithm>
@@ -20,193 +19,173 @@
 
 namespace kvd {
 
-constexpr int kAppThreads = 256;
-constexpr int kAppRows = 4;  // tokens of a block, at most
+constexpr int kAppWarps = 4;
 
-// DD: head dimension of a quantized cache (64, 128, 256), 0 for bf16 (any multiple of 8).
+// DD: head dimension 64, 128 or 256, or 0 for any other (bf16 cache only).
 template <CacheForm FORM, int DD>
-__global__ void __launch_bounds__(kAppThreads) append_rope_kernel(const AppendTarget to, const RopeTable rope,
-                                                                  const NewRows in, int rows_per_block,
-                                                                  int32_t* status) {
-    extern __shared__ float2 s_cs[];        // [tokens of the block][R / 2]
-    __shared__ long long s_pos[kAppRows];   // position, or LLONG_MIN: the row belongs to no sequence
-    __shared__ long long s_dst[kAppRows];   // cache row (fp4: block of head 0), or -1: not appended
-    __shared__ int s_slot[kAppRows];        // fp4: token's place in its block
+__global__ void __launch_bounds__(kAppWarps * 32) append_rope_kernel(const AppendTarget to, const RopeTable rope,
+                                                                     const NewRows in, int parts, int32_t* status) {
+    extern __shared__ float2 s_cs[];  // [warps][R / 2]
     pdl_launch_dependents();  // the attention that may follow waits for this grid before it reads anything
-    const int tid = threadIdx.x, lane = tid & 31;
-    const int D = DD ? DD : in.D;
-    const int R = rope.turns ? rope.rotary_dim : 0, half = R >> 1, units = (D + 15) >> 4;
-    const long long row0 = (long long)blockIdx.x * rows_per_block;
-    const int n = (int)min((long long)rows_per_block, in.rows - row0);
+    const int lane = threadIdx.x & 31;
+    const long long w = (long long)blockIdx.x * kAppWarps + (threadIdx.x >> 5);
+    const long long row = w / parts;
+    const int part = (int)(w - row * parts);
+    if (row >= in.rows) return;
 
-    // ---- each token's sequence, position and place ----
-    if (tid < 32 * n) {
-        const int r = tid >> 5;
-        const long long row = row0 + r;
-        int b;
-        long long i;
-        bool live = true;
-        if (in.offsets) {
-            int cnt = 0;  // offsets <= row, counted over all of them at once rather than by dependent steps
-            for (int j = lane; j <= in.B; j += 32) cnt += __ldg(in.offsets + j) <= row ? 1 : 0;
-            b = __reduce_add_sync(0xffffffffu, cnt) - 1;
-            live = b >= 0 && b < in.B;
-            i = live ? row - __ldg(in.offsets + b) : 0;
-            if (i < 0) live = false;
-        } else {
-            b = (int)(row / in.T);
-            i = row - (long long)b * in.T;
+    // ---- the token's sequence, position and place ----
+    int sq;  // its sequence
+    long long i;
+    if (in.offsets) {
+        if (row >= __ldg(in.offsets + in.B)) return;  // a buffer may be much longer than its sequences
+        int cnt = 0;  // offsets <= row, counted over all of them at once rather than by dependent steps
+        for (int j = lane; j <= in.B; j += 32) cnt += __ldg(in.offsets + j) <= row ? 1 : 0;
+        sq = __reduce_add_sync(0xffffffffu, cnt) - 1;
+        if (sq < 0 || sq >= in.B) return;
+        i = row - __ldg(in.offsets + sq);
+        if (i < 0) return;
+    } else {
+        sq = (int)(row / in.T);
+        i = row - (long long)sq * in.T;
+    }
+    const long long t = (long long)__ldg(in.pos + sq) + i;
+    long long dst = -1;  // cache row (fp4: block of head 0), or -1: not appended
+    int slot = 0;        // fp4: token's place in its block
+    if (t < 0 || t >= to.S_max) {
+        if (status && part == 0 && lane == 0) atomicOr(status, KVD_STATUS_POS_OUT_OF_RANGE);
+    } else {
+        long long seq = sq, cap = to.S_max, at = t;  // sequence (page), its capacity, place in it
+        bool ok = true;
+        if (to.pg.block_table) {
+            seq = __ldg(to.pg.block_table + (size_t)sq * to.pg.max_blocks + (t >> to.pg.page_shift));
+            cap = 1LL << to.pg.page_shift;
+            at = t & (cap - 1);
+            ok = seq >= 0 && seq < to.pg.num_pages;
+            if (!ok && status && part == 0 && lane == 0) atomicOr(status, KVD_STATUS_BAD_PAGE);
         }
-        if (lane == 0) {
-            long long t = live ? (long long)__ldg(in.pos + b) + i : LLONG_MIN;
-            long long dst = -1;
-            int slot = 0;
-            if (live && (t < 0 || t >= to.S_max)) {
-                if (status && blockIdx.y == 0) atomicOr(status, KVD_STATUS_POS_OUT_OF_RANGE);
-            } else if (live) {
-                long long seq = b, cap = to.S_max, at = t;  // sequence (page), its capacity, place in it
-                bool ok = true;
-                if (to.pg.block_table) {
-                    seq = __ldg(to.pg.block_table + (size_t)b * to.pg.max_blocks + (t >> to.pg.page_shift));
-                    cap = 1LL << to.pg.page_shift;
-                    at = t & (cap - 1);
-                    ok = seq >= 0 && seq < to.pg.num_pages;
-                    if (!ok && status && blockIdx.y == 0) atomicOr(status, KVD_STATUS_BAD_PAGE);
-                }
-                if (ok) {
-                    dst = FORM == CacheForm::kFp4 ? seq * in.Hkv * (cap >> 4) + (at >> 4) : seq * cap + at;
-                    slot = (int)(at & 15);
-                }
-            }
-            s_pos[r] = t;
-            s_dst[r] = dst;
-            s_slot[r] = slot;
+        if (ok) {
+            dst = FORM == CacheForm::kFp4 ? seq * in.Hkv * (cap >> 4) + (at >> 4) : seq * cap + at;
+            slot = (int)(at & 15);
         }
     }
-    __syncthreads();
-    for (int i = tid; i < n * half; i += kAppThreads) {
-        const int r = i / half;
-        s_cs[i] = rope_cos_sin(s_pos[r], __ldg(rope.turns + (i - r * half)), rope.factor);
-    }
-    __syncthreads();
+    RopeWarp<DD> rw;
+    rw.init(rope, t, in.D, s_cs + (threadIdx.x >> 5) * (rope.rotary_dim >> 1));
+    const int D = rw.D, units = rw.units;
 
-    const int start = blockIdx.y * kAppThreads + tid, step = gridDim.y * kAppThreads;
-    // ---- queries ----
-    if (in.q) {
-        const int per_row = in.Hq * units;
-        for (int i = start; i < n * per_row; i += step) {
-            const int r = i / per_row, j = i - r * per_row, h = j / units, u = j - h * units;
-            if (s_pos[r] == LLONG_MIN) continue;
-            const RopeUnit ru = rope_unit(u, D, R, rope.interleaved);
-            const size_t qe = (size_t)(row0 + r) * in.qs + (size_t)h * D, oe = (size_t)(row0 + r) * in.qos + (size_t)h * D;
-            float a[8], b[8];
-            load8<false>(in.q, qe + ru.ca, a);
-            if (ru.cb >= 0) load8<false>(in.q, qe + ru.cb, b);
-            if (ru.turn) rope_turn(a, b, s_cs + r * half + 8 * u, rope.interleaved);
-            store8<false>(in.q_out, oe + ru.ca, a);
-            if (ru.cb >= 0) store8<false>(in.q_out, oe + ru.cb, b);
+    if (in.q) rw.template heads<false, false>(in.q, (size_t)row * in.qs, in.q_out, (size_t)row * in.qos, in.Hq, part, parts);
+    if (dst < 0) return;
+    // ---- keys, then values, likewise; whole warps stay in the loop for the shuffles ----
+    const int total = 2 * in.Hkv * units;
+    for (int base = 32 * part; base < total; base += 64 * parts) {
+        RopeRaw<false> raw[2];
+#pragma unroll
+        for (int k2 = 0; k2 < 2; ++k2) {
+            const int j = base + k2 * 32 * parts + lane, hh = j / units;
+            const bool value = hh >= in.Hkv;
+            if (j < total)
+                raw[k2].load(value ? in.v : in.k, (size_t)row * (value ? in.vs : in.ks) + (size_t)(value ? hh - in.Hkv : hh) * D,
+                             rope_unit(j - hh * units, D, value ? 0 : rw.R, rope.interleaved));
         }
-    }
-    // ---- keys, then values; whole warps stay in the loop for the shuffles ----
-    const int per_row = 2 * in.Hkv * units, total = n * per_row;
-    for (int i = start; i - lane < total; i += step) {
-        const bool live0 = i < total;
-        const int ii = live0 ? i : 0;
-        const int r = ii / per_row, j = ii - r * per_row, hh = j / units, u = j - hh * units;
-        const bool value = hh >= in.Hkv;
-        const int h = value ? hh - in.Hkv : hh;
-        const long long dst = s_dst[r];
-        const bool live = live0 && dst >= 0;
-        const int Rh = value ? 0 : R;
-        const RopeUnit ru = rope_unit(u, D, Rh, rope.interleaved);
-        const void* src = value ? in.v : in.k;
-        const size_t e = (size_t)(row0 + r) * (value ? in.vs : in.ks) + (size_t)h * D;
-        float a[8] = {}, b[8] = {};
-        if (live) {
-            load8<false>(src, e + ru.ca, a);
-            if (ru.cb >= 0) load8<false>(src, e + ru.cb, b);
-            if (ru.turn) rope_turn(a, b, s_cs + r * half + 8 * u, rope.interleaved);
-        }
-        if constexpr (FORM == CacheForm::kBf16) {
-            if (live) {
+#pragma unroll
+        for (int k2 = 0; k2 < 2; ++k2) {
+            const int j0 = base + k2 * 32 * parts;
+            if (j0 >= total) break;
+            const bool live = j0 + lane < total;
+            const int j = live ? j0 + lane : 0, hh = j / units, u = j - hh * units;
+            const bool value = hh >= in.Hkv;
+            const int h = value ? hh - in.Hkv : hh;
+            const int Rh = value ? 0 : rw.R;
+            const RopeUnit ru = rope_unit(u, D, Rh, rope.interleaved);
+            if constexpr (FORM == CacheForm::kBf16) {
                 void* cache = value ? to.v : to.k;
                 const size_t o = ((size_t)dst * in.Hkv + h) * D;
-                store8<false>(cache, o + ru.ca, a);
-                if (ru.cb >= 0) store8<false>(cache, o + ru.cb, b);
-            }
-        } else {
-            constexpr int UN = DD / 16;  // threads of a row
-            unpack8(pack8(a), a);        // the rotated row as bf16, as the plain append would be given it
-            unpack8(pack8(b), b);
-            float ma = 0.f, mb = 0.f;
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                ma = fmaxf(ma, fabsf(a[k]));
-                mb = fmaxf(mb, fabsf(b[k]));
-            }
-            float m = fmaxf(ma, mb);
-#pragma unroll
-            for (int off = UN / 2; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
-            if constexpr (FORM == CacheForm::kFp4) {
-                using Blk = Fp4Block<DD>;
-                // The other 8 of each vector's 16 columns may lie with another thread (halves).
-                const int R16 = (ru.turn && !rope.interleaved) ? Rh >> 4 : 0;  // this vector's unit map, see rope_unit
-                auto partner = [&](int c) -> float {
-                    const int v = (c >> 3) ^ 1;  // the neighbour vector of the row
-                    const int pu = R16 ? (v < R16 ? v : v - R16) : v >> 1;
-                    const bool second = R16 ? v >= R16 : (v & 1);
-                    const int from = (lane & ~(UN - 1)) + pu;
-                    const float xa = __shfl_sync(0xffffffffu, ma, from), xb = __shfl_sync(0xffffffffu, mb, from);
-                    return second ? xb : xa;
-                };
-                const float na = fmaxf(ma, partner(ru.ca)), nb = fmaxf(mb, partner(ru.cb));
-                const uint32_t eb = fp4_row_exp(m);
-                const float up = eb ? fp4_row_inv(eb) : 0.f;
-                float ia, ib, z[8];
-                const uint32_t sa = fp4_block_scale(na * up, ia), sb = fp4_block_scale(nb * up, ib);
-#pragma unroll
-                for (int k = 0; k < 8; ++k) z[k] = __fmul_rn(__fmul_rn(a[k], up), ia);
-                const uint32_t wa = e2m1x8(z);
-#pragma unroll
-                for (int k = 0; k < 8; ++k) z[k] = __fmul_rn(__fmul_rn(b[k], up), ib);
-                const uint32_t wb = e2m1x8(z);
-                if (live) {
-                    const long long nblk = to.pg.block_table ? (1LL << to.pg.page_shift) >> 4 : to.S_max >> 4;
-                    uint8_t* blk = static_cast<uint8_t*>(value ? to.v : to.k) + (size_t)(dst + h * nblk) * Blk::BYTES;
-                    const int t = s_slot[r];
-                    *reinterpret_cast<uint32_t*>(blk + Blk::code(t, ru.ca)) = wa;
-                    *reinterpret_cast<uint32_t*>(blk + Blk::code(t, ru.cb)) = wb;
-                    if (!(ru.ca & 8)) blk[Blk::scale(t, ru.ca)] = (uint8_t)sa;
-                    if (!(ru.cb & 8)) blk[Blk::scale(t, ru.cb)] = (uint8_t)sb;
-                    if (u == 0) blk[Blk::exp(t)] = (uint8_t)eb;
+                if (live && !ru.turn) raw[k2].copy(cache, o, ru);
+                if (live && ru.turn) {
+                    float a[8], b[8];
+                    raw[k2].get(a, b);
+                    rw.turn(a, b, u);
+                    store8<false>(cache, o + ru.ca, a);
+                    store8<false>(cache, o + ru.cb, b);
                 }
             } else {
-                constexpr bool FP8 = FORM == CacheForm::kFp8;
-                const float sc = __fdiv_rn(m, FP8 ? 448.f : 127.f);
-                auto codes = [&](const float(&f)[8]) {
-                    uint32_t w[2] = {0u, 0u};
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        int c = 0;
-                        if (m > 0.f) {
-                            if constexpr (FP8) {
-                                c = __nv_cvt_float_to_fp8(__fdiv_rn(f[k], sc), __NV_SATFINITE, __NV_E4M3);
-                                if ((c & 0x7f) == 0) c = 0;
-                            } else {
-                                c = max(-127, min(127, __float2int_rn(__fdiv_rn(f[k], sc))));
-                            }
-                        }
-                        w[k >> 2] |= (uint32_t)(c & 0xff) << (8 * (k & 3));
-                    }
-                    return make_uint2(w[0], w[1]);
-                };
-                const uint2 wa = codes(a), wb = codes(b);
+                float a[8] = {}, b[8] = {};
                 if (live) {
-                    const size_t o = (size_t)dst * in.Hkv + h;
-                    uint8_t* c = static_cast<uint8_t*>(value ? to.v : to.k) + o * DD;
-                    *reinterpret_cast<uint2*>(c + ru.ca) = wa;
-                    *reinterpret_cast<uint2*>(c + ru.cb) = wb;
-                    if (u == 0) (value ? to.v_scale : to.k_scale)[o] = sc;
+                    raw[k2].get(a, b);
+                    if (ru.turn) rw.turn(a, b, u);
+                }
+                constexpr int UN = DD / 16;  // threads of a row
+                unpack8(pack8(a), a);        // the rotated row as bf16, as the plain append would be given it
+                unpack8(pack8(b), b);
+                float ma = 0.f, mb = 0.f;
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    ma = fmaxf(ma, fabsf(a[k]));
+                    mb = fmaxf(mb, fabsf(b[k]));
+                }
+                float m = fmaxf(ma, mb);
+#pragma unroll
+                for (int off = UN / 2; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+                if constexpr (FORM == CacheForm::kFp4) {
+                    using Blk = Fp4Block<DD>;
+                    // The other 8 of each vector's 16 columns may lie with another thread (halves).
+                    const int R16 = (ru.turn && !rope.interleaved) ? Rh >> 4 : 0;  // this vector's unit map, see rope_unit
+                    auto partner = [&](int c) -> float {
+                        const int v = (c >> 3) ^ 1;  // the neighbour vector of the row
+                        const int pu = R16 ? (v < R16 ? v : v - R16) : v >> 1;
+                        const bool second = R16 ? v >= R16 : (v & 1);
+                        const int from = (lane & ~(UN - 1)) + pu;
+                        const float xa = __shfl_sync(0xffffffffu, ma, from), xb = __shfl_sync(0xffffffffu, mb, from);
+                        return second ? xb : xa;
+                    };
+                    const float na = fmaxf(ma, partner(ru.ca)), nb = fmaxf(mb, partner(ru.cb));
+                    const uint32_t eb = fp4_row_exp(m);
+                    const float up = eb ? fp4_row_inv(eb) : 0.f;
+                    float ia, ib, z[8];
+                    const uint32_t sa = fp4_block_scale(na * up, ia), sb = fp4_block_scale(nb * up, ib);
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) z[k] = __fmul_rn(__fmul_rn(a[k], up), ia);
+                    const uint32_t wa = e2m1x8(z);
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) z[k] = __fmul_rn(__fmul_rn(b[k], up), ib);
+                    const uint32_t wb = e2m1x8(z);
+                    if (live) {
+                        const long long nblk = to.pg.block_table ? (1LL << to.pg.page_shift) >> 4 : to.S_max >> 4;
+                        uint8_t* blk = static_cast<uint8_t*>(value ? to.v : to.k) + (size_t)(dst + h * nblk) * Blk::BYTES;
+                        const int t = slot;
+                        *reinterpret_cast<uint32_t*>(blk + Blk::code(t, ru.ca)) = wa;
+                        *reinterpret_cast<uint32_t*>(blk + Blk::code(t, ru.cb)) = wb;
+                        if (!(ru.ca & 8)) blk[Blk::scale(t, ru.ca)] = (uint8_t)sa;
+                        if (!(ru.cb & 8)) blk[Blk::scale(t, ru.cb)] = (uint8_t)sb;
+                        if (u == 0) blk[Blk::exp(t)] = (uint8_t)eb;
+                    }
+                } else {
+                    constexpr bool FP8 = FORM == CacheForm::kFp8;
+                    const float sc = __fdiv_rn(m, FP8 ? 448.f : 127.f);
+                    auto codes = [&](const float(&f)[8]) {
+                        uint32_t w[2] = {0u, 0u};
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) {
+                            int c = 0;
+                            if (m > 0.f) {
+                                if constexpr (FP8) {
+                                    c = __nv_cvt_float_to_fp8(__fdiv_rn(f[k], sc), __NV_SATFINITE, __NV_E4M3);
+                                    if ((c & 0x7f) == 0) c = 0;
+                                } else {
+                                    c = max(-127, min(127, __float2int_rn(__fdiv_rn(f[k], sc))));
+                                }
+                            }
+                            w[k >> 2] |= (uint32_t)(c & 0xff) << (8 * (k & 3));
+                        }
+                        return make_uint2(w[0], w[1]);
+                    };
+                    const uint2 wa = codes(a), wb = codes(b);
+                    if (live) {
+                        const size_t o = (size_t)dst * in.Hkv + h;
+                        uint8_t* c = static_cast<uint8_t*>(value ? to.v : to.k) + o * DD;
+                        *reinterpret_cast<uint2*>(c + ru.ca) = wa;
+                        *reinterpret_cast<uint2*>(c + ru.cb) = wb;
+                        if (u == 0) (value ? to.v_scale : to.k_scale)[o] = sc;
+                    }
                 }
             }
         }
@@ -215,20 +194,19 @@ __global__ void __launch_bounds__(kAppThreads) append_rope_kernel(const AppendTa
 
 cudaError_t launch_append_rope(const AppendTarget& to, const RopeTable& rope, const NewRows& in, int32_t* status,
                                int num_sms, cudaStream_t stream) {
-    const int rpb = (int)std::max(1LL, std::min((long long)kAppRows, in.rows / (4LL * num_sms)));
-    const long long bx = (in.rows + rpb - 1) / rpb;
-    const int units = (in.D + 15) / 16;
-    const long long items = (long long)rpb * std::max(in.q ? in.Hq : 0, 2 * in.Hkv) * units;
-    const int by = (int)std::max(1LL, std::min((items + kAppThreads - 1) / kAppThreads, 2LL * num_sms / bx));
+    const long long units = (in.D + 15) / 16;
+    const long long steps = (std::max((long long)(in.q ? in.Hq : 0), 2LL * in.Hkv) * units + 31) / 32;
+    const int parts = rope_parts(in.rows, steps, num_sms);
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)bx, (unsigned)by, 1);
-    cfg.blockDim = dim3(kAppThreads, 1, 1);
-    cfg.dynamicSmemBytes = rope.turns ? (size_t)rpb * (rope.rotary_dim / 2) * sizeof(float2) : 0;
+    cfg.gridDim = dim3((unsigned)((in.rows * parts + kAppWarps - 1) / kAppWarps), 1, 1);
+    cfg.blockDim = dim3(kAppWarps * 32, 1, 1);
+    cfg.dynamicSmemBytes = rope.turns ? (size_t)kAppWarps * (rope.rotary_dim / 2) * sizeof(float2) : 0;
     cfg.stream = stream;
-#define KVD_APP(F, DD) cudaLaunchKernelEx(&cfg, append_rope_kernel<CacheForm::F, DD>, to, rope, in, rpb, status)
+#define KVD_APP(F, DD) cudaLaunchKernelEx(&cfg, append_rope_kernel<CacheForm::F, DD>, to, rope, in, parts, status)
 #define KVD_APP_D(F) (in.D == 64 ? KVD_APP(F, 64) : in.D == 128 ? KVD_APP(F, 128) : in.D == 256 ? KVD_APP(F, 256) : cudaErrorInvalidValue)
     switch (to.form) {
-        case CacheForm::kBf16: return KVD_APP(kBf16, 0);
+        case CacheForm::kBf16:
+            return in.D == 64 ? KVD_APP(kBf16, 64) : in.D == 128 ? KVD_APP(kBf16, 128) : in.D == 256 ? KVD_APP(kBf16, 256) : KVD_APP(kBf16, 0);
         case CacheForm::kInt8: return KVD_APP_D(kInt8);
         case CacheForm::kFp8: return KVD_APP_D(kFp8);
         case CacheForm::kFp4: return KVD_APP_D(kFp4);

@@ -74,18 +74,6 @@ __device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
                       pack_bf16x2(f[6], f[7]));
 }
 
-// 8 consecutive elements of a bf16 or fp32 row. Plain loads, not the read-only path: the rows may be turned in place.
-template <bool F32>
-__device__ __forceinline__ void load8(const void* base, size_t e, float (&f)[8]) {
-    if constexpr (F32) {
-        const float4 x = *reinterpret_cast<const float4*>(static_cast<const float*>(base) + e);
-        const float4 y = *(reinterpret_cast<const float4*>(static_cast<const float*>(base) + e) + 1);
-        f[0] = x.x; f[1] = x.y; f[2] = x.z; f[3] = x.w;
-        f[4] = y.x; f[5] = y.y; f[6] = y.z; f[7] = y.w;
-    } else {
-        unpack8(*reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(base) + e), f);
-    }
-}
 template <bool F32>
 __device__ __forceinline__ void store8(void* base, size_t e, const float (&f)[8]) {
     if constexpr (F32) {
@@ -95,6 +83,125 @@ __device__ __forceinline__ void store8(void* base, size_t e, const float (&f)[8]
     } else {
         *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(base) + e) = pack8(f);
     }
+}
+
+// A unit's two vectors as they lie in memory (plain loads, not the read-only path: rows may be turned in place), so that several units can be loaded before one is turned.
+template <bool F32>
+struct RopeRaw {
+    uint4 a[F32 ? 2 : 1], b[F32 ? 2 : 1];
+    __device__ __forceinline__ void load(const void* base, size_t e, const RopeUnit& u) {
+        if constexpr (F32) {
+            const uint4* p = reinterpret_cast<const uint4*>(static_cast<const float*>(base) + e + u.ca);
+            a[0] = p[0], a[1] = p[1];
+            if (u.cb >= 0) {
+                const uint4* q = reinterpret_cast<const uint4*>(static_cast<const float*>(base) + e + u.cb);
+                b[0] = q[0], b[1] = q[1];
+            }
+        } else {
+            a[0] = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(base) + e + u.ca);
+            if (u.cb >= 0) b[0] = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(base) + e + u.cb);
+        }
+    }
+    __device__ __forceinline__ void copy(void* base, size_t e, const RopeUnit& u) const {  // bit by bit, to the same type
+        if constexpr (F32) {
+            uint4* p = reinterpret_cast<uint4*>(static_cast<float*>(base) + e + u.ca);
+            p[0] = a[0], p[1] = a[1];
+            if (u.cb >= 0) {
+                uint4* q = reinterpret_cast<uint4*>(static_cast<float*>(base) + e + u.cb);
+                q[0] = b[0], q[1] = b[1];
+            }
+        } else {
+            *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(base) + e + u.ca) = a[0];
+            if (u.cb >= 0) *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(base) + e + u.cb) = b[0];
+        }
+    }
+    __device__ __forceinline__ void get(float (&x)[8], float (&y)[8]) const {
+        if constexpr (F32) {
+            const uint32_t v[8] = {a[0].x, a[0].y, a[0].z, a[0].w, a[1].x, a[1].y, a[1].z, a[1].w};
+            const uint32_t w[8] = {b[0].x, b[0].y, b[0].z, b[0].w, b[1].x, b[1].y, b[1].z, b[1].w};
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x[i] = __uint_as_float(v[i]), y[i] = __uint_as_float(w[i]);
+        } else {
+            unpack8(a[0], x);
+            unpack8(b[0], y);
+        }
+    }
+};
+
+// A warp's share of one token's work: its cosines and sines, and the turning of heads. DD: head dimension 64,
+// 128 or 256, whose units divide the warp, so that a thread keeps one unit of every
+// head and its 8 pairs' cosines and sines in registers; 0 for any other, with those in shared memory.
+template <int DD>
+struct RopeWarp {
+    static constexpr int UN = DD / 16;
+    float2 cs[DD ? 8 : 1];
+    const float2* s_cs;
+    int D, units, R;
+    bool interleaved;
+
+    // t: the token's position. buf: R / 2 entries of this warp's shared memory. Whole warps call this.
+    __device__ __forceinline__ void init(const RopeTable& rope, long long t, int D_, float2* buf) {
+        const int lane = threadIdx.x & 31;
+        D = DD ? DD : D_;
+        units = DD ? UN : (D + 15) >> 4;
+        R = rope.turns ? rope.rotary_dim : 0;
+        interleaved = rope.interleaved;
+        s_cs = buf;
+        for (int i = lane; i < R >> 1; i += 32) buf[i] = rope_cos_sin(t, __ldg(rope.turns + i), rope.factor);
+        __syncwarp();
+        if constexpr (DD > 0) {
+            const int u = lane % UN;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) cs[i] = u < R >> 4 ? buf[8 * u + i] : make_float2(1.f, 0.f);
+        }
+    }
+    __device__ __forceinline__ void turn(float (&a)[8], float (&b)[8], int u) const {
+        if constexpr (DD > 0)
+            rope_turn(a, b, cs, interleaved);
+        else
+            rope_turn(a, b, s_cs + 8 * u, interleaved);
+    }
+    // Turns the heads of one row, src to dst, this warp's steps of them: part, part + parts, ... Two steps'
+    // loads come before either is turned: one unit in flight per thread keeps too few bytes on the way.
+    template <bool IN32, bool OUT32>
+    __device__ __forceinline__ void heads(const void* src, size_t se, void* dst, size_t de, int H, int part, int parts) const {
+        const int lane = threadIdx.x & 31, total = H * units;
+        for (int base = 32 * part; base < total; base += 64 * parts) {
+            RopeRaw<IN32> raw[2];
+            RopeUnit ru[2];
+            int h[2], u[2];
+            bool live[2];
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const int j = base + k * 32 * parts + lane;
+                live[k] = j < total;
+                h[k] = j / units;
+                u[k] = j - h[k] * units;
+                ru[k] = rope_unit(u[k], D, R, interleaved);
+                if (live[k]) raw[k].load(src, se + (size_t)h[k] * D, ru[k]);
+            }
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                if (!live[k]) continue;
+                const size_t e = de + (size_t)h[k] * D;
+                if (IN32 == OUT32 && !ru[k].turn) {
+                    raw[k].copy(dst, e, ru[k]);
+                    continue;
+                }
+                float a[8], b[8];
+                raw[k].get(a, b);
+                if (ru[k].turn) turn(a, b, u[k]);
+                store8<OUT32>(dst, e + ru[k].ca, a);
+                if (ru[k].cb >= 0) store8<OUT32>(dst, e + ru[k].cb, b);
+            }
+        }
+    }
+};
+
+// How many warps share a row of `steps` steps: about 64 warps per SM, as many as it holds, where there are few rows.
+inline int rope_parts(long long rows, long long steps, int num_sms) {
+    const long long want = rows > 0 ? (64LL * num_sms + rows - 1) / rows : 1;
+    return (int)(want < 1 ? 1 : want > steps ? (steps < 1 ? 1 : steps) : want);
 }
 
 }  // namespace kvd

@@ -94,6 +94,28 @@ def test_rope_apply_strided_and_turned_back():
     assert (back[0] - keep[:, 2 * D:8 * D].view(N, H, D)).abs().max() < 2 * 4.0e-7 * 12
 
 
+def test_what_is_not_turned_is_copied_bit_by_bit():
+    """Every bf16 pattern, NaN payloads among them, in the columns past rotary_dim and in the value rows."""
+    import torch
+    import kv_cache_decode_gb300 as kvd
+    dev = cuda_or_skip()
+    bits = torch.arange(65536, dtype=torch.int32, device=dev).to(torch.int16)
+    rope = kvd.RopeTable(16, device=dev)
+    x = torch.zeros(586, 1, 128, dtype=torch.int16, device=dev)
+    x.view(586, 128)[:, 16:] = torch.nn.functional.pad(bits, (0, 586 * 112 - 65536)).view(586, 112)
+    out = torch.zeros_like(x)
+    pos = torch.arange(586, dtype=torch.int32, device=dev)
+    kvd.rope_apply(rope, x.view(torch.bfloat16), pos, out.view(torch.bfloat16))
+    v = bits.view(512, 1, 128)
+    kc = torch.zeros(1, 512, 1, 128, dtype=torch.int16, device=dev)
+    vc = torch.zeros_like(kc)
+    kvd.kv_append_rope(rope, kc.view(torch.bfloat16), vc.view(torch.bfloat16), torch.zeros_like(v).view(torch.bfloat16),
+                       v.view(torch.bfloat16), torch.zeros(1, dtype=torch.int32, device=dev),
+                       row_offsets=torch.tensor([0, 512], dtype=torch.int32, device=dev))
+    torch.cuda.synchronize()
+    assert torch.equal(out[..., 16:], x[..., 16:]) and torch.equal(vc[0], v)
+
+
 def test_rope_apply_refuses_views():
     import torch
     import kv_cache_decode_gb300 as kvd
