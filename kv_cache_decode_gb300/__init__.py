@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 import threading
 from typing import Optional, Tuple
 
@@ -155,18 +156,19 @@ def _declare(lib):
                                   P, P]
     lib.kvd_decode_ex.restype = I
     # rotary positions, rotating appends, fp4 cache
-    LL, DBL, PROPE = ctypes.c_longlong, ctypes.c_double, ctypes.POINTER(_CRope)
+    # (structs are passed as references, or as bytes packed in their layout)
+    LL, DBL, PROPE = ctypes.c_longlong, ctypes.c_double, P
     lib.kvd_rope_table.argtypes = [I, DBL, I, DBL, DBL, DBL, DBL, DBL, P, ctypes.POINTER(F)]
     lib.kvd_rope_apply.argtypes = [PROPE, P, LL, I, P, LL, I, P, LL, I, I, P]
     app = [PROPE, P, LL, P, LL, P, LL, P, LL, P, P, I, LL, I, I, I, P, P]
-    lib.kvd_kv_append_rope.argtypes = [ctypes.POINTER(_CCache)] + app
-    lib.kvd_kv_append_fp4.argtypes = [ctypes.POINTER(_CCacheFp4)] + app
+    lib.kvd_kv_append_rope.argtypes = [P] + app
+    lib.kvd_kv_append_fp4.argtypes = [P] + app
     lib.kvd_fp4_block_bytes.argtypes = [I]
     lib.kvd_fp4_block_bytes.restype = SZ
     lib.kvd_kv_quantize_fp4.argtypes = [P, P, P, I, I, I, I, I, I, P]
     lib.kvd_kv_read_fp4.argtypes = [P, P, I, I, I, I, P, I, P, I, I, I, I, P, P]
     lib.kvd_decode_plan_fp4.argtypes = [I, I, I, I, I, I, I, I, PI, PSZ]
-    lib.kvd_decode_fp4.argtypes = [ctypes.POINTER(_CCacheFp4)] + lib.kvd_decode_ex.argtypes[1:]
+    lib.kvd_decode_fp4.argtypes = [P] + lib.kvd_decode_ex.argtypes[1:]
     for name in ("kvd_rope_table", "kvd_rope_apply", "kvd_kv_append_rope", "kvd_kv_append_fp4",
                  "kvd_kv_quantize_fp4", "kvd_kv_read_fp4", "kvd_decode_plan_fp4", "kvd_decode_fp4"):
         getattr(lib, name).restype = I
@@ -944,35 +946,55 @@ class RopeTable:
         self._ref = ctypes.byref(self._struct)
 
 
-# The calls below are made once a layer and step, so their checks are written to
-# cost a few microseconds: metadata is read once per tensor, and the device is
-# only switched to when it is not the current one.
+# The calls below are made once a layer and step, so what they check is written to cost a few microseconds: a
+# chain of comparisons that a right call passes, and, when it does not, _explain, which names the tensor that is
+# wrong. The device is only switched to when it is not the current one.
 
-def _device_of(what, *named):
-    """The CUDA device all the given tensors lie on: (tensor, name, dtypes or None, dims or None), tensor None passed over."""
+_torch = None
+_raw_stream = _current_device = None
+_pack_cache = struct.Struct("PPPPPiiiii").pack   # struct kvd_cache
+_pack_fp4 = struct.Struct("PPPiiii").pack        # struct kvd_cache_fp4
+
+
+def _import_torch():
+    global _torch, _raw_stream, _current_device
     import torch
-    Tensor = torch.Tensor
+    _raw_stream, _current_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+    _torch = torch
+    return torch
+
+
+def _explain(what, *named):
+    """Raises for the first tensor that is not as asked: (tensor, name, dtypes, dims or None); None passed over."""
+    import torch
     dev = None
     for t, name, dtypes, ndim in named:
         if t is None:
             continue
-        if not isinstance(t, Tensor):
+        if not isinstance(t, torch.Tensor):
             raise TypeError(f"{what}: {name} must be a torch.Tensor")
         i = t.get_device()
-        if i != dev:
-            if i < 0:
-                raise ValueError(f"{what}: {name} must be on a CUDA device")
-            if dev is not None:
-                raise ValueError(f"{what}: {name} is on cuda:{i}, other tensors on cuda:{dev}")
-            dev = i
+        if i < 0:
+            raise ValueError(f"{what}: {name} must be on a CUDA device")
+        if dev is not None and i != dev:
+            raise ValueError(f"{what}: {name} is on cuda:{i}, other tensors on cuda:{dev}")
+        dev = i
         if dtypes is not None and t.dtype not in dtypes:
             raise TypeError(f"{what}: {name} must be {dtypes}, got {t.dtype}")
-        if ndim is not None:
-            if t.dim() != ndim:
-                raise ValueError(f"{what}: {name} must have {ndim} dims, got {t.dim()}")
-            if not t.is_contiguous():
-                raise ValueError(f"{what}: {name} must be contiguous")
-    return dev
+        if ndim is not None and t.dim() != ndim:
+            raise ValueError(f"{what}: {name} must have {ndim} dims, got {t.dim()}")
+        if ndim is not None and not t.is_contiguous():
+            raise ValueError(f"{what}: {name} must be contiguous")
+
+
+def _is(t, dtype, dev):
+    """A tensor of this type on this device (negative: the CPU, never)."""
+    return t.dtype is dtype and t.get_device() == dev >= 0
+
+
+def _whole(t, dtype, dev, ndim):
+    """The same, contiguous, of so many dimensions."""
+    return t.dtype is dtype and t.get_device() == dev >= 0 and t.dim() == ndim and t.is_contiguous()
 
 
 def _rope_on(rope, dev, what):
@@ -985,22 +1007,20 @@ def _rope_on(rope, dev, what):
 
 def _launch(fn, what, dev, stream, *args):
     """Calls fn(*args, stream handle) with device `dev` current; without a stream, on that device's current one."""
-    from torch import _C
     if stream is None:
-        h = _C._cuda_getCurrentRawStream(dev)
+        h = _raw_stream(dev)
     elif hasattr(stream, "cuda_stream"):
         if stream.device_index != dev:
             raise ValueError(f"{what}: a stream of cuda:{stream.device_index}, tensors on cuda:{dev}")
         h = stream.cuda_stream
     else:
         h = int(stream)
-    if _C._cuda_getDevice() == dev:
+    if _current_device() == dev:
         rc = fn(*args, h)
     else:
-        import torch
-        with torch.cuda.device(dev):
+        with _torch.cuda.device(dev):
             rc = fn(*args, h)
-    if rc != OK:
+    if rc:
         raise KvdError(rc, what)
 
 
@@ -1010,17 +1030,20 @@ def _rows(t, name, what):
     s, st = t.shape, t.stride()
     if len(s) == 3:
         N, H, D = s
-        step, even = st[0], True
+        step, inner, last = st
+        even = True
     elif len(s) == 4:
         B, T, H, D = s
         N = B * T
-        step = st[1] if T > 1 else st[0]
-        even = B <= 1 or T <= 1 or st[0] == T * step
+        outer, step, inner, last = st
+        if T <= 1:
+            step = outer
+        even = B <= 1 or T <= 1 or outer == T * step
     else:
         raise ValueError(f"{what}: {name} must be [N, H, D] or [B, T, H, D]")
     if N == 0 or H == 0 or D == 0:
         return N, H, D, H * D
-    if (st[-1] != 1 and D > 1) or (st[-2] != D and H > 1):
+    if (last != 1 and D > 1) or (inner != D and H > 1):
         raise ValueError(f"{what}: {name}'s heads must be contiguous")
     if not even:
         raise ValueError(f"{what}: {name}'s rows must be evenly spaced")
@@ -1031,33 +1054,51 @@ def rope_apply(rope: RopeTable, x, positions, out, stream=None):
     """out = x's rows turned by their positions: x, out [N, H, D] or [B, T, H, D],
     bf16 or fp32 each, rows evenly spaced (slices of a fused projection may be
     passed as they are); positions int32, one a row. out may be x."""
-    import torch
+    torch = _torch or _import_torch()
     what, bf, f32 = "rope_apply", torch.bfloat16, torch.float32
-    dev = _device_of(what, (x, "x", (bf, f32), None), (out, "out", (bf, f32), None),
-                     (positions, "positions", (torch.int32,), None))
+    try:
+        dev = x.get_device()
+        xc, oc = x.dtype is f32, out.dtype is f32
+        ok = (_is(x, f32 if xc else bf, dev) and _is(out, f32 if oc else bf, dev) and _is(positions, torch.int32, dev)
+              and positions.is_contiguous())
+    except AttributeError:
+        ok = False
+    if not ok:
+        _explain(what, (x, "x", (bf, f32), None), (out, "out", (bf, f32), None), (positions, "positions", (torch.int32,), None))
+        raise ValueError(f"{what}: positions must be contiguous")
     N, H, D, xs = _rows(x, "x", what)
     No, Ho, Do, ys = _rows(out, "out", what)
     if No != N or Ho != H or Do != D or positions.numel() != N:
         raise ValueError(f"{what}: inconsistent shapes")
-    if not positions.is_contiguous():
-        raise ValueError(f"{what}: positions must be contiguous")
     ref = _rope_on(rope, dev, what)
     if N == 0:
         return
     _launch((_lib or load()).kvd_rope_apply, "kvd_rope_apply", dev, stream, ref, x.data_ptr(), xs,
-            OUT_F32 if x.dtype is f32 else OUT_BF16, out.data_ptr(), ys, OUT_F32 if out.dtype is f32 else OUT_BF16,
-            positions.data_ptr(), N, H, D)
+            OUT_F32 if xc else OUT_BF16, out.data_ptr(), ys, OUT_F32 if oc else OUT_BF16, positions.data_ptr(), N, H, D)
 
 
-def _append_rows(what, rope, q, q_out, k_new, v_new, pos, row_offsets, dev):
+def _append_rows(what, rope, q, q_out, k_new, v_new, pos, row_offsets, dev, torch):
     """(batch, rows, KV heads, head_dim, the arguments of kvd_kv_append_rope between the cache and the status word)."""
+    bf, i32 = torch.bfloat16, torch.int32
+    if (q is None) != (q_out is None):
+        raise ValueError(f"{what}: q and q_out go together")
+    try:
+        ok = (_is(k_new, bf, dev) and _is(v_new, bf, dev) and _whole(pos, i32, dev, 1)
+              and (q is None or (_is(q, bf, dev) and _is(q_out, bf, dev)))
+              and (row_offsets is None or _whole(row_offsets, i32, dev, 1)))
+    except AttributeError:
+        ok = False
+    if not ok:
+        _explain(what, (k_new, "k_new", (bf,), None), (v_new, "v_new", (bf,), None), (pos, "pos", (i32,), 1), (q, "q", (bf,), None),
+                 (q_out, "q_out", (bf,), None), (row_offsets, "row_offsets", (i32,), 1))
+        raise ValueError(f"{what}: the new rows are on cuda:{pos.get_device()}, the cache on cuda:{dev}")
     N, Hkv, D, ks = _rows(k_new, "k_new", what)
     Nv, Hv, Dv, vs = _rows(v_new, "v_new", what)
-    B = pos.shape[0]
+    B = pos.numel()
     if Nv != N or Hv != Hkv or Dv != D:
         raise ValueError(f"{what}: inconsistent shapes")
     if row_offsets is not None:
-        if row_offsets.shape[0] != B + 1:
+        if row_offsets.numel() != B + 1:
             raise ValueError(f"{what}: row_offsets must be [batch + 1]")
         off = row_offsets.data_ptr()
     else:
@@ -1066,13 +1107,9 @@ def _append_rows(what, rope, q, q_out, k_new, v_new, pos, row_offsets, dev):
         off = None
     ref = None if rope is None else _rope_on(rope, dev, what)
     if q is None:
-        if q_out is not None:
-            raise ValueError(f"{what}: q and q_out go together")
         qp = op = None
         Hq = qs = os_ = 0
     else:
-        if q_out is None:
-            raise ValueError(f"{what}: q and q_out go together")
         if rope is None:
             raise ValueError(f"{what}: q needs a rope")
         Nq, Hq, Dq, qs = _rows(q, "q", what)
@@ -1084,6 +1121,14 @@ def _append_rows(what, rope, q, q_out, k_new, v_new, pos, row_offsets, dev):
                           Hkv, D)
 
 
+def _status_ptr(status, dev, what, torch):
+    if status is None:
+        return None
+    if not isinstance(status, torch.Tensor) or not _is(status, torch.int32, dev):
+        raise TypeError(f"{what}: status must be an int32 tensor on cuda:{dev}")
+    return status.data_ptr()
+
+
 def kv_append_rope(rope: RopeTable, k, v, k_new, v_new, pos, *, q=None, q_out=None, k_scales=None, v_scales=None,
                    block_table=None, row_offsets=None, status=None, stream=None):
     """New rows into a cache as decode_ex takes it (k, v contiguous [B, S_max, Hkv,
@@ -1092,39 +1137,47 @@ def kv_append_rope(rope: RopeTable, k, v, k_new, v_new, pos, *, q=None, q_out=No
     k_new, v_new, q: [B, Hkv, D] or [B, T, H, D] at pos[b] + i, or with row_offsets
     int32 [B + 1] the packed rows [N, H, D] of prompts of any lengths; rows evenly
     spaced, so slices of a fused projection may be passed as they are."""
-    import torch
-    what, bf, i32, f32 = "kv_append_rope", (torch.bfloat16,), (torch.int32,), (torch.float32,)
+    torch = _torch or _import_torch()
+    what, bf, i32, f32 = "kv_append_rope", torch.bfloat16, torch.int32, torch.float32
     if rope is None:
         raise TypeError(f"{what}: rope must be a RopeTable")
     if (k_scales is None) != (v_scales is None):
         raise ValueError(f"{what}: k_scales and v_scales go together")
     quant = k_scales is not None
-    dts = (torch.int8, torch.uint8, torch.float8_e4m3fn) if quant else bf
-    dev = _device_of(what, (k, "k", dts, 4), (v, "v", dts, 4), (k_new, "k_new", bf, None), (v_new, "v_new", bf, None),
-                     (pos, "pos", i32, 1), (q, "q", bf, None), (q_out, "q_out", bf, None),
-                     (block_table, "block_table", i32, 2), (row_offsets, "row_offsets", i32, 1),
-                     (k_scales, "k_scales", f32, 3), (v_scales, "v_scales", f32, 3), (status, "status", i32, None))
-    B, N, Hkv, D, args = _append_rows(what, rope, q, q_out, k_new, v_new, pos, row_offsets, dev)
-    shape = k.shape
-    if v.shape != shape or shape[2] != Hkv or shape[3] != D:
+    dts = (torch.int8, torch.uint8, torch.float8_e4m3fn) if quant else (bf,)
+    try:
+        dev, dt = k.get_device(), k.dtype
+        ok = (dt in dts and _whole(k, dt, dev, 4) and _whole(v, dt, dev, 4)
+              and (block_table is None or _whole(block_table, i32, dev, 2))
+              and (not quant or (_whole(k_scales, f32, dev, 3) and _whole(v_scales, f32, dev, 3))))
+    except AttributeError:
+        ok = False
+    if not ok:
+        _explain(what, (k, "k", dts, 4), (v, "v", dts, 4), (block_table, "block_table", (i32,), 2),
+                 (k_scales, "k_scales", (f32,), 3), (v_scales, "v_scales", (f32,), 3))
+        raise TypeError(f"{what}: k is {k.dtype}, v {v.dtype}")
+    B, N, Hkv, D, args = _append_rows(what, rope, q, q_out, k_new, v_new, pos, row_offsets, dev, torch)
+    n, cap, heads, width = shape = k.shape
+    if v.shape != shape or heads != Hkv or width != D:
         raise ValueError(f"{what}: inconsistent shapes")
-    c = _CCache(k.data_ptr(), v.data_ptr())
+    ksp = vsp = fp8 = 0
     if quant:
-        if v.dtype != k.dtype or k_scales.shape != shape[:3] or v_scales.shape != shape[:3]:
+        if k_scales.shape != shape[:3] or v_scales.shape != shape[:3]:
             raise ValueError(f"{what}: codes [B, S_max, Hkv, D] and scales [B, S_max, Hkv] disagree")
-        c.k_scales, c.v_scales, c.fp8 = k_scales.data_ptr(), v_scales.data_ptr(), 1 if _is_fp8(k) else 0
+        ksp, vsp, fp8 = k_scales.data_ptr(), v_scales.data_ptr(), 0 if dt is torch.int8 else 1
     if block_table is not None:
-        if block_table.shape[0] != B:
+        rows, blocks = block_table.shape
+        if rows != B:
             raise ValueError(f"{what}: inconsistent shapes")
-        c.block_table, c.max_blocks = block_table.data_ptr(), block_table.shape[1]
-        c.page_size, c.num_pages = shape[1], shape[0]
+        c = _pack_cache(k.data_ptr(), v.data_ptr(), ksp, vsp, block_table.data_ptr(), 0, blocks, cap, n, fp8)
     else:
-        if shape[0] != B:
+        if n != B:
             raise ValueError(f"{what}: inconsistent shapes")
-        c.s_max = shape[1]
+        c = _pack_cache(k.data_ptr(), v.data_ptr(), ksp, vsp, 0, cap, 0, 0, 0, fp8)
     if N == 0:
         return
-    _launch((_lib or load()).kvd_kv_append_rope, "kvd_kv_append_rope", dev, stream, ctypes.byref(c), *args, _ptr(status))
+    _launch((_lib or load()).kvd_kv_append_rope, "kvd_kv_append_rope", dev, stream, c, *args,
+            _status_ptr(status, dev, what, torch))
 
 
 def fp4_block_bytes(head_dim: int) -> int:
@@ -1145,23 +1198,34 @@ def alloc_cache_fp4(batch_or_pages: int, n_heads_kv: int, head_dim: int, tokens:
                        device=device)
 
 
-def _fp4_cache(what, k, v, D, B, block_table):
-    """(struct kvd_cache_fp4, KV heads) of the blocks k and v (v may be None)."""
-    shape = k.shape
-    if shape[3] != 9 * D + 16 or D not in (64, 128, 256):
-        raise ValueError(f"{what}: blocks of {shape[3]} bytes at head_dim {D}")
-    if v is not None and v.shape != shape:
-        raise ValueError(f"{what}: inconsistent shapes")
-    vp = None if v is None else v.data_ptr()
+def _fp4_cache(what, k, v, D, B, block_table, torch):
+    """(the packed struct kvd_cache_fp4, KV heads, capacity of a sequence, device) of the blocks k and v (v may be None)."""
+    u8, i32 = torch.uint8, torch.int32
+    try:
+        dev = k.get_device()
+        ok = (_whole(k, u8, dev, 4) and (v is None or _whole(v, u8, dev, 4))
+              and (block_table is None or _whole(block_table, i32, dev, 2)))
+    except AttributeError:
+        ok = False
+    if not ok:
+        _explain(what, (k, "k" if v is not None else "blocks", (u8,), 4), (v, "v", (u8,), 4), (block_table, "block_table", (i32,), 2))
+        raise ValueError(f"{what}: the fp4 cache must be on a CUDA device")
+    n, heads, blks, width = shape = k.shape
+    if width != 9 * D + 16 or D not in (64, 128, 256):
+        raise ValueError(f"{what}: blocks of {width} bytes at head_dim {D}")
+    vp = 0
+    if v is not None:
+        if v.shape != shape:
+            raise ValueError(f"{what}: inconsistent shapes")
+        vp = v.data_ptr()
     if block_table is not None:
-        if block_table.shape[0] != B:
+        rows, per = block_table.shape
+        if rows != B:
             raise ValueError(f"{what}: inconsistent shapes")
-        c = _CCacheFp4(k.data_ptr(), vp, block_table.data_ptr(), 0, block_table.shape[1], 16 * shape[2], shape[0])
-    else:
-        if shape[0] != B:
-            raise ValueError(f"{what}: inconsistent shapes")
-        c = _CCacheFp4(k.data_ptr(), vp, None, 16 * shape[2])
-    return c, shape[1]
+        return _pack_fp4(k.data_ptr(), vp, block_table.data_ptr(), 0, per, 16 * blks, n), heads, 16 * blks * per, dev
+    if n != B:
+        raise ValueError(f"{what}: inconsistent shapes")
+    return _pack_fp4(k.data_ptr(), vp, 0, 16 * blks, 0, 0, 0), heads, 16 * blks, dev
 
 
 def kv_append_fp4(k, v, k_new, v_new, pos, *, rope: Optional[RopeTable] = None, q=None, q_out=None, block_table=None,
@@ -1169,53 +1233,73 @@ def kv_append_fp4(k, v, k_new, v_new, pos, *, rope: Optional[RopeTable] = None, 
     """kv_append_rope for an fp4 cache (k, v uint8 [B, Hkv, S_max / 16, 9 D + 16], or
     pools [pages, Hkv, page / 16, 9 D + 16] with block_table); rope None appends
     the rows as they are (kvd_kv_append_fp4)."""
-    import torch
-    what, bf, u8, i32 = "kv_append_fp4", (torch.bfloat16,), (torch.uint8,), (torch.int32,)
-    dev = _device_of(what, (k, "k", u8, 4), (v, "v", u8, 4), (k_new, "k_new", bf, None), (v_new, "v_new", bf, None),
-                     (pos, "pos", i32, 1), (q, "q", bf, None), (q_out, "q_out", bf, None),
-                     (block_table, "block_table", i32, 2), (row_offsets, "row_offsets", i32, 1),
-                     (status, "status", i32, None))
-    B, N, Hkv, D, args = _append_rows(what, rope, q, q_out, k_new, v_new, pos, row_offsets, dev)
-    c, heads = _fp4_cache(what, k, v, D, B, block_table)
+    torch = _torch or _import_torch()
+    what = "kv_append_fp4"
+    if v is None:
+        raise TypeError(f"{what}: v must be a torch.Tensor")
+    B, N, Hkv, D, args = _append_rows(what, rope, q, q_out, k_new, v_new, pos, row_offsets, k.get_device(), torch)
+    c, heads, _, dev = _fp4_cache(what, k, v, D, B, block_table, torch)
     if heads != Hkv:
         raise ValueError(f"{what}: inconsistent shapes")
     if N == 0:
         return
-    _launch((_lib or load()).kvd_kv_append_fp4, "kvd_kv_append_fp4", dev, stream, ctypes.byref(c), *args, _ptr(status))
+    _launch((_lib or load()).kvd_kv_append_fp4, "kvd_kv_append_fp4", dev, stream, c, *args,
+            _status_ptr(status, dev, what, torch))
+
+
+def _bf16_rows_and_lens(what, cache, name, seq_lens, torch):
+    """(B, S, Hkv, D, device) of a contiguous bf16 cache [B, S, Hkv, D] and its lengths."""
+    bf, i32 = torch.bfloat16, torch.int32
+    try:
+        dev = cache.get_device()
+        ok = _whole(cache, bf, dev, 4) and _whole(seq_lens, i32, dev, 1)
+    except AttributeError:
+        ok = False
+    if not ok:
+        _explain(what, (cache, name, (bf,), 4), (seq_lens, "seq_lens", (i32,), 1))
+        raise ValueError(f"{what}: {name} must be on a CUDA device")
+    B, S, Hkv, D = cache.shape
+    if seq_lens.numel() != B:
+        raise ValueError(f"{what}: inconsistent shapes")
+    return B, S, Hkv, D, dev
 
 
 def kv_quantize_fp4(cache, blocks, seq_lens, max_seq_len: int, stream=None):
     """Rows t < seq_lens[b] of a bf16 cache [B, S_max, Hkv, D] (K or V) into the blocks
     of a contiguous fp4 cache (kvd_kv_quantize_fp4)."""
-    import torch
+    torch = _torch or _import_torch()
     what = "kv_quantize_fp4"
-    dev = _device_of(what, (cache, "cache", (torch.bfloat16,), 4), (blocks, "blocks", (torch.uint8,), 4),
-                     (seq_lens, "seq_lens", (torch.int32,), 1))
-    B, S, Hkv, D = cache.shape
-    c, heads = _fp4_cache(what, blocks, None, D, B, None)
-    if heads != Hkv or seq_lens.shape[0] != B:
+    B, S, Hkv, D, dev = _bf16_rows_and_lens(what, cache, "cache", seq_lens, torch)
+    _, heads, cap, on = _fp4_cache(what, blocks, None, D, B, None, torch)
+    if heads != Hkv:
         raise ValueError(f"{what}: inconsistent shapes")
+    if on != dev:
+        raise ValueError(f"{what}: cache on cuda:{dev}, blocks on cuda:{on}")
     if B == 0:
         return
-    _launch((_lib or load()).kvd_kv_quantize_fp4, "kvd_kv_quantize_fp4", dev, stream, cache.data_ptr(), c.k,
-            seq_lens.data_ptr(), B, S, c.s_max, int(max_seq_len), Hkv, D)
+    _launch((_lib or load()).kvd_kv_quantize_fp4, "kvd_kv_quantize_fp4", dev, stream, cache.data_ptr(), blocks.data_ptr(),
+            seq_lens.data_ptr(), B, S, cap, int(max_seq_len), Hkv, D)
 
 
 def kv_read_fp4(blocks, out, seq_lens, max_seq_len: int, block_table=None, status=None, stream=None):
     """Rows t < seq_lens[b] of an fp4 cache's K or V blocks (contiguous, or a pool
     with block_table) back to bf16 out [B, S, Hkv, D], exactly (kvd_kv_read_fp4)."""
-    import torch
-    what, i32 = "kv_read_fp4", (torch.int32,)
-    dev = _device_of(what, (out, "out", (torch.bfloat16,), 4), (blocks, "blocks", (torch.uint8,), 4),
-                     (seq_lens, "seq_lens", i32, 1), (block_table, "block_table", i32, 2), (status, "status", i32, None))
-    B, S, Hkv, D = out.shape
-    c, heads = _fp4_cache(what, blocks, None, D, B, block_table)
-    if heads != Hkv or seq_lens.shape[0] != B:
+    torch = _torch or _import_torch()
+    what = "kv_read_fp4"
+    B, S, Hkv, D, dev = _bf16_rows_and_lens(what, out, "out", seq_lens, torch)
+    _, heads, cap, on = _fp4_cache(what, blocks, None, D, B, block_table, torch)
+    if heads != Hkv:
         raise ValueError(f"{what}: inconsistent shapes")
+    if on != dev:
+        raise ValueError(f"{what}: out on cuda:{dev}, blocks on cuda:{on}")
     if B == 0:
         return
-    _launch((_lib or load()).kvd_kv_read_fp4, "kvd_kv_read_fp4", dev, stream, c.k, c.block_table, c.s_max, c.max_blocks,
-            c.page_size, c.num_pages, out.data_ptr(), S, seq_lens.data_ptr(), B, int(max_seq_len), Hkv, D, _ptr(status))
+    if block_table is None:
+        table = (None, cap, 0, 0, 0)
+    else:
+        table = (block_table.data_ptr(), 0, block_table.shape[1], 16 * blocks.shape[2], blocks.shape[0])
+    _launch((_lib or load()).kvd_kv_read_fp4, "kvd_kv_read_fp4", dev, stream, blocks.data_ptr(), *table, out.data_ptr(), S,
+            seq_lens.data_ptr(), B, int(max_seq_len), Hkv, D, _status_ptr(status, dev, what, torch))
 
 
 def decode_plan_fp4(batch: int, n_tokens: int, n_heads_q: int, n_heads_kv: int, head_dim: int, max_seq_len: int,
@@ -1234,12 +1318,21 @@ def decode_fp4(q, k, v, seq_lens, max_seq_len: int, scale: float, out, *, block_
     k, v uint8 [B, Hkv, S_max / 16, 9 D + 16], or pools [pages, Hkv, page / 16, 9 D + 16] with
     block_table [B, max_blocks]; k_new, v_new ([B, Hkv, D] or [B, T, Hkv, D]) and
     pos to append first. Workspace: decode_plan_fp4."""
-    import torch
-    what, bf, u8, i32, f32 = "decode_fp4", (torch.bfloat16,), (torch.uint8,), (torch.int32,), torch.float32
-    dev = _device_of(what, (q, "q", bf, None), (k, "k", u8, 4), (v, "v", u8, 4), (seq_lens, "seq_lens", i32, 1),
-                     (out, "out", (torch.bfloat16, f32), None), (block_table, "block_table", i32, 2),
-                     (workspace, "workspace", None, None), (lse, "lse", (f32,), None), (status, "status", i32, None),
-                     (k_new, "k_new", bf, None), (v_new, "v_new", bf, None), (pos, "pos", i32, 1))
+    torch = _torch or _import_torch()
+    what, bf, i32, f32 = "decode_fp4", torch.bfloat16, torch.int32, torch.float32
+    try:
+        dev = q.get_device()
+        f32_out = out.dtype is f32
+        ok = (_is(q, bf, dev) and _is(out, f32 if f32_out else bf, dev) and _whole(seq_lens, i32, dev, 1)
+              and q.is_contiguous() and out.is_contiguous()
+              and (lse is None or (_is(lse, f32, dev) and lse.is_contiguous()))
+              and (workspace is None or (workspace.get_device() == dev and workspace.is_contiguous())))
+    except AttributeError:
+        ok = False
+    if not ok:
+        _explain(what, (q, "q", (bf,), None), (out, "out", (bf, f32), None), (seq_lens, "seq_lens", (i32,), 1),
+                 (lse, "lse", (f32,), None), (workspace, "workspace", None, None))
+        raise ValueError(f"{what}: q, out, lse and workspace must be contiguous")
     shape = q.shape
     if len(shape) == 3:
         (B, Hq, D), T = shape, 1
@@ -1247,28 +1340,29 @@ def decode_fp4(q, k, v, seq_lens, max_seq_len: int, scale: float, out, *, block_
         B, T, Hq, D = shape
     else:
         raise ValueError(f"{what}: q must be [B, Hq, D] or [B, T, Hq, D]")
-    if out.shape != shape or seq_lens.shape[0] != B or not (q.is_contiguous() and out.is_contiguous()):
-        raise ValueError(f"{what}: q, out and seq_lens disagree, or q or out is not contiguous")
-    c, Hkv = _fp4_cache(what, k, v, D, B, block_table)
-    if lse is not None and (lse.shape != shape[:-1] or not lse.is_contiguous()):
-        raise ValueError(f"{what}: lse must be contiguous, shaped like q without its last dimension")
+    if out.shape != shape or seq_lens.numel() != B or (lse is not None and lse.shape != shape[:-1]):
+        raise ValueError(f"{what}: inconsistent shapes")
+    if v is None:
+        raise TypeError(f"{what}: v must be a torch.Tensor")
+    c, Hkv, _, on = _fp4_cache(what, k, v, D, B, block_table, torch)
+    if on != dev:
+        raise ValueError(f"{what}: q on cuda:{dev}, the cache on cuda:{on}")
     kp = vp = pp = None
     if k_new is not None or v_new is not None or pos is not None:
         if k_new is None or v_new is None or pos is None:
             raise ValueError(f"{what}: k_new, v_new and pos go together")
-        for t in (k_new, v_new):
-            if t.shape != shape[:-2] + (Hkv, D) or not t.is_contiguous():
-                raise ValueError(f"{what}: k_new and v_new must be contiguous, with a head for each KV head and token")
-        if pos.shape[0] != B:
+        n = len(shape)
+        if not (_whole(k_new, bf, dev, n) and _whole(v_new, bf, dev, n) and _whole(pos, i32, dev, 1)):
+            _explain(what, (q, "q", (bf,), None), (k_new, "k_new", (bf,), n), (v_new, "v_new", (bf,), n), (pos, "pos", (i32,), 1))
+        if k_new.shape != shape[:-2] + (Hkv, D) or v_new.shape != k_new.shape or pos.numel() != B:
             raise ValueError(f"{what}: inconsistent shapes")
         kp, vp, pp = k_new.data_ptr(), v_new.data_ptr(), pos.data_ptr()
     wp, wb = None, 0
     if workspace is not None:
-        if not workspace.is_contiguous():
-            raise ValueError(f"{what}: workspace must be contiguous")
         wp, wb = workspace.data_ptr(), workspace.numel() * workspace.element_size()
     if B == 0:
         return
-    _launch((_lib or load()).kvd_decode_fp4, "kvd_decode_fp4", dev, stream, ctypes.byref(c), q.data_ptr(),
-            seq_lens.data_ptr(), B, T, int(max_seq_len), Hq, Hkv, D, float(scale), int(n_split), wp, wb, out.data_ptr(),
-            OUT_F32 if out.dtype is f32 else OUT_BF16, _ptr(lse), kp, vp, pp, _ptr(status))
+    _launch((_lib or load()).kvd_decode_fp4, "kvd_decode_fp4", dev, stream, c, q.data_ptr(), seq_lens.data_ptr(), B, T,
+            int(max_seq_len), Hq, Hkv, D, float(scale), int(n_split), wp, wb, out.data_ptr(),
+            OUT_F32 if f32_out else OUT_BF16, None if lse is None else lse.data_ptr(), kp, vp, pp,
+            _status_ptr(status, dev, what, torch))
