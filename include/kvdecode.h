@@ -476,7 +476,8 @@ kvd_status kvd_rope_table(int rotary_dim, double base, kvd_rope_scaling scaling,
  *               and rows lie x_stride, y_stride elements apart (a slice of a fused
  *               projection, say): at least n_heads * head_dim, and a multiple
  *               of 8 for bf16, 4 for fp32. y may be x itself (same dtype and
- *               stride); any other overlap of the two is refused.
+ *               stride), or other columns of the same rows; any element in common
+ *               otherwise is refused.
  *   positions : device int32 [rows], any values
  * The angles' cosines and sines and the products are float32; the result is
  * rounded once. head_dim: a multiple of 8 up to 1024. rows = 0 is a no-op.
@@ -509,7 +510,8 @@ kvd_status kvd_rope_apply(const kvd_rope* rope, const void* x, long long x_strid
  *                  offset or from the last one on belong to no sequence and are left as they are, in q_out too.
  * A row at a position outside [0, s_max) or on a block that names no page is
  * not appended and sets KVD_STATUS_POS_OUT_OF_RANGE or KVD_STATUS_BAD_PAGE; its
- * query is turned all the same.
+ * query is turned all the same. Where two rows of a call name one place (by a page that two sequences share, say),
+ * what the place holds afterwards is not defined.
  * Errors: as the appends and kvd_rope_apply; KVD_ERR_INVALID_ARG also for n_rows
  * not a multiple of batch (row_offsets NULL), only one of q and q_out, n_rows
  * past 2^31 - 1 or written and read ranges that overlap; KVD_ERR_UNSUPPORTED for
@@ -564,7 +566,8 @@ size_t kvd_fp4_block_bytes(int head_dim);
  * the K or V blocks of an fp4 cache (contiguous, or paged with block_table) back
  * to bf16 [batch, s_out, n_heads_kv, head_dim], s_out >= max_seq_len, other rows left as
  * they are; a block that names no page reads as zero rows and sets
- * KVD_STATUS_BAD_PAGE. Errors as kvd_kv_quantize_q8; max_seq_len is at most each capacity.
+ * KVD_STATUS_BAD_PAGE. Errors as kvd_kv_quantize_q8; max_seq_len is at most each capacity, and at most
+ * 2^31 - 1024 in all the fp4 calls (KVD_ERR_UNSUPPORTED).
  */
 kvd_status kvd_kv_quantize_fp4(const void* cache, void* blocks, const int32_t* seq_lens, int batch, int s_max,
                                int s_max_blocks, int max_seq_len, int n_heads_kv, int head_dim, kvd_stream_t stream);

@@ -1237,6 +1237,8 @@ def kv_append_fp4(k, v, k_new, v_new, pos, *, rope: Optional[RopeTable] = None, 
     what = "kv_append_fp4"
     if v is None:
         raise TypeError(f"{what}: v must be a torch.Tensor")
+    if not isinstance(k, torch.Tensor):
+        raise TypeError(f"{what}: k must be a torch.Tensor")
     B, N, Hkv, D, args = _append_rows(what, rope, q, q_out, k_new, v_new, pos, row_offsets, k.get_device(), torch)
     c, heads, _, dev = _fp4_cache(what, k, v, D, B, block_table, torch)
     if heads != Hkv:

@@ -45,6 +45,26 @@ size_t span_bytes(long long rows, long long stride, long long width, size_t es) 
     return rows > 0 ? ((size_t)(rows - 1) * (size_t)stride + (size_t)width) * es : 0;
 }
 
+// Whether two sets of rows share an element. Rows of one buffer (one stride, a fused projection's slices) are apart
+// when their column windows are.
+struct Rows {
+    const void* p;
+    long long stride, width, n;
+    size_t es;
+    ByteRange range() const { return ByteRange{p, span_bytes(n, stride, width, es)}; }
+};
+bool rows_meet(const Rows& a, const Rows& b) {
+    if (!a.range().overlaps(b.range())) return false;
+    const long long S = a.stride * (long long)a.es;
+    if (S != b.stride * (long long)b.es) return true;
+    long long d = (long long)((intptr_t)b.p - (intptr_t)a.p) % S;
+    if (d < 0) d += S;  // b starts d bytes into a's row period
+    return d < a.width * (long long)a.es || d + b.width * (long long)b.es > S;
+}
+
+// Token numbers of the fp4 calls stay this far below 2^31, so that the tile after the last has one too.
+constexpr int kMaxTokens4 = 0x7ffffc00;
+
 kvd_status check_strided(const void* p, long long stride, long long width, size_t es) {
     if (!p || !aligned(p, 16) || stride < width || stride > (1LL << 40) || (stride * (long long)es) % 16 != 0)
         return KVD_ERR_INVALID_ARG;
@@ -78,34 +98,19 @@ kvd_status append_rope(AppendTarget to, size_t cache_bytes, size_t scale_bytes, 
         if ((st = check_strided(q_out, q_out_stride, qw, 2)) != KVD_OK) return st;
     }
     if (batch == 0 || n_rows == 0) return KVD_OK;
-    // What is written overlaps nothing that is read or written otherwise: the
-    // caches and their scales against the new rows and each other, q_out
-    // against everything but q itself. Rows of one fused projection interleave,
-    // so q's and k's ranges may cross: only exact row windows are compared
-    // where both are inputs (never), and q_out in place passes over k and v
-    // when they are slices of the same rows.
-    const ByteRange rk{k_new, span_bytes(n_rows, k_stride, kw, 2)}, rv{v_new, span_bytes(n_rows, v_stride, kw, 2)},
-        rq{q, span_bytes(n_rows, q_stride, qw, 2)}, ro{q_out, span_bytes(n_rows, q_out_stride, qw, 2)},
-        ck{to.k, cache_bytes}, cv{to.v, cache_bytes}, sk{to.k_scale, scale_bytes}, sv{to.v_scale, scale_bytes};
+    // What is written overlaps nothing that is read, or written otherwise: q_out against the new rows (it may be q
+    // itself), the caches and their scales against all of those and each other.
+    const Rows rk{k_new, k_stride, kw, n_rows, 2}, rv{v_new, v_stride, kw, n_rows, 2}, rq{q, q_stride, qw, n_rows, 2},
+        ro{q_out, q_out_stride, qw, n_rows, 2};
+    const ByteRange ck{to.k, cache_bytes}, cv{to.v, cache_bytes}, sk{to.k_scale, scale_bytes}, sv{to.v_scale, scale_bytes};
     const bool in_place = q && q == q_out;
     if (in_place && q_stride != q_out_stride) return KVD_ERR_INVALID_ARG;
-    // Column windows of two row sets with one stride: apart if they never meet within a row.
-    auto rows_meet = [](const ByteRange& a, const void* ap, long long as, long long aw, const ByteRange& b, const void* bp,
-                        long long bs, long long bw) {
-        if (!a.overlaps(b)) return false;
-        if (as != bs) return true;
-        const long long S = as * 2;
-        long long d = (long long)((intptr_t)bp - (intptr_t)ap) % S;
-        if (d < 0) d += S;  // b starts d bytes into a's row period
-        return d < aw * 2 || d + bw * 2 > S;
-    };
-    if (q) {
-        if (!in_place && rows_meet(ro, q_out, q_out_stride, qw, rq, q, q_stride, qw)) return KVD_ERR_INVALID_ARG;
-        if (rows_meet(ro, q_out, q_out_stride, qw, rk, k_new, k_stride, kw) ||
-            rows_meet(ro, q_out, q_out_stride, qw, rv, v_new, v_stride, kw))
-            return KVD_ERR_INVALID_ARG;
-    }
-    const ByteRange written[4] = {ck, cv, sk, sv}, other[4] = {rk, rv, rq, ro};
+    const ByteRange rp{pos, (size_t)batch * 4}, rf{row_offsets, row_offsets ? ((size_t)batch + 1) * 4 : 0};
+    if (q && ((!in_place && rows_meet(ro, rq)) || rows_meet(ro, rk) || rows_meet(ro, rv) || ro.range().overlaps(rp) ||
+              ro.range().overlaps(rf)))
+        return KVD_ERR_INVALID_ARG;
+    const ByteRange none{nullptr, 0}, written[4] = {ck, cv, sk, sv},
+                    other[6] = {rk.range(), rv.range(), q ? rq.range() : none, q ? ro.range() : none, rp, rf};
     for (int i = 0; i < 4; ++i) {
         for (int j = 0; j < i; ++j)
             if (written[i].overlaps(written[j])) return KVD_ERR_INVALID_ARG;
@@ -144,7 +149,7 @@ kvd_status plan_fp4(int batch, int T, int Hq, int Hkv, int D, int max_len, int n
     kvd_status st = check_shape(batch, Hq, Hkv, D, KVD_OUT_BF16);
     if (st != KVD_OK) return st;
     if (T < 1 || max_len < 0 || request < 0 || num_sms < 0) return KVD_ERR_INVALID_ARG;
-    if (T > KVD_MAX_TOKENS) return KVD_ERR_UNSUPPORTED;
+    if (T > KVD_MAX_TOKENS || max_len > kMaxTokens4) return KVD_ERR_UNSUPPORTED;
     const int rows = T * (Hq / Hkv);
     const ChunkKernel* k = fp4_chunk_kernel(D, false, rows);
     if (!k) return KVD_ERR_UNSUPPORTED;
@@ -219,10 +224,10 @@ kvd_status kvd_rope_apply(const kvd_rope* rope, const void* x, long long x_strid
     if (!positions || !aligned(positions, 4)) return KVD_ERR_INVALID_ARG;
     if ((st = check_strided(x, x_stride, width, ies)) != KVD_OK) return st;
     if ((st = check_strided(y, y_stride, width, oes)) != KVD_OK) return st;
-    const ByteRange rx{x, span_bytes(rows, x_stride, width, ies)}, ry{y, span_bytes(rows, y_stride, width, oes)},
-        rp{positions, (size_t)rows * 4};
+    const Rows rx{x, x_stride, width, rows, ies}, ry{y, y_stride, width, rows, oes};
     const bool in_place = x == y && x_stride == y_stride && in_dtype == out_dtype;
-    if ((!in_place && ry.overlaps(rx)) || ry.overlaps(rp)) return KVD_ERR_INVALID_ARG;
+    if ((!in_place && rows_meet(rx, ry)) || ry.range().overlaps(ByteRange{positions, (size_t)rows * 4}))
+        return KVD_ERR_INVALID_ARG;
     if (rows == 0) return KVD_OK;
     int sms = 0;
     if ((st = device_sms(&sms)) != KVD_OK) return st;
@@ -281,6 +286,7 @@ size_t kvd_fp4_block_bytes(int head_dim) {
 
 kvd_status kvd_kv_quantize_fp4(const void* cache, void* blocks, const int32_t* seq_lens, int batch, int s_max,
                                int s_max_blocks, int max_seq_len, int n_heads_kv, int head_dim, kvd_stream_t stream) {
+    if (max_seq_len > kMaxTokens4) return KVD_ERR_UNSUPPORTED;
     if (batch < 0 || s_max <= 0 || s_max_blocks <= 0 || s_max_blocks % 16 != 0 || max_seq_len < 0 || max_seq_len > s_max ||
         max_seq_len > s_max_blocks || n_heads_kv <= 0)
         return KVD_ERR_INVALID_ARG;
@@ -302,6 +308,7 @@ kvd_status kvd_kv_quantize_fp4(const void* cache, void* blocks, const int32_t* s
 kvd_status kvd_kv_read_fp4(const void* blocks, const int32_t* block_table, int s_max_blocks, int max_blocks,
                            int page_size, int num_pages, void* out, int s_out, const int32_t* seq_lens, int batch,
                            int max_seq_len, int n_heads_kv, int head_dim, int32_t* status_word, kvd_stream_t stream) {
+    if (max_seq_len > kMaxTokens4) return KVD_ERR_UNSUPPORTED;
     if (batch < 0 || s_out <= 0 || max_seq_len < 0 || max_seq_len > s_out || n_heads_kv <= 0) return KVD_ERR_INVALID_ARG;
     const kvd_cache_fp4 c{const_cast<void*>(blocks), nullptr, block_table, s_max_blocks, max_blocks, page_size, num_pages};
     PagedCache pg;

@@ -336,7 +336,7 @@ __global__ void __launch_bounds__(Fp4Shape<D, NT, F32OUT>::THREADS, Fp4Shape<D, 
             if (pos < real0) pos = real0;
             if (pos >= E) break;
             const long long te = min(pend, E);
-            const int tok_lo = (int)(pos - real0) * TILE, tok_hi = min((int)(te - real0) * TILE, L);
+            const int tok_lo = (int)(pos - real0) * TILE, tok_hi = (int)min((te - real0) * TILE, (long long)L);
             const bool covers = real0 >= S && pend <= E;
             pos = te;
             announce(Fp4Segment{b, h, L, tok_lo, tok_hi, covers, false});
