@@ -396,3 +396,99 @@ def test_two_streams():
             kvd.decode_fp4(c.qd, c.k, c.v, c.lens_d, c.S, c.scale, o, workspace=w, stream=s)
     torch.cuda.synchronize()
     assert all(torch.equal(a, o) for a, o in zip(alone, outs))
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("T,G", [(1, 7), (3, 4), (3, 7), (4, 8), (5, 9), (7, 7)])
+def test_every_number_of_column_tiles(D, T, G):
+    import torch
+    import kv_cache_decode_gb300 as kvd
+    dev = cuda_or_skip()
+    c = Case(D + T * G, 2 * G, 2, D, [290, 5, 0, 65], T=T, dev=dev)
+    for dtype in ("bf16", "f32"):
+        c.check(kvd, torch, dev, dtype)
+        c.check(kvd, torch, dev, dtype, n_split=3)
+
+
+def test_most_query_rows_and_no_tokens():
+    import torch
+    import kv_cache_decode_gb300 as kvd
+    dev = cuda_or_skip()
+    c = Case(3, 64, 1, 64, [100, 64, 1], T=64, dev=dev)
+    c.check(kvd, torch, dev, "bf16")
+    c.lens[:] = 0
+    c.lens_d.zero_()
+    c.check(kvd, torch, dev, "f32", max_len=0)
+
+
+def test_offsets_past_32_bits():
+    """Blocks further than 4 GB into a cache, by sequence, by page and within one sequence; two sequences with a
+    page in common. The long sequence's first rows are zero: each adds 1 to the sum."""
+    import torch
+    import kv_cache_decode_gb300 as kvd
+    dev = cuda_or_skip()
+    D, BLK, n = 256, 9 * 256 + 16, 1 << 20
+    big = [torch.zeros(3 * n, BLK, dtype=torch.uint8, device=dev) for _ in range(2)]  # 7.3 GB each
+    c = Case(31, 8, 1, D, [1, 3, 500], dev=dev)
+    small = [c.k, c.v]
+    c.k, c.v = (x.view(3, 1, n, BLK) for x in big)
+    for x, s in zip((c.k, c.v), small):
+        x[:, :, :s.shape[2]] = s
+    c.check(kvd, torch, dev, "f32")
+    # an append to the last block of the last sequence, and the bulk conversion to the same place
+    g = torch.Generator(device=dev).manual_seed(2)
+    kn, vn = (torch.randn(3, 1, D, generator=g, device=dev).bfloat16() for _ in range(2))
+    kvd.kv_append_fp4(c.k, c.v, kn, vn, torch.tensor([600, 600, 16 * n - 1], dtype=torch.int32, device=dev))
+    torch.cuda.synchronize()
+    for x, new in ((c.k, kn), (c.v, vn)):
+        want, _ = _blocks(bf16_tensor_bits(new).reshape(3, 1, 1, D).repeat(16, 1))
+        for b, blk in ((1, 600 // 16), (2, n - 1)):
+            w = [a[0, 0, 0] for a in oracle.unpack_fp4(want[b:b + 1], D)]
+            got = [a[0, 0] for a in oracle.unpack_fp4(x[b, :, blk:blk + 1][None].cpu().numpy(), D)]
+            at = 8 if b == 1 else 15
+            assert all(np.array_equal(p[at], q) for p, q in zip(got, w))
+            assert not any(np.delete(p, at, 0).any() for p in got)
+    # pages at the end of the pool
+    c = Case(32, 8, 1, D, [300, 290], page=16, dev=dev)
+    c.bt[1, :5] = c.bt[0, :5]
+    c.kd[1, :80], c.vd[1, :80] = c.kd[0, :80], c.vd[0, :80]
+    m = c.k.shape[0]
+    for x, s in zip(big, (c.k, c.v)):
+        x[3 * n - m:] = s.view(m, BLK)
+    c.k, c.v = (x.view(3 * n, 1, 1, BLK) for x in big)
+    c.bt += 3 * n - m
+    c.check(kvd, torch, dev, "f32")
+    # one sequence: scores up to 256 * 25 * 8 / 16, each within 256 * 25 / 2 * 2^-24 < 2e-4, so the weights too, and
+    # the outputs of size up to 5 within twice that
+    for x in big:
+        x.zero_()
+    c = Case(33, 8, 1, D, [512], dev=dev)
+    L = 48 * n - 3
+    for x, s in zip(big, (c.k, c.v)):
+        x[3 * n - 32:] = s.view(32, BLK)
+    out, lse = torch.empty(1, 8, D, device=dev), torch.empty(1, 8, device=dev)
+    _, nb = kvd.decode_plan_fp4(1, 1, 8, 1, D, L)
+    ws = torch.empty(nb, dtype=torch.uint8, device=dev)
+    k, v = (x.view(1, 1, 3 * n, BLK) for x in big)
+    kvd.decode_fp4(c.qd[:, 0], k, v, torch.tensor([L], dtype=torch.int32, device=dev), L, 0.5, out, workspace=ws, lse=lse)
+    torch.cuda.synchronize()
+    q = bf16_bits_to_f32(c.q)[0, 0].astype(np.float64)
+    s = 0.5 * q @ c.kd[0, :509, 0].T
+    e = np.exp(s)
+    total = e.sum(1) + (L - 509)
+    assert np.abs(lse.cpu().numpy()[0] - np.log(total)).max() < 3e-4
+    assert np.abs(out.cpu().numpy()[0] - (e @ c.vd[0, :509, 0]) / total[:, None]).max() < 2e-3
+    assert (e.sum(1) > (L - 509)).any()  # the end of the sequence matters
+    # rows of a bf16 cache past 4 GB, to blocks and back
+    del c, big, k, v
+    S = 1 << 23
+    rows = torch.empty(2, S, 1, D, dtype=torch.bfloat16, device=dev)
+    rows[1, :40] = torch.randn(40, 1, D, generator=g, device=dev).bfloat16()
+    want, back = _blocks(np.pad(bf16_tensor_bits(rows[1, :40]), ((0, 8), (0, 0), (0, 0)))[None])
+    lens = torch.tensor([0, 40], dtype=torch.int32, device=dev)
+    blocks = kvd.alloc_cache_fp4(2, 1, D, S, device=dev)
+    kvd.kv_quantize_fp4(rows, blocks, lens, S)
+    rows[1, :40] = 0
+    kvd.kv_read_fp4(blocks, rows, lens, S)
+    torch.cuda.synchronize()
+    assert np.array_equal(rows[1, :40].double().cpu().numpy(), back[0, :40])

@@ -323,3 +323,51 @@ def test_append_fp4_plain_and_many_rows():
     for n, x in (("k", k), ("v", v)):
         want = oracle.pack_fp4(*oracle.quantize_fp4(bf16_tensor_bits(x).transpose(0, 2, 1, 3)))
         assert np.array_equal(t[n].cpu().numpy(), want)
+
+
+def test_rope_apply_to_other_columns_of_the_same_rows():
+    import torch
+    import kv_cache_decode_gb300 as kvd
+    dev = cuda_or_skip()
+    rope = kvd.RopeTable(64, device=dev)
+    N, H, D = 41, 3, 64
+    g = torch.Generator(device=dev).manual_seed(6)
+    wide = torch.randn(N, 2 * H * D, generator=g, device=dev).bfloat16()
+    pos = torch.arange(N, dtype=torch.int32, device=dev)
+    x, y = wide[:, :H * D].view(N, H, D), wide[:, H * D:].view(N, H, D)
+    keep, ref = x.clone(), torch.empty(N, H, D, dtype=torch.bfloat16, device=dev)
+    kvd.rope_apply(rope, keep, pos, ref)
+    kvd.rope_apply(rope, x, pos, y)
+    torch.cuda.synchronize()
+    assert torch.equal(y, ref) and torch.equal(x, keep)
+
+
+def test_offsets_past_32_bits():
+    """Rows further than 4 GB into a buffer or a cache turn as they do in a small one."""
+    import torch
+    import kv_cache_decode_gb300 as kvd
+    dev = cuda_or_skip()
+    rope = kvd.RopeTable(128, device=dev)
+    g = torch.Generator(device=dev).manual_seed(9)
+    N, H, D = (1 << 19) + 9, 32, 128
+    x = torch.zeros(N, H, D, dtype=torch.bfloat16, device=dev)
+    x[-9:] = torch.randn(9, H, D, generator=g, device=dev).bfloat16()
+    last, pos = x[-9:].clone(), torch.arange(N, dtype=torch.int32, device=dev)
+    ref = torch.empty_like(last)
+    kvd.rope_apply(rope, last, pos[-9:].clone(), ref)
+    kvd.rope_apply(rope, x, pos, x)
+    torch.cuda.synchronize()
+    assert torch.equal(x[-9:], ref) and not x[:-9].any()
+    S = 1 << 23
+    kc, vc = (torch.zeros(3, S, 1, D, dtype=torch.bfloat16, device=dev) for _ in range(2))
+    k, v = (torch.randn(3, 1, D, generator=g, device=dev).bfloat16() for _ in range(2))
+    at = torch.tensor([5, S - 1, S - 2], dtype=torch.int32, device=dev)
+    kr = torch.empty_like(k)
+    kvd.rope_apply(rope, k, at, kr)
+    kvd.kv_append_rope(rope, kc, vc, k, v, at)
+    torch.cuda.synchronize()
+    i = torch.arange(3, device=dev)
+    assert torch.equal(kc[i, at.long()], kr) and torch.equal(vc[i, at.long()], v)
+    kc[i, at.long()] = 0
+    vc[i, at.long()] = 0
+    assert not kc.any() and not vc.any()

@@ -200,7 +200,7 @@ def _apply(lib, rope=None, **over):
     (dict(pos=FAKE * 3 + 2), 1), (dict(xs=1023), 1), (dict(ys=1020), 1), (dict(ys=1028), 1), (dict(rows=-1), 1),
     (dict(rows=1 << 31), 1), (dict(H=0), 1), (dict(D=12), 1), (dict(D=0), 1), (dict(D=1032, xs=8256, ys=8256), 2),
     (dict(idt=5), 1), (dict(odt=-1), 1), (dict(D=48, xs=384, ys=384), 1),   # rotary_dim 64 past the head
-    (dict(y=FAKE + 2048), 1),                                                 # overlaps x
+    (dict(y=FAKE + 2048), 1), (dict(y=FAKE + 1024, xs=2048, ys=2048), 1),     # overlaps x
     (dict(y=FAKE, ys=2048), 1), (dict(y=FAKE, odt=1), 1),                     # in place with another stride or type
     (dict(pos=FAKE * 2 + 16), 1),                                             # positions inside y
     (dict(rows=0), 0), (dict(rows=0, y=FAKE), 0),
@@ -240,6 +240,8 @@ def _append(lib, fp4=False, rope="rope", cache=None, **over):
     (dict(N=-2), 1), (dict(N=1 << 31), 1), (dict(Hkv=0), 1), (dict(Hq=0), 1), (dict(D=100), None), (dict(off=FAKE + 2), 1),
     (dict(status=FAKE + 1), 1), (dict(qo=FAKE + 512), 1), (dict(qo=FAKE, qos=2048), 1),
     (dict(qo=FAKE * 3), 1), (dict(qo=FAKE * 4 + 512), 1), (dict(qo=FAKE * 6), 1), (dict(k=FAKE * 7), 1),
+    (dict(pos=FAKE * 6 + 64), 1), (dict(qo=FAKE * 9, pos=FAKE * 9 + 16), 1), (dict(off=FAKE * 7 + 64), 1),  # indices inside what is written
+    (dict(qo=FAKE * 9, off=FAKE * 9 + 16), 1),
     (dict(cache=dict(k=None)), 1), (dict(cache=dict(v=FAKE * 6)), 1), (dict(cache=dict(v=FAKE * 6 + 1024)), 1),
     (dict(cache=dict(block_table=FAKE * 8, max_blocks=2, page_size=24, num_pages=4)), 1),
     (dict(cache=dict(block_table=FAKE * 8, max_blocks=0, page_size=16, num_pages=4)), 1),
@@ -324,6 +326,17 @@ def test_quantize_fp4_refuses(lib, args, expect):
     assert lib.kvd_kv_read_fp4(blocks, None, Sb, 0, 0, 0, cache, S, lens, B, mx, H, D, None, None) == expect
 
 
+def test_fp4_token_limit(lib):
+    top = 0x7ffffc00
+    c = dict(s_max=0x7ffffff0)
+    assert _decode4(lib, cache=c, mx=top) == kvd.ERR_WORKSPACE_TOO_SMALL
+    assert _decode4(lib, cache=c, mx=top + 1) == kvd.ERR_UNSUPPORTED
+    assert lib.kvd_kv_quantize_fp4(FAKE, FAKE * 2, FAKE * 3, 0, 0x7ffffff0, 0x7ffffff0, top + 1, 1, 64, None) == kvd.ERR_UNSUPPORTED
+    assert lib.kvd_kv_read_fp4(FAKE, None, 0x7ffffff0, 0, 0, 0, FAKE * 2, 0x7ffffff0, FAKE * 3, 0, top + 1, 1, 64, None,
+                               None) == kvd.ERR_UNSUPPORTED
+    assert lib.kvd_kv_quantize_fp4(FAKE, FAKE * 2, FAKE * 3, 0, 0x7ffffff0, 0x7ffffff0, top, 1, 64, None) == kvd.OK
+
+
 def test_read_fp4_refuses_pages(lib):
     ok = dict(max_blocks=4, page=16, pages=9, mx=64, status=None)
 
@@ -344,6 +357,11 @@ def test_python_refusals():
     for fn in (lambda: kvd.rope_apply(r, x, torch.zeros(4, dtype=torch.int32), x),
                lambda: kvd.decode_fp4(x, x, x, x, 4, 1.0, x),
                lambda: kvd.kv_append_rope(r, x[None], x[None], x, x, torch.zeros(4, dtype=torch.int32)),
+               lambda: kvd.kv_append_fp4(None, x, x, x, x), lambda: kvd.kv_append_fp4(x, None, x, x, x),
+               lambda: kvd.decode_fp4(x, None, x, x, 4, 1.0, x), lambda: kvd.decode_fp4(None, x, x, x, 4, 1.0, x),
+               lambda: kvd.rope_apply(None, x, x, x), lambda: kvd.rope_apply(r, None, x, x),
+               lambda: kvd.kv_append_rope(r, None, x, x, x, x), lambda: kvd.kv_append_rope(r, x, x, None, x, x),
+               lambda: kvd.kv_quantize_fp4(None, x, x, 3), lambda: kvd.kv_read_fp4(x, None, x, 3),
                lambda: kvd.kv_quantize_fp4(x, x, x, 3), lambda: kvd.kv_read_fp4(x, x, x, 3)):
         with pytest.raises((ValueError, TypeError)):
             fn()
