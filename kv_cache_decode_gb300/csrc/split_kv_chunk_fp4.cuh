@@ -38,6 +38,12 @@
 // KVD_STATUS_TIMEOUT, and since a segment fixes its tiles, the working warps go on to its end
 // together, on whatever the tiles hold, and stop there. The running maxima are only raised, after a vote, when a
 // score passes them by 2^15. At a segment's end the warps' states are merged through shared memory.
+//
+// Measured: 128 sequences of 1,024 to 8,192 tokens, 32 query and 8 KV heads of 128: 144 us (691 MB, 4.8 of 6.8 TB/s
+// copied; an instruction issues in 59 % of the cycles, the waits between are of many kinds). 64 sequences of 2,048, 48 query heads
+// on one KV head of 256: 38 us, 5.5 for the first tile to arrive, 6.5 a tile of 256 tokens (3.2 of it the MMAs alone), 4 a merge. 9
+// sequences of up to 4,001 with 5 drafted tokens, 32 and 8 heads of 128: 23 us. 12 or 16 working warps in place of 8 (with
+// 112 or 152 registers) took 23.6 and 26 us there, tiles of half the size 25, a schedule formed by the loading warp alone as long.
 #pragma once
 
 #include "fp4.cuh"
@@ -68,7 +74,7 @@ struct Fp4Shape {
     static constexpr bool QREG = KS * NT * 2 <= 16;  // q fragments in registers, else in shared memory
     static constexpr int LD = D + 4;             // merge buffer row, floats
     static constexpr int RING = 2 * STAGES * STAGE;  // K stages, then V stages
-    static constexpr int MBUF = GROUPS > 1 ? GROUPS / 2 : 1;
+    static constexpr int MBUF = GROUPS / 2;          // merge buffers: the upper half of the groups hands over to the lower
     static constexpr int MERGE = MBUF * ROWS * LD * 4;
     static constexpr int PBYTES = WD > 1 ? GROUPS * GB * NT * 256 * (F32OUT ? 2 : 1) : 0;  // the weights' fragments
     static constexpr int SHARED = MERGE > PBYTES ? MERGE : PBYTES;  // weights, and at a segment's end the merge
@@ -194,7 +200,7 @@ __global__ void __launch_bounds__(Fp4Shape<D, NT, F32OUT>::THREADS, Fp4Shape<D, 
     __shared__ long long s_red[THREADS / 32];
     __shared__ long long s_cum0;
     __shared__ int s_b0, s_abort;
-    __shared__ float s_ml[NW][ROWS], s_l[NW][ROWS];  // running maxima and sums; s_ml also carries raised maxima
+    __shared__ __align__(8) float s_ml[NW][ROWS], s_l[NW][ROWS];  // running maxima and sums; s_ml also carries raised maxima
     __shared__ float s_qs[ROWS], s_inv[ROWS];
     __shared__ int s_max[ROWS];  // a segment's maxima, as ordered integers
     __shared__ long long s_dst[ROWS];
@@ -644,34 +650,77 @@ __global__ void __launch_bounds__(Fp4Shape<D, NT, F32OUT>::THREADS, Fp4Shape<D, 
             }
             if (raise) {
                 float ho[NT][2];
-#pragma unroll
-                for (int j = 0; j < NT; ++j)
-#pragma unroll
-                    for (int z = 0; z < 2; ++z) {
-                        float hs = fmaxf(s[0][j][z], s[0][j][2 + z]);
-                        ho[j][z] = fmaxf(s[0][j][z] + ev[0][0], s[0][j][2 + z] + ev[0][1]);
-                        if constexpr (TB > 1) {
-                            hs = fmaxf(hs, fmaxf(s[TB - 1][j][z], s[TB - 1][j][2 + z]));
-                            ho[j][z] = fmaxf(ho[j][z], fmaxf(s[TB - 1][j][z] + ev[TB - 1][0], s[TB - 1][j][2 + z] + ev[TB - 1][1]));
-                        }
-#pragma unroll
-                        for (int off = 4; off < 32; off <<= 1) {
-                            hs = fmaxf(hs, __shfl_xor_sync(0xffffffffu, hs, off));
-                            ho[j][z] = fmaxf(ho[j][z], __shfl_xor_sync(0xffffffffu, ho[j][z], off));
-                        }
-                        const float ns = fmaxf(ms[j][z], hs);
-                        l[j][z] *= tc::ex2_approx(ms[j][z] - ns);
-                        ms[j][z] = ns;
-                        if (WD > 1 && r == 0) s_ml[warp][8 * j + 2 * c4 + z] = ho[j][z];
-                    }
-                if constexpr (WD > 1) {
-                    group_sync(1 + group, 32 * WD);
+                if constexpr (WD == 1) {
 #pragma unroll
                     for (int j = 0; j < NT; ++j)
 #pragma unroll
-                        for (int z = 0; z < 2; ++z)
+                        for (int z = 0; z < 2; ++z) {
+                            float hs = fmaxf(s[0][j][z], s[0][j][2 + z]);
+                            ho[j][z] = fmaxf(s[0][j][z] + ev[0][0], s[0][j][2 + z] + ev[0][1]);
+                            if constexpr (TB > 1) {
+                                hs = fmaxf(hs, fmaxf(s[TB - 1][j][z], s[TB - 1][j][2 + z]));
+                                ho[j][z] = fmaxf(ho[j][z], fmaxf(s[TB - 1][j][z] + ev[TB - 1][0], s[TB - 1][j][2 + z] + ev[TB - 1][1]));
+                            }
 #pragma unroll
-                            for (int w = 0; w < WD; ++w) ho[j][z] = fmaxf(ho[j][z], s_ml[group * WD + w][8 * j + 2 * c4 + z]);
+                            for (int off = 4; off < 32; off <<= 1) {
+                                hs = fmaxf(hs, __shfl_xor_sync(0xffffffffu, hs, off));
+                                ho[j][z] = fmaxf(ho[j][z], __shfl_xor_sync(0xffffffffu, ho[j][z], off));
+                            }
+                            const float ns = fmaxf(ms[j][z], hs);
+                            l[j][z] *= tc::ex2_approx(ms[j][z] - ns);
+                            ms[j][z] = ns;
+                        }
+                } else {
+                    // Of the 2 NT maxima that the 8 lanes of a column hold, each exchange leaves a lane half (an odd number is
+                    // exchanged whole); they go to s_l (scores, this warp's) and s_ml (with V's exponents, the group's).
+                    auto fold = [&](float* to, bool with_ev) {
+                        float v[2 * NT];
+#pragma unroll
+                        for (int i = 0; i < 2 * NT; ++i)
+#pragma unroll
+                            for (int x = 0; x < TB; ++x) {
+                                const float a = s[x][i / 2][i % 2] + (with_ev ? ev[x][0] : 0.f),
+                                            b = s[x][i / 2][2 + i % 2] + (with_ev ? ev[x][1] : 0.f);
+                                v[i] = x ? fmaxf(v[i], fmaxf(a, b)) : fmaxf(a, b);
+                            }
+                        int n = 2 * NT, at = 0;  // v[i] is maximum at + i
+#pragma unroll
+                        for (int off = 16; off >= 4; off >>= 1) {
+                            const bool up = lane & off;
+                            if (n % 2 == 0) {
+                                n /= 2;
+                                at += up ? n : 0;
+#pragma unroll
+                                for (int i = 0; i < n; ++i) {
+                                    const float send = up ? v[i] : v[i + n], keep = up ? v[i + n] : v[i];
+                                    v[i] = fmaxf(keep, __shfl_xor_sync(0xffffffffu, send, off));
+                                }
+                            } else {
+#pragma unroll
+                                for (int i = 0; i < n; ++i) v[i] = fmaxf(v[i], __shfl_xor_sync(0xffffffffu, v[i], off));
+                            }
+                        }
+#pragma unroll
+                        for (int i = 0; i < n; ++i) to[8 * ((at + i) >> 1) + 2 * c4 + ((at + i) & 1)] = v[i];
+                    };
+                    fold(s_l[warp], false);
+                    fold(s_ml[warp], true);
+                    group_sync(1 + group, 32 * WD);
+#pragma unroll
+                    for (int j = 0; j < NT; ++j) {
+                        const float2 a = *reinterpret_cast<const float2*>(&s_l[warp][8 * j + 2 * c4]);
+#pragma unroll
+                        for (int z = 0; z < 2; ++z) {
+                            const float ns = fmaxf(ms[j][z], z ? a.y : a.x);
+                            l[j][z] *= tc::ex2_approx(ms[j][z] - ns);
+                            ms[j][z] = ns;
+                        }
+#pragma unroll
+                        for (int w = 0; w < WD; ++w) {
+                            const float2 b = *reinterpret_cast<const float2*>(&s_ml[group * WD + w][8 * j + 2 * c4]);
+                            ho[j][0] = w ? fmaxf(ho[j][0], b.x) : b.x, ho[j][1] = w ? fmaxf(ho[j][1], b.y) : b.y;
+                        }
+                    }
                 }
 #pragma unroll
                 for (int j = 0; j < NT; ++j)
@@ -846,7 +895,7 @@ __global__ void __launch_bounds__(Fp4Shape<D, NT, F32OUT>::THREADS, Fp4Shape<D, 
             }
         };
         // Column of o[(g * VW + v) * 4 + i][j][0 / 2]: d0 + 128 g + 8 (VW r + v) + 2 i, + 1 for rows r + 8.
-        // step 0: to the buffer; 1: the buffer added, and back to it; 2: the buffer added, and out.
+        // step 0: to the buffer; 1: the buffer added, and back to it.
         auto exchange = [&](auto step) {
 #pragma unroll
             for (int g = 0; g < VG; ++g)
@@ -867,37 +916,29 @@ __global__ void __launch_bounds__(Fp4Shape<D, NT, F32OUT>::THREADS, Fp4Shape<D, 
                                     const float4 e = d[x];
                                     f = make_float4(f.x + e.x, f.y + e.y, f.z + e.z, f.w + e.w);
                                 }
-                                if constexpr (decltype(step)::value == 2) {
-                                    if (rbase + row < rend) emit(row, col + 4 * x, f);
-                                } else {
-                                    d[x] = f;
-                                }
+                                d[x] = f;
                             }
                         }
         };
+        // The last sum leaves from shared memory in a short loop of all threads: unrolled from the registers of half of
+        // them it took twice as long, much of it fetching instructions that run once.
         if (group >= Sh::MBUF) exchange(Step<0>{});
         workers_sync(WORKERS);
-        if constexpr (Sh::MBUF == 1) {
-            finish_rows(tid);
-            workers_sync(WORKERS);
-            if (group < Sh::MBUF) exchange(Step<2>{});
-        } else {
-            if (group < Sh::MBUF)
-                exchange(Step<1>{});
-            else
-                finish_rows(tid - WORKERS / 2);
-            workers_sync(WORKERS);
+        if (group < Sh::MBUF)
+            exchange(Step<1>{});
+        else
+            finish_rows(tid - WORKERS / 2);
+        workers_sync(WORKERS);
 #pragma unroll 1
-            for (int i = tid; i < (rend - rbase) * (D / 4); i += WORKERS) {
-                const int row = i / (D / 4), col = (i - row * (D / 4)) * 4;
-                float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int i = tid; i < (rend - rbase) * (D / 4); i += WORKERS) {
+            const int row = i / (D / 4), col = (i - row * (D / 4)) * 4;
+            float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-                for (int w = 0; w < Sh::MBUF; ++w) {
-                    const float4 e = *reinterpret_cast<const float4*>(s_merge + (w * ROWS + row) * Sh::LD + col);
-                    f = make_float4(f.x + e.x, f.y + e.y, f.z + e.z, f.w + e.w);
-                }
-                emit(row, col, f);
+            for (int w = 0; w < Sh::MBUF; ++w) {
+                const float4 e = *reinterpret_cast<const float4*>(s_merge + (w * ROWS + row) * Sh::LD + col);
+                f = make_float4(f.x + e.x, f.y + e.y, f.z + e.z, f.w + e.w);
             }
+            emit(row, col, f);
         }
         if (tid < ROWS) s_max[tid] = float_order(kNoMax);
         ++n;
