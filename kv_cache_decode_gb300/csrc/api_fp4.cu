@@ -6,6 +6,7 @@
 #include <cstring>
 
 #include "api_common.h"
+#include "rope_fp4.h"
 
 namespace kvd {
 

@@ -6,7 +6,6 @@
 // Measured: 32 sequences of up to 8,192 tokens, 8 heads of 128, 517 MB each way: to blocks 79 us (6.5 TB/s), back 90 (5.8).
 #include "../../include/kvdecode.h"
 #include "fp4.cuh"
-#include "params.h"
 #include "rope.cuh"
 
 namespace kvd {

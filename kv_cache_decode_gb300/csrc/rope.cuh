@@ -9,7 +9,7 @@
 #pragma once
 
 #include "common.cuh"
-#include "params.h"
+#include "rope_fp4.h"
 
 namespace kvd {
 
