@@ -300,7 +300,10 @@ kvd_status kvd_kv_quantize_fp4(const void* cache, void* blocks, const int32_t* s
     if (rb.overlaps(rc) || rb.overlaps(rl)) return KVD_ERR_INVALID_ARG;
     if (batch == 0 || max_seq_len == 0) return KVD_OK;
     if ((long long)batch * ((max_seq_len + 15) / 16) > 0x7fffffffLL) return KVD_ERR_INVALID_ARG;
-    return launch_quantize_fp4(cache, blocks, seq_lens, batch, s_max, s_max_blocks, max_seq_len, n_heads_kv, head_dim,
+    int sms = 0;
+    const kvd_status st = device_sms(&sms);
+    if (st != KVD_OK) return st;
+    return launch_quantize_fp4(cache, blocks, seq_lens, batch, s_max, s_max_blocks, max_seq_len, n_heads_kv, head_dim, sms,
                                static_cast<cudaStream_t>(stream)) == cudaSuccess
                ? KVD_OK
                : KVD_ERR_CUDA;
@@ -326,8 +329,10 @@ kvd_status kvd_kv_read_fp4(const void* blocks, const int32_t* block_table, int s
     if (ro.overlaps(rb) || ro.overlaps(rl)) return KVD_ERR_INVALID_ARG;
     if (batch == 0 || max_seq_len == 0) return KVD_OK;
     if ((long long)batch * ((max_seq_len + 15) / 16) > 0x7fffffffLL) return KVD_ERR_INVALID_ARG;
+    int sms = 0;
+    if ((st = device_sms(&sms)) != KVD_OK) return st;
     return launch_read_fp4(blocks, pg, s_max, out, s_out, seq_lens, batch, max_seq_len, n_heads_kv, head_dim, status_word,
-                           static_cast<cudaStream_t>(stream)) == cudaSuccess
+                           sms, static_cast<cudaStream_t>(stream)) == cudaSuccess
                ? KVD_OK
                : KVD_ERR_CUDA;
 }

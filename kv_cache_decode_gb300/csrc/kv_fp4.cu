@@ -12,42 +12,53 @@ namespace kvd {
 
 constexpr int kFp4Threads = 256;
 
-// Rows of a pass of the CTA: 16 tokens of HP heads, thread = (token, head, unit).
+// Rows of a pass of the CTA: 16 tokens of HP heads, thread = (token, head, unit). Where two passes would hold more heads than
+// there are (MANY), their 2 HP places are dealt to 1 << sh consecutive blocks (64 sequences of up to 30,000 tokens, one head of 64, to blocks and
+// back: 101 us, 355 with a block to a CTA).
 template <int D>
 struct Fp4Pass {
     static constexpr int UN = D / 16, HP = kFp4Threads / (16 * UN);  // D 256: 1, 128: 2, 64: 4
 };
 
-template <int D>
+template <int D, bool MANY>
 __global__ void __launch_bounds__(kFp4Threads) quantize_fp4_kernel(const uint4* __restrict__ src,
                                                                    uint8_t* __restrict__ blocks,
-                                                                   const int32_t* __restrict__ seq_lens, int n_blk,
+                                                                   const int32_t* __restrict__ seq_lens, int n_grp, int sh,
                                                                    int S_max, int S_blocks, int len_cap, int Hkv) {
     using Blk = Fp4Block<D>;
     constexpr int UN = Fp4Pass<D>::UN, HP = Fp4Pass<D>::HP;
-    const int b = blockIdx.x / n_blk, blk_i = blockIdx.x - b * n_blk;
-    const int u = threadIdx.x % UN, hp = threadIdx.x / UN % HP, r = threadIdx.x / (UN * HP), t = 16 * blk_i + r;
+    if (!MANY) sh = 0;
+    const int b = blockIdx.x / n_grp, blk0 = (blockIdx.x - b * n_grp) << sh;
+    const int u = threadIdx.x % UN, hp = threadIdx.x / UN % HP, r = threadIdx.x / (UN * HP);
     int L = __ldg(seq_lens + b);
     L = L < 0 ? 0 : (L > len_cap ? len_cap : L);
-    if (16 * blk_i >= L) return;
-    const bool live = t < L;
-    const uint4* row = src + ((size_t)b * S_max + t) * Hkv * (D / 8) + 2 * u;
-    uint8_t* out = blocks + ((size_t)b * Hkv * (S_blocks >> 4) + blk_i) * Blk::BYTES;
+    if (16 * blk0 >= L) return;
+    constexpr int NP = MANY ? 2 : 1;  // of a thread's two places, each its block, or both the one block
+    bool live[NP];
+    const uint4* row[NP];
+    uint8_t* out[NP];
+#pragma unroll
+    for (int k = 0; k < NP; ++k) {
+        const int blk_i = blk0 + ((hp + k * HP) & ((1 << sh) - 1)), t = 16 * blk_i + r;
+        live[k] = t < L;
+        row[k] = src + ((size_t)b * S_max + t) * Hkv * (D / 8) + 2 * u;
+        out[k] = blocks + ((size_t)b * Hkv * (S_blocks >> 4) + blk_i) * Blk::BYTES;
+    }
     const size_t head_bytes = (size_t)(S_blocks >> 4) * Blk::BYTES;
-    for (int h0 = hp; h0 - hp < Hkv; h0 += 2 * HP) {
+    for (int h0 = 0; h0 < Hkv; h0 += 2 * HP >> sh) {
         uint4 v[2][2];
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-            const int h = h0 + k * HP;
+            const int h = h0 + ((hp + k * HP) >> sh);
             v[k][0] = v[k][1] = make_uint4(0u, 0u, 0u, 0u);
-            if (live && h < Hkv) {
-                v[k][0] = __ldcs(row + (size_t)h * (D / 8));
-                v[k][1] = __ldcs(row + (size_t)h * (D / 8) + 1);
+            if (live[k % NP] && h < Hkv) {
+                v[k][0] = __ldcs(row[k % NP] + (size_t)h * (D / 8));
+                v[k][1] = __ldcs(row[k % NP] + (size_t)h * (D / 8) + 1);
             }
         }
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-            const int h = h0 + k * HP;
+            const int h = h0 + ((hp + k * HP) >> sh);
             const uint32_t w[8] = {v[k][0].x, v[k][0].y, v[k][0].z, v[k][0].w, v[k][1].x, v[k][1].y, v[k][1].z, v[k][1].w};
             // The largest magnitude, two bf16 values at a time (exact).
             __nv_bfloat162 m2 = __habs2(*reinterpret_cast<const __nv_bfloat162*>(&w[0]));
@@ -80,8 +91,8 @@ __global__ void __launch_bounds__(kFp4Threads) quantize_fp4_kernel(const uint4* 
                 }
                 code[q] = e2m1x8(z);
             }
-            if (live && h < Hkv) {
-                uint8_t* blk = out + h * head_bytes;
+            if (live[k % NP] && h < Hkv) {
+                uint8_t* blk = out[k % NP] + h * head_bytes;
                 *reinterpret_cast<uint2*>(blk + Blk::code(r, 16 * u)) = make_uint2(code[0], code[1]);
                 blk[Blk::scale(r, 16 * u)] = (uint8_t)s;
                 if (u == 0) blk[Blk::exp(r)] = (uint8_t)eb;
@@ -90,39 +101,48 @@ __global__ void __launch_bounds__(kFp4Threads) quantize_fp4_kernel(const uint4* 
     }
 }
 
-template <int D>
+template <int D, bool MANY>
 __global__ void __launch_bounds__(kFp4Threads) read_fp4_kernel(const uint8_t* __restrict__ blocks, const PagedCache pg,
                                                                int S_blocks, uint4* __restrict__ out, int S_out,
-                                                               const int32_t* __restrict__ seq_lens, int n_blk,
+                                                               const int32_t* __restrict__ seq_lens, int n_grp, int sh,
                                                                int len_cap, int Hkv, int32_t* status) {
     using Blk = Fp4Block<D>;
     constexpr int UN = Fp4Pass<D>::UN, HP = Fp4Pass<D>::HP;
-    const int b = blockIdx.x / n_blk, blk_i = blockIdx.x - b * n_blk;
-    const int u = threadIdx.x % UN, hp = threadIdx.x / UN % HP, r = threadIdx.x / (UN * HP), t = 16 * blk_i + r;
+    if (!MANY) sh = 0;
+    const int b = blockIdx.x / n_grp, blk0 = (blockIdx.x - b * n_grp) << sh;
+    const int u = threadIdx.x % UN, hp = threadIdx.x / UN % HP, r = threadIdx.x / (UN * HP);
     int L = __ldg(seq_lens + b);
     L = L < 0 ? 0 : (L > len_cap ? len_cap : L);
-    if (t >= L) return;
-    size_t first = (size_t)b * Hkv * (S_blocks >> 4) + blk_i;  // block of head 0; the next head's is `step` further
-    size_t step = S_blocks >> 4;
-    bool ok = true;
-    if (pg.block_table) {
-        const int page = __ldg(pg.block_table + (size_t)b * pg.max_blocks + (t >> pg.page_shift));
-        ok = page >= 0 && page < pg.num_pages;
-        if (!ok && status && threadIdx.x == 0) atomicOr(status, KVD_STATUS_BAD_PAGE);
-        step = (size_t)1 << (pg.page_shift - 4);
-        first = (size_t)(ok ? page : 0) * Hkv * step + ((t >> 4) & (step - 1));
+    if (16 * blk0 + r >= L) return;
+    const size_t step = pg.block_table ? (size_t)1 << (pg.page_shift - 4) : (size_t)(S_blocks >> 4);
+    constexpr int NP = MANY ? 2 : 1;
+    bool live[NP], ok[NP];
+    size_t first[NP];  // block of head 0; the next head's is `step` further
+    uint4* o[NP];
+#pragma unroll
+    for (int k = 0; k < NP; ++k) {
+        const int blk_i = blk0 + ((hp + k * HP) & ((1 << sh) - 1)), t = 16 * blk_i + r;
+        live[k] = !MANY || t < L;
+        ok[k] = live[k];
+        first[k] = (size_t)b * Hkv * step + blk_i;
+        if (pg.block_table && live[k]) {
+            const int page = __ldg(pg.block_table + (size_t)b * pg.max_blocks + (t >> pg.page_shift));
+            ok[k] = page >= 0 && page < pg.num_pages;
+            if (!ok[k] && status && u == 0 && r == 0) atomicOr(status, KVD_STATUS_BAD_PAGE);
+            first[k] = (size_t)(ok[k] ? page : 0) * Hkv * step + (blk_i & (step - 1));
+        }
+        o[k] = out + ((size_t)b * S_out + t) * Hkv * (D / 8) + 2 * u;
     }
-    uint4* o = out + ((size_t)b * S_out + t) * Hkv * (D / 8) + 2 * u;
-    for (int h0 = hp; h0 < Hkv; h0 += 2 * HP) {
+    for (int h0 = 0; h0 < Hkv; h0 += 2 * HP >> sh) {
         uint2 w[2];
         uint32_t sb[2], eb[2];
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-            const int h = h0 + k * HP;
+            const int h = h0 + ((hp + k * HP) >> sh);
             w[k] = make_uint2(0u, 0u);
             sb[k] = eb[k] = 0u;
-            if (ok && h < Hkv) {
-                const uint8_t* blk = blocks + (first + h * step) * Blk::BYTES;
+            if (ok[k % NP] && h < Hkv) {
+                const uint8_t* blk = blocks + (first[k % NP] + h * step) * Blk::BYTES;
                 w[k] = __ldcs(reinterpret_cast<const uint2*>(blk + Blk::code(r, 16 * u)));
                 sb[k] = __ldg(blk + Blk::scale(r, 16 * u));
                 eb[k] = __ldg(blk + Blk::exp(r));
@@ -130,8 +150,8 @@ __global__ void __launch_bounds__(kFp4Threads) read_fp4_kernel(const uint8_t* __
         }
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-            const int h = h0 + k * HP;
-            if (h >= Hkv) break;
+            const int h = h0 + ((hp + k * HP) >> sh);
+            if (!live[k % NP] || h >= Hkv) continue;
             const uint32_t s = e4m3x2_to_f16x2(sb[k] * 0x101u);
             const float up = fp4_row_scale(eb[k]);
             uint4 q[2];
@@ -146,37 +166,44 @@ __global__ void __launch_bounds__(kFp4Threads) read_fp4_kernel(const uint8_t* __
                 }
                 q[x] = make_uint4(f[0], f[1], f[2], f[3]);
             }
-            o[(size_t)h * (D / 8)] = q[0];
-            o[(size_t)h * (D / 8) + 1] = q[1];
+            o[k % NP][(size_t)h * (D / 8)] = q[0];
+            o[k % NP][(size_t)h * (D / 8) + 1] = q[1];
         }
     }
 }
 
+// log2 of the blocks a CTA takes: two passes' places over the heads, as far as about 8 CTAs per SM are left.
+static int blocks_log2(int B, int n_blk, int Hkv, int D, int num_sms) {
+    int sh = 0;
+    while ((Hkv << (sh + 1)) <= 2 * kFp4Threads / D && ((long long)B * n_blk >> (sh + 1)) >= 8LL * num_sms) ++sh;
+    return sh;
+}
+
 cudaError_t launch_quantize_fp4(const void* src, void* blocks, const int32_t* seq_lens, int B, int S_max, int S_blocks,
-                                int len_cap, int Hkv, int D, cudaStream_t stream) {
-    const int n_blk = (len_cap + 15) / 16;
+                                int len_cap, int Hkv, int D, int num_sms, cudaStream_t stream) {
+    const int n_blk = (len_cap + 15) / 16, sh = blocks_log2(B, n_blk, Hkv, D, num_sms), n_grp = (n_blk + (1 << sh) - 1) >> sh;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)((long long)B * n_blk), 1, 1);
+    cfg.gridDim = dim3((unsigned)((long long)B * n_grp), 1, 1);
     cfg.blockDim = dim3(kFp4Threads, 1, 1);
     cfg.stream = stream;
     auto* s = static_cast<const uint4*>(src);
     auto* d = static_cast<uint8_t*>(blocks);
-#define KVD_Q4(DD) cudaLaunchKernelEx(&cfg, quantize_fp4_kernel<DD>, s, d, seq_lens, n_blk, S_max, S_blocks, len_cap, Hkv)
+#define KVD_Q4(DD) cudaLaunchKernelEx(&cfg, sh ? quantize_fp4_kernel<DD, true> : quantize_fp4_kernel<DD, false>, s, d, seq_lens, n_grp, sh, S_max, S_blocks, len_cap, Hkv)
     return D == 64 ? KVD_Q4(64) : D == 128 ? KVD_Q4(128) : D == 256 ? KVD_Q4(256) : cudaErrorInvalidValue;
 #undef KVD_Q4
 }
 
 cudaError_t launch_read_fp4(const void* blocks, const PagedCache& pg, int S_blocks, void* out, int S_out,
                             const int32_t* seq_lens, int B, int len_cap, int Hkv, int D, int32_t* status,
-                            cudaStream_t stream) {
-    const int n_blk = (len_cap + 15) / 16;
+                            int num_sms, cudaStream_t stream) {
+    const int n_blk = (len_cap + 15) / 16, sh = blocks_log2(B, n_blk, Hkv, D, num_sms), n_grp = (n_blk + (1 << sh) - 1) >> sh;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)((long long)B * n_blk), 1, 1);
+    cfg.gridDim = dim3((unsigned)((long long)B * n_grp), 1, 1);
     cfg.blockDim = dim3(kFp4Threads, 1, 1);
     cfg.stream = stream;
     auto* s = static_cast<const uint8_t*>(blocks);
     auto* d = static_cast<uint4*>(out);
-#define KVD_R4(DD) cudaLaunchKernelEx(&cfg, read_fp4_kernel<DD>, s, pg, S_blocks, d, S_out, seq_lens, n_blk, len_cap, Hkv, status)
+#define KVD_R4(DD) cudaLaunchKernelEx(&cfg, sh ? read_fp4_kernel<DD, true> : read_fp4_kernel<DD, false>, s, pg, S_blocks, d, S_out, seq_lens, n_grp, sh, len_cap, Hkv, status)
     return D == 64 ? KVD_R4(64) : D == 128 ? KVD_R4(128) : D == 256 ? KVD_R4(256) : cudaErrorInvalidValue;
 #undef KVD_R4
 }

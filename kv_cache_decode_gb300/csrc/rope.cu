@@ -14,7 +14,7 @@ template <bool IN32, bool OUT32, int DD>
 __global__ void __launch_bounds__(kRopeWarps * 32) rope_kernel(const RopeTable rope, const void* x, long long xs, void* y,
                                                                long long ys, const int32_t* __restrict__ positions,
                                                                long long rows, int parts, int H, int D) {
-    extern __shared__ float2 s_cs[];  // [warps][R / 2]
+    extern __shared__ __align__(16) float2 s_cs[];  // [warps][R / 2]
     const long long w = (long long)blockIdx.x * kRopeWarps + (threadIdx.x >> 5);
     const long long row = w / parts;
     if (row >= rows) return;
@@ -23,9 +23,42 @@ __global__ void __launch_bounds__(kRopeWarps * 32) rope_kernel(const RopeTable r
     rw.template heads<IN32, OUT32>(x, (size_t)row * xs, y, (size_t)row * ys, H, (int)(w - row * parts), parts);
 }
 
+// Rows of at most 32 units (a warp's step): several rows to a warp. 500,000 bf16 rows of one head of 128 (256 MB) take 66 us,
+// by a warp each 247; 200,000 of 4 heads of 64 take 40, by a warp each 92. What is left over the copy's 38 and 30 is
+// the instructions of the cosines and sines, 64 or 32 a row.
+template <bool IN32, bool OUT32, bool ONE>
+__global__ void __launch_bounds__(kRopeWarps * 32) rope_rows_kernel(const RopeTable rope, const void* x, long long xs, void* y,
+                                                                    long long ys, const int32_t* __restrict__ positions,
+                                                                    long long rows, int per_warp, int H, int D) {
+    extern __shared__ __align__(16) float2 s_cs[];  // [warps][per_warp][R / 2]
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const long long row = ((long long)blockIdx.x * kRopeWarps + warp) * per_warp;
+    if (row >= rows) return;
+    const int n = (int)min((long long)per_warp, rows - row);
+    const RopeTokens rt{D, (D + 15) >> 4, rope.rotary_dim, n, rope.interleaved != 0, 0xffffffffu,
+                        s_cs + (size_t)warp * per_warp * (rope.rotary_dim >> 1)};
+    const long long t = lane < n ? __ldg(positions + row + lane) : 0;
+    rt.heads<IN32, OUT32, ONE>(x, (size_t)row * xs, (size_t)xs, y, (size_t)row * ys, (size_t)ys, ONE ? 1 : H, rope, t,
+                               [&]() { rt.table(rope, t); });
+}
+
 cudaError_t launch_rope(const RopeTable& rope, const void* x, long long xs, bool in32, void* y, long long ys, bool out32,
                         const int32_t* positions, long long rows, int H, int D, int num_sms, cudaStream_t stream) {
-    const long long steps = ((long long)H * ((D + 15) / 16) + 31) / 32;
+    const long long units = (long long)H * ((D + 15) / 16), steps = (units + 31) / 32;
+    const int per_warp = rope_tokens(rows, units, 64, num_sms);
+    if (per_warp > 1) {
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3((unsigned)((rows + per_warp * kRopeWarps - 1) / (per_warp * kRopeWarps)), 1, 1);
+        cfg.blockDim = dim3(kRopeWarps * 32, 1, 1);
+        if (H > 1) cfg.dynamicSmemBytes = (size_t)kRopeWarps * per_warp * (rope.rotary_dim / 2) * sizeof(float2);
+        cfg.stream = stream;
+#define KVD_ROPE(A, B)                                                                                                 \
+    cudaLaunchKernelEx(&cfg, H == 1 ? rope_rows_kernel<A, B, true> : rope_rows_kernel<A, B, false>, rope, x, xs, y, ys, \
+                       positions, rows, per_warp, H, D)
+        if (in32) return out32 ? KVD_ROPE(true, true) : KVD_ROPE(true, false);
+        return out32 ? KVD_ROPE(false, true) : KVD_ROPE(false, false);
+#undef KVD_ROPE
+    }
     const int parts = rope_parts(rows, steps, num_sms);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)((rows * parts + kRopeWarps - 1) / kRopeWarps), 1, 1);

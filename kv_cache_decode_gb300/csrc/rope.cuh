@@ -8,6 +8,8 @@
 // rounding them to float32's 24 bits moves it by at most pi * 2^-25 = 9.4e-8.
 #pragma once
 
+#include <algorithm>
+
 #include "common.cuh"
 #include "rope_fp4.h"
 
@@ -58,6 +60,22 @@ __device__ __forceinline__ void rope_turn(float (&a)[8], float (&b)[8], const fl
     } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i) rope_pair(a[i], b[i], cs[i]);
+    }
+}
+
+// A table of cosines and sines in shared memory, 16-byte chunks of two entries: chunk c lies at c ^ (c / 8 % 4), so that
+// threads with neighbouring units (8 entries each) read from different banks (30,000 rows of 40 heads of 80: 66 us, 74 without).
+__device__ __forceinline__ void rope_table_put(float2* table, int e, const float2& cs) {
+    const int c = e >> 1;
+    table[2 * (c ^ ((c >> 3) & 3)) + (e & 1)] = cs;
+}
+__device__ __forceinline__ void rope_table_get(const float2* table, int e, float2 (&cs)[8]) {  // e: a multiple of 8
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const int c = (e >> 1) + k;
+        const float4 v = reinterpret_cast<const float4*>(table)[c ^ ((c >> 3) & 3)];
+        cs[2 * k] = make_float2(v.x, v.y);
+        cs[2 * k + 1] = make_float2(v.z, v.w);
     }
 }
 
@@ -147,19 +165,20 @@ struct RopeWarp {
         R = rope.turns ? rope.rotary_dim : 0;
         interleaved = rope.interleaved;
         s_cs = buf;
-        for (int i = lane; i < R >> 1; i += 32) buf[i] = rope_cos_sin(t, __ldg(rope.turns + i), rope.factor);
+        for (int i = lane; i < R >> 1; i += 32) rope_table_put(buf, i, rope_cos_sin(t, __ldg(rope.turns + i), rope.factor));
         __syncwarp();
         if constexpr (DD > 0) {
-            const int u = lane % UN;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) cs[i] = u < R >> 4 ? buf[8 * u + i] : make_float2(1.f, 0.f);
+            if (lane % UN < R >> 4) rope_table_get(buf, 8 * (lane % UN), cs);
         }
     }
     __device__ __forceinline__ void turn(float (&a)[8], float (&b)[8], int u) const {
-        if constexpr (DD > 0)
+        if constexpr (DD > 0) {
             rope_turn(a, b, cs, interleaved);
-        else
-            rope_turn(a, b, s_cs + 8 * u, interleaved);
+        } else {
+            float2 w[8];
+            rope_table_get(s_cs, 8 * u, w);
+            rope_turn(a, b, w, interleaved);
+        }
     }
     // Turns the heads of one row, src to dst, this warp's steps of them: part, part + parts, ... Two steps'
     // loads come before either is turned: one unit in flight per thread keeps too few bytes on the way.
@@ -197,6 +216,91 @@ struct RopeWarp {
         }
     }
 };
+
+// A warp's work on several tokens at once, whose rows are too short to keep it busy one by one: the units of all of them
+// are dealt to the lanes, and the cosines and sines of all lie in shared memory, [token][R / 2].
+struct RopeTokens {
+    int D, units, R, n;  // n: tokens
+    bool interleaved;
+    uint32_t ok;         // bit i: token i takes part
+    float2* s_cs;
+
+    // t: lane i's is token i's position. Whole warps call this.
+    __device__ __forceinline__ void table(const RopeTable& rope, long long t) const {
+        const int lane = threadIdx.x & 31, half = R >> 1;
+        int tok = 0, i = lane;
+        for (int e = 0; e < n * half; e += 32) {
+            while (i >= half) i -= half, ++tok;
+            const long long at = __shfl_sync(0xffffffffu, t, tok & 31);
+            if (tok < n) rope_table_put(s_cs, tok * half + i, rope_cos_sin(at, __ldg(rope.turns + i), rope.factor));
+            i += 32;
+        }
+        __syncwarp();
+    }
+    // Unit j of rows of H heads: its token, head and unit of the head.
+    __device__ __forceinline__ void item(int j, int H, int& tok, int& h, int& u) const {
+        tok = j / (H * units);
+        const int m = j - tok * H * units;
+        h = m / units;
+        u = m - h * units;
+    }
+    __device__ __forceinline__ void turn(float (&a)[8], float (&b)[8], int tok, int u) const {
+        float2 cs[8];
+        rope_table_get(s_cs, tok * (R >> 1) + 8 * u, cs);
+        rope_turn(a, b, cs, interleaved);
+    }
+    // The tokens' rows (ss, ds elements apart), src to dst; ready() forms the table behind the first loads. ONE: rows of one
+    // head, where no thread shares a pair's cosine and sine with another and each forms its own (t as for the table): 66 us instead of 94
+    // for 500,000 rows of 128.
+    template <bool IN32, bool OUT32, bool ONE, class F>
+    __device__ __forceinline__ void heads(const void* src, size_t se, size_t ss, void* dst, size_t de, size_t ds, int H,
+                                          const RopeTable& rope, long long t, F&& ready) const {
+        const int lane = threadIdx.x & 31, total = n * H * units;
+        for (int base = 0; base < total; base += 64) {
+            RopeRaw<IN32> raw[2];
+            RopeUnit ru[2];
+            int tok[2], h[2], u[2];
+            bool live[2];
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const int j = base + 32 * k + lane;
+                item(j, H, tok[k], h[k], u[k]);
+                live[k] = j < total && ((ok >> tok[k]) & 1u);
+                ru[k] = rope_unit(u[k], D, R, interleaved);
+                if (live[k]) raw[k].load(src, se + tok[k] * ss + (size_t)h[k] * D, ru[k]);
+            }
+            if (!ONE && base == 0) ready();
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const long long at = ONE ? __shfl_sync(0xffffffffu, t, tok[k] & 31) : 0;
+                if (!live[k]) continue;
+                const size_t e = de + tok[k] * ds + (size_t)h[k] * D;
+                if (IN32 == OUT32 && !ru[k].turn) {
+                    raw[k].copy(dst, e, ru[k]);
+                    continue;
+                }
+                float a[8], b[8];
+                raw[k].get(a, b);
+                if (ONE && ru[k].turn) {
+                    float2 cs[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) cs[i] = rope_cos_sin(at, __ldg(rope.turns + 8 * u[k] + i), rope.factor);
+                    rope_turn(a, b, cs, interleaved);
+                } else if (ru[k].turn) {
+                    turn(a, b, tok[k], u[k]);
+                }
+                store8<OUT32>(dst, e + ru[k].ca, a);
+                if (ru[k].cb >= 0) store8<OUT32>(dst, e + ru[k].cb, b);
+            }
+        }
+    }
+};
+
+// How many tokens a warp takes: as many as give it `want` units, as far as about 64 warps per SM are left.
+inline int rope_tokens(long long rows, long long row_units, int want, int num_sms) {
+    const long long n = std::min({want / row_units, rows / (64LL * num_sms), 32LL});
+    return (int)(n < 1 ? 1 : n);
+}
 
 // How many warps share a row of `steps` steps: about 64 warps per SM, as many as it holds, where there are few rows.
 inline int rope_parts(long long rows, long long steps, int num_sms) {

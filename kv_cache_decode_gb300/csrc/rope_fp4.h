@@ -44,10 +44,10 @@ cudaError_t launch_append_rope(const AppendTarget& to, const RopeTable& rope, co
 
 // fp4 cache (kv_fp4.cu).
 cudaError_t launch_quantize_fp4(const void* src, void* blocks, const int32_t* seq_lens, int B, int S_max, int S_blocks,
-                                int len_cap, int Hkv, int D, cudaStream_t stream);
+                                int len_cap, int Hkv, int D, int num_sms, cudaStream_t stream);
 cudaError_t launch_read_fp4(const void* blocks, const PagedCache& pg, int S_blocks, void* out, int S_out,
                             const int32_t* seq_lens, int B, int len_cap, int Hkv, int D, int32_t* status,
-                            cudaStream_t stream);
+                            int num_sms, cudaStream_t stream);
 // The attention kernel over an fp4 cache for a pair of `rows` (n_tokens * group) query rows.
 const ChunkKernel* fp4_chunk_kernel(int head_dim, bool f32_out, int rows);
 

@@ -492,3 +492,46 @@ def test_offsets_past_32_bits():
     kvd.kv_read_fp4(blocks, rows, lens, S)
     torch.cuda.synchronize()
     assert np.array_equal(rows[1, :40].double().cpu().numpy(), back[0, :40])
+
+
+@pytest.mark.parametrize("D,Hkv", [(64, 1), (64, 2), (64, 3), (128, 1), (128, 2), (256, 1)])
+def test_quantize_and_read_few_heads(D, Hkv):
+    """Few heads and many blocks: a CTA takes several blocks."""
+    import torch
+    import kv_cache_decode_gb300 as kvd
+    dev = cuda_or_skip()
+    r = np.random.default_rng(D + Hkv)
+    B, S = 40, 2080
+    bits = _rows(r, (B, S, Hkv, D), 12.0)
+    lens = r.integers(0, S, B).astype(np.int32)
+    lens[[0, 3, 4, 5, 39]] = [S, 0, 1, 16, 17]
+    blocks = torch.full((B, Hkv, S // 16 + 3, 9 * D + 16), 0x5a, dtype=torch.uint8, device=dev)
+    kvd.kv_quantize_fp4(to_dev_bf16(bits, dev), blocks, torch.from_numpy(lens).to(dev), S)
+    torch.cuda.synchronize()
+    want, rows = _blocks(bits)
+    old = [a.copy() for a in oracle.unpack_fp4(np.full((B, Hkv, S // 16 + 3, 9 * D + 16), 0x5a, np.uint8), D)]
+    new = oracle.unpack_fp4(want, D)
+    exp = np.full((B, S, Hkv, D), 3.0)
+    for b in range(B):
+        for o, n in zip(old, new):
+            o[b, :, :lens[b]] = n[b, :, :lens[b]]
+        exp[b, :lens[b]] = rows[b, :lens[b]]
+    assert np.array_equal(blocks.cpu().numpy(), oracle.pack_fp4(*old))
+    out = torch.full((B, S, Hkv, D), 3.0, dtype=torch.bfloat16, device=dev)
+    ld = torch.from_numpy(lens).to(dev)
+    kvd.kv_read_fp4(blocks, out, ld, S)
+    torch.cuda.synchronize()
+    assert np.array_equal(out.double().cpu().numpy(), exp)
+    # pages of 32 tokens, one of them unnamed
+    nb = S // 32
+    table = torch.randperm(B * nb + 1, device=dev)[:B * nb].view(B, nb).int()
+    pool = torch.zeros(B * nb + 1, Hkv, 2, 9 * D + 16, dtype=torch.uint8, device=dev)
+    pool[table.long()] = blocks[:, :, :2 * nb].reshape(B, Hkv, nb, 2, -1).transpose(1, 2).contiguous()
+    table[0, 7] = -1
+    exp[0, 7 * 32:8 * 32] = 0
+    out.fill_(3.0)
+    status = torch.zeros(1, dtype=torch.int32, device=dev)
+    kvd.kv_read_fp4(pool, out, ld, S, block_table=table, status=status)
+    torch.cuda.synchronize()
+    assert int(status.item()) == kvd.STATUS_BAD_PAGE
+    assert np.array_equal(out.double().cpu().numpy(), exp)

@@ -371,3 +371,89 @@ def test_offsets_past_32_bits():
     kc[i, at.long()] = 0
     vc[i, at.long()] = 0
     assert not kc.any() and not vc.any()
+
+
+@pytest.mark.parametrize("D,R,H,inter", [(128, 128, 1, False), (64, 64, 1, True), (24, 16, 1, False), (16, 16, 1, True), (256, 240, 1, False),
+                                         (80, 48, 3, False), (256, 256, 2, False), (64, 32, 4, True), (1024, 256, 1, True), (72, 64, 2, False)])
+def test_many_short_rows(D, R, H, inter):
+    """Rows of few heads go several to a warp when there are enough of them: the same bits as a few at a time."""
+    import torch
+    import kv_cache_decode_gb300 as kvd
+    dev = cuda_or_skip()
+    rope = kvd.RopeTable(R, interleaved=inter, device=dev)
+    g = torch.Generator(device=dev).manual_seed(D + H)
+    for N in (20003, 200003 if D <= 128 else 50003):
+        wide = torch.randn(N, H * D + 8, generator=g, device=dev)
+        pos = torch.randint(-2 ** 31, 2 ** 31 - 1, (N,), generator=g, device=dev).int()
+        for idt in (torch.bfloat16, torch.float32):
+            x = wide.to(idt)[:, 8:].view(N, H, D)
+            for odt in (torch.bfloat16, torch.float32):
+                out, ref = (torch.full((N, H, D), float("nan"), dtype=odt, device=dev) for _ in range(2))
+                kvd.rope_apply(rope, x, pos, out)
+                for i in range(0, N, 5000):
+                    kvd.rope_apply(rope, x[i:i + 5000], pos[i:i + 5000], ref[i:i + 5000])
+                torch.cuda.synchronize()
+                assert torch.equal(out, ref)
+            full = wide.to(idt, copy=True)
+            y = full[:, 8:].view(N, H, D)
+            kvd.rope_apply(rope, y, pos, y)
+            kvd.rope_apply(rope, x, pos, ref := torch.empty(N, H, D, dtype=idt, device=dev))
+            torch.cuda.synchronize()
+            assert torch.equal(y, ref) and torch.equal(full[:, :8], wide.to(idt)[:, :8])
+
+
+@pytest.mark.parametrize("form,D,R,Hq,Hkv,page", [
+    ("bf16", 64, 64, 2, 1, 16), ("bf16", 24, 16, 1, 1, 0), ("bf16", 256, 128, 1, 1, 64), ("int8", 128, 64, 2, 1, 0), ("fp8", 64, 48, 0, 2, 32),
+    ("fp4", 64, 64, 0, 1, 16), ("fp4", 128, 128, 3, 1, 0), ("fp4", 256, 0, 0, 1, 32),
+])
+def test_append_many_short_rows(form, D, R, Hq, Hkv, page):
+    """Likewise the appends: packed prompts in one call against a few sequences at a time, and uniform ones."""
+    import torch
+    import kv_cache_decode_gb300 as kvd
+    dev = cuda_or_skip()
+    g = torch.Generator(device=dev).manual_seed(D + Hq)
+    rope = kvd.RopeTable(R, interleaved=Hq == 2, device=dev) if R else None
+    B, S, G = 48, 2048, 4
+    r = np.random.default_rng(D)
+    lens = r.integers(0, 2000, B)
+    lens[[0, 7, 8, 9, 20, B - 1]] = [0, 0, 0, 1, 2, 0]
+    start = np.minimum(r.integers(0, 500, B), S - lens)
+    start[[3, 30]] = [S - 100, -50]                       # past the end, before the start
+    off = np.concatenate([[0], np.cumsum(lens)]) + 3
+    N = int(off[-1]) + 70
+    q, k, v = (torch.randn(N, max(h, 1), D, generator=g, device=dev).bfloat16() for h in (Hq, Hkv, Hkv))
+    t, bt = _cache(kvd, torch, form, B, S, Hkv, D, page, dev, g)
+    if page:
+        bt[5, start[5] // page], bt[40, start[40] // page] = -1, t["k"].shape[0]  # pages that rows go to
+    t2 = {n: x.clone() for n, x in t.items()}
+    pos = torch.tensor(start, dtype=torch.int32, device=dev)
+    outs = [torch.full_like(q, 9.0) for _ in range(2)]
+    st = torch.zeros(2, dtype=torch.int32, device=dev)
+    i32 = lambda a: torch.tensor(a, dtype=torch.int32, device=dev)  # noqa: E731
+    kw = lambda i, a, b: dict(q=q[a:b], q_out=outs[i][a:b]) if Hq else {}  # noqa: E731
+    _call(kvd, form, rope, t, k, v, pos, row_offsets=i32(off), block_table=bt, status=st[:1], **kw(0, 0, N))
+    for b in range(0, B, G):
+        a, e = int(off[b]), int(off[b + G])
+        if a == e:
+            continue
+        part = t2 if page else {n: x[b:b + G] for n, x in t2.items()}
+        _call(kvd, form, rope, part, k[a:e], v[a:e], pos[b:b + G].contiguous(), row_offsets=i32(off[b:b + G + 1] - a),
+              block_table=bt[b:b + G].contiguous() if page else None, status=st[1:], **kw(1, a, e))
+    torch.cuda.synchronize()
+    assert st.tolist() == [kvd.STATUS_POS_OUT_OF_RANGE | (kvd.STATUS_BAD_PAGE if page else 0)] * 2
+    assert torch.equal(outs[0], outs[1])
+    for n in t:
+        assert torch.equal(t[n], t2[n]), n
+    # uniform: T rows to each sequence
+    T = 700
+    a, pos = (x[:B * T].view(B, T, -1, D) for x in (k, v)), (pos.clamp(0, 400) + 3).contiguous()
+    kk, vv = a
+    if N >= B * T:
+        _call(kvd, form, rope, t, kk, vv, pos, block_table=bt)
+        for b in range(0, B, G):
+            part = t2 if page else {n: x[b:b + G] for n, x in t2.items()}
+            _call(kvd, form, rope, part, kk[b:b + G], vv[b:b + G], pos[b:b + G].contiguous(),
+                  block_table=bt[b:b + G].contiguous() if page else None)
+        torch.cuda.synchronize()
+        for n in t:
+            assert torch.equal(t[n], t2[n]), n
