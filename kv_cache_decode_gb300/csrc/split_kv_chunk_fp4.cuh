@@ -74,13 +74,16 @@ struct Fp4Shape {
     static constexpr bool QREG = KS * NT * 2 <= 16;  // q fragments in registers, else in shared memory
     static constexpr int LD = D + 4;             // merge buffer row, floats
     static constexpr int RING = 2 * STAGES * STAGE;  // K stages, then V stages
-    static constexpr int MBUF = GROUPS / 2;          // merge buffers: the upper half of the groups hands over to the lower
+    // With 8 query rows and warps that work alone every warp's state has room beside the rings, and one barrier stands
+    // between them and the joined rows: 64 sequences of 500 to 1,500 tokens, 40 heads of 128, 102.7 us instead of 107.9.
+    static constexpr bool FLAT = WD == 1 && NT == 1;
+    static constexpr int MBUF = FLAT ? GROUPS : GROUPS / 2;          // merge buffers: the upper half of the groups hands over to the lower
     static constexpr int MERGE = MBUF * ROWS * LD * 4;
     static constexpr int PBYTES = WD > 1 ? GROUPS * GB * NT * 256 * (F32OUT ? 2 : 1) : 0;  // the weights' fragments
     static constexpr int SHARED = MERGE > PBYTES ? MERGE : PBYTES;  // weights, and at a segment's end the merge
     static constexpr int QBYTES = QREG ? 0 : KS * NT * 32 * 8;
     static constexpr int SMEM = RING + SHARED + QBYTES;
-    static constexpr int STATIC = 4096 + 2 * NW * ROWS * 4 + 24 * ROWS;  // an upper bound of the static arrays
+    static constexpr int STATIC = 4096 + (FLAT ? 3 : 2) * NW * ROWS * 4 + 28 * ROWS;  // an upper bound of the static arrays
     static constexpr int MINB = (ACC <= 32 && 2 * (SMEM + STATIC + 1024) <= 228 * 1024) ? 2 : 1;
     // The loading warp is a ninth; a CTA alone on its SM launches a warpgroup for it, whose
     // registers the working warps then take (168 a thread at launch, 232 and 40 after: 2 * 232 + 40 = 3 * 168).
@@ -202,6 +205,7 @@ __global__ void __launch_bounds__(Fp4Shape<D, NT, F32OUT>::THREADS, Fp4Shape<D, 
     __shared__ int s_b0, s_abort;
     __shared__ __align__(8) float s_ml[NW][ROWS], s_l[NW][ROWS];  // running maxima and sums; s_ml also carries raised maxima
     __shared__ float s_qs[ROWS], s_inv[ROWS];
+    __shared__ float s_mo[Sh::FLAT ? NW : 1][ROWS];  // running maxima of the outputs
     __shared__ int s_max[ROWS];  // a segment's maxima, as ordered integers
     __shared__ long long s_dst[ROWS];
     __shared__ int s_short[ROWS];
@@ -839,108 +843,164 @@ __global__ void __launch_bounds__(Fp4Shape<D, NT, F32OUT>::THREADS, Fp4Shape<D, 
             if (++stage == STAGES) stage = 0, ++round;
         }
 
-        // ---- merge the warps' states ----
-        // The rows' maxima first, by atomics on ordered integers (a maximum does not depend on their order).
-#pragma unroll
-        for (int j = 0; j < NT; ++j)
-#pragma unroll
-            for (int z = 0; z < 2; ++z)
-                if (r == 0) atomicMax(&s_max[8 * j + 2 * c4 + z], float_order(ms[j][z]));
-        workers_sync(WORKERS);
-#pragma unroll
-        for (int j = 0; j < NT; ++j)
+        if constexpr (Sh::FLAT) {
+            // ---- merge the warps' states: each leaves its own as it is, and every thread joins 4 columns of a row ----
 #pragma unroll
             for (int z = 0; z < 2; ++z) {
-                const float M = float_unorder(s_max[8 * j + 2 * c4 + z]);
-                const float f = mo[j][z] > kNoMax ? tc::ex2_approx(mo[j][z] - M) : 0.f;
-#pragma unroll
-                for (int i = 0; i < MT; ++i) {
-                    o[i][j][z] *= f;
-                    o[i][j][2 + z] *= f;
-                }
-                float sum = l[j][z] * tc::ex2_approx(ms[j][z] - M);
+                float sum = l[0][z];
 #pragma unroll
                 for (int off = 4; off < 32; off <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-                if (r == 0) s_l[warp][8 * j + 2 * c4 + z] = sum;
+                if (r == 0) {
+                    s_ml[warp][2 * c4 + z] = ms[0][z];
+                    s_l[warp][2 * c4 + z] = sum;
+                    s_mo[warp][2 * c4 + z] = mo[0][z];
+                }
             }
-        auto finish_rows = [&](int i) {  // a thread per row: sum, and where the row goes
-            if (i < 0 || i >= rend - rbase) return;
-            float L = 0.f;
 #pragma unroll
-            for (int w = 0; w < NW; ++w) L += s_l[w][i];
-            const float M = float_unorder(s_max[i]);
-            if (ct.full) {
-                const size_t orow = out_row(ct.b, ct.h, rbase + i);
-                s_inv[i] = L > 0.f ? 1.f / L : 0.f;
-                s_dst[i] = (long long)orow * D;
-                if (p.lse) p.lse[orow] = L > 0.f ? (M + log2f(L)) * 0.69314718055994531f : -CUDART_INF_F;
-            } else {
-                const size_t slot = ((size_t)c + ct.b * p.Hkv + ct.h) * TG + rbase + i;
-                s_dst[i] = (long long)slot * D;
-                p.ws_ml[slot] = make_float2(M, L);
-            }
-        };
-        auto emit = [&](int row, int col, const float4& f) {  // four columns of a merged row
-            float* ws = p.ws_o + s_dst[row] + col;
-            if (ct.full) {
-                const float inv = s_inv[row];
-                if constexpr (F32OUT)
-                    *reinterpret_cast<float4*>(reinterpret_cast<float*>(p.out) + s_dst[row] + col) =
-                        make_float4(f.x * inv, f.y * inv, f.z * inv, f.w * inv);
-                else
-                    *reinterpret_cast<uint2*>(reinterpret_cast<__nv_bfloat16*>(p.out) + s_dst[row] + col) =
-                        make_uint2(pack_bf16x2(f.x * inv, f.y * inv), pack_bf16x2(f.z * inv, f.w * inv));
-            } else {
-                *reinterpret_cast<float4*>(ws) = f;
-            }
-        };
-        // Column of o[(g * VW + v) * 4 + i][j][0 / 2]: d0 + 128 g + 8 (VW r + v) + 2 i, + 1 for rows r + 8.
-        // step 0: to the buffer; 1: the buffer added, and back to it.
-        auto exchange = [&](auto step) {
+            for (int v = 0; v < VW; ++v)
 #pragma unroll
-            for (int g = 0; g < VG; ++g)
+                for (int z = 0; z < 2; ++z) {  // columns as in exchange below
+                    float4* d = reinterpret_cast<float4*>(s_merge + (warp * ROWS + 2 * c4 + z) * Sh::LD + 8 * (VW * r + v));
 #pragma unroll
-                for (int v = 0; v < VW; ++v)
-#pragma unroll
-                    for (int j = 0; j < NT; ++j)
-#pragma unroll
-                        for (int z = 0; z < 2; ++z) {
-                            const int row = 8 * j + 2 * c4 + z, col = wg * DW + 128 * g + 8 * (VW * r + v);
-                            float4* d = reinterpret_cast<float4*>(s_merge + ((group % Sh::MBUF) * ROWS + row) * Sh::LD + col);
-                            const int m = (g * VW + v) * 4;
-#pragma unroll
-                            for (int x = 0; x < 2; ++x) {
-                                float4 f = make_float4(o[m + 2 * x][j][z], o[m + 2 * x][j][2 + z], o[m + 2 * x + 1][j][z],
-                                                       o[m + 2 * x + 1][j][2 + z]);
-                                if constexpr (decltype(step)::value > 0) {
-                                    const float4 e = d[x];
-                                    f = make_float4(f.x + e.x, f.y + e.y, f.z + e.z, f.w + e.w);
-                                }
-                                d[x] = f;
-                            }
-                        }
-        };
-        // The last sum leaves from shared memory in a short loop of all threads: unrolled from the registers of half of
-        // them it took twice as long, much of it fetching instructions that run once.
-        if (group >= Sh::MBUF) exchange(Step<0>{});
-        workers_sync(WORKERS);
-        if (group < Sh::MBUF)
-            exchange(Step<1>{});
-        else
-            finish_rows(tid - WORKERS / 2);
-        workers_sync(WORKERS);
+                    for (int x = 0; x < 2; ++x)
+                        d[x] = make_float4(o[4 * v + 2 * x][0][z], o[4 * v + 2 * x][0][2 + z], o[4 * v + 2 * x + 1][0][z],
+                                           o[4 * v + 2 * x + 1][0][2 + z]);
+                }
+            workers_sync(WORKERS);
 #pragma unroll 1
-        for (int i = tid; i < (rend - rbase) * (D / 4); i += WORKERS) {
-            const int row = i / (D / 4), col = (i - row * (D / 4)) * 4;
-            float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int i = tid; i < (rend - rbase) * (D / 4); i += WORKERS) {
+                const int row = i / (D / 4), col = (i - row * (D / 4)) * 4;
+                float M = kNoMax, L = 0.f;
+                float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-            for (int w = 0; w < Sh::MBUF; ++w) {
-                const float4 e = *reinterpret_cast<const float4*>(s_merge + (w * ROWS + row) * Sh::LD + col);
-                f = make_float4(f.x + e.x, f.y + e.y, f.z + e.z, f.w + e.w);
+                for (int w = 0; w < NW; ++w) M = fmaxf(M, s_ml[w][row]);
+#pragma unroll
+                for (int w = 0; w < NW; ++w) {
+                    L += s_l[w][row] * tc::ex2_approx(s_ml[w][row] - M);
+                    const float m = s_mo[w][row], g = m > kNoMax ? tc::ex2_approx(m - M) : 0.f;
+                    const float4 e = *reinterpret_cast<const float4*>(s_merge + (w * ROWS + row) * Sh::LD + col);
+                    f = make_float4(f.x + g * e.x, f.y + g * e.y, f.z + g * e.z, f.w + g * e.w);
+                }
+                if (ct.full) {
+                    const size_t orow = out_row(ct.b, ct.h, rbase + row);
+                    const float inv = L > 0.f ? 1.f / L : 0.f;
+                    if constexpr (F32OUT)
+                        *reinterpret_cast<float4*>(reinterpret_cast<float*>(p.out) + orow * D + col) =
+                            make_float4(f.x * inv, f.y * inv, f.z * inv, f.w * inv);
+                    else
+                        *reinterpret_cast<uint2*>(reinterpret_cast<__nv_bfloat16*>(p.out) + orow * D + col) =
+                            make_uint2(pack_bf16x2(f.x * inv, f.y * inv), pack_bf16x2(f.z * inv, f.w * inv));
+                    if (p.lse && col == 0) p.lse[orow] = L > 0.f ? (M + log2f(L)) * 0.69314718055994531f : -CUDART_INF_F;
+                } else {
+                    const size_t slot = ((size_t)c + ct.b * p.Hkv + ct.h) * TG + rbase + row;
+                    *reinterpret_cast<float4*>(p.ws_o + slot * D + col) = f;
+                    if (col == 0) p.ws_ml[slot] = make_float2(M, L);
+                }
             }
-            emit(row, col, f);
+        } else {
+            // ---- merge the warps' states ----
+            // The rows' maxima first, by atomics on ordered integers (a maximum does not depend on their order).
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+#pragma unroll
+                for (int z = 0; z < 2; ++z)
+                    if (r == 0) atomicMax(&s_max[8 * j + 2 * c4 + z], float_order(ms[j][z]));
+            workers_sync(WORKERS);
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+#pragma unroll
+                for (int z = 0; z < 2; ++z) {
+                    const float M = float_unorder(s_max[8 * j + 2 * c4 + z]);
+                    const float f = mo[j][z] > kNoMax ? tc::ex2_approx(mo[j][z] - M) : 0.f;
+#pragma unroll
+                    for (int i = 0; i < MT; ++i) {
+                        o[i][j][z] *= f;
+                        o[i][j][2 + z] *= f;
+                    }
+                    float sum = l[j][z] * tc::ex2_approx(ms[j][z] - M);
+#pragma unroll
+                    for (int off = 4; off < 32; off <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+                    if (r == 0) s_l[warp][8 * j + 2 * c4 + z] = sum;
+                }
+            auto finish_rows = [&](int i) {  // a thread per row: sum, and where the row goes
+                if (i < 0 || i >= rend - rbase) return;
+                float L = 0.f;
+#pragma unroll
+                for (int w = 0; w < NW; ++w) L += s_l[w][i];
+                const float M = float_unorder(s_max[i]);
+                if (ct.full) {
+                    const size_t orow = out_row(ct.b, ct.h, rbase + i);
+                    s_inv[i] = L > 0.f ? 1.f / L : 0.f;
+                    s_dst[i] = (long long)orow * D;
+                    if (p.lse) p.lse[orow] = L > 0.f ? (M + log2f(L)) * 0.69314718055994531f : -CUDART_INF_F;
+                } else {
+                    const size_t slot = ((size_t)c + ct.b * p.Hkv + ct.h) * TG + rbase + i;
+                    s_dst[i] = (long long)slot * D;
+                    p.ws_ml[slot] = make_float2(M, L);
+                }
+            };
+            auto emit = [&](int row, int col, const float4& f) {  // four columns of a merged row
+                float* ws = p.ws_o + s_dst[row] + col;
+                if (ct.full) {
+                    const float inv = s_inv[row];
+                    if constexpr (F32OUT)
+                        *reinterpret_cast<float4*>(reinterpret_cast<float*>(p.out) + s_dst[row] + col) =
+                            make_float4(f.x * inv, f.y * inv, f.z * inv, f.w * inv);
+                    else
+                        *reinterpret_cast<uint2*>(reinterpret_cast<__nv_bfloat16*>(p.out) + s_dst[row] + col) =
+                            make_uint2(pack_bf16x2(f.x * inv, f.y * inv), pack_bf16x2(f.z * inv, f.w * inv));
+                } else {
+                    *reinterpret_cast<float4*>(ws) = f;
+                }
+            };
+            // Column of o[(g * VW + v) * 4 + i][j][0 / 2]: d0 + 128 g + 8 (VW r + v) + 2 i, + 1 for rows r + 8.
+            // step 0: to the buffer; 1: the buffer added, and back to it.
+            auto exchange = [&](auto step) {
+#pragma unroll
+                for (int g = 0; g < VG; ++g)
+#pragma unroll
+                    for (int v = 0; v < VW; ++v)
+#pragma unroll
+                        for (int j = 0; j < NT; ++j)
+#pragma unroll
+                            for (int z = 0; z < 2; ++z) {
+                                const int row = 8 * j + 2 * c4 + z, col = wg * DW + 128 * g + 8 * (VW * r + v);
+                                float4* d = reinterpret_cast<float4*>(s_merge + ((group % Sh::MBUF) * ROWS + row) * Sh::LD + col);
+                                const int m = (g * VW + v) * 4;
+#pragma unroll
+                                for (int x = 0; x < 2; ++x) {
+                                    float4 f = make_float4(o[m + 2 * x][j][z], o[m + 2 * x][j][2 + z], o[m + 2 * x + 1][j][z],
+                                                           o[m + 2 * x + 1][j][2 + z]);
+                                    if constexpr (decltype(step)::value > 0) {
+                                        const float4 e = d[x];
+                                        f = make_float4(f.x + e.x, f.y + e.y, f.z + e.z, f.w + e.w);
+                                    }
+                                    d[x] = f;
+                                }
+                            }
+            };
+            // The last sum leaves from shared memory in a short loop of all threads: unrolled from the registers of half of
+            // them it took twice as long, much of it fetching instructions that run once.
+            if (group >= Sh::MBUF) exchange(Step<0>{});
+            workers_sync(WORKERS);
+            if (group < Sh::MBUF)
+                exchange(Step<1>{});
+            else
+                finish_rows(tid - WORKERS / 2);
+            workers_sync(WORKERS);
+#pragma unroll 1
+            for (int i = tid; i < (rend - rbase) * (D / 4); i += WORKERS) {
+                const int row = i / (D / 4), col = (i - row * (D / 4)) * 4;
+                float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                for (int w = 0; w < Sh::MBUF; ++w) {
+                    const float4 e = *reinterpret_cast<const float4*>(s_merge + (w * ROWS + row) * Sh::LD + col);
+                    f = make_float4(f.x + e.x, f.y + e.y, f.z + e.z, f.w + e.w);
+                }
+                emit(row, col, f);
+            }
+            if (tid < ROWS) s_max[tid] = float_order(kNoMax);
         }
-        if (tid < ROWS) s_max[tid] = float_order(kNoMax);
         ++n;
         wait(told + 8u * (n & (SEGS - 1)), n / SEGS);
         if (workers_any(WORKERS, !fine)) break;  // also: the merge buffers and q are free again
