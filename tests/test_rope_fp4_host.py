@@ -365,3 +365,11 @@ def test_python_refusals():
                lambda: kvd.kv_quantize_fp4(x, x, x, 3), lambda: kvd.kv_read_fp4(x, x, x, 3)):
         with pytest.raises((ValueError, TypeError)):
             fn()
+
+
+def test_plan_fp4_short_sequences(lib):
+    """A CTA for every pair, however short, as far as the SMs hold them."""
+    for B, T, Hq, Hkv, D, L in ((41, 1, 64, 8, 256, 1), (108, 1, 2, 2, 128, 31), (7, 4, 8, 8, 64, 16)):
+        n, _ = kvd.decode_plan_fp4(B, T, Hq, Hkv, D, L, num_sms=152)
+        assert min(B * Hkv, 152) <= n <= B * Hkv
+    assert kvd.decode_plan_fp4(5, 1, 8, 1, 128, 0, num_sms=152)[0] == 1
