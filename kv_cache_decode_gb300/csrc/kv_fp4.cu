@@ -12,28 +12,30 @@ namespace kvd {
 
 constexpr int kFp4Threads = 256;
 
-// Rows of a pass of the CTA: 16 tokens of HP heads, thread = (token, head, unit). Where two passes would hold more heads than
-// there are (MANY), their 2 HP places are dealt to 1 << sh consecutive blocks (64 sequences of up to 30,000 tokens, one head of 64, to blocks and
-// back: 101 us, 355 with a block to a CTA).
+// Rows of a pass of the CTA: 16 tokens of HP heads, thread = (token, head, unit). What a CTA takes: all heads of one block;
+// where two passes hold more heads than there are, as many of 1 << sh consecutive blocks (64 sequences of up to 30,000
+// tokens, one head of 64, to blocks and back: 101 us, 355 with a block to a CTA); or, where there are few blocks, a share
+// of the heads of one (6 sequences of up to 432 tokens, 19 heads of 256: 16 us, 26 with all heads).
+enum class Fp4Deal { kBlock, kBlocks, kHeads };
 template <int D>
 struct Fp4Pass {
     static constexpr int UN = D / 16, HP = kFp4Threads / (16 * UN);  // D 256: 1, 128: 2, 64: 4
 };
 
-template <int D, bool MANY>
+template <int D, Fp4Deal DEAL>
 __global__ void __launch_bounds__(kFp4Threads) quantize_fp4_kernel(const uint4* __restrict__ src,
                                                                    uint8_t* __restrict__ blocks,
                                                                    const int32_t* __restrict__ seq_lens, int n_grp, int sh,
                                                                    int S_max, int S_blocks, int len_cap, int Hkv) {
     using Blk = Fp4Block<D>;
     constexpr int UN = Fp4Pass<D>::UN, HP = Fp4Pass<D>::HP;
-    if (!MANY) sh = 0;
+    if (DEAL != Fp4Deal::kBlocks) sh = 0;
     const int b = blockIdx.x / n_grp, blk0 = (blockIdx.x - b * n_grp) << sh;
     const int u = threadIdx.x % UN, hp = threadIdx.x / UN % HP, r = threadIdx.x / (UN * HP);
     int L = __ldg(seq_lens + b);
     L = L < 0 ? 0 : (L > len_cap ? len_cap : L);
     if (16 * blk0 >= L) return;
-    constexpr int NP = MANY ? 2 : 1;  // of a thread's two places, each its block, or both the one block
+    constexpr int NP = DEAL == Fp4Deal::kBlocks ? 2 : 1;  // of a thread's two places, each its block, or both the one block
     bool live[NP];
     const uint4* row[NP];
     uint8_t* out[NP];
@@ -45,7 +47,8 @@ __global__ void __launch_bounds__(kFp4Threads) quantize_fp4_kernel(const uint4* 
         out[k] = blocks + ((size_t)b * Hkv * (S_blocks >> 4) + blk_i) * Blk::BYTES;
     }
     const size_t head_bytes = (size_t)(S_blocks >> 4) * Blk::BYTES;
-    for (int h0 = 0; h0 < Hkv; h0 += 2 * HP >> sh) {
+    constexpr bool PARTS = DEAL == Fp4Deal::kHeads;
+    for (int h0 = PARTS ? blockIdx.y * 2 * HP : 0; h0 < Hkv; h0 += PARTS ? gridDim.y * 2 * HP : 2 * HP >> sh) {
         uint4 v[2][2];
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
@@ -101,28 +104,28 @@ __global__ void __launch_bounds__(kFp4Threads) quantize_fp4_kernel(const uint4* 
     }
 }
 
-template <int D, bool MANY>
+template <int D, Fp4Deal DEAL>
 __global__ void __launch_bounds__(kFp4Threads) read_fp4_kernel(const uint8_t* __restrict__ blocks, const PagedCache pg,
                                                                int S_blocks, uint4* __restrict__ out, int S_out,
                                                                const int32_t* __restrict__ seq_lens, int n_grp, int sh,
                                                                int len_cap, int Hkv, int32_t* status) {
     using Blk = Fp4Block<D>;
     constexpr int UN = Fp4Pass<D>::UN, HP = Fp4Pass<D>::HP;
-    if (!MANY) sh = 0;
+    if (DEAL != Fp4Deal::kBlocks) sh = 0;
     const int b = blockIdx.x / n_grp, blk0 = (blockIdx.x - b * n_grp) << sh;
     const int u = threadIdx.x % UN, hp = threadIdx.x / UN % HP, r = threadIdx.x / (UN * HP);
     int L = __ldg(seq_lens + b);
     L = L < 0 ? 0 : (L > len_cap ? len_cap : L);
     if (16 * blk0 + r >= L) return;
     const size_t step = pg.block_table ? (size_t)1 << (pg.page_shift - 4) : (size_t)(S_blocks >> 4);
-    constexpr int NP = MANY ? 2 : 1;
+    constexpr int NP = DEAL == Fp4Deal::kBlocks ? 2 : 1;
     bool live[NP], ok[NP];
     size_t first[NP];  // block of head 0; the next head's is `step` further
     uint4* o[NP];
 #pragma unroll
     for (int k = 0; k < NP; ++k) {
         const int blk_i = blk0 + ((hp + k * HP) & ((1 << sh) - 1)), t = 16 * blk_i + r;
-        live[k] = !MANY || t < L;
+        live[k] = NP == 1 || t < L;
         ok[k] = live[k];
         first[k] = (size_t)b * Hkv * step + blk_i;
         if (pg.block_table && live[k]) {
@@ -133,7 +136,8 @@ __global__ void __launch_bounds__(kFp4Threads) read_fp4_kernel(const uint8_t* __
         }
         o[k] = out + ((size_t)b * S_out + t) * Hkv * (D / 8) + 2 * u;
     }
-    for (int h0 = 0; h0 < Hkv; h0 += 2 * HP >> sh) {
+    constexpr bool PARTS = DEAL == Fp4Deal::kHeads;
+    for (int h0 = PARTS ? blockIdx.y * 2 * HP : 0; h0 < Hkv; h0 += PARTS ? gridDim.y * 2 * HP : 2 * HP >> sh) {
         uint2 w[2];
         uint32_t sb[2], eb[2];
 #pragma unroll
@@ -179,16 +183,26 @@ static int blocks_log2(int B, int n_blk, int Hkv, int D, int num_sms) {
     return sh;
 }
 
+// CTAs that share a block's heads where there are few blocks: up to about 4 CTAs per SM, two passes each at least.
+static unsigned head_parts(long long ctas, int Hkv, int D, int sh, int num_sms) {
+    const int heads = 2 * kFp4Threads / D >> sh;
+    const long long most = (Hkv + heads - 1) / heads, want = (4LL * num_sms + ctas - 1) / ctas;
+    return (unsigned)(want < most ? want : most);
+}
+
 cudaError_t launch_quantize_fp4(const void* src, void* blocks, const int32_t* seq_lens, int B, int S_max, int S_blocks,
                                 int len_cap, int Hkv, int D, int num_sms, cudaStream_t stream) {
     const int n_blk = (len_cap + 15) / 16, sh = blocks_log2(B, n_blk, Hkv, D, num_sms), n_grp = (n_blk + (1 << sh) - 1) >> sh;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)((long long)B * n_grp), 1, 1);
+    cfg.gridDim = dim3((unsigned)((long long)B * n_grp), head_parts((long long)B * n_grp, Hkv, D, sh, num_sms), 1);
     cfg.blockDim = dim3(kFp4Threads, 1, 1);
     cfg.stream = stream;
     auto* s = static_cast<const uint4*>(src);
     auto* d = static_cast<uint8_t*>(blocks);
-#define KVD_Q4(DD) cudaLaunchKernelEx(&cfg, sh ? quantize_fp4_kernel<DD, true> : quantize_fp4_kernel<DD, false>, s, d, seq_lens, n_grp, sh, S_max, S_blocks, len_cap, Hkv)
+#define KVD_Q4(DD)                                                                                       \
+    cudaLaunchKernelEx(&cfg, sh ? quantize_fp4_kernel<DD, Fp4Deal::kBlocks> \
+                             : cfg.gridDim.y > 1 ? quantize_fp4_kernel<DD, Fp4Deal::kHeads> \
+                             : quantize_fp4_kernel<DD, Fp4Deal::kBlock>, s, d, seq_lens, n_grp, sh, S_max, S_blocks, len_cap, Hkv)
     return D == 64 ? KVD_Q4(64) : D == 128 ? KVD_Q4(128) : D == 256 ? KVD_Q4(256) : cudaErrorInvalidValue;
 #undef KVD_Q4
 }
@@ -198,12 +212,15 @@ cudaError_t launch_read_fp4(const void* blocks, const PagedCache& pg, int S_bloc
                             int num_sms, cudaStream_t stream) {
     const int n_blk = (len_cap + 15) / 16, sh = blocks_log2(B, n_blk, Hkv, D, num_sms), n_grp = (n_blk + (1 << sh) - 1) >> sh;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)((long long)B * n_grp), 1, 1);
+    cfg.gridDim = dim3((unsigned)((long long)B * n_grp), head_parts((long long)B * n_grp, Hkv, D, sh, num_sms), 1);
     cfg.blockDim = dim3(kFp4Threads, 1, 1);
     cfg.stream = stream;
     auto* s = static_cast<const uint8_t*>(blocks);
     auto* d = static_cast<uint4*>(out);
-#define KVD_R4(DD) cudaLaunchKernelEx(&cfg, sh ? read_fp4_kernel<DD, true> : read_fp4_kernel<DD, false>, s, pg, S_blocks, d, S_out, seq_lens, n_grp, sh, len_cap, Hkv, status)
+#define KVD_R4(DD)                                                                                       \
+    cudaLaunchKernelEx(&cfg, sh ? read_fp4_kernel<DD, Fp4Deal::kBlocks> \
+                             : cfg.gridDim.y > 1 ? read_fp4_kernel<DD, Fp4Deal::kHeads> \
+                             : read_fp4_kernel<DD, Fp4Deal::kBlock>, s, pg, S_blocks, d, S_out, seq_lens, n_grp, sh, len_cap, Hkv, status)
     return D == 64 ? KVD_R4(64) : D == 128 ? KVD_R4(128) : D == 256 ? KVD_R4(256) : cudaErrorInvalidValue;
 #undef KVD_R4
 }

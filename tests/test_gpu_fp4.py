@@ -535,3 +535,28 @@ def test_quantize_and_read_few_heads(D, Hkv):
     torch.cuda.synchronize()
     assert int(status.item()) == kvd.STATUS_BAD_PAGE
     assert np.array_equal(out.double().cpu().numpy(), exp)
+
+
+@pytest.mark.parametrize("D,Hkv", [(64, 19), (128, 19), (256, 5), (128, 8)])
+def test_quantize_and_read_few_blocks(D, Hkv):
+    """Few blocks and many heads: several CTAs share a block's heads."""
+    import torch
+    import kv_cache_decode_gb300 as kvd
+    dev = cuda_or_skip()
+    bits = _rows(np.random.default_rng(D + Hkv), (3, 64, Hkv, D), 12.0)
+    lens = np.array([64, 0, 23], np.int32)
+    blocks = torch.full((3, Hkv, 4, 9 * D + 16), 0x5a, dtype=torch.uint8, device=dev)
+    ld = torch.from_numpy(lens).to(dev)
+    kvd.kv_quantize_fp4(to_dev_bf16(bits, dev), blocks, ld, 64)
+    out = torch.full((3, 64, Hkv, D), 3.0, dtype=torch.bfloat16, device=dev)
+    kvd.kv_read_fp4(blocks, out, ld, 64)
+    torch.cuda.synchronize()
+    want, rows = _blocks(bits)
+    old = [a.copy() for a in oracle.unpack_fp4(np.full((3, Hkv, 4, 9 * D + 16), 0x5a, np.uint8), D)]
+    exp = np.full((3, 64, Hkv, D), 3.0)
+    for b in range(3):
+        for o, n in zip(old, oracle.unpack_fp4(want, D)):
+            o[b, :, :lens[b]] = n[b, :, :lens[b]]
+        exp[b, :lens[b]] = rows[b, :lens[b]]
+    assert np.array_equal(blocks.cpu().numpy(), oracle.pack_fp4(*old))
+    assert np.array_equal(out.double().cpu().numpy(), exp)
