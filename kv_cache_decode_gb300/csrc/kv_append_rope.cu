@@ -11,8 +11,8 @@
 // threads as in rope.cuh; where the cache is quantized these threads find the row's (and,
 // fp4, the 16 columns') largest magnitude by shuffles, so a row goes from its
 // load to its codes in registers. Measured: 24 prompts of up to 4,096 tokens, 32 query and 8 KV heads of 128, into
-// bf16 pages: 185 us (1.21 GB, 6.5 of 6.8 TB/s copied); a persistent loop over the tokens took 280. One token of each of
-// 64 sequences: 3.9 us, where the rotation of as many query rows alone takes 2.7.
+// bf16 pages: 187 us (1.21 GB, 6.4 of 6.8 TB/s copied); a persistent loop over the tokens took 280. One token of each of
+// 64 sequences: 3.5 us, where the rotation of as many query rows alone takes 2.3.
 #include <algorithm>
 
 #include "../../include/kvdecode.h"
