@@ -998,6 +998,8 @@ def _whole(t, dtype, dev, ndim):
 
 
 def _rope_on(rope, dev, what):
+    if rope.__class__ is RopeTable and rope._device == dev:
+        return rope._ref
     if not isinstance(rope, RopeTable):
         raise TypeError(f"{what}: rope must be a RopeTable")
     if rope._device != dev:
@@ -1031,11 +1033,15 @@ def _rows(t, name, what):
     if len(s) == 3:
         N, H, D = s
         step, inner, last = st
+        if last == 1 and inner == D and N > 1 and H:  # the usual rows, at once
+            return N, H, D, step
         even = True
     elif len(s) == 4:
         B, T, H, D = s
         N = B * T
         outer, step, inner, last = st
+        if last == 1 and inner == D and T > 1 and outer == T * step and N and H:
+            return N, H, D, step
         if T <= 1:
             step = outer
         even = B <= 1 or T <= 1 or outer == T * step
@@ -1050,6 +1056,14 @@ def _rows(t, name, what):
     return N, H, D, step if N > 1 else H * D
 
 
+def _alike(t, name, what, N, H, D):
+    """Elements between the rows of t, which has as many rows, heads and columns."""
+    n, h, d, step = _rows(t, name, what)
+    if n != N or h != H or d != D:
+        raise ValueError(f"{what}: inconsistent shapes")
+    return step
+
+
 def rope_apply(rope: RopeTable, x, positions, out, stream=None):
     """out = x's rows turned by their positions: x, out [N, H, D] or [B, T, H, D],
     bf16 or fp32 each, rows evenly spaced (slices of a fused projection may be
@@ -1058,17 +1072,18 @@ def rope_apply(rope: RopeTable, x, positions, out, stream=None):
     what, bf, f32 = "rope_apply", torch.bfloat16, torch.float32
     try:
         dev = x.get_device()
-        xc, oc = x.dtype is f32, out.dtype is f32
-        ok = (_is(x, f32 if xc else bf, dev) and _is(out, f32 if oc else bf, dev) and _is(positions, torch.int32, dev)
-              and positions.is_contiguous())
+        xt, ot = x.dtype, out.dtype
+        xc, oc = xt is f32, ot is f32
+        ok = (dev >= 0 and (xc or xt is bf) and (oc or ot is bf) and out.get_device() == dev
+              and positions.dtype is torch.int32 and positions.get_device() == dev and positions.is_contiguous())
     except AttributeError:
         ok = False
     if not ok:
         _explain(what, (x, "x", (bf, f32), None), (out, "out", (bf, f32), None), (positions, "positions", (torch.int32,), None))
         raise ValueError(f"{what}: positions must be contiguous")
     N, H, D, xs = _rows(x, "x", what)
-    No, Ho, Do, ys = _rows(out, "out", what)
-    if No != N or Ho != H or Do != D or positions.numel() != N:
+    ys = xs if out is x else _alike(out, "out", what, N, H, D)
+    if positions.numel() != N:
         raise ValueError(f"{what}: inconsistent shapes")
     ref = _rope_on(rope, dev, what)
     if N == 0:
@@ -1083,8 +1098,9 @@ def _append_rows(what, rope, q, q_out, k_new, v_new, pos, row_offsets, dev, torc
     if (q is None) != (q_out is None):
         raise ValueError(f"{what}: q and q_out go together")
     try:
-        ok = (_is(k_new, bf, dev) and _is(v_new, bf, dev) and _whole(pos, i32, dev, 1)
-              and (q is None or (_is(q, bf, dev) and _is(q_out, bf, dev)))
+        ok = (dev >= 0 and k_new.dtype is bf and k_new.get_device() == dev and v_new.dtype is bf and v_new.get_device() == dev
+              and pos.dtype is i32 and pos.get_device() == dev and pos.dim() == 1 and pos.is_contiguous()
+              and (q is None or (q.dtype is bf and q.get_device() == dev and q_out.dtype is bf and q_out.get_device() == dev))
               and (row_offsets is None or _whole(row_offsets, i32, dev, 1)))
     except AttributeError:
         ok = False
@@ -1093,10 +1109,8 @@ def _append_rows(what, rope, q, q_out, k_new, v_new, pos, row_offsets, dev, torc
                  (q_out, "q_out", (bf,), None), (row_offsets, "row_offsets", (i32,), 1))
         raise ValueError(f"{what}: the new rows are on cuda:{pos.get_device()}, the cache on cuda:{dev}")
     N, Hkv, D, ks = _rows(k_new, "k_new", what)
-    Nv, Hv, Dv, vs = _rows(v_new, "v_new", what)
+    vs = _alike(v_new, "v_new", what, N, Hkv, D)
     B = pos.numel()
-    if Nv != N or Hv != Hkv or Dv != D:
-        raise ValueError(f"{what}: inconsistent shapes")
     if row_offsets is not None:
         if row_offsets.numel() != B + 1:
             raise ValueError(f"{what}: row_offsets must be [batch + 1]")
@@ -1113,8 +1127,8 @@ def _append_rows(what, rope, q, q_out, k_new, v_new, pos, row_offsets, dev, torc
         if rope is None:
             raise ValueError(f"{what}: q needs a rope")
         Nq, Hq, Dq, qs = _rows(q, "q", what)
-        No, Ho, Do, os_ = _rows(q_out, "q_out", what)
-        if Nq != N or Dq != D or No != N or Ho != Hq or Do != D:
+        os_ = qs if q_out is q else _alike(q_out, "q_out", what, N, Hq, D)
+        if Nq != N or Dq != D:
             raise ValueError(f"{what}: inconsistent shapes")
         qp, op = q.data_ptr(), q_out.data_ptr()
     return B, N, Hkv, D, (ref, qp, qs, op, os_, k_new.data_ptr(), ks, v_new.data_ptr(), vs, pos.data_ptr(), off, B, N, Hq,
@@ -1147,7 +1161,8 @@ def kv_append_rope(rope: RopeTable, k, v, k_new, v_new, pos, *, q=None, q_out=No
     dts = (torch.int8, torch.uint8, torch.float8_e4m3fn) if quant else (bf,)
     try:
         dev, dt = k.get_device(), k.dtype
-        ok = (dt in dts and _whole(k, dt, dev, 4) and _whole(v, dt, dev, 4)
+        ok = (dev >= 0 and (dt is bf if not quant else dt in dts) and k.dim() == 4 and k.is_contiguous()
+              and v.dtype is dt and v.get_device() == dev and v.is_contiguous()
               and (block_table is None or _whole(block_table, i32, dev, 2))
               and (not quant or (_whole(k_scales, f32, dev, 3) and _whole(v_scales, f32, dev, 3))))
     except AttributeError:
@@ -1177,7 +1192,7 @@ def kv_append_rope(rope: RopeTable, k, v, k_new, v_new, pos, *, q=None, q_out=No
     if N == 0:
         return
     _launch((_lib or load()).kvd_kv_append_rope, "kvd_kv_append_rope", dev, stream, c, *args,
-            _status_ptr(status, dev, what, torch))
+            None if status is None else _status_ptr(status, dev, what, torch))
 
 
 def fp4_block_bytes(head_dim: int) -> int:
@@ -1203,7 +1218,8 @@ def _fp4_cache(what, k, v, D, B, block_table, torch):
     u8, i32 = torch.uint8, torch.int32
     try:
         dev = k.get_device()
-        ok = (_whole(k, u8, dev, 4) and (v is None or _whole(v, u8, dev, 4))
+        ok = (dev >= 0 and k.dtype is u8 and k.dim() == 4 and k.is_contiguous()
+              and (v is None or (v.dtype is u8 and v.get_device() == dev and v.is_contiguous()))
               and (block_table is None or _whole(block_table, i32, dev, 2)))
     except AttributeError:
         ok = False
@@ -1246,7 +1262,7 @@ def kv_append_fp4(k, v, k_new, v_new, pos, *, rope: Optional[RopeTable] = None, 
     if N == 0:
         return
     _launch((_lib or load()).kvd_kv_append_fp4, "kvd_kv_append_fp4", dev, stream, c, *args,
-            _status_ptr(status, dev, what, torch))
+            None if status is None else _status_ptr(status, dev, what, torch))
 
 
 def _bf16_rows_and_lens(what, cache, name, seq_lens, torch):
@@ -1254,7 +1270,8 @@ def _bf16_rows_and_lens(what, cache, name, seq_lens, torch):
     bf, i32 = torch.bfloat16, torch.int32
     try:
         dev = cache.get_device()
-        ok = _whole(cache, bf, dev, 4) and _whole(seq_lens, i32, dev, 1)
+        ok = (dev >= 0 and cache.dtype is bf and cache.dim() == 4 and cache.is_contiguous()
+              and seq_lens.dtype is i32 and seq_lens.get_device() == dev and seq_lens.dim() == 1 and seq_lens.is_contiguous())
     except AttributeError:
         ok = False
     if not ok:
@@ -1301,7 +1318,8 @@ def kv_read_fp4(blocks, out, seq_lens, max_seq_len: int, block_table=None, statu
     else:
         table = (block_table.data_ptr(), 0, block_table.shape[1], 16 * blocks.shape[2], blocks.shape[0])
     _launch((_lib or load()).kvd_kv_read_fp4, "kvd_kv_read_fp4", dev, stream, blocks.data_ptr(), *table, out.data_ptr(), S,
-            seq_lens.data_ptr(), B, int(max_seq_len), Hkv, D, _status_ptr(status, dev, what, torch))
+            seq_lens.data_ptr(), B, int(max_seq_len), Hkv, D,
+            None if status is None else _status_ptr(status, dev, what, torch))
 
 
 def decode_plan_fp4(batch: int, n_tokens: int, n_heads_q: int, n_heads_kv: int, head_dim: int, max_seq_len: int,
@@ -1324,9 +1342,11 @@ def decode_fp4(q, k, v, seq_lens, max_seq_len: int, scale: float, out, *, block_
     what, bf, i32, f32 = "decode_fp4", torch.bfloat16, torch.int32, torch.float32
     try:
         dev = q.get_device()
-        f32_out = out.dtype is f32
-        ok = (_is(q, bf, dev) and _is(out, f32 if f32_out else bf, dev) and _whole(seq_lens, i32, dev, 1)
-              and q.is_contiguous() and out.is_contiguous()
+        ot = out.dtype
+        f32_out = ot is f32
+        ok = (dev >= 0 and q.dtype is bf and q.is_contiguous() and (f32_out or ot is bf) and out.get_device() == dev
+              and out.is_contiguous() and seq_lens.dtype is i32 and seq_lens.get_device() == dev and seq_lens.dim() == 1
+              and seq_lens.is_contiguous()
               and (lse is None or (_is(lse, f32, dev) and lse.is_contiguous()))
               and (workspace is None or (workspace.get_device() == dev and workspace.is_contiguous())))
     except AttributeError:
@@ -1367,4 +1387,4 @@ def decode_fp4(q, k, v, seq_lens, max_seq_len: int, scale: float, out, *, block_
     _launch((_lib or load()).kvd_decode_fp4, "kvd_decode_fp4", dev, stream, c, q.data_ptr(), seq_lens.data_ptr(), B, T,
             int(max_seq_len), Hq, Hkv, D, float(scale), int(n_split), wp, wb, out.data_ptr(),
             OUT_F32 if f32_out else OUT_BF16, None if lse is None else lse.data_ptr(), kp, vp, pp,
-            _status_ptr(status, dev, what, torch))
+            None if status is None else _status_ptr(status, dev, what, torch))
