@@ -560,3 +560,31 @@ def test_quantize_and_read_few_blocks(D, Hkv):
         exp[b, :lens[b]] = rows[b, :lens[b]]
     assert np.array_equal(blocks.cpu().numpy(), oracle.pack_fp4(*old))
     assert np.array_equal(out.double().cpu().numpy(), exp)
+
+
+def test_two_graphs_share_a_workspace():
+    """Two captured calls of different shapes over one workspace, replayed in turn with new lengths and queries in place."""
+    import torch
+    import kv_cache_decode_gb300 as kvd
+    dev = cuda_or_skip()
+    cases = [Case(41, 16, 2, 128, [300, 0, 129], dev=dev), Case(42, 48, 1, 256, [900, 17], page=16, dev=dev)]
+    need = max(kvd.decode_plan_fp4(c.B, 1, c.Hq, c.Hkv, c.D, c.S)[1] for c in cases)
+    ws = torch.full((need,), 0xa5, dtype=torch.uint8, device=dev)
+    outs = [torch.empty(c.B, c.Hq, c.D, device=dev) for c in cases]
+    graphs = []
+    for c, o in zip(cases, outs):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            kvd.decode_fp4(c.qd[:, 0], c.k, c.v, c.lens_d, c.S, c.scale, o, block_table=c.bt, workspace=ws)
+        graphs.append(g)
+    for shrink in (0, 1, 5):
+        for c in cases:
+            c.lens = np.maximum(c.lens - shrink, 0).astype(np.int32)
+            c.lens_d.copy_(torch.from_numpy(c.lens))
+            c.qd.copy_(c.qd.flip(2))
+            c.q = np.ascontiguousarray(c.q[:, :, ::-1])
+        for g in graphs + graphs[::-1]:
+            g.replay()
+        torch.cuda.synchronize()
+        for c, o in zip(cases, outs):
+            assert_close(o.cpu().numpy().astype(np.float64), c.want()[0][:, 0], "f32", "graph")
