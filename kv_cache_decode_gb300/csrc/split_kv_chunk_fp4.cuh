@@ -604,8 +604,9 @@ __global__ void __launch_bounds__(Fp4Shape<D, NT, F32OUT>::THREADS, Fp4Shape<D, 
                 for (int x = 0; x < TB; ++x)
 #pragma unroll
                     for (int y = 0; y < 2; ++y) {
-                        const float2 v = mul2(mul2(make_float2(s[x][j][2 * y], s[x][j][2 * y + 1]), make_float2(kf[x][y], kf[x][y])),
-                                              make_float2(q0, q1));
+                        // The two factors first: neither the row's exponent nor the query's alone takes a score out of range.
+                        const float2 v = mul2(make_float2(s[x][j][2 * y], s[x][j][2 * y + 1]),
+                                              mul2(make_float2(kf[x][y], kf[x][y]), make_float2(q0, q1)));
                         s[x][j][2 * y] = v.x;
                         s[x][j][2 * y + 1] = v.y;
                     }

@@ -588,3 +588,20 @@ def test_two_graphs_share_a_workspace():
         torch.cuda.synchronize()
         for c, o in zip(cases, outs):
             assert_close(o.cpu().numpy().astype(np.float64), c.want()[0][:, 0], "f32", "graph")
+
+
+@pytest.mark.parametrize("up", [124, -126])
+@pytest.mark.parametrize("Hq,Hkv,D", [(8, 2, 128), (24, 1, 64), (48, 1, 256)])
+def test_keys_at_the_ends_of_the_range(Hq, Hkv, D, up):
+    """Keys near the largest and the smallest bf16 numbers with queries as far the other way: ordinary scores."""
+    import torch
+    import kv_cache_decode_gb300 as kvd
+    dev = cuda_or_skip()
+    c = Case(61, Hq, Hkv, D, [200, 333], dev=dev)
+    x = bf16_bits_to_f32(_rows(np.random.default_rng(7), (c.B, c.S, Hkv, D)))
+    kb, c.kd = _blocks(f32_to_bf16_bits((np.clip(x, -3.5, 3.5).astype(np.float64) * 2.0 ** up).astype(np.float32)))
+    c.k = torch.from_numpy(_poison(kb, c.lens, D)).to(dev)
+    c.q = f32_to_bf16_bits((np.clip(bf16_bits_to_f32(c.q), -3.5, 3.5).astype(np.float64) * 2.0 ** -up).astype(np.float32))
+    c.qd = to_dev_bf16(c.q, dev)
+    for dtype in ("f32", "bf16"):
+        c.check(kvd, torch, dev, dtype)
