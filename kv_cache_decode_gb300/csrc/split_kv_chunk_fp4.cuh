@@ -149,6 +149,9 @@ constexpr float kNoMax = -3e38f;  // running maximum before any score
 // How far (in powers of two) a score may pass its running maximum: a weight of 2^15 is still an f16 (the largest is
 // 65504), and one of 2^-14 of the maximum a normal one. Raising costs up to a fifth of a tile's time.
 constexpr float kRoom = 15.f;
+// 2^(x / 2), to be multiplied in twice: an output's factor 2^(mo - M) may lie below the smallest float where the output,
+// of V rows near that, does not.
+__device__ __forceinline__ float half_ex2(float x) { return tc::ex2_approx(0.5f * x); }
 // Integers ordered as the floats they stand for.
 __device__ __forceinline__ int float_order(float f) {
     const int i = __float_as_int(f);
@@ -878,9 +881,9 @@ __global__ void __launch_bounds__(Fp4Shape<D, NT, F32OUT>::THREADS, Fp4Shape<D, 
 #pragma unroll
                 for (int w = 0; w < NW; ++w) {
                     L += s_l[w][row] * tc::ex2_approx(s_ml[w][row] - M);
-                    const float m = s_mo[w][row], g = m > kNoMax ? tc::ex2_approx(m - M) : 0.f;
+                    const float m = s_mo[w][row], g = m > kNoMax ? half_ex2(m - M) : 0.f;
                     const float4 e = *reinterpret_cast<const float4*>(s_merge + (w * ROWS + row) * Sh::LD + col);
-                    f = make_float4(f.x + g * e.x, f.y + g * e.y, f.z + g * e.z, f.w + g * e.w);
+                    f = make_float4(f.x + g * e.x * g, f.y + g * e.y * g, f.z + g * e.z * g, f.w + g * e.w * g);
                 }
                 if (ct.full) {
                     const size_t orow = out_row(ct.b, ct.h, rbase + row);
@@ -912,11 +915,11 @@ __global__ void __launch_bounds__(Fp4Shape<D, NT, F32OUT>::THREADS, Fp4Shape<D, 
 #pragma unroll
                 for (int z = 0; z < 2; ++z) {
                     const float M = float_unorder(s_max[8 * j + 2 * c4 + z]);
-                    const float f = mo[j][z] > kNoMax ? tc::ex2_approx(mo[j][z] - M) : 0.f;
+                    const float f = mo[j][z] > kNoMax ? half_ex2(mo[j][z] - M) : 0.f;
 #pragma unroll
                     for (int i = 0; i < MT; ++i) {
-                        o[i][j][z] *= f;
-                        o[i][j][2 + z] *= f;
+                        o[i][j][z] = o[i][j][z] * f * f;
+                        o[i][j][2 + z] = o[i][j][2 + z] * f * f;
                     }
                     float sum = l[j][z] * tc::ex2_approx(ms[j][z] - M);
 #pragma unroll

@@ -605,3 +605,24 @@ def test_keys_at_the_ends_of_the_range(Hq, Hkv, D, up):
     c.qd = to_dev_bf16(c.q, dev)
     for dtype in ("f32", "bf16"):
         c.check(kvd, torch, dev, dtype)
+
+
+@pytest.mark.parametrize("up", [-118, 100])
+@pytest.mark.parametrize("Hq,Hkv,D", [(8, 2, 128), (40, 1, 64), (24, 1, 128), (48, 1, 256)])
+def test_values_at_the_ends_of_the_range(Hq, Hkv, D, up):
+    """V rows near the smallest and far towards the largest numbers: outputs as exact, relative to their terms, as of ordinary
+    rows (test_magnitudes' bounds; below 2^-126 half a step of bf16 is 2^-134, of fp32 2^-150)."""
+    import torch
+    import kv_cache_decode_gb300 as kvd
+    dev = cuda_or_skip()
+    c = Case(71, Hq, Hkv, D, [300, 17, 500], dev=dev)
+    x = bf16_bits_to_f32(_rows(np.random.default_rng(8), (c.B, c.S, Hkv, D))).astype(np.float64)
+    vb, c.vd = _blocks(f32_to_bf16_bits((x * 2.0 ** up).astype(np.float32)))
+    c.v = torch.from_numpy(_poison(vb, c.lens, D)).to(dev)
+    want, _ = c.want()
+    mag, _ = oracle.decode_attention_f64kv(c.q[:, 0], c.kd, np.abs(c.vd), c.lens, c.scale)
+    for n_split in (0, 1, 5):
+        got, _ = c.run(kvd, torch, dev, "f32", n_split=n_split)
+        assert (np.abs(got[:, 0] - want[:, 0]) <= 1e-4 * mag + 2.0 ** -148).all()
+        got, _ = c.run(kvd, torch, dev, "bf16", n_split=n_split)
+        assert (np.abs(got[:, 0] - want[:, 0]) <= (1e-4 + 2.0 ** -10) * mag + np.abs(want[:, 0]) * 2.0 ** -8 + 2.0 ** -134).all()
