@@ -593,8 +593,10 @@ kvd_status kvd_kv_append_fp4(const kvd_cache_fp4* cache, const kvd_rope* rope, c
  * (k_new, v_new [batch, n_tokens, n_heads_kv, head_dim] and pos, no rotation) or
  * without it (all three NULL). The cache rows enter the products exactly (a
  * code times its scale fits f16), q is taken to f16 relative to its row's
- * largest element, the softmax weights are rounded to f16 (fp32 output: carried
- * to ~2^-22 as two f16 values), sums and statistics are fp32.
+ * largest element, sums and statistics are fp32. The softmax weights, each with its V row's power of two, are
+ * f16: off by 2^-12 of themselves, or by 2^-37 of the largest of their run where they are below 2^-25 of that; fp32 output
+ * carries a second f16 part: 2^-22 of themselves, or 2^-48 of the largest. So n weights far below one large weight leave an
+ * output off by at most n * 2^-37 (2^-48) of the largest term.
  * kvd_decode_plan_fp4 gives the split count and the workspace, as
  * kvd_decode_plan_multi does for the other caches (the fp4 kernel has its own
  * launch shape, so the two are not interchangeable).

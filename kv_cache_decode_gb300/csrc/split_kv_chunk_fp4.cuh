@@ -6,8 +6,10 @@
 // scale has at most 6 significant bits and enters the MMAs as f16 exactly; the
 // row exponents stay out of them: ek_t multiplies the score, and ev_t is added
 // to the exponent of the weight, w_t = 2^(s_t + ev_t - mo) with a running
-// maximum mo of its own, so that the f16 weights never leave f16's range
-// however the rows' magnitudes differ.
+// reference mo of its own, 12 to 15 below the largest s_t + ev_t, so that the f16 weights lie in the upper part of
+// f16's range. A weight is off by 2^-12 of itself, or, 2^-26 of the largest and less, by up to 2^-37 of the largest. For
+// fp32 output a second f16 holds 2^11 times the rest and meets A times 2^-11 (still exact: a code times its
+// scale is a multiple of 2^-10): 2^-22 of the weight, or 2^-48 of the largest.
 //
 // The products are turned round so that tokens fill the 16 rows of m16n8k16 MMAs
 // and the query rows its 8 columns: S^T = K q^T (A = K rows, B = q) and
@@ -146,9 +148,13 @@ __device__ __forceinline__ uint32_t nib(uint32_t a, uint32_t b) {
 }
 
 constexpr float kNoMax = -3e38f;  // running maximum before any score
-// How far (in powers of two) a score may pass its running maximum: a weight of 2^15 is still an f16 (the largest is
-// 65504), and one of 2^-14 of the maximum a normal one. Raising costs up to a fifth of a tile's time.
+// How far (in powers of two) a score may pass its running maximum, and a weight's exponent its reference mo: 2^15 is still
+// an f16 (the largest is 65504). Raising costs up to a fifth of a tile's time.
 constexpr float kRoom = 15.f;
+// Where mo is put when it is raised: so far below the largest exponent. What f16 has below its normal numbers' 2^-14 is lost to light
+// weights, which the sum of the weights holds in 32 bits: 65,536 tokens of 2^-25 of the largest weight each were left out
+// of the output when mo was put at the maximum itself.
+constexpr float kLift = 12.f;
 // 2^(x / 2), to be multiplied in twice: an output's factor 2^(mo - M) may lie below the smallest float where the output,
 // of V rows near that, does not.
 __device__ __forceinline__ float half_ex2(float x) { return tc::ex2_approx(0.5f * x); }
@@ -734,7 +740,7 @@ __global__ void __launch_bounds__(Fp4Shape<D, NT, F32OUT>::THREADS, Fp4Shape<D, 
                 for (int j = 0; j < NT; ++j)
 #pragma unroll
                     for (int z = 0; z < 2; ++z) {
-                        const float no = fmaxf(mo[j][z], ho[j][z]);
+                        const float no = fmaxf(mo[j][z], ho[j][z] - kLift);
                         const float f = tc::ex2_approx(mo[j][z] - no);
                         mo[j][z] = no;
 #pragma unroll
@@ -746,7 +752,7 @@ __global__ void __launch_bounds__(Fp4Shape<D, NT, F32OUT>::THREADS, Fp4Shape<D, 
             }
 
             // ---- weights, as B fragments ----
-            constexpr int PL = F32OUT ? 2 : 1;  // f16 parts of a weight
+            constexpr int PL = F32OUT ? 2 : 1;  // f16 parts of a weight, the second times 2^11
             uint2 wf[WD == 1 ? TB : 1][NT][PL];
             uint2* s_p = reinterpret_cast<uint2*>(s_merge) + group * (GB * NT * PL * 32) + lane;
 #pragma unroll
@@ -764,7 +770,7 @@ __global__ void __launch_bounds__(Fp4Shape<D, NT, F32OUT>::THREADS, Fp4Shape<D, 
                         const float wv[2] = {tc::ex2_approx(b.x), tc::ex2_approx(b.y)};
                         const uint32_t h = pack_f16x2(wv[0], wv[1]);
                         hi[y] = movmatrix_trans(h);
-                        if constexpr (F32OUT) lo[y] = movmatrix_trans(pack_f16x2(wv[0] - f16_lo(h), wv[1] - f16_hi(h)));
+                        if constexpr (F32OUT) lo[y] = movmatrix_trans(pack_f16x2(2048.f * (wv[0] - f16_lo(h)), 2048.f * (wv[1] - f16_hi(h))));
                     }
                     if constexpr (WD == 1) {
                         wf[x][j][0] = make_uint2(hi[0], hi[1]);
@@ -812,9 +818,13 @@ __global__ void __launch_bounds__(Fp4Shape<D, NT, F32OUT>::THREADS, Fp4Shape<D, 
                                                    hmul2(od1[i], sc[1])};
                             const int m = (g * VW + v) * 4 + i;
 #pragma unroll
-                            for (int j = 0; j < NT; ++j)
+                            for (int j = 0; j < NT; ++j) mma_free(o[m][j], a, wx[j][0].x, wx[j][0].y);
+                            if constexpr (F32OUT) {
+                                const uint32_t r = 0x10001000u;  // 2^-11, twice
+                                const uint32_t a1[4] = {hmul2(a[0], r), hmul2(a[1], r), hmul2(a[2], r), hmul2(a[3], r)};
 #pragma unroll
-                                for (int k = 0; k < PL; ++k) mma_free(o[m][j], a, wx[j][k].x, wx[j][k].y);
+                                for (int j = 0; j < NT; ++j) mma_free(o[m][j], a1, wx[j][1].x, wx[j][1].y);
+                            }
                         }
                     }
                 }

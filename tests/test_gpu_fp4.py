@@ -590,6 +590,80 @@ def test_two_graphs_share_a_workspace():
             assert_close(o.cpu().numpy().astype(np.float64), c.want()[0][:, 0], "f32", "graph")
 
 
+@pytest.mark.parametrize("gap", [23.6, 25.4, 31.0])
+@pytest.mark.parametrize("rows,D", [(8, 64), (40, 64), (8, 128), (24, 128), (8, 256), (48, 256)])
+def test_many_light_tokens_beside_heavy_ones(rows, D, gap):
+    """16 tokens, one in each of the first 16 blocks, score `gap` powers of two above n like ones and have V rows of
+    one value in the first column, so that an output in the others is the light tokens' share of the sum times their V row.
+
+    Tolerance, relative to that: a weight of 2^-g of the heaviest term, g = gap, is off by 2^-12 or an absolute 2^-37 of that
+    term (bf16 output), 2^-22 or 2^-48 of it (fp32 output); scores of 32 at most are off by 2^-22 of themselves in all
+    (three roundings and scale * log2(e)). An output is summed from n / 16 / groups products of 16 tokens, twice that for fp32
+    output, where the 8 / WD groups are 2 at the least, each sum cut to 24 bits (2^-23, all terms of one sign); the weights' sum from n / 64 to
+    a thread, each rounded (2^-24). bf16 outputs half a step, 2^-8."""
+    import torch
+    import kv_cache_decode_gb300 as kvd
+    dev = cuda_or_skip()
+    n = 1 << 16
+    k, v = np.zeros((2, 16, D), np.float32), np.ones((2, 16, D), np.float32)
+    v *= 1.0 + np.arange(D, dtype=np.float32) / D
+    k[0, 0, 0], v[0, 0, 1:] = 1.0, 0.0
+    kc, vc = (oracle.quantize_fp4(f32_to_bf16_bits(x)) for x in (k, v))
+    kb, vb = (oracle.pack_fp4(*x)[:, 0] for x in (kc, vc))
+    kd, vd = (oracle.dequantize_fp4(*x) for x in (kc, vc))
+    scale = float(np.float32(D ** -0.5))
+    q = np.zeros((1, rows, D), np.float32)
+    q[..., 0] = gap * math.log(2) / (scale * kd[0, 0, 0])
+    q = f32_to_bf16_bits(q)
+    g = scale * float(bf16_bits_to_f32(q)[0, 0, 0]) * kd[0, 0, 0]  # nats
+    light = n - 16
+    share = light / (16 * math.exp(g) + light)
+    want = share * vd[1, 1, 1:]
+    octaves = g / math.log(2)
+    kt, vt = _tiled(kb[0], kb[1], n, dev), _tiled(vb[0], vb[1], n, dev)
+    lens = torch.tensor([n], dtype=torch.int32, device=dev)
+    for n_split in (1, 0):
+        _, nb = kvd.decode_plan_fp4(1, 1, rows, 1, D, n, 0, n_split)
+        ws = torch.empty(max(nb, 1), dtype=torch.uint8, device=dev)
+        for dt, parts, tol in ((torch.bfloat16, 1, max(2.0 ** -12, 2.0 ** (octaves - 37)) + 2.0 ** -8),
+                               (torch.float32, 2, max(2.0 ** -22, 2.0 ** (octaves - 48)))):
+            tol += 2.0 ** -22 * 32 + parts * n / 32 * 2.0 ** -23 + n / 64 * 2.0 ** -24
+            out, lse = torch.empty(1, rows, D, dtype=dt, device=dev), torch.empty(1, rows, device=dev)
+            kvd.decode_fp4(to_dev_bf16(q, dev), kt, vt, lens, n, scale, out, workspace=ws, n_split=n_split, lse=lse)
+            torch.cuda.synchronize()
+            rel = np.abs(out[0, :, 1:].double().cpu().numpy() / want - 1).max()
+            assert rel <= tol, (n_split, dt, rel, tol)
+            assert np.abs(lse.cpu().numpy() - math.log(16 * math.exp(g) + light)).max() < 1e-4
+
+
+@pytest.mark.parametrize("Hq,Hkv,D", [(8, 2, 128), (40, 1, 64), (24, 1, 128), (48, 1, 256)])
+def test_one_large_value(Hq, Hkv, D):
+    """A token whose V row is 2^16 in one column and zero elsewhere takes no bits from the other tokens' weights: their
+    terms, 2^-15 of its in V's exponent and 2^-11 at the least in the scores, stay above 2^-26 of the largest, so the other
+    columns are as exact as ever (test_magnitudes' bounds, relative to the terms that make up an output)."""
+    import torch
+    import kv_cache_decode_gb300 as kvd
+    dev = cuda_or_skip()
+    c = Case(51, Hq, Hkv, D, [300, 417], dev=dev)
+    r = np.random.default_rng(6)
+    v = bf16_bits_to_f32(_rows(r, (c.B, c.S, Hkv, D))).copy()
+    v[:, 3::40] = 0
+    v[:, 3::40, :, 5] = 2.0 ** 16
+    vb, c.vd = _blocks(f32_to_bf16_bits(v))
+    c.v = torch.from_numpy(_poison(vb, c.lens, D)).to(dev)
+    other = np.arange(D) != 5
+    want, wl = c.want()
+    mag, _ = oracle.decode_attention_f64kv(c.q[:, 0], c.kd, np.abs(c.vd), c.lens, c.scale)
+    for n_split in (0, 1):
+        got, lse = c.run(kvd, torch, dev, "f32", n_split=n_split)
+        err = np.abs(got[:, 0] - want[:, 0])
+        assert (err <= 1e-4 * mag).all(), (err / mag).max()
+        assert np.abs(lse - wl).max() < 1e-4
+        got, _ = c.run(kvd, torch, dev, "bf16", n_split=n_split)
+        err = np.abs(got[:, 0] - want[:, 0]) - np.abs(want[:, 0]) * 2.0 ** -8
+        assert (err <= (1e-4 + 2.0 ** -11) * mag).all(), (err / mag)[..., other].max()
+
+
 @pytest.mark.parametrize("up", [124, -126])
 @pytest.mark.parametrize("Hq,Hkv,D", [(8, 2, 128), (24, 1, 64), (48, 1, 256)])
 def test_keys_at_the_ends_of_the_range(Hq, Hkv, D, up):
