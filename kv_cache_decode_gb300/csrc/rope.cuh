@@ -4,8 +4,9 @@
 // A pair's frequency is given in turns per position as a fraction of 2^64, so
 // position * turns modulo 2^64 (an integer product that wraps) is the exact
 // fraction of a turn: no argument reduction is left to floating point, at any
-// position. The top 32 bits, signed, are then the angle in units of pi / 2^31;
-// rounding them to float32's 24 bits moves it by at most pi * 2^-25 = 9.4e-8.
+// position. Its nearest quarter turn is taken off too, as an integer; only what is left, at most pi / 4, becomes a
+// float32, which moves the angle by at most pi * 2^-27 = 2.4e-8 (of a half turn rounded whole it was up to 9.4e-8, the
+// larger part of the error of a cosine or sine).
 #pragma once
 
 #include <algorithm>
@@ -15,13 +16,27 @@
 
 namespace kvd {
 
-// factor * (cos, sin) of the pair's angle at position t.
+// factor * (cos, sin) of the pair's angle at position t. Within half a quarter turn of zero two short
+// polynomials in u = x^2 do: interpolations of sin(pi x) / x and (cos(pi x) - 1) / u at the four Chebyshev nodes of
+// [0, 1/16], pi as a float and what that lacks. Both stay within 1 unit in the last place (2 million x compared with
+// 64 bits). The error of a cosine or sine is 1.7e-8 RMS. 500,000 bf16 rows of one head of 128 take 57 us; sincospif of the angle
+// rounded whole took 66, with an error of 3.3e-8; sincospif behind the quarter turn 74. The step of 64 rows of 32 heads takes
+// 2.45 us and took 2.35.
 __device__ __forceinline__ float2 rope_cos_sin(long long t, uint64_t turns, float factor) {
     const uint64_t phase = (uint64_t)t * turns;
-    const float half_turns = (float)(int32_t)(phase >> 32) * 4.656612873077393e-10f;  // 2^-31: [-1, 1]
-    float s, c;
-    sincospif(half_turns, &s, &c);
-    return make_float2(__fmul_rn(factor, c), __fmul_rn(factor, s));
+    const uint32_t near = (uint32_t)(phase >> 32) + 0x20000000u;  // the nearest quarter turn in the top two bits
+    const float x = (float)(int32_t)(uint32_t)(phase >> 30) * 1.1641532182693481e-10f;  // 2^-33: half turns, [-1/4, 1/4]
+    const float u = __fmul_rn(x, x);
+    float s = __fmaf_rn(u, -0.5890751f, 2.549767f);
+    s = __fmaf_rn(__fmaf_rn(s, u, -5.167708f), u, -9.71061e-8f);
+    s = __fmaf_rn(x, 3.1415927f, __fmul_rn(x, s));
+    float c = __fmaf_rn(u, 0.23212542f, -1.3351378f);
+    c = __fmaf_rn(__fmaf_rn(c, u, 4.0587106f), u, -4.934802f);
+    c = __fmaf_rn(c, u, 1.f);
+    const bool odd = near & 0x40000000u;
+    const uint32_t a = __float_as_uint(odd ? s : c), b = __float_as_uint(odd ? c : s);
+    return make_float2(__fmul_rn(factor, __uint_as_float(a ^ ((near + 0x40000000u) & 0x80000000u))),
+                       __fmul_rn(factor, __uint_as_float(b ^ (near & 0x80000000u))));
 }
 
 // A head's columns are dealt out to threads in units of two vectors of 8
@@ -165,6 +180,7 @@ struct RopeWarp {
         R = rope.turns ? rope.rotary_dim : 0;
         interleaved = rope.interleaved;
         s_cs = buf;
+#pragma unroll 1  // (4 at most: unrolled it is 0.1 us slower for a few tokens)
         for (int i = lane; i < R >> 1; i += 32) rope_table_put(buf, i, rope_cos_sin(t, __ldg(rope.turns + i), rope.factor));
         __syncwarp();
         if constexpr (DD > 0) {

@@ -457,3 +457,39 @@ def test_append_many_short_rows(form, D, R, Hq, Hkv, page):
         torch.cuda.synchronize()
         for n in t:
             assert torch.equal(t[n], t2[n]), n
+
+
+@pytest.mark.parametrize("inter", [False, True])
+def test_cosines_and_sines(inter):
+    """(a, b) = (1, 0) gives an angle's cosine and sine. The nearest quarter turn is taken off in integers, and what is left, x of at most
+    1/4 in units of pi, is rounded to 24 bits: the angle is off by pi * 2^-27 at most (near the middle of a quarter
+    turn by far less). The cosine 1 + u q(u), u = x^2 <= 1/16, |q| < 4.94: the sum's rounding 2^-25, q's and its first
+    coefficient's 2^-22 each times u, u's own 2^-24 of u q < 0.31: 2^-25 + 2^-25 + 0.31 * 2^-24 + 2e-9 (the interpolation) < 8.1e-8. The
+    sine x pi + x (...): the sum's 2^-24 of itself, the second term, below 0.08, 2^-22 of itself and the interpolation 2e-9 of x: 5 * 2^-24 of itself in all.
+    Near a sine's or cosine's zero the small one of the two is that sine, and must be as exact relative to itself but for the angle."""
+    import torch
+    import kv_cache_decode_gb300 as kvd
+    dev = cuda_or_skip()
+    N, D = 200_000, 64
+    rope = kvd.RopeTable(D, interleaved=inter, device=dev)
+    turns = rope.turns.cpu().numpy().view(np.uint64)
+    pos = torch.randint(-2 ** 31, 2 ** 31 - 1, (N,), device=dev, generator=torch.Generator(device=dev).manual_seed(1)).int()
+    pos[:3] = torch.tensor([0, 1, -1], dtype=torch.int32)
+    x = torch.zeros(N, 1, D, device=dev)
+    ia, ib = (slice(0, D, 2), slice(1, D, 2)) if inter else (slice(0, D // 2), slice(D // 2, D))
+    x[..., ia] = 1.0
+    out = torch.empty_like(x)
+    kvd.rope_apply(rope, x, pos, out)
+    torch.cuda.synchronize()
+    phase = (pos.cpu().numpy().astype(np.int64).view(np.uint64)[:, None] * turns[None]).view(np.int64)  # wraps
+    half = phase.astype(np.float64) / 2.0 ** 63  # in units of pi, [-1, 1)
+    near = np.where(half > 0, half - 1.0, half + 1.0)  # sin(pi half) = -sin(pi near)
+    got = out[:, 0].double().cpu().numpy()
+    sin = np.where(np.abs(half) > 0.5, -np.sin(np.pi * near), np.sin(np.pi * half))
+    assert (got[0, ia] == 1).all() and (got[0, ib] == 0).all()
+    for name, g, want, small in (("sin", got[:, ib], sin, np.abs(near) < 2.0 ** -6),
+                                 ("cos", got[:, ia], np.cos(np.pi * half), np.abs(np.abs(half) - 0.5) < 2.0 ** -6)):
+        err = np.abs(g - want)
+        assert err.max() <= np.pi * 2.0 ** -27 + 8.1e-8, (name, err.max())
+        tol = (np.pi * 2.0 ** -27 + np.abs(want) * 5 * 2.0 ** -24)[small]
+        assert small.sum() > 10_000 and (err[small] <= tol).all(), (name, int((err[small] > tol).sum()), float(err[small].max()))
