@@ -1064,10 +1064,17 @@ def _alike(t, name, what, N, H, D):
     return step
 
 
+def _same_batch(what, *shapes):
+    """Refuses [B, T] shapes of as many rows that are not alike; one with a 1 in it is the rows in order."""
+    two = {tuple(s) for s in shapes if len(s) == 2 and 1 not in s}
+    if len(two) > 1:
+        raise ValueError(f"{what}: inconsistent shapes")
+
+
 def rope_apply(rope: RopeTable, x, positions, out, stream=None):
     """out = x's rows turned by their positions: x, out [N, H, D] or [B, T, H, D],
     bf16 or fp32 each, rows evenly spaced (slices of a fused projection may be
-    passed as they are); positions int32, one a row. out may be x."""
+    passed as they are); positions int32, one a row: [N] or [B, T]. out may be x."""
     torch = _torch or _import_torch()
     what, bf, f32 = "rope_apply", torch.bfloat16, torch.float32
     try:
@@ -1085,6 +1092,8 @@ def rope_apply(rope: RopeTable, x, positions, out, stream=None):
     ys = xs if out is x else _alike(out, "out", what, N, H, D)
     if positions.numel() != N:
         raise ValueError(f"{what}: inconsistent shapes")
+    if positions.dim() > 1 or (out is not x and x.dim() == 4):
+        _same_batch(what, positions.shape, x.shape[:-2], out.shape[:-2])
     ref = _rope_on(rope, dev, what)
     if N == 0:
         return
@@ -1111,14 +1120,19 @@ def _append_rows(what, rope, q, q_out, k_new, v_new, pos, row_offsets, dev, torc
     N, Hkv, D, ks = _rows(k_new, "k_new", what)
     vs = _alike(v_new, "v_new", what, N, Hkv, D)
     B = pos.numel()
+    lead = B  # the first of four dimensions
     if row_offsets is not None:
         if row_offsets.numel() != B + 1:
             raise ValueError(f"{what}: row_offsets must be [batch + 1]")
-        off = row_offsets.data_ptr()
+        off, lead = row_offsets.data_ptr(), 1
     else:
         if (N % B if B else N):
             raise ValueError(f"{what}: {N} new rows for {B} sequences")
         off = None
+    if ((k_new.dim() == 4 and k_new.shape[0] != lead) or (v_new.dim() == 4 and v_new.shape[0] != lead)
+            or (q is not None and ((q.dim() == 4 and q.shape[0] != lead) or (q_out.dim() == 4 and q_out.shape[0] != lead)))):
+        raise ValueError(f"{what}: new rows must be [batch, T, H, D]" if row_offsets is None
+                         else f"{what}: rows with row_offsets must be packed, [N, H, D]")
     ref = None if rope is None else _rope_on(rope, dev, what)
     if q is None:
         qp = op = None
@@ -1148,7 +1162,7 @@ def kv_append_rope(rope: RopeTable, k, v, k_new, v_new, pos, *, q=None, q_out=No
     """New rows into a cache as decode_ex takes it (k, v contiguous [B, S_max, Hkv,
     D], or pools with block_table; bf16, or 8-bit codes with scales), keys
     turned by their positions, and q turned into q_out (kvd_kv_append_rope).
-    k_new, v_new, q: [B, Hkv, D] or [B, T, H, D] at pos[b] + i, or with row_offsets
+    k_new, v_new, q: [B, T, H, D] or [B * T, H, D] at pos[b] + i, or with row_offsets
     int32 [B + 1] the packed rows [N, H, D] of prompts of any lengths; rows evenly
     spaced, so slices of a fused projection may be passed as they are."""
     torch = _torch or _import_torch()

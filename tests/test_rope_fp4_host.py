@@ -373,3 +373,83 @@ def test_plan_fp4_short_sequences(lib):
         n, _ = kvd.decode_plan_fp4(B, T, Hq, Hkv, D, L, num_sms=152)
         assert min(B * Hkv, 152) <= n <= B * Hkv
     assert kvd.decode_plan_fp4(5, 1, 8, 1, 128, 0, num_sms=152)[0] == 1
+
+
+# ---------------------------------------------------------------------------
+# shapes, before any launch: CPU tensors that say they lie on a device
+# ---------------------------------------------------------------------------
+
+@pytest.fixture
+def on_device(monkeypatch):
+    """(a maker of tensors, the list of launches): nothing is launched, the call's name is noted."""
+    import torch
+
+    class There(torch.Tensor):
+        def get_device(self):
+            return 0
+
+    made, launched = [], []
+
+    def make(*shape, dtype=torch.bfloat16):
+        made.append(torch.zeros(*shape, dtype=dtype).as_subclass(There))
+        return made[-1]
+    monkeypatch.setattr(kvd, "_launch", lambda fn, what, dev, stream, *args: launched.append(what))
+    monkeypatch.setattr(kvd, "_rope_on", lambda rope, dev, what: rope._ref)
+    return make, launched
+
+
+def _append_call(make, form, **shapes):
+    import torch
+    B, Hq, Hkv, D, S = 3, 4, 2, 64, 32
+    a = dict(k_new=(B, 4, Hkv, D), v_new=(B, 4, Hkv, D), q=(B, 4, Hq, D), q_out=(B, 4, Hq, D), offsets=None)
+    a.update(shapes)
+    kw = dict(q=make(*a["q"]) if a["q"] else None, q_out=make(*a["q_out"]) if a["q"] else None,
+              row_offsets=None if a["offsets"] is None else make(B + 1, dtype=torch.int32))
+    args = make(*a["k_new"]), make(*a["v_new"]), make(B, dtype=torch.int32)
+    rope = kvd.RopeTable(64, device="cpu")
+    if form == "fp4":
+        kvd.kv_append_fp4(*(make(B, Hkv, S // 16, 9 * D + 16, dtype=torch.uint8) for _ in range(2)), *args, rope=rope, **kw)
+    else:
+        kvd.kv_append_rope(rope, *(make(B, S, Hkv, D) for _ in range(2)), *args, **kw)
+
+
+@pytest.mark.parametrize("form", ["bf16", "fp4"])
+def test_new_rows_of_another_batch_are_refused(lib, on_device, form):
+    """[T, B, H, D] where [B, T, H, D] is asked has as many rows, but they are other sequences'."""
+    make, launched = on_device
+    flat = dict(k_new=(12, 2, 64), v_new=(12, 2, 64), q=(12, 4, 64), q_out=(12, 4, 64))
+    _append_call(make, form)
+    _append_call(make, form, q=None)
+    _append_call(make, form, **flat)                                  # packed rows, 4 to a sequence
+    _append_call(make, form, offsets=True, **flat)
+    _append_call(make, form, offsets=True, **{n: (1,) + s for n, s in flat.items()})
+    _append_call(make, form, k_new=(3, 2, 64), v_new=(3, 1, 2, 64), q=(3, 1, 4, 64), q_out=(3, 4, 64))
+    assert len(launched) == 6
+    for name in ("k_new", "v_new", "q", "q_out"):
+        heads = 4 if name in ("q", "q_out") else 2
+        for lead in ((4, 3), (2, 6), (1, 12), (12, 1)):
+            with pytest.raises(ValueError):
+                _append_call(make, form, **{name: lead + (heads, 64)})
+        with pytest.raises(ValueError):
+            _append_call(make, form, offsets=True, **{**flat, name: (3, 4, heads, 64)})
+    assert len(launched) == 6
+
+
+def test_positions_and_results_of_another_shape_are_refused(lib, on_device):
+    import torch
+    make, launched = on_device
+    r = kvd.RopeTable(64, device="cpu")
+
+    def call(x, pos, out):
+        kvd.rope_apply(r, make(*x), make(*pos, dtype=torch.int32), make(*out))
+    right = [((3, 4, 2, 64), (3, 4), (3, 4, 2, 64)), ((3, 4, 2, 64), (12,), (3, 4, 2, 64)), ((12, 2, 64), (12,), (12, 2, 64)),
+             ((12, 2, 64), (3, 4), (3, 4, 2, 64)), ((3, 4, 2, 64), (3, 4), (12, 2, 64)),
+             ((3, 4, 2, 64), (12, 1), (1, 12, 2, 64))]  # (a one is no batch: the rows in order)
+    for x, pos, out in right:
+        call(x, pos, out)
+    assert len(launched) == len(right)
+    for x, pos, out in (((3, 4, 2, 64), (4, 3), (3, 4, 2, 64)), ((3, 4, 2, 64), (3, 4), (4, 3, 2, 64)),
+                        ((12, 2, 64), (4, 3), (3, 4, 2, 64)), ((3, 4, 2, 64), (12,), (2, 6, 2, 64)), ((12, 2, 64), (11,), (12, 2, 64))):
+        with pytest.raises(ValueError):
+            call(x, pos, out)
+    assert len(launched) == len(right)
