@@ -952,8 +952,8 @@ class RopeTable:
 
 _torch = None
 _raw_stream = _current_device = None
-_pack_cache = struct.Struct("PPPPPiiiii").pack   # struct kvd_cache
-_pack_fp4 = struct.Struct("PPPiiii").pack        # struct kvd_cache_fp4
+_pack_cache = struct.Struct("PPPPPiiiii0P").pack   # struct kvd_cache (0P: padded to its full size)
+_pack_fp4 = struct.Struct("PPPiiii0P").pack        # struct kvd_cache_fp4
 
 
 def _import_torch():

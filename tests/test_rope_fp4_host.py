@@ -453,3 +453,14 @@ def test_positions_and_results_of_another_shape_are_refused(lib, on_device):
         with pytest.raises(ValueError):
             call(x, pos, out)
     assert len(launched) == len(right)
+
+
+def test_packed_structs_are_the_declared_ones():
+    """The bytes that the calls send are the C structs', field by field and to their full size."""
+    for pack, struct_type in ((kvd._pack_cache, kvd._CCache), (kvd._pack_fp4, kvd._CCacheFp4)):
+        n = len(struct_type._fields_)
+        for values in ([0x1111111111111111 * (i + 1) if t is ctypes.c_void_p else 0x01020304 * (i + 1)
+                        for i, (_, t) in enumerate(struct_type._fields_)], [0] * n):
+            s = struct_type(*values)
+            assert len(pack(*values)) == ctypes.sizeof(s)
+            assert pack(*values) == bytes(s)
