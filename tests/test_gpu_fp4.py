@@ -590,6 +590,13 @@ def test_two_graphs_share_a_workspace():
             assert_close(o.cpu().numpy().astype(np.float64), c.want()[0][:, 0], "f32", "graph")
 
 
+def _tiled(first, rest, n, dev):
+    """Blocks [1, 1, n / 16, ...]: 16 of `first`, then `rest`."""
+    import torch
+    f, r = (torch.from_numpy(x).to(dev) for x in (first, rest))
+    return torch.cat([f.expand(16, -1), r.expand(n // 16 - 16, -1)]).contiguous()[None, None]
+
+
 @pytest.mark.parametrize("gap", [23.6, 25.4, 31.0])
 @pytest.mark.parametrize("rows,D", [(8, 64), (40, 64), (8, 128), (24, 128), (8, 256), (48, 256)])
 def test_many_light_tokens_beside_heavy_ones(rows, D, gap):
@@ -700,3 +707,60 @@ def test_values_at_the_ends_of_the_range(Hq, Hkv, D, up):
         assert (np.abs(got[:, 0] - want[:, 0]) <= 1e-4 * mag + 2.0 ** -148).all()
         got, _ = c.run(kvd, torch, dev, "bf16", n_split=n_split)
         assert (np.abs(got[:, 0] - want[:, 0]) <= (1e-4 + 2.0 ** -10) * mag + np.abs(want[:, 0]) * 2.0 ** -8 + 2.0 ** -134).all()
+
+
+@pytest.mark.parametrize("Hq,Hkv,D,T,page", [(8, 1, 128, 1, 0), (32, 8, 128, 5, 16), (48, 1, 256, 1, 64), (40, 2, 64, 1, 16)])
+def test_repeats_itself(Hq, Hkv, D, T, page):
+    """The same call gives the same bits, whatever the workspace held."""
+    import torch
+    import kv_cache_decode_gb300 as kvd
+    dev = cuda_or_skip()
+    c = Case(81, Hq, Hkv, D, [2300, 1, 700, 4001], T=T, page=page, dev=dev)
+    _, n = kvd.decode_plan_fp4(c.B, T, Hq, Hkv, D, c.S)
+    for dt in (torch.bfloat16, torch.float32):
+        first = None
+        for i in range(20):
+            ws = torch.full((n + 1,), 17 * i % 256, dtype=torch.uint8, device=dev)
+            out, lse = torch.empty(c.B, T, Hq, D, dtype=dt, device=dev), torch.empty(c.B, T, Hq, device=dev)
+            kvd.decode_fp4(c.qd, c.k, c.v, c.lens_d, c.S, c.scale, out, block_table=c.bt, workspace=ws, lse=lse)
+            torch.cuda.synchronize()
+            if first is None:
+                first = out, lse
+            assert torch.equal(out, first[0]) and torch.equal(lse, first[1])
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_quantizers_at_the_ends_of_the_range(D):
+    """Rows from below the smallest row exponent to the largest numbers, rows of one large and otherwise tiny blocks of 16 columns: the
+    bulk quantizer and the append give the oracle's bytes, and the reader the values, where bf16 holds them."""
+    import torch
+    import kv_cache_decode_gb300 as kvd
+    dev = cuda_or_skip()
+    r = np.random.default_rng(D)
+    B, S, Hkv = 2, 272, 3
+    x = r.uniform(-1, 1, (B, S, Hkv, D))
+    x *= np.exp2(np.linspace(-133, 127.9, S))[None, :, None, None]
+    tiny = np.exp2(r.integers(-24, 1, (S, D // 16)).astype(np.float64)).repeat(16, -1)
+    x[1] *= tiny[:, None, :]
+    x[1, :, :, :16] *= 1.0 / tiny[:, None, :16]  # the first block keeps the row's size
+    bits = f32_to_bf16_bits(x.astype(np.float32))
+    assert (np.abs(bf16_bits_to_f32(bits)) < np.inf).all()
+    want, rows = _blocks(bits)
+    xd, lens = to_dev_bf16(bits, dev), torch.full((B,), S, dtype=torch.int32, device=dev)
+    blocks = kvd.alloc_cache_fp4(B, Hkv, D, S, device=dev)
+    kvd.kv_quantize_fp4(xd, blocks, lens, S)
+    k, v = (kvd.alloc_cache_fp4(B, Hkv, D, S, device=dev) for _ in range(2))
+    kvd.kv_append_fp4(k, v, xd, xd, torch.zeros(B, dtype=torch.int32, device=dev))
+    k1, v1 = (kvd.alloc_cache_fp4(B, Hkv, D, S, device=dev) for _ in range(2))
+    for t in range(S):  # a token at a time takes the other kernel
+        kvd.kv_append_fp4(k1, v1, xd[:, t], xd[:, t], torch.full((B,), t, dtype=torch.int32, device=dev))
+    out = torch.empty(B, S, Hkv, D, dtype=torch.bfloat16, device=dev)
+    kvd.kv_read_fp4(blocks, out, lens, S)
+    torch.cuda.synchronize()
+    for got in (blocks, k, v, k1, v1):
+        g = got.cpu().numpy()
+        if not np.array_equal(g, want):
+            a, b = oracle.unpack_fp4(g, D), oracle.unpack_fp4(want, D)
+            raise AssertionError([np.argwhere(p != q)[:5].tolist() for p, q in zip(a, b)])
+    held = bf16_bits_to_f32(f32_to_bf16_bits(np.where(np.abs(rows) < 3.3e38, rows, 0.0).astype(np.float32))).astype(np.float64) == rows
+    assert held.mean() > 0.9 and np.array_equal(out.double().cpu().numpy()[held], rows[held])
