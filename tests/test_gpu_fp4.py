@@ -764,3 +764,28 @@ def test_quantizers_at_the_ends_of_the_range(D):
             raise AssertionError([np.argwhere(p != q)[:5].tolist() for p, q in zip(a, b)])
     held = bf16_bits_to_f32(f32_to_bf16_bits(np.where(np.abs(rows) < 3.3e38, rows, 0.0).astype(np.float32))).astype(np.float64) == rows
     assert held.mean() > 0.9 and np.array_equal(out.double().cpu().numpy()[held], rows[held])
+
+
+@pytest.mark.parametrize("Hq,Hkv,D", [(4, 2, 64), (24, 1, 128)])
+def test_more_sequences_than_threads(Hq, Hkv, D):
+    """A thread of the schedule's scan takes several sequences, many of them empty."""
+    import torch
+    import kv_cache_decode_gb300 as kvd
+    dev = cuda_or_skip()
+    r = np.random.default_rng(9)
+    lens = r.integers(0, 49, 1000) * (r.random(1000) < 0.6)
+    lens[[0, 1, 500, 999]] = [0, 0, 300, 0]
+    c = Case(91, Hq, Hkv, D, lens.tolist(), dev=dev)
+    for n in (0, 1, 151, 3000):
+        c.check(kvd, torch, dev, "f32", n_split=n)
+    c.check(kvd, torch, dev, "bf16")
+
+
+@pytest.mark.parametrize("Hq,Hkv,D,T", [(8, 2, 128, 1), (48, 1, 256, 1), (6, 3, 64, 4)])
+def test_pages_longer_than_a_tile(Hq, Hkv, D, T):
+    import torch
+    import kv_cache_decode_gb300 as kvd
+    dev = cuda_or_skip()
+    c = Case(95, Hq, Hkv, D, [1100, 0, 511, 512, 513, T], T=T, page=512, dev=dev)
+    c.check(kvd, torch, dev, "f32")
+    c.check(kvd, torch, dev, "bf16", n_split=7)
