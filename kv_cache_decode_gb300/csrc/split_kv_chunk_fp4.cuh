@@ -42,10 +42,10 @@
 // score passes them by 2^15. At a segment's end the warps' states are merged through shared memory.
 //
 // Measured: 128 sequences of 1,024 to 8,192 tokens, 32 query and 8 KV heads of 128: 144 us (691 MB, 4.8 of 6.8 TB/s
-// copied; an instruction issues in 61 % of the cycles, the waits between are of many kinds). 64 sequences of 2,048, 48 query heads
-// on one KV head of 256: 38 us, 5.5 for the first tile to arrive, 6.5 a tile of 256 tokens (3.2 of it the MMAs alone), 4 a merge. 9
-// sequences of up to 4,001 with 5 drafted tokens, 32 and 8 heads of 128: 23 us. 12 or 16 working warps in place of 8 (with
-// 152 or 112 registers) took 23.6 and 26 us there, tiles of half the size 25, a schedule formed by the loading warp alone as long.
+// copied; an instruction issues in 62 % of the cycles, the waits between are of many kinds). 64 sequences of 2,048, 48 query heads
+// on one KV head of 256: 38.6 us, 5.5 for the first tile to arrive, 6.5 a tile of 256 tokens (3.2 of it the MMAs alone), 4 a merge. 9
+// sequences of up to 4,001 with 5 drafted tokens, 32 and 8 heads of 128: 23.3 us. 12 or 16 working warps in place of 8 (with
+// 152 or 112 registers) took 0.5 and 3 us more there, tiles of half the size 2, a schedule formed by the loading warp alone as long.
 #pragma once
 
 #include "fp4.cuh"
@@ -77,7 +77,7 @@ struct Fp4Shape {
     static constexpr int LD = D + 4;             // merge buffer row, floats
     static constexpr int RING = 2 * STAGES * STAGE;  // K stages, then V stages
     // With 8 query rows and warps that work alone every warp's state has room beside the rings, and one barrier stands
-    // between them and the joined rows: 64 sequences of 500 to 1,500 tokens, 40 heads of 128, 102.7 us instead of 107.9.
+    // between them and the joined rows: 64 sequences of 500 to 1,500 tokens, 40 heads of 128, take 103.6 us, about 5 less than without.
     static constexpr bool FLAT = WD == 1 && NT == 1;
     static constexpr int MBUF = FLAT ? GROUPS : GROUPS / 2;          // merge buffers: the upper half of the groups hands over to the lower
     static constexpr int MERGE = MBUF * ROWS * LD * 4;
@@ -85,7 +85,7 @@ struct Fp4Shape {
     static constexpr int SHARED = MERGE > PBYTES ? MERGE : PBYTES;  // weights, and at a segment's end the merge
     static constexpr int QBYTES = QREG ? 0 : KS * NT * 32 * 8;
     static constexpr int SMEM = RING + SHARED + QBYTES;
-    static constexpr int STATIC = 4096 + (FLAT ? 3 : 2) * NW * ROWS * 4 + 28 * ROWS;  // an upper bound of the static arrays
+    static constexpr int STATIC = 4096 + (FLAT ? 3 : 2) * NW * ROWS * 4 + (QREG ? 28 + 4 * NW : 32) * ROWS;  // an upper bound of the static arrays
     static constexpr int MINB = (ACC <= 32 && 2 * (SMEM + STATIC + 1024) <= 228 * 1024) ? 2 : 1;
     // The loading warp is a ninth; a CTA alone on its SM launches a warpgroup for it, whose
     // registers the working warps then take (168 a thread at launch, 232 and 40 after: 2 * 232 + 40 = 3 * 168).
@@ -153,7 +153,8 @@ constexpr float kNoMax = -3e38f;  // running maximum before any score
 constexpr float kRoom = 15.f;
 // Where mo is put when it is raised: so far below the largest exponent. What f16 has below its normal numbers' 2^-14 is lost to light
 // weights, which the sum of the weights holds in 32 bits: 65,536 tokens of 2^-25 of the largest weight each were left out
-// of the output when mo was put at the maximum itself.
+// of the output when mo was put at the maximum itself. Maxima are raised more often so: 0.8 % of the grouped-query
+// case above, 0.5 % with 10 and 0.4 % with 8.
 constexpr float kLift = 12.f;
 // 2^(x / 2), to be multiplied in twice: an output's factor 2^(mo - M) may lie below the smallest float where the output,
 // of V rows near that, does not.
@@ -214,6 +215,7 @@ __global__ void __launch_bounds__(Fp4Shape<D, NT, F32OUT>::THREADS, Fp4Shape<D, 
     __shared__ int s_b0, s_abort;
     __shared__ __align__(8) float s_ml[NW][ROWS], s_l[NW][ROWS];  // running maxima and sums; s_ml also carries raised maxima
     __shared__ float s_qs[ROWS], s_inv[ROWS];
+    __shared__ __align__(8) float s_qfar[Sh::QREG ? NW : 1][ROWS];  // the rest of the queries' factors above 2^10, else 1
     __shared__ float s_mo[Sh::FLAT ? NW : 1][ROWS];  // running maxima of the outputs
     __shared__ int s_max[ROWS];  // a segment's maxima, as ordered integers
     __shared__ long long s_dst[ROWS];
@@ -474,7 +476,10 @@ __global__ void __launch_bounds__(Fp4Shape<D, NT, F32OUT>::THREADS, Fp4Shape<D, 
                 dst[(2 * k) * stride] = make_uint2(y[0], y[1]);
                 dst[(2 * k + 1) * stride] = make_uint2(y[2], y[3]);
             }
-            return fabsf(p.scale_log2) * __uint_as_float(eb << 23);
+            // A factor above 2^10 goes in apart, behind the rest: with the cache row's it could overflow, and a score of zero become a NaN.
+            const float f = fabsf(p.scale_log2) * __uint_as_float(eb << 23);
+            if (c4 == 0) s_qfar[Sh::QREG ? warp : 0][8 * j + r] = f > 1024.f ? f * 9.765625e-4f : 1.f;
+            return fminf(f, 1024.f);
         };
         if constexpr (Sh::QREG) {
 #pragma unroll
@@ -491,6 +496,13 @@ __global__ void __launch_bounds__(Fp4Shape<D, NT, F32OUT>::THREADS, Fp4Shape<D, 
             }
             workers_sync(WORKERS);
         }
+        __syncwarp();
+        bool far = false;  // some query's factor is in two parts
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+            for (int z = 0; z < 2; ++z) far |= s_qfar[Sh::QREG ? warp : 0][8 * j + 2 * c4 + z] != 1.f;
+        far = __any_sync(0xffffffffu, far);
         float o[MT][NT][4];
         float ms[NT][2], mo[NT][2], l[NT][2];  // mo is the group's, ms and l this warp's
 #pragma unroll
@@ -613,7 +625,7 @@ __global__ void __launch_bounds__(Fp4Shape<D, NT, F32OUT>::THREADS, Fp4Shape<D, 
                 for (int x = 0; x < TB; ++x)
 #pragma unroll
                     for (int y = 0; y < 2; ++y) {
-                        // The two factors first: neither the row's exponent nor the query's alone takes a score out of range.
+                        // The two factors first: the row's (up to 2^117) alone may take a score out of range that the query's brings back.
                         const float2 v = mul2(make_float2(s[x][j][2 * y], s[x][j][2 * y + 1]),
                                               mul2(make_float2(kf[x][y], kf[x][y]), make_float2(q0, q1)));
                         s[x][j][2 * y] = v.x;
@@ -624,7 +636,7 @@ __global__ void __launch_bounds__(Fp4Shape<D, NT, F32OUT>::THREADS, Fp4Shape<D, 
             wait_tile(1);
             // Rows past the sequence or without a page hold anything: this warp's V blocks of the tile are put
             // right in shared memory, and scores that a query row does not see masked, so that nothing below has to ask.
-            const bool edge = (tile0 + 16 * GB > ct.L - T + 1) || badm;
+            const bool edge = (tile0 + 16 * GB > ct.L - T + 1) || badm || far;
             if (edge) {
 #pragma unroll 1
                 for (int x = 0; x < TB; ++x)
@@ -637,7 +649,7 @@ __global__ void __launch_bounds__(Fp4Shape<D, NT, F32OUT>::THREADS, Fp4Shape<D, 
 #pragma unroll
                 for (int y = 0; y < 2; ++y)  // the byte b as 2^23 + b, less 2^23 + 127
                     ev[x][y] = __uint_as_float(0x4b000000u | lds<uint8_t>(kb + Sh::RING / 2 + x * BLK + Blk::EXPS + ta + 8 * y)) - 8388735.f;
-            if (edge) {
+            if (edge) {  // (a branch of its own for the large factors cost 1 to 2 % of every case)
 #pragma unroll
                 for (int x = 0; x < TB; ++x)
 #pragma unroll
@@ -645,8 +657,10 @@ __global__ void __launch_bounds__(Fp4Shape<D, NT, F32OUT>::THREADS, Fp4Shape<D, 
 #pragma unroll
                         for (int j = 0; j < NT; ++j)
 #pragma unroll
-                            for (int z = 0; z < 2; ++z)
+                            for (int z = 0; z < 2; ++z) {
+                                s[x][j][2 * y + z] *= s_qfar[Sh::QREG ? warp : 0][8 * j + 2 * c4 + z];
                                 if (tok0 + 16 * x + ta + 8 * y >= ct.L - s_short[8 * j + 2 * c4 + z]) s[x][j][2 * y + z] = -CUDART_INF_F;
+                            }
             }
             bool raise = false;
 #pragma unroll
@@ -820,8 +834,8 @@ __global__ void __launch_bounds__(Fp4Shape<D, NT, F32OUT>::THREADS, Fp4Shape<D, 
 #pragma unroll
                             for (int j = 0; j < NT; ++j) mma_free(o[m][j], a, wx[j][0].x, wx[j][0].y);
                             if constexpr (F32OUT) {
-                                const uint32_t r = 0x10001000u;  // 2^-11, twice
-                                const uint32_t a1[4] = {hmul2(a[0], r), hmul2(a[1], r), hmul2(a[2], r), hmul2(a[3], r)};
+                                const uint32_t cut = 0x10001000u;  // 2^-11, twice
+                                const uint32_t a1[4] = {hmul2(a[0], cut), hmul2(a[1], cut), hmul2(a[2], cut), hmul2(a[3], cut)};
 #pragma unroll
                                 for (int j = 0; j < NT; ++j) mma_free(o[m][j], a1, wx[j][1].x, wx[j][1].y);
                             }

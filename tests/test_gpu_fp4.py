@@ -789,3 +789,23 @@ def test_pages_longer_than_a_tile(Hq, Hkv, D, T):
     c = Case(95, Hq, Hkv, D, [1100, 0, 511, 512, 513, T], T=T, page=512, dev=dev)
     c.check(kvd, torch, dev, "f32")
     c.check(kvd, torch, dev, "bf16", n_split=7)
+
+
+@pytest.mark.parametrize("Hq,Hkv,D", [(8, 2, 128), (24, 1, 64), (48, 1, 256)])
+@pytest.mark.parametrize("kup,qup", [(124, 100), (124, -100), (-124, 100), (-124, -124), (0, 124)])
+def test_keys_that_queries_do_not_meet(Hq, Hkv, D, kup, qup):
+    """Keys in the even columns, queries in the odd ones, however large or small: every score is zero, the output the mean."""
+    import torch
+    import kv_cache_decode_gb300 as kvd
+    dev = cuda_or_skip()
+    c = Case(67, Hq, Hkv, D, [200, 333], dev=dev)
+    x = np.clip(bf16_bits_to_f32(_rows(np.random.default_rng(7), (c.B, c.S, Hkv, D))), -3.5, 3.5).astype(np.float64)
+    x[..., 1::2] = 0
+    kb, c.kd = _blocks(f32_to_bf16_bits((x * 2.0 ** kup).astype(np.float32)))
+    c.k = torch.from_numpy(_poison(kb, c.lens, D)).to(dev)
+    q = np.clip(bf16_bits_to_f32(c.q), -3.5, 3.5).astype(np.float64)
+    q[..., 0::2] = 0
+    c.q = f32_to_bf16_bits((q * 2.0 ** qup).astype(np.float32))
+    c.qd = to_dev_bf16(c.q, dev)
+    for dtype in ("f32", "bf16"):
+        c.check(kvd, torch, dev, dtype)
