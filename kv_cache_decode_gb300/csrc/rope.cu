@@ -6,8 +6,8 @@
 
 namespace kvd {
 
-// Blocks of 4 warps: with 8, 4,099 fp32 rows of 40 x 128 took 33.0 us instead of 31.6, and 65,536 bf16 rows of
-// 32 x 128 157.2 instead of 156.1 (1.07 GB: 6.9 TB/s, the copy rate).
+// Blocks of 4 warps: with 8, 4,099 fp32 rows of 40 x 128 take 33.1 us instead of 30.0, and 65,536 bf16 rows of
+// 32 x 128 160.4 instead of 156.0 (1.07 GB: 6.9 TB/s, the copy rate).
 constexpr int kRopeWarps = 4;
 
 template <bool IN32, bool OUT32, int DD>
@@ -23,9 +23,9 @@ __global__ void __launch_bounds__(kRopeWarps * 32) rope_kernel(const RopeTable r
     rw.template heads<IN32, OUT32>(x, (size_t)row * xs, y, (size_t)row * ys, H, (int)(w - row * parts), parts);
 }
 
-// Rows of at most 32 units (a warp's step): several rows to a warp. 500,000 bf16 rows of one head of 128 (256 MB) take 66 us,
-// by a warp each 247; 200,000 of 4 heads of 64 take 40, by a warp each 92. What is left over the copy's 38 and 30 is
-// the instructions of the cosines and sines, 64 or 32 a row.
+// Rows of at most 32 units (a warp's step): several rows to a warp. 500,000 bf16 rows of one head of 128 (256 MB) take 57 us,
+// by a warp each 219; 200,000 of 4 heads of 64 take 38, by a warp each 88. What is left over the copy's 38 and 30 is in part
+// the instructions of the cosines and sines, 64 or 32 a row: shorter ones took 66 to 57, and 40 to 38.
 template <bool IN32, bool OUT32, bool ONE>
 __global__ void __launch_bounds__(kRopeWarps * 32) rope_rows_kernel(const RopeTable rope, const void* x, long long xs, void* y,
                                                                     long long ys, const int32_t* __restrict__ positions,

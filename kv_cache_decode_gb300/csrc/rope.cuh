@@ -79,7 +79,7 @@ __device__ __forceinline__ void rope_turn(float (&a)[8], float (&b)[8], const fl
 }
 
 // A table of cosines and sines in shared memory, 16-byte chunks of two entries: chunk c lies at c ^ (c / 8 % 4), so that
-// threads with neighbouring units (8 entries each) read from different banks (30,000 rows of 40 heads of 80: 66 us, 74 without).
+// threads with neighbouring units (8 entries each) read from different banks (30,000 rows of 40 heads of 80: 65 us, 75 without).
 __device__ __forceinline__ void rope_table_put(float2* table, int e, const float2& cs) {
     const int c = e >> 1;
     table[2 * (c ^ ((c >> 3) & 3)) + (e & 1)] = cs;
@@ -266,7 +266,7 @@ struct RopeTokens {
         rope_turn(a, b, cs, interleaved);
     }
     // The tokens' rows (ss, ds elements apart), src to dst; ready() forms the table behind the first loads. ONE: rows of one
-    // head, where no thread shares a pair's cosine and sine with another and each forms its own (t as for the table): 66 us instead of 94
+    // head, where no thread shares a pair's cosine and sine with another and each forms its own (t as for the table): 57 us instead of 86
     // for 500,000 rows of 128.
     template <bool IN32, bool OUT32, bool ONE, class F>
     __device__ __forceinline__ void heads(const void* src, size_t se, size_t ss, void* dst, size_t de, size_t ds, int H,

@@ -42,9 +42,9 @@
 // score passes them by 2^15. At a segment's end the warps' states are merged through shared memory.
 //
 // Measured: 128 sequences of 1,024 to 8,192 tokens, 32 query and 8 KV heads of 128: 144 us (691 MB, 4.8 of 6.8 TB/s
-// copied; an instruction issues in 62 % of the cycles, the waits between are of many kinds). 64 sequences of 2,048, 48 query heads
-// on one KV head of 256: 38.6 us, 5.5 for the first tile to arrive, 6.5 a tile of 256 tokens (3.2 of it the MMAs alone), 4 a merge. 9
-// sequences of up to 4,001 with 5 drafted tokens, 32 and 8 heads of 128: 23.3 us. 12 or 16 working warps in place of 8 (with
+// copied; an instruction issues in 61 % of the cycles, the waits between are of many kinds). 64 sequences of 2,048, 48 query heads
+// on one KV head of 256: 38.8 us, 5.5 for the first tile to arrive, 6.5 a tile of 256 tokens (3.2 of it the MMAs alone), 4 a merge. 9
+// sequences of up to 4,001 with 5 drafted tokens, 32 and 8 heads of 128: 23.5 us. 12 or 16 working warps in place of 8 (with
 // 152 or 112 registers) took 0.5 and 3 us more there, tiles of half the size 2, a schedule formed by the loading warp alone as long.
 #pragma once
 
