@@ -27,6 +27,7 @@ STATUS_SEQ_LEN_CLAMPED = 0x1
 STATUS_POS_OUT_OF_RANGE = 0x2
 STATUS_BAD_PAGE = 0x8
 STATUS_UMAX_FALLBACK = 0x10
+STATUS_NO_PAGES = 0x20
 
 # Every symbol include/kvdecode.h declares.
 EXPORTED = (
@@ -40,6 +41,8 @@ EXPORTED = (
     "kvd_kv_quantize_fp8", "kvd_kv_append_fp8", "kvd_kv_append_fp8_paged", "kvd_merge_attention",
     "kvd_probe_read", "kvd_rope_table", "kvd_rope_apply", "kvd_kv_append_rope", "kvd_fp4_block_bytes",
     "kvd_kv_quantize_fp4", "kvd_kv_read_fp4", "kvd_kv_append_fp4", "kvd_decode_plan_fp4", "kvd_decode_fp4",
+    "kvd_pages_update", "kvd_rope_axes_table", "kvd_rope_apply_axes", "kvd_kv_append_axes", "kvd_kv_block_bounds",
+    "kvd_block_select_plan", "kvd_block_select", "kvd_decode_blocks_plan", "kvd_decode_blocks",
 )
 STATIC_WORKSPACE_BYTES = 16 << 20  # KVD_STATIC_WORKSPACE_BYTES
 
@@ -82,6 +85,19 @@ class _CRope(ctypes.Structure):
     """struct kvd_rope of kvdecode.h."""
     _fields_ = [("turns", ctypes.c_void_p), ("factor", ctypes.c_float), ("rotary_dim", ctypes.c_int),
                 ("interleaved", ctypes.c_int)]
+
+
+class _CRopeAxes(ctypes.Structure):
+    """struct kvd_rope_axes of kvdecode.h."""
+    _fields_ = [("turns", ctypes.c_void_p), ("axes", ctypes.c_void_p), ("factor", ctypes.c_float),
+                ("rotary_dim", ctypes.c_int), ("interleaved", ctypes.c_int), ("n_axes", ctypes.c_int)]
+
+
+class _CBlockBounds(ctypes.Structure):
+    """struct kvd_block_bounds of kvdecode.h."""
+    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("block_table", ctypes.c_void_p),
+                ("s_max", ctypes.c_int), ("max_blocks", ctypes.c_int), ("page_size", ctypes.c_int),
+                ("num_pages", ctypes.c_int), ("block_tokens", ctypes.c_int)]
 
 
 class _CCacheFp4(ctypes.Structure):
@@ -171,6 +187,19 @@ def _declare(lib):
     lib.kvd_decode_fp4.argtypes = [P] + lib.kvd_decode_ex.argtypes[1:]
     for name in ("kvd_rope_table", "kvd_rope_apply", "kvd_kv_append_rope", "kvd_kv_append_fp4",
                  "kvd_kv_quantize_fp4", "kvd_kv_read_fp4", "kvd_decode_plan_fp4", "kvd_decode_fp4"):
+        getattr(lib, name).restype = I
+    # page tables, rotary positions of several axes, attention over selected blocks
+    lib.kvd_pages_update.argtypes = [P, P, P, P, P, I, I, I, I, P, P, P, P, LL, P, P]
+    lib.kvd_rope_axes_table.argtypes = [P, I, I, I, DBL, I, DBL, DBL, DBL, DBL, DBL, P, P, ctypes.POINTER(F)]
+    lib.kvd_rope_apply_axes.argtypes = [P, P, LL, I, P, LL, I, P, LL, LL, I, I, P]
+    lib.kvd_kv_append_axes.argtypes = [P, P, P, LL, P, LL, P, LL, P, LL, P, P, LL, I, LL, I, I, I, P, P]
+    lib.kvd_kv_block_bounds.argtypes = [P, P, P, P, I, I, I, I, P, P]
+    lib.kvd_block_select_plan.argtypes = [I, I, I, I, I, PSZ]
+    lib.kvd_block_select.argtypes = [P, P, P, I, I, I, I, I, I, I, I, I, P, SZ, P, P, P]
+    lib.kvd_decode_blocks_plan.argtypes = [I, I, I, I, I, I, I, I, PSZ]
+    lib.kvd_decode_blocks.argtypes = [P, P, P, P, I, I, I, I, I, I, I, F, P, SZ, P, I, P, P, P]
+    for name in ("kvd_pages_update", "kvd_rope_axes_table", "kvd_rope_apply_axes", "kvd_kv_append_axes", "kvd_kv_block_bounds",
+                 "kvd_block_select_plan", "kvd_block_select", "kvd_decode_blocks_plan", "kvd_decode_blocks"):
         getattr(lib, name).restype = I
     lib.kvd_schedule_describe.argtypes = [P, I, I, I, I, I, I, I, I, P, I, PI, PI]
     lib.kvd_kernel_info.argtypes = [I, I, I, I, PI, PI, PI, PI, PI, PI]
@@ -1401,4 +1430,376 @@ def decode_fp4(q, k, v, seq_lens, max_seq_len: int, scale: float, out, *, block_
     _launch((_lib or load()).kvd_decode_fp4, "kvd_decode_fp4", dev, stream, c, q.data_ptr(), seq_lens.data_ptr(), B, T,
             int(max_seq_len), Hq, Hkv, D, float(scale), int(n_split), wp, wb, out.data_ptr(),
             OUT_F32 if f32_out else OUT_BF16, None if lse is None else lse.data_ptr(), kp, vp, pp,
+            None if status is None else _status_ptr(status, dev, what, torch))
+
+
+# ---------------------------------------------------------------------------
+# Page tables, rotary positions of several axes, attention over selected blocks
+# ---------------------------------------------------------------------------
+
+_pack_bounds = struct.Struct("PPPiiiii0P").pack  # struct kvd_block_bounds
+
+
+def pages_update(block_table, free_pages, free_count, seq_lens, new_lens, page_size: int, *, pos=None, row_offsets=None,
+                 slots=None, positions=None, status=None, stream=None):
+    """Every sequence from seq_lens[b] tokens to new_lens[b], pages from the stack of free ones and back to it
+    (kvd_pages_update). int32 on one device: block_table [B, max_blocks], free_pages [num_pages] and free_count [1], and
+    seq_lens [B] are updated; new_lens [B]. Written where given: pos [B] (the lengths before), row_offsets [B + 1],
+    and for the new tokens packed end to end slots [N] and positions [N], -1 behind the last
+    (empty ones are as none)."""
+    torch = _torch or _import_torch()
+    what, i32 = "pages_update", torch.int32
+    try:
+        dev = block_table.get_device()
+        ok = (_whole(block_table, i32, dev, 2) and _whole(free_pages, i32, dev, 1) and _whole(free_count, i32, dev, 1)
+              and _whole(seq_lens, i32, dev, 1) and _whole(new_lens, i32, dev, 1) and (pos is None or _whole(pos, i32, dev, 1))
+              and (row_offsets is None or _whole(row_offsets, i32, dev, 1)) and (slots is None or _whole(slots, i32, dev, 1))
+              and (positions is None or _whole(positions, i32, dev, 1)))
+    except AttributeError:
+        ok = False
+    if not ok:
+        d = (i32,)
+        _explain(what, (block_table, "block_table", d, 2), (free_pages, "free_pages", d, 1), (free_count, "free_count", d, 1),
+                 (seq_lens, "seq_lens", d, 1), (new_lens, "new_lens", d, 1), (pos, "pos", d, 1), (row_offsets, "row_offsets", d, 1),
+                 (slots, "slots", d, 1), (positions, "positions", d, 1))
+        raise TypeError(f"{what}: block_table, free_pages, free_count, seq_lens and new_lens must be tensors")
+    B, max_blocks = block_table.shape
+    n = slots.numel() if slots is not None else positions.numel() if positions is not None else 0
+    if (seq_lens.numel() != B or new_lens.numel() != B or free_count.numel() != 1 or (pos is not None and pos.numel() != B)
+            or (row_offsets is not None and row_offsets.numel() != B + 1) or (positions is not None and positions.numel() != n)):
+        raise ValueError(f"{what}: inconsistent shapes")
+    if B == 0 and row_offsets is None and n == 0:
+        return
+    _launch((_lib or load()).kvd_pages_update, "kvd_pages_update", dev, stream, block_table.data_ptr(), free_pages.data_ptr(),
+            free_count.data_ptr(), seq_lens.data_ptr(), new_lens.data_ptr(), B, max_blocks, int(page_size), free_pages.numel(),
+            None if pos is None else pos.data_ptr(), None if row_offsets is None else row_offsets.data_ptr(),
+            None if slots is None else slots.data_ptr(), None if positions is None else positions.data_ptr(), n,
+            None if status is None else _status_ptr(status, dev, what, torch))
+
+
+def rope_axes_table(sections, base: float = 10000.0, order: str = "blocks", per_axis: bool = False, scaling: str = "none",
+                    factor: float = 1.0, original_len: float = 0.0, slow: Optional[float] = None, fast: Optional[float] = None,
+                    attn_factor: float = 0.0):
+    """(turns, axes, factor) of pairs shared out to axes, sections[a] to axis a (kvd_rope_axes_table): frequencies
+    as rope_table's and the axis of each pair, uint8, both [sum of sections] (numpy, on the host). order "blocks": an
+    axis' pairs are neighbours; "dealt": dealt out in turn. per_axis: frequencies by a pair's index among its axis' own."""
+    if scaling not in ROPE_SCALINGS:
+        raise ValueError(f"scaling must be one of {sorted(ROPE_SCALINGS)}, got {scaling!r}")
+    if order not in ("blocks", "dealt"):
+        raise ValueError(f"order must be 'blocks' or 'dealt', got {order!r}")
+    dslow, dfast = _ROPE_TURNS.get(scaling, (0.0, 0.0))
+    sec = [int(n) for n in sections]
+    room = max(sum(max(n, 0) for n in sec), 1)
+    turns, axes = np.zeros(room, np.uint64), np.zeros(room, np.uint8)
+    out = ctypes.c_float(0.0)
+    _check(load().kvd_rope_axes_table((ctypes.c_int * max(len(sec), 1))(*sec), len(sec), int(order == "dealt"), int(bool(per_axis)),
+                                      float(base), ROPE_SCALINGS[scaling], float(factor), float(original_len),
+                                      float(dslow if slow is None else slow), float(dfast if fast is None else fast),
+                                      float(attn_factor), turns.ctypes.data_as(ctypes.c_void_p),
+                                      axes.ctypes.data_as(ctypes.c_void_p), ctypes.byref(out)), "kvd_rope_axes_table")
+    return turns, axes, out.value
+
+
+class RopeAxes:
+    """Rotary positions of several axes, made once: the tables of rope_axes_table (same arguments) on `device`,
+    adjacent pairs when `interleaved`, else halves. The rotary dimension is twice the sum of sections."""
+
+    def __init__(self, sections, base: float = 10000.0, order: str = "blocks", per_axis: bool = False, scaling: str = "none",
+                 factor: float = 1.0, original_len: float = 0.0, slow: Optional[float] = None, fast: Optional[float] = None,
+                 attn_factor: float = 0.0, interleaved: bool = False, device="cuda"):
+        import torch
+        turns, axes, self.factor = rope_axes_table(sections, base, order, per_axis, scaling, factor, original_len, slow, fast,
+                                                   attn_factor)
+        self.n_axes, self.rotary_dim, self.interleaved = len(sections), 2 * len(axes), bool(interleaved)
+        self.turns = torch.from_numpy(turns.view(np.int64)).to(device)
+        self.axes = torch.from_numpy(axes).to(device)
+        self._device = self.turns.get_device()  # -1 on the CPU
+        self._struct = _CRopeAxes(self.turns.data_ptr(), self.axes.data_ptr(), self.factor, self.rotary_dim,
+                                  1 if self.interleaved else 0, self.n_axes)
+        self._ref = ctypes.byref(self._struct)
+
+
+def _axes_on(rope, dev, what):
+    if not isinstance(rope, RopeAxes):
+        raise TypeError(f"{what}: rope must be a RopeAxes")
+    if rope._device != dev:
+        raise ValueError(f"{what}: the rope table is on {rope.turns.device}, the tensors on cuda:{dev}")
+    return rope._ref
+
+
+def _axis_stride(rope, positions, N, what):
+    """Elements between the axes of positions [axes, N] or [axes, B, T], each axis contiguous."""
+    s, st = positions.shape, positions.stride()
+    if len(s) not in (2, 3) or s[0] != rope.n_axes or positions.numel() != N * rope.n_axes:
+        raise ValueError(f"{what}: positions must be [{rope.n_axes}, {N}] (or [axes, B, T])")
+    if N == 0:
+        return 0
+    if not positions[0].is_contiguous() or (s[0] > 1 and st[0] < N):
+        raise ValueError(f"{what}: each axis of positions must be contiguous")
+    return st[0] if s[0] > 1 else N
+
+
+def rope_apply_axes(rope: RopeAxes, x, positions, out, stream=None):
+    """rope_apply by positions of several axes: positions int32 [axes, N] or [axes, B, T], each axis contiguous
+    (kvd_rope_apply_axes). out may be x."""
+    torch = _torch or _import_torch()
+    what, bf, f32 = "rope_apply_axes", torch.bfloat16, torch.float32
+    try:
+        dev = x.get_device()
+        xt, ot = x.dtype, out.dtype
+        xc, oc = xt is f32, ot is f32
+        ok = (dev >= 0 and (xc or xt is bf) and (oc or ot is bf) and out.get_device() == dev
+              and positions.dtype is torch.int32 and positions.get_device() == dev)
+    except AttributeError:
+        ok = False
+    if not ok:
+        _explain(what, (x, "x", (bf, f32), None), (out, "out", (bf, f32), None), (positions, "positions", (torch.int32,), None))
+        raise TypeError(f"{what}: x, positions and out must be tensors")
+    N, H, D, xs = _rows(x, "x", what)
+    ys = xs if out is x else _alike(out, "out", what, N, H, D)
+    ref = _axes_on(rope, dev, what)
+    step = _axis_stride(rope, positions, N, what)
+    _same_batch(what, positions.shape[1:], x.shape[:-2], out.shape[:-2])
+    if N == 0:
+        return
+    _launch((_lib or load()).kvd_rope_apply_axes, "kvd_rope_apply_axes", dev, stream, ref, x.data_ptr(), xs,
+            OUT_F32 if xc else OUT_BF16, out.data_ptr(), ys, OUT_F32 if oc else OUT_BF16, positions.data_ptr(), step, N, H, D)
+
+
+def kv_append_axes(rope: RopeAxes, k, v, k_new, v_new, slots, positions, *, q=None, q_out=None, k_scales=None, v_scales=None,
+                   paged: bool = True, status=None, stream=None):
+    """New rows into the cache rows that slots names (kvd_kv_append_axes): row n's key, turned by positions[:, n], and
+    value to row slots[n] of k and v, pools [pages, page, Hkv, D] (or, paged False, caches [B, S_max, Hkv, D]; either way slot s is
+    row s % shape[1] of k[s // shape[1]]); bf16, or 8-bit codes with scales; q turned into q_out. k_new,
+    v_new, q: [N, H, D] or [B, T, H, D], rows evenly spaced; slots int32 [N], negative: not stored; positions int32
+    [axes, N]."""
+    torch = _torch or _import_torch()
+    what, bf, i32, f32 = "kv_append_axes", torch.bfloat16, torch.int32, torch.float32
+    if (k_scales is None) != (v_scales is None):
+        raise ValueError(f"{what}: k_scales and v_scales go together")
+    if (q is None) != (q_out is None):
+        raise ValueError(f"{what}: q and q_out go together")
+    quant = k_scales is not None
+    dts = (torch.int8, torch.uint8, torch.float8_e4m3fn) if quant else (bf,)
+    try:
+        dev, dt = k.get_device(), k.dtype
+        ok = (dev >= 0 and (dt is bf if not quant else dt in dts) and k.dim() == 4 and k.is_contiguous()
+              and v.dtype is dt and v.get_device() == dev and v.is_contiguous() and _is(k_new, bf, dev) and _is(v_new, bf, dev)
+              and (q is None or (_is(q, bf, dev) and _is(q_out, bf, dev)))
+              and _is(slots, i32, dev) and slots.is_contiguous() and _is(positions, i32, dev)
+              and (not quant or (_whole(k_scales, f32, dev, 3) and _whole(v_scales, f32, dev, 3))))
+    except AttributeError:
+        ok = False
+    if not ok:
+        _explain(what, (k, "k", dts, 4), (v, "v", dts, 4), (k_new, "k_new", (bf,), None), (v_new, "v_new", (bf,), None),
+                 (q, "q", (bf,), None), (q_out, "q_out", (bf,), None), (slots, "slots", (i32,), None),
+                 (positions, "positions", (i32,), None), (k_scales, "k_scales", (f32,), 3), (v_scales, "v_scales", (f32,), 3))
+        raise TypeError(f"{what}: k and v must be alike, slots contiguous, and no tensor missing")
+    N, Hkv, D, ks = _rows(k_new, "k_new", what)
+    vs = _alike(v_new, "v_new", what, N, Hkv, D)
+    n, cap, heads, width = shape = k.shape
+    if v.shape != shape or heads != Hkv or width != D or slots.numel() != N:
+        raise ValueError(f"{what}: inconsistent shapes")
+    ksp = vsp = fp8 = 0
+    if quant:
+        if k_scales.shape != shape[:3] or v_scales.shape != shape[:3]:
+            raise ValueError(f"{what}: codes [B, S_max, Hkv, D] and scales [B, S_max, Hkv] disagree")
+        ksp, vsp, fp8 = k_scales.data_ptr(), v_scales.data_ptr(), 0 if dt is torch.int8 else 1
+    ref = _axes_on(rope, dev, what)
+    step = _axis_stride(rope, positions, N, what)
+    qp = op = None
+    Hq = qs = os_ = 0
+    if q is not None:
+        Nq, Hq, Dq, qs = _rows(q, "q", what)
+        os_ = qs if q_out is q else _alike(q_out, "q_out", what, N, Hq, D)
+        if Nq != N or Dq != D:
+            raise ValueError(f"{what}: inconsistent shapes")
+        qp, op = q.data_ptr(), q_out.data_ptr()
+    _same_batch(what, positions.shape[1:], slots.shape, k_new.shape[:-2], v_new.shape[:-2],
+                *(() if q is None else (q.shape[:-2], q_out.shape[:-2])))
+    if N == 0 or n == 0:
+        return
+    c = (_pack_cache(k.data_ptr(), v.data_ptr(), ksp, vsp, 0, 0, 0, cap, n, fp8) if paged else
+         _pack_cache(k.data_ptr(), v.data_ptr(), ksp, vsp, 0, cap, 0, 0, 0, fp8))
+    _launch((_lib or load()).kvd_kv_append_axes, "kvd_kv_append_axes", dev, stream, c, ref, qp, qs, op, os_, k_new.data_ptr(), ks,
+            v_new.data_ptr(), vs, slots.data_ptr(), positions.data_ptr(), step, 0 if paged else n, N, Hq, Hkv, D,
+            None if status is None else _status_ptr(status, dev, what, torch))
+
+
+def alloc_block_bounds(k, block_tokens: int):
+    """(codes, scales), zeroed, for the bounds of a cache or pool k [n, tokens, Hkv, D] (kvd_kv_block_bounds)."""
+    import torch
+    n, tokens, Hkv, D = k.shape
+    codes = torch.zeros(n, tokens // int(block_tokens), Hkv, 2, D, dtype=torch.int8, device=k.device)
+    return codes, torch.zeros(codes.shape[:3], dtype=torch.float32, device=k.device)
+
+
+def _bounds(what, codes, scales, block_tokens, B, block_table, torch):
+    """(the packed struct kvd_block_bounds, KV heads, head_dim, blocks a sequence, device)."""
+    i32, f32 = torch.int32, torch.float32
+    try:
+        dev = codes.get_device()
+        ok = (_whole(codes, torch.int8, dev, 5) and _whole(scales, f32, dev, 3)
+              and (block_table is None or _whole(block_table, i32, dev, 2)))
+    except AttributeError:
+        ok = False
+    if not ok:
+        _explain(what, (codes, "codes", (torch.int8,), 5), (scales, "scales", (f32,), 3), (block_table, "block_table", (i32,), 2))
+        raise TypeError(f"{what}: codes and scales must be tensors")
+    n, per, Hkv, two, D = codes.shape
+    if two != 2 or scales.shape != codes.shape[:3]:
+        raise ValueError(f"{what}: codes must be [n, blocks, Hkv, 2, D] and scales [n, blocks, Hkv]")
+    blk = int(block_tokens)
+    if block_table is not None:
+        rows, table = block_table.shape
+        if rows != B:
+            raise ValueError(f"{what}: inconsistent shapes")
+        return (_pack_bounds(codes.data_ptr(), scales.data_ptr(), block_table.data_ptr(), 0, table, per * blk, n, blk), Hkv, D,
+                per * table, dev)
+    if n != B:
+        raise ValueError(f"{what}: inconsistent shapes")
+    return _pack_bounds(codes.data_ptr(), scales.data_ptr(), 0, per * blk, 0, 0, 0, blk), Hkv, D, per, dev
+
+
+def kv_block_bounds(k, codes, scales, seq_lens, max_new: int, block_tokens: int, *, from_lens=None, block_table=None, status=None,
+                    stream=None):
+    """The bounds of the keys of each block of block_tokens tokens that is full at seq_lens[b] and was not at from_lens[b]
+    (None: 0), at most max_new tokens between them (kvd_kv_block_bounds). k bf16 [B, S_max, Hkv, D], or a pool with
+    block_table; codes and scales as alloc_block_bounds makes them."""
+    torch = _torch or _import_torch()
+    what, bf, i32 = "kv_block_bounds", torch.bfloat16, torch.int32
+    try:
+        dev = k.get_device()
+        ok = (_whole(k, bf, dev, 4) and _whole(seq_lens, i32, dev, 1) and (from_lens is None or _whole(from_lens, i32, dev, 1)))
+    except AttributeError:
+        ok = False
+    if not ok:
+        _explain(what, (k, "k", (bf,), 4), (seq_lens, "seq_lens", (i32,), 1), (from_lens, "from_lens", (i32,), 1))
+        raise TypeError(f"{what}: k and seq_lens must be tensors")
+    B = seq_lens.numel()
+    c, Hkv, D, _, on = _bounds(what, codes, scales, block_tokens, B, block_table, torch)
+    n, cap, heads, width = k.shape
+    if on != dev:
+        raise ValueError(f"{what}: k on cuda:{dev}, the bounds on cuda:{on}")
+    if (heads != Hkv or width != D or n != codes.shape[0] or cap // int(block_tokens) != codes.shape[1]
+            or (block_table is not None and cap % int(block_tokens)) or (from_lens is not None and from_lens.numel() != B)):
+        raise ValueError(f"{what}: inconsistent shapes")
+    if block_table is None:
+        c = _pack_bounds(codes.data_ptr(), scales.data_ptr(), 0, cap, 0, 0, 0, int(block_tokens))
+    if B == 0:
+        return
+    _launch((_lib or load()).kvd_kv_block_bounds, "kvd_kv_block_bounds", dev, stream, k.data_ptr(), c,
+            None if from_lens is None else from_lens.data_ptr(), seq_lens.data_ptr(), B, int(max_new), Hkv, D,
+            None if status is None else _status_ptr(status, dev, what, torch))
+
+
+def block_select_plan(batch: int, n_tokens: int, n_heads_kv: int, max_seq_len: int, block_tokens: int) -> int:
+    """Workspace bytes of a block_select call of this shape."""
+    ws = ctypes.c_size_t(0)
+    _check(load().kvd_block_select_plan(int(batch), int(n_tokens), int(n_heads_kv), int(max_seq_len), int(block_tokens),
+                                        ctypes.byref(ws)), "kvd_block_select_plan")
+    return ws.value
+
+
+def block_select(q, codes, scales, seq_lens, max_seq_len: int, block_tokens: int, blocks, *, n_first: int = 1, n_last: int = 2,
+                 block_table=None, workspace=None, status=None, stream=None):
+    """The blocks of the highest scores by their bounds, for every query token and KV head (kvd_block_select): q bf16
+    [B, Hq, D] or [B, T, Hq, D]; blocks int32 [B, Hkv, K] or [B, T, Hkv, K] receives the K kept, ascending, -1 behind the last.
+    The first n_first and the last n_last that a token sees are always kept. Workspace: block_select_plan."""
+    torch = _torch or _import_torch()
+    what, bf, i32 = "block_select", torch.bfloat16, torch.int32
+    try:
+        dev = q.get_device()
+        ok = (dev >= 0 and q.dtype is bf and q.is_contiguous() and _whole(seq_lens, i32, dev, 1) and blocks.dtype is i32
+              and blocks.get_device() == dev and blocks.is_contiguous()
+              and (workspace is None or (workspace.get_device() == dev and workspace.is_contiguous())))
+    except AttributeError:
+        ok = False
+    if not ok:
+        _explain(what, (q, "q", (bf,), None), (seq_lens, "seq_lens", (i32,), 1), (blocks, "blocks", (i32,), None),
+                 (workspace, "workspace", None, None))
+        raise ValueError(f"{what}: q, blocks and workspace must be contiguous tensors")
+    shape = q.shape
+    if len(shape) == 3:
+        (B, Hq, D), T = shape, 1
+    elif len(shape) == 4:
+        B, T, Hq, D = shape
+    else:
+        raise ValueError(f"{what}: q must be [B, Hq, D] or [B, T, Hq, D]")
+    c, Hkv, Dc, _, on = _bounds(what, codes, scales, block_tokens, B, block_table, torch)
+    if on != dev:
+        raise ValueError(f"{what}: q on cuda:{dev}, the bounds on cuda:{on}")
+    if Dc != D or seq_lens.numel() != B or blocks.dim() != len(shape) or blocks.shape[:-1] != shape[:-2] + (Hkv,):
+        raise ValueError(f"{what}: inconsistent shapes")
+    wp, wb = None, 0
+    if workspace is not None:
+        wp, wb = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    if B == 0:
+        return
+    _launch((_lib or load()).kvd_block_select, "kvd_block_select", dev, stream, c, q.data_ptr(), seq_lens.data_ptr(), B, T,
+            int(max_seq_len), blocks.shape[-1], int(n_first), int(n_last), Hq, Hkv, D, wp, wb, blocks.data_ptr(),
+            None if status is None else _status_ptr(status, dev, what, torch))
+
+
+def decode_blocks_plan(batch: int, n_tokens: int, n_heads_q: int, n_heads_kv: int, head_dim: int, n_blocks: int, block_tokens: int,
+                       num_sms: int = 0) -> int:
+    """Workspace bytes of a decode_blocks call of this shape (often 0)."""
+    ws = ctypes.c_size_t(0)
+    _check(load().kvd_decode_blocks_plan(int(batch), int(n_tokens), int(n_heads_q), int(n_heads_kv), int(head_dim), int(n_blocks),
+                                         int(block_tokens), int(num_sms), ctypes.byref(ws)), "kvd_decode_blocks_plan")
+    return ws.value
+
+
+def decode_blocks(q, k, v, blocks, seq_lens, block_tokens: int, scale: float, out, *, block_table=None, workspace=None, lse=None,
+                  status=None, stream=None):
+    """Attention of new tokens over the listed blocks of block_tokens tokens (kvd_decode_blocks): q, out [B, Hq, D] or
+    [B, T, Hq, D]; k, v bf16 [B, S_max, Hkv, D], or pools with block_table; blocks int32 [B, Hkv, K] or [B, T, Hkv, K],
+    block_select's or any. Workspace: decode_blocks_plan."""
+    torch = _torch or _import_torch()
+    what, bf, i32, f32 = "decode_blocks", torch.bfloat16, torch.int32, torch.float32
+    try:
+        dev = q.get_device()
+        ot = out.dtype
+        f32_out = ot is f32
+        ok = (dev >= 0 and q.dtype is bf and q.is_contiguous() and (f32_out or ot is bf) and out.get_device() == dev
+              and out.is_contiguous() and _whole(k, bf, dev, 4) and _whole(v, bf, dev, 4) and _whole(seq_lens, i32, dev, 1)
+              and blocks.dtype is i32 and blocks.get_device() == dev and blocks.is_contiguous()
+              and (block_table is None or _whole(block_table, i32, dev, 2))
+              and (lse is None or (_is(lse, f32, dev) and lse.is_contiguous()))
+              and (workspace is None or (workspace.get_device() == dev and workspace.is_contiguous())))
+    except AttributeError:
+        ok = False
+    if not ok:
+        _explain(what, (q, "q", (bf,), None), (out, "out", (bf, f32), None), (k, "k", (bf,), 4), (v, "v", (bf,), 4),
+                 (blocks, "blocks", (i32,), None), (seq_lens, "seq_lens", (i32,), 1), (block_table, "block_table", (i32,), 2),
+                 (lse, "lse", (f32,), None), (workspace, "workspace", None, None))
+        raise ValueError(f"{what}: q, blocks, out, lse and workspace must be contiguous tensors")
+    shape = q.shape
+    if len(shape) == 3:
+        (B, Hq, D), T = shape, 1
+    elif len(shape) == 4:
+        B, T, Hq, D = shape
+    else:
+        raise ValueError(f"{what}: q must be [B, Hq, D] or [B, T, Hq, D]")
+    n, cap, Hkv, width = kshape = k.shape
+    if (v.shape != kshape or width != D or out.shape != shape or seq_lens.numel() != B or blocks.dim() != len(shape)
+            or blocks.shape[:-1] != shape[:-2] + (Hkv,) or (lse is not None and lse.shape != shape[:-1])):
+        raise ValueError(f"{what}: inconsistent shapes")
+    if block_table is not None:
+        rows, per = block_table.shape
+        if rows != B:
+            raise ValueError(f"{what}: inconsistent shapes")
+        c = _pack_cache(k.data_ptr(), v.data_ptr(), 0, 0, block_table.data_ptr(), 0, per, cap, n, 0)
+    else:
+        if n != B:
+            raise ValueError(f"{what}: inconsistent shapes")
+        c = _pack_cache(k.data_ptr(), v.data_ptr(), 0, 0, 0, cap, 0, 0, 0, 0)
+    wp, wb = None, 0
+    if workspace is not None:
+        wp, wb = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    if B == 0:
+        return
+    _launch((_lib or load()).kvd_decode_blocks, "kvd_decode_blocks", dev, stream, c, q.data_ptr(), blocks.data_ptr(),
+            seq_lens.data_ptr(), B, T, blocks.shape[-1], int(block_tokens), Hq, Hkv, D, float(scale), wp, wb, out.data_ptr(),
+            OUT_F32 if f32_out else OUT_BF16, None if lse is None else lse.data_ptr(),
             None if status is None else _status_ptr(status, dev, what, torch))

@@ -25,6 +25,34 @@ struct ByteRange {
     }
 };
 
+// Bytes from the first to the last element of `rows` rows of `width` elements `stride` apart.
+inline size_t span_bytes(long long rows, long long stride, long long width, size_t es) {
+    return rows > 0 ? ((size_t)(rows - 1) * (size_t)stride + (size_t)width) * es : 0;
+}
+
+// Whether two sets of rows share an element. Rows of one buffer (one stride, a fused projection's slices) are apart
+// when their column windows are.
+struct Rows {
+    const void* p;
+    long long stride, width, n;
+    size_t es;
+    ByteRange range() const { return ByteRange{p, span_bytes(n, stride, width, es)}; }
+};
+inline bool rows_meet(const Rows& a, const Rows& b) {
+    if (!a.range().overlaps(b.range())) return false;
+    const long long S = a.stride * (long long)a.es;
+    if (S != b.stride * (long long)b.es) return true;
+    long long d = (long long)((intptr_t)b.p - (intptr_t)a.p) % S;
+    if (d < 0) d += S;  // b starts d bytes into a's row period
+    return d < a.width * (long long)a.es || d + b.width * (long long)b.es > S;
+}
+
+inline kvd_status check_strided(const void* p, long long stride, long long width, size_t es) {
+    if (!p || !aligned(p, 16) || stride < width || stride > (1LL << 40) || (stride * (long long)es) % 16 != 0)
+        return KVD_ERR_INVALID_ARG;
+    return KVD_OK;
+}
+
 kvd_status check_shape(int batch, int Hq, int Hkv, int D, kvd_out_dtype dt);
 // Paged cache arguments, checked; s_max of the contiguous calls becomes
 // max_blocks * page_size.

@@ -41,36 +41,8 @@ kvd_status check_rope(const kvd_rope* rope, int head_dim, RopeTable* out) {
     return KVD_OK;
 }
 
-// Bytes from the first to the last element of `rows` rows of `width` elements `stride` apart.
-size_t span_bytes(long long rows, long long stride, long long width, size_t es) {
-    return rows > 0 ? ((size_t)(rows - 1) * (size_t)stride + (size_t)width) * es : 0;
-}
-
-// Whether two sets of rows share an element. Rows of one buffer (one stride, a fused projection's slices) are apart
-// when their column windows are.
-struct Rows {
-    const void* p;
-    long long stride, width, n;
-    size_t es;
-    ByteRange range() const { return ByteRange{p, span_bytes(n, stride, width, es)}; }
-};
-bool rows_meet(const Rows& a, const Rows& b) {
-    if (!a.range().overlaps(b.range())) return false;
-    const long long S = a.stride * (long long)a.es;
-    if (S != b.stride * (long long)b.es) return true;
-    long long d = (long long)((intptr_t)b.p - (intptr_t)a.p) % S;
-    if (d < 0) d += S;  // b starts d bytes into a's row period
-    return d < a.width * (long long)a.es || d + b.width * (long long)b.es > S;
-}
-
 // Token numbers of the fp4 calls stay this far below 2^31, so that the tile after the last has one too.
 constexpr int kMaxTokens4 = 0x7ffffc00;
-
-kvd_status check_strided(const void* p, long long stride, long long width, size_t es) {
-    if (!p || !aligned(p, 16) || stride < width || stride > (1LL << 40) || (stride * (long long)es) % 16 != 0)
-        return KVD_ERR_INVALID_ARG;
-    return KVD_OK;
-}
 
 // The checks the two rotating appends share, and the launch.
 kvd_status append_rope(AppendTarget to, size_t cache_bytes, size_t scale_bytes, const kvd_rope* rope, const void* q,

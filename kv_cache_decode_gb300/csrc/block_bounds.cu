@@ -1,0 +1,175 @@
+// Bounds of the keys of each block of tokens: for every column the largest and the smallest value over the block's
+// tokens, in 8 bits rounded outwards, with one float32 scale a (block, KV head):
+//   a = max |k|, scale = a / 127, hi_d = ceil(max_t k_td / scale), lo_d = floor(min_t k_td / scale), in [-127, 127],
+// the divisions IEEE float32. For any query, sum_d max(q_d hi_d, q_d lo_d) * scale is then at least q . k_t for
+// every token of the block (up to float32's rounding): what block_select.cu scores blocks by. A block with a key that is not
+// finite gets the scale NaN and codes 0.
+//
+// A CTA takes one KV head of one block: 2 * block * D bytes read once, 2 D + 4 written; bound by memory for prompts, by latency for
+// the few blocks that a step fills. Thread i of a row's D / 8 holds 8 columns' running maxima and minima of every
+// (128 * 8 / D)-th token as bf16 pairs (exact).
+#include "../../include/kvdecode.h"
+#include "blocks.h"
+#include "common.cuh"
+
+namespace kvd {
+
+constexpr int kBoundsThreads = 128;
+
+__device__ __forceinline__ uint32_t max_bf16x2_nan(uint32_t a, uint32_t b) {
+    const __nv_bfloat162 r = __hmax2_nan(*reinterpret_cast<const __nv_bfloat162*>(&a), *reinterpret_cast<const __nv_bfloat162*>(&b));
+    return *reinterpret_cast<const uint32_t*>(&r);
+}
+__device__ __forceinline__ uint32_t min_bf16x2(uint32_t a, uint32_t b) {
+    const __nv_bfloat162 r = __hmin2(*reinterpret_cast<const __nv_bfloat162*>(&a), *reinterpret_cast<const __nv_bfloat162*>(&b));
+    return *reinterpret_cast<const uint32_t*>(&r);
+}
+
+template <int D>
+__global__ void __launch_bounds__(kBoundsThreads) block_bounds_kernel(const BoundsParams p, int per_seq) {
+    constexpr int TPR = D / 8, RPP = kBoundsThreads / TPR;  // threads of a row, rows of a pass
+    __shared__ uint4 s_hi[4][TPR], s_lo[4][TPR];
+    pdl_wait();
+    pdl_launch_dependents();
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int h = blockIdx.x % p.Hkv;
+    const long long rest = blockIdx.x / p.Hkv;
+    const int i = (int)(rest % per_seq), b = (int)(rest / per_seq);
+    const int raw = __ldg(p.seq_lens + b), len = raw < 0 ? 0 : raw > p.S_max ? p.S_max : raw;
+    const int raw0 = p.from_lens ? __ldg(p.from_lens + b) : 0, from = raw0 < 0 ? 0 : raw0;
+    const int bs = p.block_shift, n_tok = 1 << bs;
+    if (i == 0 && h == 0 && tid == 0 && p.status && (raw != len || raw0 != from || (long long)len - from > p.max_new))
+        atomicOr(p.status, KVD_STATUS_SEQ_LEN_CLAMPED);
+    const int j = (from >> bs) + i;
+    if (j >= (len >> bs)) return;  // not full
+    // ---- where the block and its bounds lie ----
+    const long long tok = (long long)j << bs;
+    long long row, block;
+    if (p.pg.block_table) {
+        const int page = __ldg(p.pg.block_table + (size_t)b * p.pg.max_blocks + (tok >> p.pg.page_shift));
+        if ((unsigned)page >= (unsigned)p.pg.num_pages) {
+            if (h == 0 && tid == 0 && p.status) atomicOr(p.status, KVD_STATUS_BAD_PAGE);
+            return;
+        }
+        row = ((long long)page << p.pg.page_shift) + (tok & ((1LL << p.pg.page_shift) - 1));
+        block = row >> bs;
+    } else {
+        row = (long long)b * p.S_max + tok;
+        block = (long long)b * (p.S_max >> bs) + j;
+    }
+    // ---- maxima and minima of this thread's columns ----
+    const int c = tid % TPR;
+    const uint4* k = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.k) + ((size_t)row * p.Hkv + h) * D) + c;
+    const size_t step = (size_t)p.Hkv * TPR;  // 16-byte vectors between tokens
+    uint32_t hi[4], lo[4];
+    int t = tid / TPR;
+    {
+        const uint4 v = __ldg(k + min(t, n_tok - 1) * step);  // (a thread past a short block's tokens repeats its last)
+        hi[0] = lo[0] = v.x, hi[1] = lo[1] = v.y, hi[2] = lo[2] = v.z, hi[3] = lo[3] = v.w;
+        t += RPP;
+    }
+    auto take = [&](const uint4& v) {
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            hi[e] = max_bf16x2_nan(hi[e], w[e]);
+            lo[e] = min_bf16x2(lo[e], w[e]);
+        }
+    };
+    for (; t + 3 * RPP < n_tok; t += 4 * RPP) {  // four loads in flight
+        uint4 v[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = __ldg(k + (size_t)(t + e * RPP) * step);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) take(v[e]);
+    }
+    {  // up to three more, at once
+        uint4 v[3];
+#pragma unroll
+        for (int e = 0; e < 3; ++e)
+            if (t + e * RPP < n_tok) v[e] = __ldg(k + (size_t)(t + e * RPP) * step);
+#pragma unroll
+        for (int e = 0; e < 3; ++e)
+            if (t + e * RPP < n_tok) take(v[e]);
+    }
+#pragma unroll
+    for (int off = TPR; off < 32; off <<= 1)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            hi[e] = max_bf16x2_nan(hi[e], __shfl_xor_sync(0xffffffffu, hi[e], off));
+            lo[e] = min_bf16x2(lo[e], __shfl_xor_sync(0xffffffffu, lo[e], off));
+        }
+    if (lane < TPR) {
+        s_hi[warp][lane] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+        s_lo[warp][lane] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+    }
+    __syncthreads();
+    if (warp != 0) return;
+    // ---- the scale and the codes ----
+    float fh[8], fl[8], a = 0.f;
+    bool bad = false;
+    if (lane < TPR) {
+#pragma unroll
+        for (int w = 1; w < 4; ++w) {
+            const uint4 x = s_hi[w][lane], y = s_lo[w][lane];
+            const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                hi[e] = max_bf16x2_nan(hi[e], xs[e]);
+                lo[e] = min_bf16x2(lo[e], ys[e]);
+            }
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            fh[2 * e] = bf16_lo(hi[e]), fh[2 * e + 1] = bf16_hi(hi[e]);
+            fl[2 * e] = bf16_lo(lo[e]), fl[2 * e + 1] = bf16_hi(lo[e]);
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            bad |= !isfinite(fh[e]) || !isfinite(fl[e]);  // a NaN shows in the maximum, infinities in either
+            a = fmaxf(a, fmaxf(fabsf(fh[e]), fabsf(fl[e])));
+        }
+    }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, off));
+    bad = __any_sync(0xffffffffu, bad);
+    const float s = bad ? __uint_as_float(0x7fffffffu) : __fdiv_rn(a, 127.f);
+    const size_t at = (size_t)block * p.Hkv + h;
+    if (lane == 0) p.scales[at] = s;
+    if (lane < TPR) {
+        uint32_t up[2] = {0u, 0u}, down[2] = {0u, 0u};
+        if (!bad && s > 0.f) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const int x = max(-127, min(127, __float2int_ru(__fdiv_rn(fh[e], s))));
+                const int y = max(-127, min(127, __float2int_rd(__fdiv_rn(fl[e], s))));
+                up[e >> 2] |= (uint32_t)(x & 0xff) << (8 * (e & 3));
+                down[e >> 2] |= (uint32_t)(y & 0xff) << (8 * (e & 3));
+            }
+        }
+        uint2* dst = reinterpret_cast<uint2*>(p.codes + at * 2 * D);
+        dst[lane] = make_uint2(up[0], up[1]);
+        dst[TPR + lane] = make_uint2(down[0], down[1]);
+    }
+}
+
+cudaError_t launch_block_bounds(const BoundsParams& p, cudaStream_t stream) {
+    const int per_seq = (int)(((long long)p.max_new + (1 << p.block_shift) - 1) >> p.block_shift);  // blocks max_new tokens can fill
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)((long long)p.B * per_seq * p.Hkv), 1, 1);
+    cfg.blockDim = dim3(kBoundsThreads, 1, 1);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    switch (p.D) {
+        case 64: return cudaLaunchKernelEx(&cfg, block_bounds_kernel<64>, p, per_seq);
+        case 128: return cudaLaunchKernelEx(&cfg, block_bounds_kernel<128>, p, per_seq);
+        case 256: return cudaLaunchKernelEx(&cfg, block_bounds_kernel<256>, p, per_seq);
+        default: return cudaErrorInvalidValue;
+    }
+}
+
+}  // namespace kvd

@@ -174,6 +174,11 @@ struct RopeWarp {
 
     // t: the token's position. buf: R / 2 entries of this warp's shared memory. Whole warps call this.
     __device__ __forceinline__ void init(const RopeTable& rope, long long t, int D_, float2* buf) {
+        init(rope, D_, buf, [t](int) { return t; });
+    }
+    // The same, pair i turned by position at(i).
+    template <class F>
+    __device__ __forceinline__ void init(const RopeTable& rope, int D_, float2* buf, F&& at) {
         const int lane = threadIdx.x & 31;
         D = DD ? DD : D_;
         units = DD ? UN : (D + 15) >> 4;
@@ -181,7 +186,7 @@ struct RopeWarp {
         interleaved = rope.interleaved;
         s_cs = buf;
 #pragma unroll 1  // (4 at most: unrolled it is 0.1 us slower for a few tokens)
-        for (int i = lane; i < R >> 1; i += 32) rope_table_put(buf, i, rope_cos_sin(t, __ldg(rope.turns + i), rope.factor));
+        for (int i = lane; i < R >> 1; i += 32) rope_table_put(buf, i, rope_cos_sin(at(i), __ldg(rope.turns + i), rope.factor));
         __syncwarp();
         if constexpr (DD > 0) {
             if (lane % UN < R >> 4) rope_table_get(buf, 8 * (lane % UN), cs);

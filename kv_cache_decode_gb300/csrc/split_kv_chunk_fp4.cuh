@@ -103,11 +103,6 @@ struct Fp4Geom {
     KVD_HD constexpr int x() const { return X; }
 };
 
-__device__ __forceinline__ uint32_t movmatrix_trans(uint32_t x) {
-    uint32_t y;
-    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;\n" : "=r"(y) : "r"(x));
-    return y;
-}
 // The f16 MMA of common.cuh without its ordering against other instructions: the
 // scheduler may move conversions and loads between the products.
 __device__ __forceinline__ void mma_free(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
