@@ -1520,6 +1520,8 @@ class RopeAxes:
 
 
 def _axes_on(rope, dev, what):
+    if rope.__class__ is RopeAxes and rope._device == dev:
+        return rope._ref
     if not isinstance(rope, RopeAxes):
         raise TypeError(f"{what}: rope must be a RopeAxes")
     if rope._device != dev:
@@ -1530,13 +1532,21 @@ def _axes_on(rope, dev, what):
 def _axis_stride(rope, positions, N, what):
     """Elements between the axes of positions [axes, N] or [axes, B, T], each axis contiguous."""
     s, st = positions.shape, positions.stride()
-    if len(s) not in (2, 3) or s[0] != rope.n_axes or positions.numel() != N * rope.n_axes:
-        raise ValueError(f"{what}: positions must be [{rope.n_axes}, {N}] (or [axes, B, T])")
-    if N == 0:
-        return 0
-    if not positions[0].is_contiguous() or (s[0] > 1 and st[0] < N):
-        raise ValueError(f"{what}: each axis of positions must be contiguous")
-    return st[0] if s[0] > 1 else N
+    n = len(s)
+    if n == 2:
+        A, rows = s
+        step, last = st
+        if A == rope.n_axes and rows == N and (last == 1 or N <= 1):
+            if A == 1 or step >= N:
+                return step if A > 1 else N
+            raise ValueError(f"{what}: each axis of positions must be contiguous and apart from the others")
+    elif n == 3 and s[0] == rope.n_axes and s[1] * s[2] == N:
+        if N == 0:
+            return 0
+        if (st[2] == 1 or s[2] == 1) and (st[1] == s[2] or s[1] == 1) and (s[0] == 1 or st[0] >= N):
+            return st[0] if s[0] > 1 else N
+        raise ValueError(f"{what}: each axis of positions must be contiguous and apart from the others")
+    raise ValueError(f"{what}: positions must be [{rope.n_axes}, {N}] (or [axes, B, T]), each axis contiguous")
 
 
 def rope_apply_axes(rope: RopeAxes, x, positions, out, stream=None):
@@ -1559,7 +1569,8 @@ def rope_apply_axes(rope: RopeAxes, x, positions, out, stream=None):
     ys = xs if out is x else _alike(out, "out", what, N, H, D)
     ref = _axes_on(rope, dev, what)
     step = _axis_stride(rope, positions, N, what)
-    _same_batch(what, positions.shape[1:], x.shape[:-2], out.shape[:-2])
+    if positions.dim() > 2 or (out is not x and x.dim() == 4):
+        _same_batch(what, positions.shape[1:], x.shape[:-2], out.shape[:-2])
     if N == 0:
         return
     _launch((_lib or load()).kvd_rope_apply_axes, "kvd_rope_apply_axes", dev, stream, ref, x.data_ptr(), xs,
@@ -1615,8 +1626,9 @@ def kv_append_axes(rope: RopeAxes, k, v, k_new, v_new, slots, positions, *, q=No
         if Nq != N or Dq != D:
             raise ValueError(f"{what}: inconsistent shapes")
         qp, op = q.data_ptr(), q_out.data_ptr()
-    _same_batch(what, positions.shape[1:], slots.shape, k_new.shape[:-2], v_new.shape[:-2],
-                *(() if q is None else (q.shape[:-2], q_out.shape[:-2])))
+    if positions.dim() > 2 or slots.dim() > 1 or k_new.dim() > 3 or v_new.dim() > 3 or (q is not None and (q.dim() > 3 or q_out.dim() > 3)):
+        _same_batch(what, positions.shape[1:], slots.shape, k_new.shape[:-2], v_new.shape[:-2],
+                    *(() if q is None else (q.shape[:-2], q_out.shape[:-2])))
     if N == 0 or n == 0:
         return
     c = (_pack_cache(k.data_ptr(), v.data_ptr(), ksp, vsp, 0, 0, 0, cap, n, fp8) if paged else

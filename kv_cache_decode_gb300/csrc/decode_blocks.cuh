@@ -57,7 +57,9 @@ struct BlocksShape {
     static constexpr int OFF_CML = OFF_ML + 3 * ROWS * 4;    // of the CTA's rows
     static constexpr int OFF_W = OFF_CML + 3 * 64 * 4;       // weights of the cluster's CTAs, and 1 / sum
     static constexpr int OFF_FLAG = OFF_W + 17 * 64 * 4;
-    static constexpr int SMEM = OFF_FLAG + 16;
+    static constexpr int OFF_IN = OFF_FLAG + 16;             // what the cluster's CTAs send this one
+    static constexpr int IN_FLOATS = 2048;
+    static constexpr int SMEM = OFF_IN + IN_FLOATS * 4;
     static_assert(ROWS * ST * 4 <= RING, "the states take the ring's place");
     static_assert(2 * (SMEM + 1024) <= 227 * 1024, "two CTAs an SM");
 };
@@ -87,10 +89,11 @@ __global__ void __launch_bounds__(kBlocksWarps * 32, 2) decode_blocks_kernel(con
     float* s_clr = s_cl + 64;
     float* s_w = reinterpret_cast<float*>(smem + Sh::OFF_W);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + Sh::OFF_FLAG);
+    float* s_in = reinterpret_cast<float*>(smem + Sh::OFF_IN);
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nthreads = blockDim.x;
     const int HT = p.head_warps, teams = (nthreads >> 5) / HT, team = warp / HT, wt = warp - team * HT;
-    const int rank = blockIdx.x % p.parts, cl = blockIdx.x / p.parts;
+    const int rank = blockIdx.x & (p.parts - 1), cl = blockIdx.x >> (__ffs(p.parts) - 1);  // (parts: a power of two)
     const int pair = cl % p.pairs, shard = cl / p.pairs;
     const int h = pair % p.Hkv, bt = pair / p.Hkv, t = bt % p.T, b = bt / p.T;
     const int R = Sh::SLOTS / teams, slot0 = team * R;  // this team's ring
@@ -108,9 +111,28 @@ __global__ void __launch_bounds__(kBlocksWarps * 32, 2) decode_blocks_kernel(con
         asm volatile("prefetch.tensormap [%0];\n" ::"l"(reinterpret_cast<uint64_t>(&maps.k)) : "memory");
         asm volatile("prefetch.tensormap [%0];\n" ::"l"(reinterpret_cast<uint64_t>(&maps.v)) : "memory");
     }
+    // States of few rows are sent to the CTA that joins them, which has to have started by then.
+    const bool send = p.parts > 1 && p.G <= 16 && p.G * D <= Sh::IN_FLOATS;
+    if (send) cluster_arrive_relaxed();
     __syncthreads();
     pdl_wait();
     pdl_launch_dependents();
+
+    // ---- q: column tile n's rows wt * RW + 8 n + lane / 4 as B fragments ----
+    uint32_t qf[NT][KS][2];
+    {
+        const uint32_t* q32 = reinterpret_cast<const uint32_t*>(p.q);
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            const int r = wt * RW + 8 * n + (lane >> 2);
+            const uint32_t* qr = q32 + ((size_t)pair * p.G + r) * (D / 2) + (lane & 3);
+#pragma unroll
+            for (int kk = 0; kk < KS; ++kk) {
+                qf[n][kk][0] = r < p.G ? __ldg(qr + kk * 8) : 0u;
+                qf[n][kk][1] = r < p.G ? __ldg(qr + kk * 8 + 4) : 0u;
+            }
+        }
+    }
 
     // ---- the tokens this query token sees, and the units of this team ----
     const int raw = __ldg(p.seq_lens + b), L = raw < 0 ? 0 : raw > p.S_max ? p.S_max : raw;
@@ -119,10 +141,10 @@ __global__ void __launch_bounds__(kBlocksWarps * 32, 2) decode_blocks_kernel(con
     const int32_t* list = p.blocks + (size_t)pair * p.K;
     const int units = p.K << p.unit_shift, submask = (1 << p.unit_shift) - 1;
     const int W = p.shards * p.parts * teams, wid = (shard * p.parts + rank) * teams + team;
-    const int last_block = seen > 0 ? (seen - 1) >> (p.unit_shift + 4) : -1;
+    const int last_block = (p.S_max - 1) >> (p.unit_shift + 4);  // of the cache's
 
     // Units are looked up 32 at a time, one a lane: how many of its tokens count, and its cache row. Those of entries
-    // that name no block the token sees have none and are passed over.
+    // that name no block the token sees have none and are passed over. (List and table are read beside the length, not behind it.)
     struct Cursor {
         int u;          // the next look-up's first unit of this team
         uint32_t mask;  // lanes whose unit is still to come
@@ -131,28 +153,22 @@ __global__ void __launch_bounds__(kBlocksWarps * 32, 2) decode_blocks_kernel(con
     auto look_up = [&](Cursor& c, bool rows) {
         do {
             const long long u = c.u + (long long)lane * W;
-            c.n = 0;
-            if (u < units) {
-                const int blk = __ldg(list + ((int)u >> p.unit_shift));
-                if (blk >= 0 && blk <= last_block) {
-                    const int tok = ((blk << p.unit_shift) + ((int)u & submask)) << 4;
-                    c.n = min(16, seen - tok);
-                    if (rows && c.n > 0) {
-                        if (p.pg.block_table) {
-                            const int page = __ldg(p.pg.block_table + (size_t)b * p.pg.max_blocks + (tok >> p.pg.page_shift));
-                            // an entry that names no page reads as zero rows: past the pool's end
-                            if ((unsigned)page < (unsigned)p.pg.num_pages) {
-                                c.row = (page << p.pg.page_shift) + (tok & ((1 << p.pg.page_shift) - 1));
-                            } else {
-                                c.row = p.pg.num_pages << p.pg.page_shift;
-                                if (p.status) atomicOr(p.status, KVD_STATUS_BAD_PAGE);
-                            }
-                        } else {
-                            c.row = b * p.S_max + tok;
-                        }
-                    }
+            const int blk = u < units ? __ldg(list + ((int)u >> p.unit_shift)) : -1;
+            const bool named = blk >= 0 && blk <= last_block;
+            const int tok = named ? ((blk << p.unit_shift) + ((int)u & submask)) << 4 : 0;
+            const bool held = named && tok < p.S_max;
+            bool bad = false;
+            if (rows && held) {
+                if (p.pg.block_table) {
+                    const int page = __ldg(p.pg.block_table + (size_t)b * p.pg.max_blocks + (tok >> p.pg.page_shift));
+                    bad = (unsigned)page >= (unsigned)p.pg.num_pages;  // reads as zero rows: past the pool's end
+                    c.row = bad ? p.pg.num_pages << p.pg.page_shift : (page << p.pg.page_shift) + (tok & ((1 << p.pg.page_shift) - 1));
+                } else {
+                    c.row = b * p.S_max + tok;
                 }
             }
+            c.n = held ? min(16, seen - tok) : 0;
+            if (bad && c.n > 0 && p.status) atomicOr(p.status, KVD_STATUS_BAD_PAGE);
             c.mask = __ballot_sync(0xffffffffu, c.n > 0);
             const long long next = c.u + 32LL * W;
             c.u = next < units ? (int)next : units;
@@ -193,21 +209,6 @@ __global__ void __launch_bounds__(kBlocksWarps * 32, 2) decode_blocks_kernel(con
         for (int i = 0; i < R && more; ++i) issue();
     }
 
-    // ---- q: column tile n's rows wt * RW + 8 n + lane / 4 as B fragments ----
-    uint32_t qf[NT][KS][2];
-    {
-        const uint32_t* q32 = reinterpret_cast<const uint32_t*>(p.q);
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            const int r = wt * RW + 8 * n + (lane >> 2);
-            const uint32_t* qr = q32 + ((size_t)pair * p.G + r) * (D / 2) + (lane & 3);
-#pragma unroll
-            for (int kk = 0; kk < KS; ++kk) {
-                qf[n][kk][0] = r < p.G ? __ldg(qr + kk * 8) : 0u;
-                qf[n][kk][1] = r < p.G ? __ldg(qr + kk * 8 + 4) : 0u;
-            }
-        }
-    }
     // l: the weights' sum, for lse. lr: of the weights as V meets them, so that the output is a convex combination of V
     // rows (the same where float32 output carries both parts).
     float o[MT][NT][4], m[NT][2], l[NT][2], lr[F32OUT ? 1 : NT][2];
@@ -406,7 +407,10 @@ __global__ void __launch_bounds__(kBlocksWarps * 32, 2) decode_blocks_kernel(con
     };
     auto inverse = [](float sum) { return sum == 0.f ? 0.f : 1.f / sum; };
     const bool alone = p.parts == 1;
-    for (int i = tid; i < p.G * (D / 4); i += nthreads) {
+    const int vecs = p.G * (D / 4);             // float4 of the pair's output
+    const int share = (vecs + p.parts - 1) / p.parts;  // of one CTA, where states are sent
+    if (send) cluster_wait();  // the others have started
+    for (int i = tid; i < vecs; i += nthreads) {
         const int r = i / (D / 4), c = i - r * (D / 4), step = HT * RW;  // team j's state of row r: r + j * step
         float M = -FLT_MAX, sum = 0.f, sumr = 0.f;
         for (int j = 0; j < teams; ++j) M = fmaxf(M, s_m[r + j * step]);
@@ -421,6 +425,15 @@ __global__ void __launch_bounds__(kBlocksWarps * 32, 2) decode_blocks_kernel(con
         if (alone) {
             put(r, c, inverse(sumr), v);
             if (c == 0) put_lse(r, M, sum);
+        } else if (send) {
+            const int to = i / share;
+            st_cluster4(map_to_rank(smem_u32(s_in + 4 * (rank * share + i - to * share)), to), v);
+            if (c < p.parts) {  // (D / 4 >= 16 threads of a row, one a CTA)
+                const uint32_t ml = map_to_rank(smem_u32(s_w + (rank * 16 + r) * 3), c);
+                st_cluster(ml, M);
+                st_cluster(ml + 4, sum);
+                st_cluster(ml + 8, sumr);
+            }
         } else {
             *reinterpret_cast<float4*>(states + r * ST + 4 * c) = v;  // only this thread reads it
             if (c == 0) s_cm[r] = M, s_cl[r] = sum, s_clr[r] = sumr;
@@ -428,6 +441,25 @@ __global__ void __launch_bounds__(kBlocksWarps * 32, 2) decode_blocks_kernel(con
     }
     if (alone) return;
     cluster_sync();
+    if (send) {  // all that came is here, and nothing more is read elsewhere
+        for (int i = tid; i < share && rank * share + i < vecs; i += nthreads) {
+            const int r = (rank * share + i) / (D / 4), c = rank * share + i - r * (D / 4);
+            float M = -FLT_MAX, sum = 0.f, sumr = 0.f;
+            for (int j = 0; j < p.parts; ++j) M = fmaxf(M, s_w[(j * 16 + r) * 3]);
+            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int j = 0; j < p.parts; ++j) {
+                const float* ml = s_w + (j * 16 + r) * 3;
+                const float f = exp2f(ml[0] - M);
+                const float4 x = *reinterpret_cast<const float4*>(s_in + 4 * (j * share + i));
+                sum += f * ml[1];
+                sumr += f * ml[2];
+                v.x += f * x.x, v.y += f * x.y, v.z += f * x.z, v.w += f * x.w;
+            }
+            put(r, c, inverse(sumr), v);
+            if (c == 0) put_lse(r, M, sum);
+        }
+        return;
+    }
     for (int i = tid; i < p.G * p.parts; i += nthreads) {  // row r's maximum of CTA j
         const int r = i / p.parts, j = i - r * p.parts;
         s_w[j * 64 + r] = ld_cluster(map_to_rank(smem_u32(s_cm + r), j));

@@ -97,6 +97,7 @@ __global__ void __launch_bounds__(kPagesThreads, 1) pages_kernel(const PagesPara
         block_scan2(v, tot, s_warp);
         if (b < p.B) {
             s_old[b] = old;
+            s_row[b] = want;
             s_rel[b] = (int)(released + v[0]);
             s_need[b] = (int)(needed + v[1]);
         }
@@ -110,8 +111,8 @@ __global__ void __launch_bounds__(kPagesThreads, 1) pages_kernel(const PagesPara
     for (int b0 = 0; b0 < p.B; b0 += kPagesThreads) {
         const int b = b0 + tid;
         int old = 0, want = 0, need = 0;
-        if (b < p.B) {
-            lengths(b, old, want);
+        if (b < p.B) {  // (this thread's own entries)
+            old = s_old[b], want = s_row[b];
             need = max(pages_of(want) - pages_of(old), 0);
             if (need > 0 && (long long)s_need[b] + need > have) {
                 need = 0;
@@ -178,35 +179,53 @@ __global__ void __launch_bounds__(kPagesThreads, 1) pages_kernel(const PagesPara
     if (p.slots || p.positions) {
         sync();
         const long long total = min((long long)rows, p.rows);
-        auto slot_of = [&](int n, int& b, int& t) {
-            while (n >= s_row[b + 1]) ++b;
-            t = s_old[b] + (n - s_row[b]);
-            const int page = __ldcg(p.table + (size_t)b * p.max_blocks + (t >> shift));
-            if ((unsigned)page >= (unsigned)p.num_pages) {
-                flags |= KVD_STATUS_BAD_PAGE;
-                return -1;
-            }
-            return (page << shift) + (t & (psize - 1));
-        };
-        // Four rows a thread: one search for all.
-        for (long long n0 = 4LL * gtid; n0 < p.rows; n0 += 4LL * gthreads) {
-            int slot[4] = {-1, -1, -1, -1}, at[4] = {-1, -1, -1, -1};
-            if (n0 < total) {
-                int b = owner_of(s_row, p.B, (int)n0);
+        // A warp takes a stretch of rows, 128 at a time, four neighbours a lane: the sequence is searched for once, then
+        // followed; four steps' table entries are on the way at once.
+        const bool wide = ((reinterpret_cast<uintptr_t>(p.slots) | reinterpret_cast<uintptr_t>(p.positions)) & 15) == 0;
+        const int lane = tid & 31, gwarp = gtid >> 5, gwarps = gthreads >> 5;
+        const long long per = ((p.rows + gwarps - 1) / gwarps + 127) & ~127LL;
+        const long long end = min(p.rows, (gwarp + 1) * per);
+        long long n0 = gwarp * per + 4 * lane;
+        int b = n0 < total ? owner_of(s_row, p.B, (int)n0) : 0;
+        for (; n0 < end; n0 += 512) {
+            int slot[4][4], at[4][4];
 #pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    if (n0 + k < total) slot[k] = slot_of((int)n0 + k, b, at[k]);
-            }
-            if (n0 + 4 <= p.rows && ((reinterpret_cast<uintptr_t>(p.slots) | reinterpret_cast<uintptr_t>(p.positions)) & 15) == 0) {
-                if (p.slots) *reinterpret_cast<int4*>(p.slots + n0) = make_int4(slot[0], slot[1], slot[2], slot[3]);
-                if (p.positions) *reinterpret_cast<int4*>(p.positions + n0) = make_int4(at[0], at[1], at[2], at[3]);
-            } else {
+            for (int u = 0; u < 4; ++u)
 #pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    if (n0 + k < p.rows) {
-                        if (p.slots) p.slots[n0 + k] = slot[k];
-                        if (p.positions) p.positions[n0 + k] = at[k];
+                for (int k = 0; k < 4; ++k) {
+                    const long long n = n0 + 128 * u + k;
+                    slot[u][k] = at[u][k] = -1;
+                    if (n < min(total, end)) {
+                        while (n >= s_row[b + 1]) ++b;
+                        at[u][k] = s_old[b] + ((int)n - s_row[b]);
+                        slot[u][k] = __ldcg(p.table + (size_t)b * p.max_blocks + (at[u][k] >> shift));
                     }
+                }
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    if (at[u][k] >= 0) {
+                        if ((unsigned)slot[u][k] >= (unsigned)p.num_pages) {
+                            flags |= KVD_STATUS_BAD_PAGE;
+                            slot[u][k] = -1;
+                        } else {
+                            slot[u][k] = (slot[u][k] << shift) + (at[u][k] & (psize - 1));
+                        }
+                    }
+                const long long n = n0 + 128 * u;
+                if (n >= end) break;
+                if (wide && n + 4 <= end) {
+                    if (p.slots) *reinterpret_cast<int4*>(p.slots + n) = make_int4(slot[u][0], slot[u][1], slot[u][2], slot[u][3]);
+                    if (p.positions) *reinterpret_cast<int4*>(p.positions + n) = make_int4(at[u][0], at[u][1], at[u][2], at[u][3]);
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        if (n + k < end) {
+                            if (p.slots) p.slots[n + k] = slot[u][k];
+                            if (p.positions) p.positions[n + k] = at[u][k];
+                        }
+                }
             }
         }
     }
