@@ -114,6 +114,9 @@ kvd_status plan_blocks(int batch, int T, int Hq, int Hkv, int D, int K, int bloc
     return KVD_OK;
 }
 
+// Keys of a query token in the workspace: whole 16-byte vectors.
+int select_key_stride(int max_seq_len, int block_tokens) { return (max_seq_len / block_tokens + 3) & ~3; }
+
 kvd_status check_bounds(const kvd_block_bounds* b, int batch, int Hkv, int D, PagedCache* pg, int* cap, size_t* blocks) {
     if (!b || !power_of_two(b->block_tokens, 16, 4096) || batch < 0 || Hkv <= 0 || D <= 0) return KVD_ERR_INVALID_ARG;
     if (D != 64 && D != 128 && D != 256) return KVD_ERR_UNSUPPORTED;
@@ -306,7 +309,7 @@ kvd_status kvd_block_select_plan(int batch, int n_tokens, int n_heads_kv, int ma
     if (!workspace_bytes_out || batch < 0 || n_tokens < 1 || n_heads_kv <= 0 || max_seq_len < 0 || !power_of_two(block_tokens, 16, 4096))
         return KVD_ERR_INVALID_ARG;
     if (n_tokens > KVD_MAX_TOKENS) return KVD_ERR_UNSUPPORTED;
-    *workspace_bytes_out = align256((size_t)batch * n_tokens * n_heads_kv * (size_t)(max_seq_len / block_tokens) * 4);
+    *workspace_bytes_out = align256((size_t)batch * n_tokens * n_heads_kv * select_key_stride(max_seq_len, block_tokens) * 4);
     return KVD_OK;
 }
 
@@ -364,12 +367,14 @@ kvd_status kvd_block_select(const kvd_block_bounds* bounds, const void* q, const
     p.block_shift = log2_of(bounds->block_tokens);
     p.n_first = n_first;
     p.n_last = n_last;
-    p.key_stride = max_seq_len / bounds->block_tokens;
+    p.key_stride = select_key_stride(max_seq_len, bounds->block_tokens);
     p.pg = pg;
-    // CTAs of a pair: two a multiprocessor, as far as every warp has a tile of 16 blocks or there are query tokens to select for.
+    // CTAs of a pair: as many as are resident, as far as every warp has a tile of 16 blocks or there are query tokens to select for.
+    // Clusters of 16 only where a multiprocessor holds two of their CTAs (a cluster has to fit into one part of the GPU).
     int parts = 1;
+    const int per_sm = select_ctas(head_dim, p.G, n_tokens);
     const long long work = std::max((p.key_stride + 127LL) / 128, (long long)n_tokens);
-    while (parts < 16 && pairs * parts * 2 <= 2LL * sms && parts < work) parts *= 2;
+    while (parts < (per_sm > 1 ? 16 : 8) && pairs * parts <= (long long)per_sm * sms && parts < work) parts *= 2;
     p.parts = parts;
     return launch_block_select(p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? KVD_OK : KVD_ERR_CUDA;
 }

@@ -9,12 +9,13 @@
 //
 // Reads 2 D + 4 bytes a (block, KV head) once for all query tokens; bound by memory for batches, by latency for one
 // sequence. A cluster of up to 16 CTAs takes a (sequence, KV head). First its warps score tiles of 16 blocks: f16 MMAs
-// m16n8k16 with the blocks as rows and the query rows as columns, I = [hi lo] [max(c, 0) min(c, 0)]^T, exact since
-// f16 holds the codes, products and sums. A lane's 16-byte load is 16 consecutive codes of a row; the MMA's k order is the permutation of
-// columns that fits, the same for both operands, so codes go from the load to fragments in registers. Keys
+// m16n8k16 with the blocks as rows and the query rows as columns, I = [hi lo] [max(c, 0) min(c, 0)]^T. A code enters as code + 128
+// in the low bits of an f16, a subnormal; products and sums of these are whole numbers below 2^24 (times 2^-24), so exact. A lane's 16-byte
+// copy is 16 consecutive codes of a row; the MMA's k order is the permutation of columns that fits, the same for both operands, so codes
+// go from the lane's own place in shared memory to fragments without a shuffle, and a warp waits for its own copies alone. Keys
 // (scores as ordered integers) go to the workspace, the cluster meets at a barrier, and CTA i selects for the query tokens i, i + CTAs, ...: a
-// histogram over 2,048 equal parts of the range [smallest, largest] of the keys, then over the part that holds the border, until
-// the border's value or a part that fits whole is found (two rounds as a rule, three at most).
+// histogram over 2,048 equal parts of the range [smallest, largest] of the keys, then (seldom) over the part that holds the border, until
+// that part has few keys, which are ranked one by one.
 #include <math_constants.h>
 
 #include <algorithm>
@@ -26,10 +27,24 @@
 
 namespace kvd {
 
-constexpr int kSelThreads = 256, kSelWarps = kSelThreads / 32;
 constexpr int kSelBins = 2048;
 constexpr int kSelTiles = 8;        // column tiles of 8 query rows scored at once
-constexpr int kSelRoom = 64 * 1024; // shared memory: the query rows' fragments, later the keys
+constexpr int kSelTies = 64;        // keys around the border that are ranked one by one
+
+// Shared memory of the scoring: the query rows' fragments, then a ring of tiles a warp, in which every lane has its own
+// 16 bytes of each load and its two rows' scales. The selection puts the keys in its place.
+template <int D>
+struct SelectShape {
+    static constexpr int KS = 2 * D / 16, LOADS = 2 * D / 64;  // k-steps; 16-byte loads of a lane and row
+    static constexpr int WARPS = D == 256 ? 16 : 8, THREADS = 32 * WARPS;
+    static constexpr int STAGES = D == 256 ? 1 : D == 128 ? 2 : 3;  // three CTAs an SM, at head_dim 256 one of twice the warps
+    static constexpr int TILE = 2 * LOADS * 512 + 2 * 128;     // 16 blocks' codes, and scales
+    static constexpr int RING = WARPS * STAGES * TILE;
+    static constexpr int FRAG = KS * 32 * 8;                   // a column tile's fragments
+    static constexpr int MOST = kSelTiles * FRAG + RING;
+    static_assert(MOST + 2 * 1024 <= 227 * 1024, "shared memory of a CTA");
+    static_assert(RING >= kSelBins * 4 + kSelTies * 8, "the selection's counts");
+};
 
 __device__ __forceinline__ uint32_t score_key(float s) {  // larger score, larger key; NaN as +inf, -0 as +0
     if (s != s) return 0xff800000u;
@@ -40,21 +55,33 @@ __device__ __forceinline__ uint32_t score_key(float s) {  // larger score, large
 // How many query rows of a token share a column tile's 8 columns, in powers of two; a wider group takes whole tiles.
 __host__ __device__ inline int sel_columns(int G) { return G <= 1 ? 1 : G <= 2 ? 2 : G <= 4 ? 4 : 8; }
 
-template <int D>
-__global__ void __launch_bounds__(kSelThreads, D == 256 ? 1 : 2) block_select_kernel(const SelectParams p) {
-    constexpr int KS = 2 * D / 16, LOADS = 2 * D / 64;  // k-steps; 16-byte loads of a lane and row
+// Column tiles that the query rows of T tokens take at once: 1, 2, 4, 6 or 8 (the last may be without rows).
+static int select_tiles(int G, int T) {
+    const int per_tok = (G + 7) / 8;
+    const int n = std::min(kSelTiles, G > 8 ? std::min(T, kSelTiles / per_tok) * per_tok : (T * sel_columns(G) + 7) / 8);
+    return n == 1 ? 1 : (n + 1) / 2 * 2;
+}
+
+// NT: column tiles of a round.
+template <int D, int NT>
+__global__ void __launch_bounds__(SelectShape<D>::THREADS, D == 256 ? 1 : NT == 1 ? 3 : 2) block_select_kernel(const SelectParams p, int room) {
+    using Sh = SelectShape<D>;
+    constexpr int kSelThreads = Sh::THREADS, kSelWarps = Sh::WARPS;
+    constexpr int KS = Sh::KS, LOADS = Sh::LOADS, STAGES = Sh::STAGES;
     extern __shared__ __align__(16) uint8_t smem[];
     uint2* s_q = reinterpret_cast<uint2*>(smem);         // [tile][k-step][lane]: B fragments
-    uint32_t* s_key = reinterpret_cast<uint32_t*>(smem); // later: the keys of one query token
+    uint32_t* s_hist = reinterpret_cast<uint32_t*>(smem); // later: a histogram, keys around the border, and one query token's keys
+    uint2* s_tie = reinterpret_cast<uint2*>(s_hist + kSelBins);
+    uint32_t* s_key = reinterpret_cast<uint32_t*>(s_tie + kSelTies);
     __shared__ float s_sc[kSelTiles * 8];                // the columns' scales, NaN: no query row
-    __shared__ uint32_t s_hist[kSelBins];
+    __shared__ float s_bias[kSelTiles * 8];              // what their sums start from
     __shared__ uint32_t s_a[kSelWarps], s_b[kSelWarps];
-    __shared__ uint32_t s_lo, s_hi, s_need, s_done;
-    pdl_wait();
-    pdl_launch_dependents();
+    __shared__ uint32_t s_lo, s_hi, s_need, s_count, s_ties;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, j4 = lane & 3, g8 = lane >> 2;
     const int rank = blockIdx.x % p.parts, pair = blockIdx.x / p.parts, h = pair % p.Hkv, b = pair / p.Hkv;
     const int bs = p.block_shift, G = p.G;
+    pdl_wait();
+    pdl_launch_dependents();
     const int raw = __ldg(p.seq_lens + b), L = raw < 0 ? 0 : raw > p.len_cap ? p.len_cap : raw;
     if (raw != L && h == 0 && rank == 0 && tid == 0 && p.status) atomicOr(p.status, KVD_STATUS_SEQ_LEN_CLAMPED);
     const int full = L >> bs;  // blocks with bounds
@@ -64,10 +91,51 @@ __global__ void __launch_bounds__(kSelThreads, D == 256 ? 1 : 2) block_select_ke
     if ((int)(((long long)L + (1 << bs) - 1) >> bs) > p.K) {
         const int cols = sel_columns(G);                 // columns of a token in a tile
         const int per_tok = (G + 7) / 8;                 // tiles of a token (G > 8: several)
-        const int toks = G > 8 ? kSelTiles / per_tok : kSelTiles * (8 / cols);  // tokens of a round
+        const int toks = G > 8 ? NT / per_tok : NT * (8 / cols);  // tokens of a round
+        const int first = (rank * kSelWarps + warp) * 16, step = p.parts * kSelWarps * 16;
+        uint8_t* ring = smem + NT * Sh::FRAG + warp * STAGES * Sh::TILE;
+        // A tile's rows of this lane: blocks j0 + g8 and j0 + g8 + 8, by their place among all bounds (-1: none).
+        auto look_up = [&](int j0, long long (&at)[2]) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int j = j0 + g8 + 8 * e;
+                at[e] = -1;
+                if (j < full) {
+                    long long blk;
+                    if (p.pg.block_table) {
+                        const int tok = j << bs;
+                        const int page = __ldg(p.pg.block_table + (size_t)b * p.pg.max_blocks + (tok >> p.pg.page_shift));
+                        blk = -1;
+                        if ((unsigned)page < (unsigned)p.pg.num_pages)
+                            blk = ((long long)page << (p.pg.page_shift - bs)) + ((tok & ((1 << p.pg.page_shift) - 1)) >> bs);
+                        else if (j4 == 0 && p.status)
+                            atomicOr(p.status, KVD_STATUS_BAD_PAGE);
+                    } else {
+                        blk = (long long)b * (p.S_max >> bs) + j;
+                    }
+                    if (blk >= 0) at[e] = blk * p.Hkv + h;
+                }
+            }
+        };
+        // Their codes and scales on the way to the lane's own places of a stage; `have` keeps which rows are there.
+        uint32_t have = 0;
+        const uint64_t policy = l2_evict_first_policy();
+        auto fetch = [&](int stage, const long long (&at)[2]) {
+            const uint32_t dst = smem_u32(ring) + stage * Sh::TILE + lane * 16;
+            have &= ~(3u << (2 * stage));
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const bool ok = at[e] >= 0;
+                const size_t a = ok ? (size_t)at[e] : 0;
+                have |= (ok ? 1u : 0u) << (2 * stage + e);
+                const int8_t* src = p.codes + a * 2 * D + 16 * j4;
+#pragma unroll
+                for (int c = 0; c < LOADS; ++c) cp_async_16(dst + (e * LOADS + c) * 512, src + 64 * c, ok ? 16 : 0, policy);
+                cp_async_4(dst - lane * 12 + 2 * LOADS * 512 + e * 128, p.scales + a, ok ? 4 : 0);
+            }
+        };
         for (int t0 = 0; t0 < p.T; t0 += toks) {
             const int nt = min(toks, p.T - t0);
-            const int tiles = G > 8 ? nt * per_tok : (nt * cols + 7) / 8;
             // Column x of a round: token x / (8 per_tok) row x % (8 per_tok) for wide groups, else token x / cols, row x % cols.
             auto column = [&](int x, int& t, int& r) {
                 const int w = G > 8 ? 8 * per_tok : cols;
@@ -75,97 +143,122 @@ __global__ void __launch_bounds__(kSelThreads, D == 256 ? 1 : 2) block_select_ke
                 r = x - t * w;
                 return t < nt && r < G;
             };
-            __syncthreads();
-            for (int x = warp; x < tiles * 8; x += kSelWarps) {  // the columns' scales
+            // The first tiles' loads run while the query rows become fragments.
+            constexpr int WORDS = D / 64;  // a lane's words of a query row
+            uint32_t qw[WORDS];
+            auto load_row = [&](int x) {
                 int t, r;
-                float s = __uint_as_float(0x7fffffffu);
-                if (column(x, t, r)) {
-                    const uint32_t* q = reinterpret_cast<const uint32_t*>(static_cast<const __nv_bfloat16*>(p.q) +
-                                                                          (((size_t)b * p.T + t0 + t) * p.Hq + (size_t)h * G + r) * D);
-                    uint32_t a = 0;  // magnitudes as integers: a NaN is the largest
-                    for (int i = lane; i < D / 2; i += 32) {
-                        const uint32_t w = __ldg(q + i);
-                        a = max(a, max(w & 0x7fffu, (w >> 16) & 0x7fffu));
+                const bool live = column(x, t, r);
+                const uint32_t* q = reinterpret_cast<const uint32_t*>(static_cast<const __nv_bfloat16*>(p.q) +
+                                                                      (((size_t)b * p.T + t0 + (live ? t : 0)) * p.Hq + (size_t)h * G + (live ? r : 0)) * D);
+#pragma unroll
+                for (int i = 0; i < WORDS; ++i) qw[i] = live ? __ldg(q + lane + 32 * i) : 0x7fc07fc0u;  // no row: NaN
+            };
+            if (warp < NT * 8) load_row(warp);
+            long long at[2];
+            look_up(first, at);
+#pragma unroll
+            for (int k = 0; k < STAGES - 1; ++k) {
+                fetch(k, at);
+                cp_async_commit();
+                look_up(first + (k + 1) * step, at);
+            }
+            if (t0 > 0) __syncthreads();
+#pragma unroll 1
+            for (int x = warp; x < NT * 8; x += kSelWarps) {
+                if (x > warp) load_row(x);
+                uint32_t a = 0;  // magnitudes as integers: a NaN is the largest
+#pragma unroll
+                for (int i = 0; i < WORDS; ++i) a = max(a, max(qw[i] & 0x7fffu, (qw[i] >> 16) & 0x7fffu));
+                a = __reduce_max_sync(0xffffffffu, a);
+                // A row that is not finite takes no part, as a column without a row: codes 0, scale NaN.
+                const float s = a < 0x7f80u ? __fdiv_rn(__uint_as_float(a << 16), 127.f) : __uint_as_float(0x7fffffffu);
+                int sum = 0;  // of the row's codes
+                // round(q / s): by the reciprocal, but where that may lie on the other side of a half by the quotient itself.
+                const float inv = s > 1e-30f ? __frcp_rn(s) : 0.f;
+#pragma unroll
+                for (int i = 0; i < WORDS; ++i) {
+                    const int col = 2 * (lane + 32 * i);  // of two neighbours: their fragment's lane, k-step and half
+                    float c[2] = {0.f, 0.f};
+                    if (s > 0.f) {
+                        bool near = inv == 0.f;
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const float x = (e ? bf16_hi(qw[i]) : bf16_lo(qw[i])) * inv;  // off by 2^-22 of itself at most, below 2^7
+                            c[e] = rintf(x);
+                            near |= fabsf(fabsf(x - c[e]) - 0.5f) < 1e-4f;
+                        }
+                        if (near) {
+#pragma unroll
+                            for (int e = 0; e < 2; ++e) c[e] = rintf(__fdiv_rn(e ? bf16_hi(qw[i]) : bf16_lo(qw[i]), s));
+                        }
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) c[e] = fminf(fmaxf(c[e], -127.f), 127.f);
                     }
-                    a = __reduce_max_sync(0xffffffffu, a);
-                    if (a < 0x7f80u) s = __fdiv_rn(__uint_as_float(a << 16), 127.f);  // a row that is not finite takes no part
+                    const int ks = 4 * (col >> 6) + ((col >> 2) & 3), ln = 4 * (x & 7) + ((col >> 4) & 3);
+                    uint32_t* f = reinterpret_cast<uint32_t*>(s_q + ((size_t)(x >> 3) * KS + ks) * 32 + ln) + ((col >> 1) & 1);
+                    f[0] = pack_f16x2(fmaxf(c[0], 0.f), fmaxf(c[1], 0.f));
+                    f[KS / 2 * 64] = pack_f16x2(fminf(c[0], 0.f), fminf(c[1], 0.f));
+                    sum += (int)c[0] + (int)c[1];
                 }
-                if (lane == 0) s_sc[x] = s;
+                sum = __reduce_add_sync(0xffffffffu, sum);
+                if (lane == 0) s_sc[x] = s, s_bias[x] = (float)sum * -0x1p-17f;  // -128 of them, in units of 2^-24
             }
             __syncthreads();
-            for (int i = tid; i < tiles * KS * 32; i += kSelThreads) {  // and their codes as fragments
-                const int ln = i & 31, ks = (i >> 5) % KS, x = (i >> 5) / KS * 8 + (ln >> 2);
-                const int col = 64 * (ks >> 2) + 16 * (ln & 3) + 4 * (ks & 3);  // the first of four, of the 2 D columns
-                int t, r;
-                uint2 f = make_uint2(0u, 0u);
-                const float s = s_sc[x];
-                if (column(x, t, r) && s > 0.f) {
-                    const uint2 w = __ldg(reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(p.q) +
-                                                                         (((size_t)b * p.T + t0 + t) * p.Hq + (size_t)h * G + r) * D + (col & (D - 1))));
-                    const float v[4] = {bf16_lo(w.x), bf16_hi(w.x), bf16_lo(w.y), bf16_hi(w.y)};
-                    float c[4];
+            int stage = 0;
+            for (int j0 = first; j0 < full; j0 += step) {
+                const int next = stage == 0 ? STAGES - 1 : stage - 1;  // the stage read last
+                asm volatile("" ::: "memory");  // (a lane waits for its own copies alone: no barrier orders its loads)
+                if (j0 + (STAGES - 1) * step < full) fetch(next, at);
+                cp_async_commit();
+                look_up(j0 + STAGES * step, at);
+                cp_async_wait<STAGES - 1>();
+                asm volatile("" ::: "memory");
+                const uint8_t* mine = ring + stage * Sh::TILE + lane * 16;
+                // Codes enter the MMAs as code + 128 in the low bits of an f16, a subnormal of that many 2^-24; the sums start
+                // from what that adds. Products and sums are whole numbers below 2^24 in these units: exact.
+                float acc[NT][4], acc2[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        c[e] = fminf(fmaxf(rintf(__fdiv_rn(v[e], s)), -127.f), 127.f);
-                        c[e] = col < D ? fmaxf(c[e], 0.f) : fminf(c[e], 0.f);
-                    }
-                    f = make_uint2(pack_f16x2(c[0], c[1]), pack_f16x2(c[2], c[3]));
+                for (int n = 0; n < NT; ++n) {
+                    acc[n][0] = acc[n][2] = s_bias[8 * n + 2 * j4];
+                    acc[n][1] = acc[n][3] = s_bias[8 * n + 2 * j4 + 1];
                 }
-                s_q[i] = f;
-            }
-            __syncthreads();
-            for (int j0 = (rank * kSelWarps + warp) * 16; j0 < full; j0 += p.parts * kSelWarps * 16) {
-                // Rows j0 + g8 and j0 + g8 + 8: their codes, 16 bytes a load, and scales.
-                uint4 w[2][LOADS];
-                float sc[2];
-                bool ok[2];
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const int j = j0 + g8 + 8 * e;
-                    long long blk = -1;
-                    if (j < full) {
-                        if (p.pg.block_table) {
-                            const int tok = j << bs;
-                            const int page = __ldg(p.pg.block_table + (size_t)b * p.pg.max_blocks + (tok >> p.pg.page_shift));
-                            if ((unsigned)page < (unsigned)p.pg.num_pages)
-                                blk = ((long long)page << (p.pg.page_shift - bs)) + ((tok & ((1 << p.pg.page_shift) - 1)) >> bs);
-                            else if (j4 == 0 && p.status)
-                                atomicOr(p.status, KVD_STATUS_BAD_PAGE);
-                        } else {
-                            blk = (long long)b * (p.S_max >> bs) + j;
+                for (int c = 0; c < LOADS; ++c) {
+                    const uint4 wx = *reinterpret_cast<const uint4*>(mine + c * 512), wy = *reinterpret_cast<const uint4*>(mine + (LOADS + c) * 512);
+                    const uint32_t x[4] = {wx.x, wx.y, wx.z, wx.w}, y[4] = {wy.x, wy.y, wy.z, wy.w};
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const uint32_t ux = x[i] ^ 0x80808080u, uy = y[i] ^ 0x80808080u;
+                        const uint32_t a[4] = {__byte_perm(ux, 0, 0x4140), __byte_perm(uy, 0, 0x4140), __byte_perm(ux, 0, 0x4342),
+                                               __byte_perm(uy, 0, 0x4342)};
+                        const uint2* fq = s_q + (4 * c + i) * 32 + lane;
+#pragma unroll
+                        for (int n = 0; n < NT; ++n) {
+                            const uint2 f = fq[n * KS * 32];
+                            mma_f16_16816((NT == 1 && (i & 1)) ? acc2 : acc[n], a, f.x, f.y);
                         }
                     }
-                    ok[e] = blk >= 0;
-                    const size_t at = (size_t)(ok[e] ? blk : 0) * p.Hkv + h;
-                    const uint4* src = reinterpret_cast<const uint4*>(p.codes + at * 2 * D) + j4;
+                }
+                const bool ok[2] = {(bool)((have >> (2 * stage)) & 1u), (bool)((have >> (2 * stage + 1)) & 1u)};
+                float sc[2];
 #pragma unroll
-                    for (int c = 0; c < LOADS; ++c) w[e][c] = ok[e] ? __ldg(src + 4 * c) : make_uint4(0u, 0u, 0u, 0u);
-                    sc[e] = ok[e] ? __ldg(p.scales + at) : 0.f;
+                for (int e = 0; e < 2; ++e) sc[e] = *reinterpret_cast<const float*>(mine - lane * 12 + 2 * LOADS * 512 + e * 128);
+                stage = stage + 1 == STAGES ? 0 : stage + 1;
+                if constexpr (NT == 1) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) acc[0][e] += acc2[e];
                 }
                 float best[2][2];  // [block][column of the lane's two]
-                for (int n = 0; n < tiles; ++n) {
-                    float acc[4] = {0.f, 0.f, 0.f, 0.f}, acc2[4] = {0.f, 0.f, 0.f, 0.f};
-                    const uint2* fq = s_q + (size_t)n * KS * 32 + lane;
 #pragma unroll
-                    for (int c = 0; c < LOADS; ++c) {
-                        const uint32_t x[4] = {w[0][c].x, w[0][c].y, w[0][c].z, w[0][c].w};
-                        const uint32_t y[4] = {w[1][c].x, w[1][c].y, w[1][c].z, w[1][c].w};
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            uint32_t a[4];
-                            i8x4_to_f16x2x2(x[i], a[0], a[2]);
-                            i8x4_to_f16x2x2(y[i], a[1], a[3]);
-                            const uint2 f = fq[(4 * c + i) * 32];
-                            mma_f16_16816((i & 1) ? acc2 : acc, a, f.x, f.y);
-                        }
-                    }
+                for (int n = 0; n < NT; ++n) {
                     const float s0 = s_sc[8 * n + 2 * j4], s1 = s_sc[8 * n + 2 * j4 + 1];
-                    const bool first = G <= 8 || n % per_tok == 0;
+                    const bool fresh = G <= 8 || n % per_tok == 0;
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {  // (fmaxf passes the NaN of a column without a row over)
-                        const float v0 = __fmul_rn(acc[2 * e] + acc2[2 * e], s0), v1 = __fmul_rn(acc[2 * e + 1] + acc2[2 * e + 1], s1);
-                        best[e][0] = fmaxf(first ? -CUDART_INF_F : best[e][0], v0);
-                        best[e][1] = fmaxf(first ? -CUDART_INF_F : best[e][1], v1);
+                        const float v0 = __fmul_rn(acc[n][2 * e] * 0x1p24f, s0), v1 = __fmul_rn(acc[n][2 * e + 1] * 0x1p24f, s1);
+                        best[e][0] = fmaxf(fresh ? -CUDART_INF_F : best[e][0], v0);
+                        best[e][1] = fmaxf(fresh ? -CUDART_INF_F : best[e][1], v1);
                     }
                     if (G > 8 && n % per_tok != per_tok - 1) continue;
                     // The maximum over a token's columns, and its key: `cols` columns a token, tokens side by side.
@@ -189,6 +282,7 @@ __global__ void __launch_bounds__(kSelThreads, D == 256 ? 1 : 2) block_select_ke
                     }
                 }
             }
+            cp_async_wait<0>();
         }
     }
     if (p.parts > 1)
@@ -206,91 +300,141 @@ __global__ void __launch_bounds__(kSelThreads, D == 256 ? 1 : 2) block_select_ke
             continue;
         }
         // Blocks [lo_j, hi_j) compete for the places that the first and last ones leave; all of them have bounds.
-        const int lo_j = p.n_first, hi_j = nb - p.n_last, n = hi_j - lo_j, want = p.K - p.n_first - p.n_last;
-        const uint32_t* src = keys + (size_t)t * p.key_stride + lo_j;
-        const bool fits = n <= kSelRoom / 4;
-        const int chunk = ((n + kSelThreads - 1) / kSelThreads) | 1;  // a thread's keys in a row; odd: lanes in different banks
-        __syncthreads();
+        const int lo_j = p.n_first, hi_j = nb - p.n_last, want = p.K - p.n_first - p.n_last;
+        const uint32_t* src = keys + (size_t)t * p.key_stride;
+        for (int i = tid; i < p.n_first; i += kSelThreads) out[i] = i;
+        for (int i = tid; i < p.n_last; i += kSelThreads) out[p.K - p.n_last + i] = hi_j + i;
+        if (want == 0) continue;
+        // Keys, four at a time, in shared memory where they fit, else where they lie (the workspace, in L2). Of the first and
+        // the last vector some do not compete.
+        const int vecs = (hi_j + 3) / 4;
+        const bool fits = (long long)vecs * 16 + kSelBins * 4 + kSelTies * 8 <= room;
+        __syncthreads();  // the token before is done with the shared memory
+        for (int i = tid; i < kSelBins / 4; i += kSelThreads) reinterpret_cast<uint4*>(s_hist)[i] = make_uint4(0u, 0u, 0u, 0u);
+        if (tid == 0) s_ties = 0;
+        const uint4* far4 = reinterpret_cast<const uint4*>(src);
+        uint4* near4 = reinterpret_cast<uint4*>(s_key);
+        auto each = [&](int v, const uint4& x, auto&& f) {
+            const uint32_t k[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (4 * v + e >= lo_j && 4 * v + e < hi_j) f(4 * v + e, k[e]);
+        };
+        // f(index, key) for vectors from, from + step, ... below `to`, four loads at once where they lie far.
+        auto sweep = [&](int from, int to, int step, auto&& f) {
+            if (fits) {
+#pragma unroll 1
+                for (int v = from; v < to; v += step) each(v, near4[v], f);
+            } else {
+#pragma unroll 1
+                for (int v = from; v < to; v += 4 * step) {
+                    uint4 x[4];
+#pragma unroll
+                    for (int u = 0; u < 4; ++u)
+                        if (v + u * step < to) x[u] = __ldcg(far4 + v + u * step);
+#pragma unroll
+                    for (int u = 0; u < 4; ++u)
+                        if (v + u * step < to) each(v + u * step, x[u], f);
+                }
+            }
+        };
         uint32_t mn = 0xffffffffu, mx = 0u;
-        for (int i = tid; i < n; i += kSelThreads) {
-            const uint32_t k = __ldcg(src + i);
-            if (fits) s_key[i] = k;
-            mn = min(mn, k);
-            mx = max(mx, k);
+        auto span = [&](int, uint32_t k) { mn = min(mn, k), mx = max(mx, k); };
+        if (fits) {
+            for (int v = tid; v < vecs; v += kSelThreads) {
+                const uint4 x = __ldcg(far4 + v);
+                near4[v] = x;
+                each(v, x, span);
+            }
+        } else {
+            sweep(tid, vecs, kSelThreads, span);
         }
         mn = __reduce_min_sync(0xffffffffu, mn);
         mx = __reduce_max_sync(0xffffffffu, mx);
         if (lane == 0) s_a[warp] = mn, s_b[warp] = mx;
         __syncthreads();
-        if (tid == 0) {
-            for (int w = 1; w < kSelWarps; ++w) mn = min(mn, s_a[w]), mx = max(mx, s_b[w]);
-            s_lo = mn;
-            s_hi = mx;
-            s_need = (uint32_t)want;
-            s_done = 0;
-        }
-        auto key = [&](int i) { return fits ? s_key[i] : __ldcg(src + i); };
-        // Keys above s_hi are kept, s_need of those in [s_lo, s_hi] too.
-        uint32_t lo, hi, need;
-        bool whole = false;  // the border's part is kept whole
-        if (want > 0) {
-            while (true) {
-                for (int i = tid; i < kSelBins; i += kSelThreads) s_hist[i] = 0;
-                __syncthreads();
-                lo = s_lo, hi = s_hi, need = s_need;
-                const int shift = max(0, 21 - __clz(hi - lo));  // (hi - lo) >> shift is below 2,048
-                for (int i = tid; i < n; i += kSelThreads) {
-                    const uint32_t k = key(i);
-                    if (k >= lo && k <= hi) atomicAdd(&s_hist[(k - lo) >> shift], 1u);
-                }
-                __syncthreads();
-                // Thread i adds up 8 parts, from the top; the one in which the running sum reaches `need` has the border.
-                constexpr int PER = kSelBins / kSelThreads;
-                uint32_t cnt[PER], sum = 0;
+        uint32_t lo = s_a[0], hi = s_b[0], need = (uint32_t)want;
+#pragma unroll
+        for (int w = 1; w < kSelWarps; ++w) lo = min(lo, s_a[w]), hi = max(hi, s_b[w]);
+        // Keys above hi are kept, `need` of those in [lo, hi] too: rounds of a histogram over 2,048 equal parts of that range,
+        // until few keys are left in the part that has the border, or all of them are kept, or it is one value.
+        // (A round takes 11 bits off the range: three at most.)
+        uint32_t count = 0;
+#pragma unroll 1
+        for (int round = 0; round < 3; ++round) {
+            const int shift = max(0, 21 - __clz(hi - lo));  // (hi - lo) >> shift is below 2,048
+            sweep(tid, vecs, kSelThreads, [&](int, uint32_t k) {
+                if (k >= lo && k <= hi) atomicAdd(&s_hist[(k - lo) >> shift], 1u);
+            });
+            __syncthreads();
+            // Thread i adds up 8 parts, from the top, and leaves zeros; the one in which the running sum reaches `need` has the border.
+            constexpr int PER = kSelBins / kSelThreads;
+            static_assert(PER % 4 == 0, "whole vectors");
+            uint4* hp = reinterpret_cast<uint4*>(s_hist + kSelBins - PER * (tid + 1));
+            uint32_t cnt[PER], sum = 0;
+#pragma unroll
+            for (int e = 0; e < PER / 4; ++e) {
+                const uint4 x = hp[PER / 4 - 1 - e];
+                hp[PER / 4 - 1 - e] = make_uint4(0u, 0u, 0u, 0u);
+                cnt[4 * e] = x.w, cnt[4 * e + 1] = x.z, cnt[4 * e + 2] = x.y, cnt[4 * e + 3] = x.x;
+                sum += x.x + x.y + x.z + x.w;
+            }
+            uint32_t incl = sum;
+#pragma unroll
+            for (int off = 1; off < 32; off <<= 1) {
+                const uint32_t x = __shfl_up_sync(0xffffffffu, incl, off);
+                if (lane >= off) incl += x;
+            }
+            if (lane == 31) s_a[warp] = incl;
+            __syncthreads();
+            uint32_t before = incl - sum;
+#pragma unroll
+            for (int w = 0; w < kSelWarps; ++w) before += w < warp ? s_a[w] : 0u;
+            if (before < need && before + sum >= need) {
+                uint32_t at = before;
 #pragma unroll
                 for (int e = 0; e < PER; ++e) {
-                    cnt[e] = s_hist[kSelBins - 1 - (tid * PER + e)];
-                    sum += cnt[e];
-                }
-                uint32_t incl = sum;
-#pragma unroll
-                for (int off = 1; off < 32; off <<= 1) {
-                    const uint32_t x = __shfl_up_sync(0xffffffffu, incl, off);
-                    if (lane >= off) incl += x;
-                }
-                if (lane == 31) s_a[warp] = incl;
-                __syncthreads();
-                uint32_t before = incl - sum;
-                for (int w = 0; w < warp; ++w) before += s_a[w];
-                if (before < need && before + sum >= need) {
-                    uint32_t at = before;
-#pragma unroll
-                    for (int e = 0; e < PER; ++e) {
-                        if (at < need && at + cnt[e] >= need) {
-                            const uint32_t part = kSelBins - 1 - (tid * PER + e), low = lo + (part << shift);
-                            s_lo = low;
-                            s_hi = shift == 0 ? low : min(hi, low + ((1u << shift) - 1));
-                            s_need = need - at;
-                            s_done = (shift == 0 || cnt[e] == need - at) ? 1 : 0;
-                        }
-                        at += cnt[e];
+                    if (at < need && at + cnt[e] >= need) {
+                        const uint32_t part = kSelBins - 1 - (tid * PER + e), low = lo + (part << shift);
+                        s_lo = low;
+                        s_hi = shift == 0 ? low : min(hi, low + ((1u << shift) - 1));
+                        s_need = need - at;
+                        s_count = cnt[e];
                     }
+                    at += cnt[e];
                 }
-                __syncthreads();
-                if (s_done) break;
             }
-            lo = s_lo, hi = s_hi, need = s_need;
-            whole = lo != hi;  // (one value: the first `need` of them in order)
-        } else {
-            lo = hi = 0xffffffffu, need = 0;
+            __syncthreads();
+            lo = s_lo, hi = s_hi, need = s_need, count = s_count;
+            if (lo == hi || count == need || count <= kSelTies) break;
         }
-        // ---- kept blocks in order: a thread's run of keys, counted, then written behind the runs before ----
-        const int i0 = min(tid * chunk, n), i1 = min(i0 + chunk, n);
+        // ---- which are kept: a thread's run of keys; those at the border by their rank among each other ----
+        const bool value = lo == hi;                                             // one value: the first `need` of them in order
+        const bool ranked = !value && count != need && count <= kSelTies;
+        const int run = ((vecs + kSelThreads - 1) / kSelThreads) | 1;            // a thread's vectors; odd: lanes in different banks
+        const int v0 = min(tid * run, vecs), v1 = min(v0 + run, vecs);
         uint32_t above = 0, equal = 0;
-        for (int i = i0; i < i1; ++i) {
-            const uint32_t k = key(i);
-            above += k > hi || (whole && k >= lo);
-            equal += !whole && k == lo;
+        sweep(v0, v1, 1, [&](int i, uint32_t k) {
+            above += k > hi || (!value && !ranked && k >= lo);
+            if (k >= lo && k <= hi) {
+                equal += value;
+                if (ranked) s_tie[atomicAdd(&s_ties, 1u) & (kSelTies - 1)] = make_uint2(k, (uint32_t)i);
+            }
+        });
+        auto keeps = [&](uint32_t k, int i) {  // of the ranked ones
+            uint32_t ahead = 0;
+            for (uint32_t e = 0; e < count; ++e) {
+                const uint2 x = s_tie[e];
+                ahead += x.x > k || (x.x == k && x.y < (uint32_t)i);
+            }
+            return ahead < need;
+        };
+        if (ranked) {
+            __syncthreads();
+            for (uint32_t e = 0; e < count; ++e) {
+                const uint2 x = s_tie[e];
+                if ((int)x.y >= 4 * v0 && (int)x.y < 4 * v1) above += keeps(x.x, (int)x.y);
+            }
         }
         uint32_t ia = above, ie = equal;
 #pragma unroll
@@ -298,29 +442,25 @@ __global__ void __launch_bounds__(kSelThreads, D == 256 ? 1 : 2) block_select_ke
             const uint32_t x = __shfl_up_sync(0xffffffffu, ia, off), y = __shfl_up_sync(0xffffffffu, ie, off);
             if (lane >= off) ia += x, ie += y;
         }
-        __syncthreads();
-        if (lane == 31) s_a[warp] = ia, s_b[warp] = ie;
+        if (lane == 31) s_b[warp] = ia, s_a[warp] = ie;  // (s_a was read before the barrier above)
         __syncthreads();
         uint32_t pa = ia - above, pe = ie - equal;
-        for (int w = 0; w < warp; ++w) pa += s_a[w], pe += s_b[w];
-        uint32_t at = pa + min(pe, need);
-        for (int i = i0; i < i1; ++i) {
-            const uint32_t k = key(i);
-            bool keep = k > hi || (whole && k >= lo);
-            if (!whole && k == lo) keep = pe++ < need;
-            if (keep) out[p.n_first + at++] = lo_j + i;
-        }
-        for (int i = tid; i < p.n_first; i += kSelThreads) out[i] = i;
-        for (int i = tid; i < p.n_last; i += kSelThreads) out[p.K - p.n_last + i] = hi_j + i;
+#pragma unroll
+        for (int w = 0; w < kSelWarps; ++w) pa += w < warp ? s_b[w] : 0u, pe += w < warp ? s_a[w] : 0u;
+        uint32_t at = pa + (value ? min(pe, need) : 0u);
+        if (above + equal > 0)
+            sweep(v0, v1, 1, [&](int i, uint32_t k) {
+                bool keep = k > hi;
+                if (k >= lo && k <= hi) keep = value ? pe++ < need : ranked ? keeps(k, i) : true;
+                if (keep && at < (uint32_t)want) out[p.n_first + at++] = i;
+            });
     }
 }
 
 cudaError_t launch_block_select(const SelectParams& p, cudaStream_t stream) {
-    static std::atomic<uint64_t> ready[3];
+    static std::atomic<uint64_t> ready[15];
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)((long long)p.B * p.Hkv * p.parts), 1, 1);
-    cfg.blockDim = dim3(kSelThreads, 1, 1);
-    cfg.dynamicSmemBytes = kSelRoom;
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -330,11 +470,22 @@ cudaError_t launch_block_select(const SelectParams& p, cudaStream_t stream) {
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-#define KVD_SELECT(DD, i)                                                                                                \
-    ([&]() {                                                                                                             \
-        const cudaError_t e = allow_clusters(reinterpret_cast<const void*>(block_select_kernel<DD>), kSelRoom, &ready[i]); \
-        return e == cudaSuccess ? cudaLaunchKernelEx(&cfg, block_select_kernel<DD>, p) : e;                              \
-    }())
+    auto launch = [&](auto shape, auto kernel, int tiles, std::atomic<uint64_t>* done) {
+        using Sh = decltype(shape);
+        const int smem = tiles * Sh::FRAG + Sh::RING;
+        const cudaError_t e = allow_clusters(reinterpret_cast<const void*>(kernel), smem, done);
+        if (e != cudaSuccess) return e;
+        cfg.blockDim = dim3(Sh::THREADS, 1, 1);
+        cfg.dynamicSmemBytes = (size_t)smem;
+        return cudaLaunchKernelEx(&cfg, kernel, p, smem);
+    };
+#define KVD_SELECT(DD, i)                                                                                \
+    (tiles == 1   ? launch(SelectShape<DD>(), block_select_kernel<DD, 1>, 1, &ready[5 * i])              \
+     : tiles == 2 ? launch(SelectShape<DD>(), block_select_kernel<DD, 2>, 2, &ready[5 * i + 1])          \
+     : tiles == 4 ? launch(SelectShape<DD>(), block_select_kernel<DD, 4>, 4, &ready[5 * i + 2])          \
+     : tiles == 6 ? launch(SelectShape<DD>(), block_select_kernel<DD, 6>, 6, &ready[5 * i + 3])          \
+                  : launch(SelectShape<DD>(), block_select_kernel<DD, 8>, 8, &ready[5 * i + 4]))
+    const int tiles = select_tiles(p.G, p.T);
     switch (p.D) {
         case 64: return KVD_SELECT(64, 0);
         case 128: return KVD_SELECT(128, 1);
@@ -342,6 +493,14 @@ cudaError_t launch_block_select(const SelectParams& p, cudaStream_t stream) {
         default: return cudaErrorInvalidValue;
     }
 #undef KVD_SELECT
+}
+
+int select_ctas(int D, int G, int T) {
+    const int tiles = select_tiles(G, T);
+    const int smem = D == 64 ? tiles * SelectShape<64>::FRAG + SelectShape<64>::RING
+                   : D == 128 ? tiles * SelectShape<128>::FRAG + SelectShape<128>::RING
+                              : tiles * SelectShape<256>::FRAG + SelectShape<256>::RING;
+    return std::max(1, std::min(D == 256 ? 1 : tiles == 1 ? 3 : 2, 227 * 1024 / (smem + 2048)));
 }
 
 }  // namespace kvd

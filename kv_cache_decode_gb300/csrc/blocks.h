@@ -59,6 +59,7 @@ struct SelectParams {
     PagedCache pg;
 };
 cudaError_t launch_block_select(const SelectParams& p, cudaStream_t stream);
+int select_ctas(int D, int G, int T);  // resident CTAs of a multiprocessor
 
 // Page tables from lengths (pages.cu).
 struct PagesParams {
