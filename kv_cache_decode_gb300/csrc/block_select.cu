@@ -8,26 +8,27 @@
 // matter of definition and not of the order of additions.
 //
 // Reads 2 D + 4 bytes a (block, KV head) once for all query tokens; bound by memory for batches, by latency for one
-// sequence. A cluster of up to 16 CTAs takes a (sequence, KV head). First its warps score tiles of 16 blocks: f16 MMAs
+// sequence. The first launch scores, some CTAs a (sequence, KV head), a warp tiles of 16 blocks: f16 MMAs
 // m16n8k16 with the blocks as rows and the query rows as columns, I = [hi lo] [max(c, 0) min(c, 0)]^T. A code enters as code + 128
 // in the low bits of an f16, a subnormal; products and sums of these are whole numbers below 2^24 (times 2^-24), so exact. A lane's 16-byte
 // copy is 16 consecutive codes of a row; the MMA's k order is the permutation of columns that fits, the same for both operands, so codes
 // go from the lane's own place in shared memory to fragments without a shuffle, and a warp waits for its own copies alone. Keys
-// (scores as ordered integers) go to the workspace, the cluster meets at a barrier, and CTA i selects for the query tokens i, i + CTAs, ...: a
+// (scores as ordered integers) go to the workspace. A second launch selects, a CTA a (sequence, query token, KV head): a
 // histogram over 2,048 equal parts of the range [smallest, largest] of the keys, then (seldom) over the part that holds the border, until
-// that part has few keys, which are ranked one by one.
+// that part has few keys, which are ranked one by one; the kept ones become bits, the bits the list.
 #include <math_constants.h>
 
 #include <algorithm>
 
 #include "../../include/kvdecode.h"
 #include "blocks.h"
-#include "cluster.cuh"
 #include "common.cuh"
 
 namespace kvd {
 
+constexpr uint32_t kSelNoPage = 1u; // key of a block that has no page: below every score's; 0 is below all
 constexpr int kSelBins = 2048;
+constexpr int kPickThreads = 512;
 constexpr int kSelTiles = 8;        // column tiles of 8 query rows scored at once
 constexpr int kSelTies = 64;        // keys around the border that are ranked one by one
 
@@ -43,7 +44,6 @@ struct SelectShape {
     static constexpr int FRAG = KS * 32 * 8;                   // a column tile's fragments
     static constexpr int MOST = kSelTiles * FRAG + RING;
     static_assert(MOST + 2 * 1024 <= 227 * 1024, "shared memory of a CTA");
-    static_assert(RING >= kSelBins * 4 + kSelTies * 8, "the selection's counts");
 };
 
 __device__ __forceinline__ uint32_t score_key(float s) {  // larger score, larger key; NaN as +inf, -0 as +0
@@ -64,35 +64,30 @@ static int select_tiles(int G, int T) {
 
 // NT: column tiles of a round.
 template <int D, int NT>
-__global__ void __launch_bounds__(SelectShape<D>::THREADS, D == 256 ? 1 : NT == 1 ? 3 : 2) block_select_kernel(const SelectParams p, int room) {
+__global__ void __launch_bounds__(SelectShape<D>::THREADS, D == 256 ? 1 : NT == 1 ? 3 : 2) block_score_kernel(const SelectParams p) {
     using Sh = SelectShape<D>;
-    constexpr int kSelThreads = Sh::THREADS, kSelWarps = Sh::WARPS;
+    constexpr int WARPS = Sh::WARPS;
     constexpr int KS = Sh::KS, LOADS = Sh::LOADS, STAGES = Sh::STAGES;
     extern __shared__ __align__(16) uint8_t smem[];
     uint2* s_q = reinterpret_cast<uint2*>(smem);         // [tile][k-step][lane]: B fragments
-    uint32_t* s_hist = reinterpret_cast<uint32_t*>(smem); // later: a histogram, keys around the border, and one query token's keys
-    uint2* s_tie = reinterpret_cast<uint2*>(s_hist + kSelBins);
-    uint32_t* s_key = reinterpret_cast<uint32_t*>(s_tie + kSelTies);
     __shared__ float s_sc[kSelTiles * 8];                // the columns' scales, NaN: no query row
     __shared__ float s_bias[kSelTiles * 8];              // what their sums start from
-    __shared__ uint32_t s_a[kSelWarps], s_b[kSelWarps];
-    __shared__ uint32_t s_lo, s_hi, s_need, s_count, s_ties;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, j4 = lane & 3, g8 = lane >> 2;
     const int rank = blockIdx.x % p.parts, pair = blockIdx.x / p.parts, h = pair % p.Hkv, b = pair / p.Hkv;
     const int bs = p.block_shift, G = p.G;
     pdl_wait();
     pdl_launch_dependents();
     const int raw = __ldg(p.seq_lens + b), L = raw < 0 ? 0 : raw > p.len_cap ? p.len_cap : raw;
-    if (raw != L && h == 0 && rank == 0 && tid == 0 && p.status) atomicOr(p.status, KVD_STATUS_SEQ_LEN_CLAMPED);
     const int full = L >> bs;  // blocks with bounds
     uint32_t* keys = p.keys + (size_t)pair * p.T * p.key_stride;  // [T][key_stride]
 
-    // ---- scores, unless the last query token keeps every block ----
-    if ((int)(((long long)L + (1 << bs) - 1) >> bs) > p.K) {
+    // (Nothing to score where the last query token keeps every block.)
+    const int first = (rank * WARPS + warp) * 16, step = p.parts * WARPS * 16;
+    if ((int)(((long long)L + (1 << bs) - 1) >> bs) <= p.K || rank * WARPS * 16 >= full) return;
+    {
         const int cols = sel_columns(G);                 // columns of a token in a tile
         const int per_tok = (G + 7) / 8;                 // tiles of a token (G > 8: several)
         const int toks = G > 8 ? NT / per_tok : NT * (8 / cols);  // tokens of a round
-        const int first = (rank * kSelWarps + warp) * 16, step = p.parts * kSelWarps * 16;
         uint8_t* ring = smem + NT * Sh::FRAG + warp * STAGES * Sh::TILE;
         // A tile's rows of this lane: blocks j0 + g8 and j0 + g8 + 8, by their place among all bounds (-1: none).
         auto look_up = [&](int j0, long long (&at)[2]) {
@@ -165,7 +160,7 @@ __global__ void __launch_bounds__(SelectShape<D>::THREADS, D == 256 ? 1 : NT == 
             }
             if (t0 > 0) __syncthreads();
 #pragma unroll 1
-            for (int x = warp; x < NT * 8; x += kSelWarps) {
+            for (int x = warp; x < NT * 8; x += WARPS) {
                 if (x > warp) load_row(x);
                 uint32_t a = 0;  // magnitudes as integers: a NaN is the largest
 #pragma unroll
@@ -272,10 +267,10 @@ __global__ void __launch_bounds__(SelectShape<D>::THREADS, D == 256 ? 1 : NT == 
                         const int j = j0 + g8 + 8 * e;
                         if (j >= full) continue;
                         const int t = G > 8 ? n / per_tok : (8 * n + 2 * j4) / cols;  // of this round
-                        const uint32_t k0 = ok[e] ? score_key(__fmul_rn(v0, sc[e])) : 0u;
+                        const uint32_t k0 = ok[e] ? score_key(__fmul_rn(v0, sc[e])) : kSelNoPage;
                         if (width == 1) {
                             if (t < nt) keys[(size_t)(t0 + t) * p.key_stride + j] = k0;
-                            if (t + 1 < nt) keys[(size_t)(t0 + t + 1) * p.key_stride + j] = ok[e] ? score_key(__fmul_rn(v1, sc[e])) : 0u;
+                            if (t + 1 < nt) keys[(size_t)(t0 + t + 1) * p.key_stride + j] = ok[e] ? score_key(__fmul_rn(v1, sc[e])) : kSelNoPage;
                         } else if ((2 * j4) % width == 0 && t < nt) {
                             keys[(size_t)(t0 + t) * p.key_stride + j] = k0;
                         }
@@ -285,191 +280,182 @@ __global__ void __launch_bounds__(SelectShape<D>::THREADS, D == 256 ? 1 : NT == 
             cp_async_wait<0>();
         }
     }
-    if (p.parts > 1)
-        cluster_sync();
-    else
-        __syncthreads();
+}
 
-    // ---- the selection ----
-    for (int t = rank; t < p.T; t += p.parts) {
-        const int seen = L - p.T + 1 + t;
-        const int nb = seen > 0 ? (int)(((long long)seen + (1 << bs) - 1) >> bs) : 0;  // blocks the token sees
-        int32_t* out = p.blocks + (((size_t)b * p.T + t) * p.Hkv + h) * p.K;
-        if (nb <= p.K) {
-            for (int i = tid; i < p.K; i += kSelThreads) out[i] = i < nb ? i : -1;
-            continue;
+// The selection: a CTA for a (sequence, query token, KV head).
+__global__ void __launch_bounds__(kPickThreads) block_pick_kernel(const SelectParams p, int room) {
+    constexpr int WARPS = kPickThreads / 32;
+    extern __shared__ __align__(16) uint8_t smem[];
+    uint32_t* s_hist = reinterpret_cast<uint32_t*>(smem);
+    uint2* s_tie = reinterpret_cast<uint2*>(s_hist + kSelBins);
+    uint32_t* s_key = reinterpret_cast<uint32_t*>(s_tie + kSelTies);
+    __shared__ uint32_t s_a[WARPS], s_b[WARPS];
+    __shared__ uint32_t s_lo, s_hi, s_need, s_count, s_ties;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int h = blockIdx.x % p.Hkv, bt = blockIdx.x / p.Hkv, t = bt % p.T, b = bt / p.T, bs = p.block_shift;
+    for (int i = tid; i < kSelBins / 4; i += kPickThreads) reinterpret_cast<uint4*>(s_hist)[i] = make_uint4(0u, 0u, 0u, 0u);
+    if (tid == 0) s_ties = 0;
+    pdl_wait();
+    pdl_launch_dependents();
+    const int raw = __ldg(p.seq_lens + b), L = raw < 0 ? 0 : raw > p.len_cap ? p.len_cap : raw;
+    if (raw != L && h == 0 && t == 0 && tid == 0 && p.status) atomicOr(p.status, KVD_STATUS_SEQ_LEN_CLAMPED);
+    const int seen = L - p.T + 1 + t;
+    const int nb = seen > 0 ? (int)(((long long)seen + (1 << bs) - 1) >> bs) : 0;  // blocks the token sees
+    int32_t* out = p.blocks + (size_t)blockIdx.x * p.K;
+    if (nb <= p.K) {
+        for (int i = tid; i < p.K; i += kPickThreads) out[i] = i < nb ? i : -1;
+        return;
+    }
+    // Blocks [lo_j, hi_j) compete for the places that the first and last ones leave; all of them have bounds.
+    const int lo_j = p.n_first, hi_j = nb - p.n_last, want = p.K - p.n_first - p.n_last;
+    const uint32_t* src = p.keys + (((size_t)b * p.Hkv + h) * p.T + t) * p.key_stride;
+    for (int i = tid; i < p.n_first; i += kPickThreads) out[i] = i;
+    for (int i = tid; i < p.n_last; i += kPickThreads) out[p.K - p.n_last + i] = hi_j + i;
+    if (want == 0) return;
+    // Keys in shared memory where they fit (0 for those of the first and last vector that do not compete), else where they
+    // lie (the workspace, in L2).
+    const int vecs = (hi_j + 3) / 4;
+    const bool fits = (long long)vecs * 16 + kSelBins * 4 + kSelTies * 8 <= room;
+    const uint32_t* key = fits ? s_key : src;
+    uint32_t mn = 0xffffffffu, mx = 0u;
+#pragma unroll 2
+    for (int v = tid; v < vecs; v += kPickThreads) {
+        const uint4 x = __ldcg(reinterpret_cast<const uint4*>(src) + v);
+        uint32_t k[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const bool in = 4 * v + e >= lo_j && 4 * v + e < hi_j;
+            if (!in) k[e] = 0u;
+            mn = min(mn, in ? k[e] : 0xffffffffu);
+            mx = max(mx, k[e]);
         }
-        // Blocks [lo_j, hi_j) compete for the places that the first and last ones leave; all of them have bounds.
-        const int lo_j = p.n_first, hi_j = nb - p.n_last, want = p.K - p.n_first - p.n_last;
-        const uint32_t* src = keys + (size_t)t * p.key_stride;
-        for (int i = tid; i < p.n_first; i += kSelThreads) out[i] = i;
-        for (int i = tid; i < p.n_last; i += kSelThreads) out[p.K - p.n_last + i] = hi_j + i;
-        if (want == 0) continue;
-        // Keys, four at a time, in shared memory where they fit, else where they lie (the workspace, in L2). Of the first and
-        // the last vector some do not compete.
-        const int vecs = (hi_j + 3) / 4;
-        const bool fits = (long long)vecs * 16 + kSelBins * 4 + kSelTies * 8 <= room;
-        __syncthreads();  // the token before is done with the shared memory
-        for (int i = tid; i < kSelBins / 4; i += kSelThreads) reinterpret_cast<uint4*>(s_hist)[i] = make_uint4(0u, 0u, 0u, 0u);
-        if (tid == 0) s_ties = 0;
-        const uint4* far4 = reinterpret_cast<const uint4*>(src);
-        uint4* near4 = reinterpret_cast<uint4*>(s_key);
-        auto each = [&](int v, const uint4& x, auto&& f) {
-            const uint32_t k[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                if (4 * v + e >= lo_j && 4 * v + e < hi_j) f(4 * v + e, k[e]);
-        };
-        // f(index, key) for vectors from, from + step, ... below `to`, four loads at once where they lie far.
-        auto sweep = [&](int from, int to, int step, auto&& f) {
-            if (fits) {
-#pragma unroll 1
-                for (int v = from; v < to; v += step) each(v, near4[v], f);
-            } else {
-#pragma unroll 1
-                for (int v = from; v < to; v += 4 * step) {
-                    uint4 x[4];
-#pragma unroll
-                    for (int u = 0; u < 4; ++u)
-                        if (v + u * step < to) x[u] = __ldcg(far4 + v + u * step);
-#pragma unroll
-                    for (int u = 0; u < 4; ++u)
-                        if (v + u * step < to) each(v + u * step, x[u], f);
-                }
-            }
-        };
-        uint32_t mn = 0xffffffffu, mx = 0u;
-        auto span = [&](int, uint32_t k) { mn = min(mn, k), mx = max(mx, k); };
-        if (fits) {
-            for (int v = tid; v < vecs; v += kSelThreads) {
-                const uint4 x = __ldcg(far4 + v);
-                near4[v] = x;
-                each(v, x, span);
-            }
-        } else {
-            sweep(tid, vecs, kSelThreads, span);
-        }
-        mn = __reduce_min_sync(0xffffffffu, mn);
-        mx = __reduce_max_sync(0xffffffffu, mx);
-        if (lane == 0) s_a[warp] = mn, s_b[warp] = mx;
-        __syncthreads();
-        uint32_t lo = s_a[0], hi = s_b[0], need = (uint32_t)want;
-#pragma unroll
-        for (int w = 1; w < kSelWarps; ++w) lo = min(lo, s_a[w]), hi = max(hi, s_b[w]);
-        // Keys above hi are kept, `need` of those in [lo, hi] too: rounds of a histogram over 2,048 equal parts of that range,
-        // until few keys are left in the part that has the border, or all of them are kept, or it is one value.
-        // (A round takes 11 bits off the range: three at most.)
-        uint32_t count = 0;
-#pragma unroll 1
-        for (int round = 0; round < 3; ++round) {
-            const int shift = max(0, 21 - __clz(hi - lo));  // (hi - lo) >> shift is below 2,048
-            sweep(tid, vecs, kSelThreads, [&](int, uint32_t k) {
-                if (k >= lo && k <= hi) atomicAdd(&s_hist[(k - lo) >> shift], 1u);
-            });
-            __syncthreads();
-            // Thread i adds up 8 parts, from the top, and leaves zeros; the one in which the running sum reaches `need` has the border.
-            constexpr int PER = kSelBins / kSelThreads;
-            static_assert(PER % 4 == 0, "whole vectors");
-            uint4* hp = reinterpret_cast<uint4*>(s_hist + kSelBins - PER * (tid + 1));
-            uint32_t cnt[PER], sum = 0;
-#pragma unroll
-            for (int e = 0; e < PER / 4; ++e) {
-                const uint4 x = hp[PER / 4 - 1 - e];
-                hp[PER / 4 - 1 - e] = make_uint4(0u, 0u, 0u, 0u);
-                cnt[4 * e] = x.w, cnt[4 * e + 1] = x.z, cnt[4 * e + 2] = x.y, cnt[4 * e + 3] = x.x;
-                sum += x.x + x.y + x.z + x.w;
-            }
-            uint32_t incl = sum;
-#pragma unroll
-            for (int off = 1; off < 32; off <<= 1) {
-                const uint32_t x = __shfl_up_sync(0xffffffffu, incl, off);
-                if (lane >= off) incl += x;
-            }
-            if (lane == 31) s_a[warp] = incl;
-            __syncthreads();
-            uint32_t before = incl - sum;
-#pragma unroll
-            for (int w = 0; w < kSelWarps; ++w) before += w < warp ? s_a[w] : 0u;
-            if (before < need && before + sum >= need) {
-                uint32_t at = before;
-#pragma unroll
-                for (int e = 0; e < PER; ++e) {
-                    if (at < need && at + cnt[e] >= need) {
-                        const uint32_t part = kSelBins - 1 - (tid * PER + e), low = lo + (part << shift);
-                        s_lo = low;
-                        s_hi = shift == 0 ? low : min(hi, low + ((1u << shift) - 1));
-                        s_need = need - at;
-                        s_count = cnt[e];
-                    }
-                    at += cnt[e];
-                }
-            }
-            __syncthreads();
-            lo = s_lo, hi = s_hi, need = s_need, count = s_count;
-            if (lo == hi || count == need || count <= kSelTies) break;
-        }
-        // ---- which are kept: a thread's run of keys; those at the border by their rank among each other ----
-        const bool value = lo == hi;                                             // one value: the first `need` of them in order
-        const bool ranked = !value && count != need && count <= kSelTies;
-        const int run = ((vecs + kSelThreads - 1) / kSelThreads) | 1;            // a thread's vectors; odd: lanes in different banks
-        const int v0 = min(tid * run, vecs), v1 = min(v0 + run, vecs);
-        uint32_t above = 0, equal = 0;
-        sweep(v0, v1, 1, [&](int i, uint32_t k) {
-            above += k > hi || (!value && !ranked && k >= lo);
-            if (k >= lo && k <= hi) {
-                equal += value;
-                if (ranked) s_tie[atomicAdd(&s_ties, 1u) & (kSelTies - 1)] = make_uint2(k, (uint32_t)i);
-            }
-        });
-        auto keeps = [&](uint32_t k, int i) {  // of the ranked ones
-            uint32_t ahead = 0;
-            for (uint32_t e = 0; e < count; ++e) {
-                const uint2 x = s_tie[e];
-                ahead += x.x > k || (x.x == k && x.y < (uint32_t)i);
-            }
-            return ahead < need;
-        };
-        if (ranked) {
-            __syncthreads();
-            for (uint32_t e = 0; e < count; ++e) {
-                const uint2 x = s_tie[e];
-                if ((int)x.y >= 4 * v0 && (int)x.y < 4 * v1) above += keeps(x.x, (int)x.y);
-            }
-        }
-        uint32_t ia = above, ie = equal;
+        if (fits) reinterpret_cast<uint4*>(s_key)[v] = make_uint4(k[0], k[1], k[2], k[3]);
+    }
+    mn = __reduce_min_sync(0xffffffffu, mn);
+    mx = __reduce_max_sync(0xffffffffu, mx);
+    if (lane == 0) s_a[warp] = mn, s_b[warp] = mx;
+    __syncthreads();
+    uint32_t lo = __reduce_min_sync(0xffffffffu, s_a[lane % WARPS]), hi = __reduce_max_sync(0xffffffffu, s_b[lane % WARPS]);
+    uint32_t need = (uint32_t)want, count = 0;
+    // The numbers of the warps before this one, and of all, of what each left in s_a.
+    auto before_me = [&](uint32_t& all) {
+        const uint32_t x = lane < WARPS ? s_a[lane] : 0u;
+        all = __reduce_add_sync(0xffffffffu, x);
+        return __reduce_add_sync(0xffffffffu, lane < warp ? x : 0u);
+    };
+    auto warp_scan = [&](uint32_t x) {  // inclusive
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) {
-            const uint32_t x = __shfl_up_sync(0xffffffffu, ia, off), y = __shfl_up_sync(0xffffffffu, ie, off);
-            if (lane >= off) ia += x, ie += y;
+            const uint32_t y = __shfl_up_sync(0xffffffffu, x, off);
+            if (lane >= off) x += y;
         }
-        if (lane == 31) s_b[warp] = ia, s_a[warp] = ie;  // (s_a was read before the barrier above)
+        return x;
+    };
+    // Keys above hi are kept, `need` of those in [lo, hi] too: rounds of a histogram over 2,048 equal parts of that range,
+    // until few keys are left in the part that has the border, or all of them are kept, or it is one value.
+    // (A round takes 11 bits off the range: three at most.)
+#pragma unroll 1
+    for (int round = 0; round < 3; ++round) {
+        const int shift = max(0, 21 - __clz(hi - lo));  // (hi - lo) >> shift is below 2,048
+#pragma unroll 4
+        for (int i = lo_j + tid; i < hi_j; i += kPickThreads) {
+            const uint32_t k = key[i];
+            if (k >= lo && k <= hi) atomicAdd(&s_hist[(k - lo) >> shift], 1u);
+        }
         __syncthreads();
-        uint32_t pa = ia - above, pe = ie - equal;
-#pragma unroll
-        for (int w = 0; w < kSelWarps; ++w) pa += w < warp ? s_b[w] : 0u, pe += w < warp ? s_a[w] : 0u;
-        uint32_t at = pa + (value ? min(pe, need) : 0u);
-        if (above + equal > 0)
-            sweep(v0, v1, 1, [&](int i, uint32_t k) {
-                bool keep = k > hi;
-                if (k >= lo && k <= hi) keep = value ? pe++ < need : ranked ? keeps(k, i) : true;
-                if (keep && at < (uint32_t)want) out[p.n_first + at++] = i;
-            });
+        // Thread i adds up 4 parts, from the top, and leaves zeros; the one in which the running sum reaches `need` has the border.
+        static_assert(kSelBins == 4 * kPickThreads, "a vector of parts a thread");
+        uint4* hp = reinterpret_cast<uint4*>(s_hist) + kPickThreads - 1 - tid;
+        const uint4 x = *hp;
+        *hp = make_uint4(0u, 0u, 0u, 0u);
+        const uint32_t sum = x.x + x.y + x.z + x.w, incl = warp_scan(sum);
+        if (lane == 31) s_a[warp] = incl;
+        __syncthreads();
+        uint32_t all;
+        const uint32_t before = before_me(all) + incl - sum;
+        if (before < need && before + sum >= need) {
+            const uint32_t c1 = before + x.w, c2 = c1 + x.z, c3 = c2 + x.y;  // running sums, from the top
+            const int e = need <= c1 ? 3 : need <= c2 ? 2 : need <= c3 ? 1 : 0;
+            const uint32_t low = lo + ((uint32_t)(4 * (kPickThreads - 1 - tid) + e) << shift);
+            s_lo = low;
+            s_hi = shift == 0 ? low : min(hi, low + ((1u << shift) - 1));
+            s_need = need - (e == 3 ? before : e == 2 ? c1 : e == 1 ? c2 : c3);
+            s_count = e == 3 ? x.w : e == 2 ? x.z : e == 1 ? x.y : x.x;
+        }
+        __syncthreads();
+        lo = s_lo, hi = s_hi, need = s_need, count = s_count;
+        if (lo == hi || count == need || count <= kSelTies) break;
+    }
+    // ---- which are kept, a bit a key; those at the border by their rank among each other; then the list from the bits ----
+    const bool value = lo == hi;                                  // one value: the first `need` of them in order
+    const bool ranked = !value && count != need && count <= kSelTies;
+    constexpr int CHUNK = 32 * kPickThreads;                      // a word of bits a thread, in the histogram's place
+    uint32_t* s_keep = s_hist;
+    uint32_t* s_same = s_hist + kPickThreads;
+    auto tie = [&](uint32_t k, int i) { s_tie[atomicAdd(&s_ties, 1u) & (kSelTies - 1)] = make_uint2(k, (uint32_t)i); };
+    const bool one_chunk = hi_j - lo_j <= CHUNK;
+    if (ranked && !one_chunk) {
+        for (int i = lo_j + tid; i < hi_j; i += kPickThreads)
+            if (key[i] >= lo && key[i] <= hi) tie(key[i], i);
+    }
+    uint32_t base = 0;  // kept before this chunk
+#pragma unroll 1
+    for (int c0 = lo_j; c0 < hi_j; c0 += CHUNK) {
+        const int words = (min(CHUNK, hi_j - c0) + 31) / 32;
+#pragma unroll 4
+        for (int w = warp; w < words; w += WARPS) {
+            const int i = c0 + 32 * w + lane;
+            const uint32_t k = i < hi_j ? key[i] : 0u;
+            const bool border = k >= lo && k <= hi;
+            const uint32_t keep = __ballot_sync(0xffffffffu, k > hi || (border && !value && !ranked));
+            const uint32_t same = __ballot_sync(0xffffffffu, border);
+            if (lane == 0) s_keep[w] = keep;
+            if (lane == 1) s_same[w] = same;
+            if (ranked && one_chunk && border) tie(k, i);
+        }
+        __syncthreads();
+        if (ranked) {
+            if (tid < (int)count) {
+                const uint2 x = s_tie[tid];
+                uint32_t ahead = 0;
+                for (uint32_t e = 0; e < count; ++e) ahead += s_tie[e].x > x.x || (s_tie[e].x == x.x && s_tie[e].y < x.y);
+                const int at = (int)x.y - c0;
+                if (ahead < need && at >= 0 && at < CHUNK) atomicOr(&s_keep[at >> 5], 1u << (at & 31));
+            }
+            __syncthreads();
+        }
+        uint32_t word = tid < words ? s_keep[tid] : 0u;
+        const uint32_t same = value && tid < words ? s_same[tid] : 0u;
+        const uint32_t cnt = __popc(word) | (__popc(same) << 16);  // (2^14 each at most)
+        const uint32_t incl = warp_scan(cnt);
+        if (lane == 31) s_a[warp] = incl;
+        __syncthreads();
+        uint32_t all;
+        const uint32_t pre = before_me(all) + incl - cnt;
+        // Of the border's value the first ones in order, as far as `need` goes.
+        uint32_t seen_same = pre >> 16, to = base + (pre & 0xffffu) + min(seen_same, need);
+        for (uint32_t m = same; m && seen_same < need; m &= m - 1, ++seen_same) word |= m & (0u - m);
+        for (uint32_t m = word; m; m &= m - 1) {
+            if (to < (uint32_t)want) out[p.n_first + to] = c0 + 32 * tid + __ffs(m) - 1;
+            ++to;
+        }
+        const uint32_t taken = value ? min(all >> 16, need) : 0u;
+        base += (all & 0xffffu) + taken;
+        if (value) need -= taken;
+        __syncthreads();
     }
 }
 
 cudaError_t launch_block_select(const SelectParams& p, cudaStream_t stream) {
-    static std::atomic<uint64_t> ready[15];
+    static std::atomic<uint64_t> ready[15], pick_ready;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)((long long)p.B * p.Hkv * p.parts), 1, 1);
     cfg.stream = stream;
-    cudaLaunchAttribute attr[2];
+    cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = (unsigned)p.parts;
-    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 2;
+    cfg.numAttrs = 1;
+    cfg.gridDim = dim3((unsigned)((long long)p.B * p.Hkv * p.parts), 1, 1);
     auto launch = [&](auto shape, auto kernel, int tiles, std::atomic<uint64_t>* done) {
         using Sh = decltype(shape);
         const int smem = tiles * Sh::FRAG + Sh::RING;
@@ -477,22 +463,33 @@ cudaError_t launch_block_select(const SelectParams& p, cudaStream_t stream) {
         if (e != cudaSuccess) return e;
         cfg.blockDim = dim3(Sh::THREADS, 1, 1);
         cfg.dynamicSmemBytes = (size_t)smem;
-        return cudaLaunchKernelEx(&cfg, kernel, p, smem);
+        return cudaLaunchKernelEx(&cfg, kernel, p);
     };
-#define KVD_SELECT(DD, i)                                                                                \
-    (tiles == 1   ? launch(SelectShape<DD>(), block_select_kernel<DD, 1>, 1, &ready[5 * i])              \
-     : tiles == 2 ? launch(SelectShape<DD>(), block_select_kernel<DD, 2>, 2, &ready[5 * i + 1])          \
-     : tiles == 4 ? launch(SelectShape<DD>(), block_select_kernel<DD, 4>, 4, &ready[5 * i + 2])          \
-     : tiles == 6 ? launch(SelectShape<DD>(), block_select_kernel<DD, 6>, 6, &ready[5 * i + 3])          \
-                  : launch(SelectShape<DD>(), block_select_kernel<DD, 8>, 8, &ready[5 * i + 4]))
+#define KVD_SCORE(DD, i)                                                                                 \
+    (tiles == 1   ? launch(SelectShape<DD>(), block_score_kernel<DD, 1>, 1, &ready[5 * i])               \
+     : tiles == 2 ? launch(SelectShape<DD>(), block_score_kernel<DD, 2>, 2, &ready[5 * i + 1])           \
+     : tiles == 4 ? launch(SelectShape<DD>(), block_score_kernel<DD, 4>, 4, &ready[5 * i + 2])           \
+     : tiles == 6 ? launch(SelectShape<DD>(), block_score_kernel<DD, 6>, 6, &ready[5 * i + 3])           \
+                  : launch(SelectShape<DD>(), block_score_kernel<DD, 8>, 8, &ready[5 * i + 4]))
     const int tiles = select_tiles(p.G, p.T);
-    switch (p.D) {
-        case 64: return KVD_SELECT(64, 0);
-        case 128: return KVD_SELECT(128, 1);
-        case 256: return KVD_SELECT(256, 2);
-        default: return cudaErrorInvalidValue;
+    cudaError_t e = cudaSuccess;
+    if (p.key_stride > 0) {  // (else no sequence has a full block)
+        switch (p.D) {
+            case 64: e = KVD_SCORE(64, 0); break;
+            case 128: e = KVD_SCORE(128, 1); break;
+            case 256: e = KVD_SCORE(256, 2); break;
+            default: e = cudaErrorInvalidValue;
+        }
     }
-#undef KVD_SELECT
+#undef KVD_SCORE
+    if (e != cudaSuccess) return e;
+    const long long most = 216 * 1024, room = kSelBins * 4 + kSelTies * 8 + (long long)p.key_stride * 4;
+    const int smem = (int)(room <= most ? room : kSelBins * 4 + kSelTies * 8);
+    if ((e = allow_clusters(reinterpret_cast<const void*>(block_pick_kernel), (int)most, &pick_ready)) != cudaSuccess) return e;
+    cfg.gridDim = dim3((unsigned)((long long)p.B * p.T * p.Hkv), 1, 1);
+    cfg.blockDim = dim3(kPickThreads, 1, 1);
+    cfg.dynamicSmemBytes = (size_t)smem;
+    return cudaLaunchKernelEx(&cfg, block_pick_kernel, p, smem);
 }
 
 int select_ctas(int D, int G, int T) {
