@@ -16,7 +16,7 @@
 
 namespace kvd {
 
-constexpr int kPagesThreads = 512;
+constexpr int kPagesThreads = 1024;
 
 // First index i in [0, n) with a[i + 1] > x, for a not decreasing with a[n] > x.
 __device__ __forceinline__ int owner_of(const int* a, int n, int x) {
@@ -28,35 +28,31 @@ __device__ __forceinline__ int owner_of(const int* a, int n, int x) {
     return lo;
 }
 
-// Exclusive prefix sums of two numbers over the block; tot receives their sums.
-__device__ __forceinline__ void block_scan2(long long (&v)[2], long long (&tot)[2], long long (*s_warp)[2]) {
+// Exclusive prefix sums of two numbers over the block; tot receives their sums. s_warp: not used by the call before this one.
+__device__ __forceinline__ void block_scan2(uint32_t (&v)[2], uint32_t (&tot)[2], uint32_t (*s_warp)[2]) {
+    static_assert(kPagesThreads == 1024, "a lane a warp");
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const long long own[2] = {v[0], v[1]};
+    const uint32_t own[2] = {v[0], v[1]};
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1)
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-            const long long n = __shfl_up_sync(0xffffffffu, v[k], off);
+            const uint32_t n = __shfl_up_sync(0xffffffffu, v[k], off);
             if (lane >= off) v[k] += n;
         }
     if (lane == 31) s_warp[warp][0] = v[0], s_warp[warp][1] = v[1];
     __syncthreads();
-    long long pre[2] = {0, 0};
-    tot[0] = tot[1] = 0;
-    for (int w = 0; w < kPagesThreads / 32; ++w)
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            if (w < warp) pre[k] += s_warp[w][k];
-            tot[k] += s_warp[w][k];
-        }
-    __syncthreads();
-    v[0] += pre[0] - own[0];
-    v[1] += pre[1] - own[1];
+    for (int k = 0; k < 2; ++k) {
+        const uint32_t x = s_warp[lane][k];
+        tot[k] = __reduce_add_sync(0xffffffffu, x);
+        v[k] += __reduce_add_sync(0xffffffffu, lane < warp ? x : 0u) - own[k];
+    }
 }
 
 __global__ void __launch_bounds__(kPagesThreads, 1) pages_kernel(const PagesParams p, int parts) {
     extern __shared__ int s_dyn[];  // four arrays of B + 1
-    __shared__ long long s_warp[kPagesThreads / 32][2];
+    __shared__ uint32_t s_warp[2][kPagesThreads / 32][2];
     int* s_old = s_dyn;                 // length before
     int* s_rel = s_old + p.B + 1;       // pages released before sequence b, then by all
     int* s_need = s_rel + p.B + 1;      // pages taken before sequence b
@@ -88,13 +84,14 @@ __global__ void __launch_bounds__(kPagesThreads, 1) pages_kernel(const PagesPara
         }
     };
     // ---- pages released and pages needed before each sequence (batch * max_blocks is below 2^31) ----
-    long long released = 0, needed = 0, tot[2];
+    uint32_t released = 0, needed = 0, tot[2];
+    int turn = 0;  // of the scan's two buffers
     for (int b0 = 0; b0 < p.B; b0 += kPagesThreads) {
         const int b = b0 + tid;
         int old = 0, want = 0;
         if (b < p.B) lengths(b, old, want);
-        long long v[2] = {max(pages_of(old) - pages_of(want), 0), max(pages_of(want) - pages_of(old), 0)};
-        block_scan2(v, tot, s_warp);
+        uint32_t v[2] = {(uint32_t)max(pages_of(old) - pages_of(want), 0), (uint32_t)max(pages_of(want) - pages_of(old), 0)};
+        block_scan2(v, tot, s_warp[turn ^= 1]);
         if (b < p.B) {
             s_old[b] = old;
             s_row[b] = want;
@@ -107,7 +104,7 @@ __global__ void __launch_bounds__(kPagesThreads, 1) pages_kernel(const PagesPara
     const int R = (int)released;
     // ---- a sequence grows when all that is needed up to it fits; one that needs no page always ----
     const long long have = (long long)F + R;
-    long long taken_l = 0, rows_l = 0;
+    uint32_t taken_u = 0, rows_u = 0;  // (the tokens of all pages, and of every sequence's last one, are below 2^32)
     for (int b0 = 0; b0 < p.B; b0 += kPagesThreads) {
         const int b = b0 + tid;
         int old = 0, want = 0, need = 0;
@@ -120,20 +117,20 @@ __global__ void __launch_bounds__(kPagesThreads, 1) pages_kernel(const PagesPara
                 flags |= KVD_STATUS_NO_PAGES;
             }
         }
-        long long v[2] = {need, max(want - old, 0)};
-        block_scan2(v, tot, s_warp);
+        uint32_t v[2] = {(uint32_t)need, (uint32_t)max(want - old, 0)};
+        block_scan2(v, tot, s_warp[turn ^= 1]);
         if (b < p.B) {
-            s_need[b] = (int)(taken_l + v[0]);
-            s_row[b] = (int)min(rows_l + v[1], 0x7fffffffLL);
+            s_need[b] = (int)(taken_u + v[0]);
+            s_row[b] = (int)min(rows_u + v[1], 0x7fffffffu);
             if (rank == 0) {
                 if (p.pos) p.pos[b] = old;
                 if (p.offsets) p.offsets[b] = s_row[b];
             }
         }
-        taken_l += tot[0];
-        rows_l += tot[1];
+        taken_u += tot[0];
+        rows_u += tot[1];
     }
-    const int taken = (int)taken_l, rows = (int)min(rows_l, 0x7fffffffLL);
+    const int taken = (int)taken_u, rows = (int)min(rows_u, 0x7fffffffu);
     if (tid == 0) {
         s_rel[p.B] = R;
         s_need[p.B] = taken;
@@ -143,6 +140,7 @@ __global__ void __launch_bounds__(kPagesThreads, 1) pages_kernel(const PagesPara
     if ((p.slots || p.positions) && rows > p.rows) flags |= KVD_STATUS_POS_OUT_OF_RANGE;  // rows behind the buffers are not written
     sync();  // every CTA has read the lengths and the count
     // ---- released pages: the r-th in order of sequence and block to place F + R - 1 - r of the stack ----
+#pragma unroll 4
     for (int r = gtid; r < R; r += gthreads) {
         const int b = owner_of(s_rel, p.B, r), held = pages_of(s_old[b]), n = s_rel[b + 1] - s_rel[b];
         int32_t* e = p.table + (size_t)b * p.max_blocks + (held - n + (r - s_rel[b]));
@@ -158,6 +156,7 @@ __global__ void __launch_bounds__(kPagesThreads, 1) pages_kernel(const PagesPara
     const int top = (int)min(have, (long long)p.num_pages);
     sync();
     // ---- pages taken: the i-th from place top - 1 - i ----
+#pragma unroll 4
     for (int i = gtid; i < taken; i += gthreads) {
         const int b = owner_of(s_need, p.B, i), held = pages_of(s_old[b]);
         const int at = top - 1 - i, page = at >= 0 ? __ldcg(p.free_pages + at) : -1;
@@ -180,29 +179,47 @@ __global__ void __launch_bounds__(kPagesThreads, 1) pages_kernel(const PagesPara
         sync();
         const long long total = min((long long)rows, p.rows);
         // A warp takes a stretch of rows, 128 at a time, four neighbours a lane: the sequence is searched for once, then
-        // followed; four steps' table entries are on the way at once.
+        // followed; two steps' table entries are on the way at once.
         const bool wide = ((reinterpret_cast<uintptr_t>(p.slots) | reinterpret_cast<uintptr_t>(p.positions)) & 15) == 0;
-        const int lane = tid & 31, gwarp = gtid >> 5, gwarps = gthreads >> 5;
-        const long long per = ((p.rows + gwarps - 1) / gwarps + 127) & ~127LL;
-        const long long end = min(p.rows, (gwarp + 1) * per);
-        long long n0 = gwarp * per + 4 * lane;
-        int b = n0 < total ? owner_of(s_row, p.B, (int)n0) : 0;
-        for (; n0 < end; n0 += 512) {
-            int slot[4][4], at[4][4];
+        auto put = [&](long long n, long long end, const int (&slot)[4], const int (&at)[4]) {
+            if (wide && n + 4 <= end) {
+                if (p.slots) *reinterpret_cast<int4*>(p.slots + n) = make_int4(slot[0], slot[1], slot[2], slot[3]);
+                if (p.positions) *reinterpret_cast<int4*>(p.positions + n) = make_int4(at[0], at[1], at[2], at[3]);
+            } else {
 #pragma unroll
-            for (int u = 0; u < 4; ++u)
+                for (int k = 0; k < 4; ++k)
+                    if (n + k < end) {
+                        if (p.slots) p.slots[n + k] = slot[k];
+                        if (p.positions) p.positions[n + k] = at[k];
+                    }
+            }
+        };
+        const int lane = tid & 31, gwarp = gtid >> 5, gwarps = gthreads >> 5;
+        const long long per = ((total + gwarps - 1) / gwarps + 127) & ~127LL;
+        const long long end = min(total, (gwarp + 1) * per);
+        long long n0 = gwarp * per + 4 * lane;
+        int b = n0 < end ? owner_of(s_row, p.B, (int)n0) : 0;
+        for (; n0 < end; n0 += 256) {
+            int slot[2][4], at[2][4];
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     const long long n = n0 + 128 * u + k;
                     slot[u][k] = at[u][k] = -1;
-                    if (n < min(total, end)) {
+                    if (n < end) {
+                        const int was = b;
                         while (n >= s_row[b + 1]) ++b;
                         at[u][k] = s_old[b] + ((int)n - s_row[b]);
-                        slot[u][k] = __ldcg(p.table + (size_t)b * p.max_blocks + (at[u][k] >> shift));
+                        // (neighbours of one sequence on one page: one entry for both)
+                        if (k > 0 && b == was && (at[u][k] & (psize - 1)) != 0)
+                            slot[u][k] = slot[u][k - 1];
+                        else
+                            slot[u][k] = __ldcg(p.table + (size_t)b * p.max_blocks + (at[u][k] >> shift));
                     }
                 }
 #pragma unroll
-            for (int u = 0; u < 4; ++u) {
+            for (int u = 0; u < 2; ++u) {
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
                     if (at[u][k] >= 0) {
@@ -213,21 +230,17 @@ __global__ void __launch_bounds__(kPagesThreads, 1) pages_kernel(const PagesPara
                             slot[u][k] = (slot[u][k] << shift) + (at[u][k] & (psize - 1));
                         }
                     }
-                const long long n = n0 + 128 * u;
-                if (n >= end) break;
-                if (wide && n + 4 <= end) {
-                    if (p.slots) *reinterpret_cast<int4*>(p.slots + n) = make_int4(slot[u][0], slot[u][1], slot[u][2], slot[u][3]);
-                    if (p.positions) *reinterpret_cast<int4*>(p.positions + n) = make_int4(at[u][0], at[u][1], at[u][2], at[u][3]);
-                } else {
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        if (n + k < end) {
-                            if (p.slots) p.slots[n + k] = slot[u][k];
-                            if (p.positions) p.positions[n + k] = at[u][k];
-                        }
-                }
+                if (n0 + 128 * u < end) put(n0 + 128 * u, end, slot[u], at[u]);
             }
         }
+        // What lies behind the last token.
+        const int none[4] = {-1, -1, -1, -1};
+        const long long tail = wide ? min((total + 3) & ~3LL, p.rows) : total;
+        if (gtid < tail - total) {
+            if (p.slots) p.slots[total + gtid] = -1;
+            if (p.positions) p.positions[total + gtid] = -1;
+        }
+        for (long long n = tail + 4LL * gtid; n < p.rows; n += 4LL * gthreads) put(n, p.rows, none, none);
     }
     if (flags && p.status) atomicOr(p.status, flags);
 }
@@ -237,9 +250,10 @@ cudaError_t launch_pages(const PagesParams& p, cudaStream_t stream) {
     const int smem = 4 * (p.B + 1) * (int)sizeof(int);
     const cudaError_t e = allow_clusters(reinterpret_cast<const void*>(pages_kernel), 4 * (kPagesMaxBatch + 1) * (int)sizeof(int), &ready);
     if (e != cudaSuccess) return e;
-    // A CTA for 4,096 rows, which it writes in two steps of its threads.
+    // A CTA for 8,192 rows, two steps of its threads, and for 16,384 table entries (few of which change in a call).
+    const long long rows = p.slots || p.positions ? p.rows : 0, entries = (long long)p.B * p.max_blocks;
     int parts = 1;
-    while (parts < 16 && (p.slots || p.positions) && (long long)parts * 4096 < p.rows) parts *= 2;
+    while (parts < 16 && (parts * 8192LL < rows || parts * 16384LL < entries)) parts *= 2;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)parts, 1, 1);
     cfg.blockDim = dim3(kPagesThreads, 1, 1);
