@@ -74,15 +74,14 @@ kvd_status check_place(const int32_t* block_table, int s_max, int max_blocks, in
     return KVD_OK;
 }
 
-// CTAs of a pair: enough that all together fill two a multiprocessor, as far as every warp keeps two
-// units; joined in a cluster up to 16, beyond that (few pairs of long lists) in several clusters of which each warp keeps four.
-void split_blocks(long long pairs, long long units, int teams, int num_sms, int* parts, int* shards) {
-    const long long slots = 2LL * num_sms;
+// CTAs of a pair: enough that all together fill the multiprocessors' places, as far as every team keeps two
+// stages; joined in a cluster up to 16, beyond that (few pairs of long lists) in several clusters of which each team keeps four.
+void split_blocks(long long pairs, long long stages, int teams, long long places, int* parts, int* shards) {
     int n = 1;
-    while (n < 16 && pairs * n * 2 <= slots && units >= 4LL * n * teams) n *= 2;
+    while (n < 16 && pairs * n * 2 <= places && stages >= 4LL * n * teams) n *= 2;
     *parts = n;
     *shards = 1;
-    if (n == 16) *shards = (int)std::max(1LL, std::min(slots / (pairs * 16), units / (64LL * teams)));
+    if (n == 16) *shards = (int)std::max(1LL, std::min(places / (pairs * 16), stages / (64LL * teams)));
 }
 
 kvd_status plan_blocks(int batch, int T, int Hq, int Hkv, int D, int K, int block_tokens, int num_sms, BlocksParams* p, size_t* ws) {
@@ -98,15 +97,19 @@ kvd_status plan_blocks(int batch, int T, int Hq, int Hkv, int D, int K, int bloc
     p->Hkv = Hkv;
     p->G = Hq / Hkv;
     p->K = K;
-    p->unit_shift = log2_of(block_tokens) - 4;
+    p->block_log2 = log2_of(block_tokens);
     const long long pairs = (long long)batch * T * Hkv;
-    p->head_warps = p->G <= 16 ? 1 : (p->G + 15) / 16;
+    // Query rows to warps: 16 each (two column tiles), at head_dim 256, whose accumulators take the registers of one, 8. As many teams as
+    // the warps give, with three stages each at least.
+    p->head_rows = p->G <= 8 || D == 256 ? 8 : 16;
+    p->head_warps = (p->G + p->head_rows - 1) / p->head_rows;
+    p->teams = std::max(1, std::min(blocks_warps(D) / p->head_warps, blocks_slots(D) / 3));
     if (pairs > (1 << 26)) return KVD_ERR_UNSUPPORTED;
     p->pairs = (int)pairs;
     *ws = 0;
     p->parts = p->shards = 1;
     if (pairs == 0) return KVD_OK;
-    split_blocks(pairs, (long long)K << p->unit_shift, 4 / p->head_warps, sms, &p->parts, &p->shards);
+    split_blocks(pairs, (long long)K * block_tokens / kBlocksStage, p->teams, (D == 256 ? 1LL : 2LL) * sms, &p->parts, &p->shards);
     if (p->shards > 1) {
         const size_t rows = (size_t)pairs * p->G;
         *ws = align256(p->shards * rows * D * sizeof(float)) + align256(p->shards * rows * sizeof(float));
@@ -414,6 +417,7 @@ kvd_status kvd_decode_blocks(const kvd_cache* cache, const void* q, const int32_
         if (!aligned(workspace, 256)) return KVD_ERR_INVALID_ARG;
     }
     if (batch == 0) return KVD_OK;
+    p.unit_log2 = block_tokens >= 32 && (!p.pg.block_table || p.pg.page_shift >= 5) ? 5 : 4;
     const bool f32 = out_dtype == KVD_OUT_F32;
     const size_t out_rows = (size_t)p.pairs * p.G;
     p.q = q;

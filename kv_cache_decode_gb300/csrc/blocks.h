@@ -9,7 +9,11 @@
 
 namespace kvd {
 
-// Attention over listed blocks (decode_blocks.cuh). A pair is a (sequence, query token, KV head).
+// Tokens of a stage of the attention over listed blocks, working warps of a CTA at most, stages of a CTA's ring (see BlocksShape).
+constexpr int kBlocksStage = 32;
+constexpr int blocks_warps(int D) { return D == 256 ? 8 : 4; }
+constexpr int blocks_slots(int D) { return (D == 256 ? 192 : 96) * 1024 / (4 * D * kBlocksStage); }
+// The attention over listed blocks (decode_blocks.cuh). A pair is a (sequence, query token, KV head).
 struct BlocksParams {
     const void* q;            // bf16 [B, T, Hq, D]
     const void* k;            // bf16 cache [B, S_max, Hkv, D], or pool
@@ -21,9 +25,9 @@ struct BlocksParams {
     int32_t* status;
     float scale_log2;
     int B, T, Hq, Hkv, G, K, S_max;
-    int unit_shift;           // log2 of the 16-token units of a block
+    int block_log2, unit_log2;  // tokens of a block, and of a unit: 32 or 16 (the rows of a TMA box)
     int pairs, parts, shards; // CTAs of a pair that join over distributed shared memory, and groups of them over global memory
-    int head_warps;           // warps that share a pair's query rows
+    int teams, head_warps, head_rows;  // teams of a CTA; warps of a team, which share a pair's query rows; rows of each
     PagedCache pg;
 };
 // Lets a kernel use so much shared memory and clusters of 16, once a device (a bit of *ready each).

@@ -4,15 +4,16 @@
 // It reads K * block rows of K and V a pair where the attention over all tokens reads the sequence;
 // bound by memory for batches, by latency for one sequence.
 //
-// A unit is 16 tokens of a listed block, whose K rows and V rows a warp brings
-// by TMA into its ring (128-byte swizzle) and works on alone: units are dealt to
-// the warps of a pair's CTAs in turn, so every warp has its own loads in flight and waits for no other. The
+// A stage is 32 tokens, K rows and V rows, brought by TMA into a ring (128-byte swizzle): as one box
+// where blocks and pages have 32 tokens, else two units of 16 of any listed blocks. A loading warp looks the list up, 32 units at a
+// time, and deals the stages to the CTA's teams in turn; a team works on its stages alone, so that nothing but its own
+// loads holds it up. (Loads issued by the working warps themselves took 950 of a 16-token step's 2,200 cycles.) The
 // products are turned round so that tokens fill the 16 rows of m16n8k16 MMAs and query rows
 // their 8 columns (a group of 4 to 8 query heads is one column tile): S^T = K q^T, O^T = V^T w, the weights
 // transposed by movmatrix. The running maximum of a column is raised only where a score passes it by 2^8
-// (a vote a unit otherwise): weights stay below 2^8 and keep their relative precision, bf16's 2^-8, the same
+// (a vote a stage otherwise): weights stay below 2^8 and keep their relative precision, bf16's 2^-8, the same
 // rounding as the other attention kernels' of this library; for float32 output a second bf16 carries the rest to 2^-16.
-// Groups of more than 16 query heads are shared out to head_warps warps over one ring.
+// Teams are single warps for groups of up to 16 query heads (head_dim 256: 8); wider ones are shared out to the head_warps warps of a team.
 //
 // A pair's CTAs (parts, up to 16) are a cluster: their states are joined over
 // distributed shared memory, each CTA writing a share of the output, without a second launch or a workspace. Where even
@@ -38,30 +39,33 @@ bool tc_encode_map(CUtensorMap* m, const void* base, int rank, const cuuint64_t*
                    const cuuint32_t* box, bool u8);
 
 struct BlocksMaps {
-    CUtensorMap k;  // 3D: [rows of the cache, Hkv, D], box 16 x 1 x 64, 128-byte swizzle
+    CUtensorMap k;  // 3D: [rows of the cache, Hkv, D], box 32 or 16 x 1 x 64, 128-byte swizzle
     CUtensorMap v;
 };
 
-constexpr int kBlocksWarps = 4;
-
 template <int D, int NT>
 struct BlocksShape {
+    static constexpr int ROWS_S = kBlocksStage;
     static constexpr int RW = 8 * NT;                    // query rows of a warp
-    static constexpr int ELEM = 16 * D * 2;              // a unit's rows of one tensor
-    static constexpr int RING = 96 * 1024;               // shared out to the teams: two CTAs an SM
-    static constexpr int SLOTS = RING / ELEM;
-    static constexpr int ROWS = kBlocksWarps * RW;       // state rows of a CTA
+    static constexpr int WARPS = blocks_warps(D);        // working warps of a CTA, at most
+    static constexpr int CTAS = D == 256 ? 1 : 2;        // of an SM
+    static constexpr int ELEM = ROWS_S * D * 2;          // a stage's rows of one tensor
+    static constexpr int RING = (D == 256 ? 192 : 96) * 1024;  // shared out to the teams
+    static constexpr int SLOTS = blocks_slots(D);
+    static constexpr int ROWS = WARPS * RW;              // state rows of a CTA
     static constexpr int ST = D + 4;                     // floats between state rows: neighbours in different banks
     static constexpr int OFF_BAR = RING;                 // full and empty barriers
-    static constexpr int OFF_ML = OFF_BAR + 2 * SLOTS * 8;   // m and the two sums of the states
+    static constexpr int OFF_N = OFF_BAR + 2 * SLOTS * 8;    // tokens of each stage
+    static constexpr int OFF_ML = OFF_N + SLOTS * 8;         // m and the two sums of the states
     static constexpr int OFF_CML = OFF_ML + 3 * ROWS * 4;    // of the CTA's rows
     static constexpr int OFF_W = OFF_CML + 3 * 64 * 4;       // weights of the cluster's CTAs, and 1 / sum
     static constexpr int OFF_FLAG = OFF_W + 17 * 64 * 4;
     static constexpr int OFF_IN = OFF_FLAG + 16;             // what the cluster's CTAs send this one
     static constexpr int IN_FLOATS = 2048;
     static constexpr int SMEM = OFF_IN + IN_FLOATS * 4;
+    static_assert(SLOTS * 2 * ELEM == RING, "stages fill the ring");
     static_assert(ROWS * ST * 4 <= RING, "the states take the ring's place");
-    static_assert(2 * (SMEM + 1024) <= 227 * 1024, "two CTAs an SM");
+    static_assert(CTAS * (SMEM + 1024) <= 227 * 1024, "shared memory of an SM");
 };
 
 // The bf16 MMA of common.cuh without its ordering against other instructions.
@@ -72,10 +76,10 @@ __device__ __forceinline__ void mma_bf16_free(float (&d)[4], const uint32_t (&a)
 }
 
 template <int D, int NT, bool F32OUT>
-__global__ void __launch_bounds__(kBlocksWarps * 32, 2) decode_blocks_kernel(const BlocksParams p,
-                                                                          const __grid_constant__ BlocksMaps maps) {
+__global__ void __launch_bounds__((BlocksShape<D, NT>::WARPS + 1) * 32, BlocksShape<D, NT>::CTAS)
+    decode_blocks_kernel(const BlocksParams p, const __grid_constant__ BlocksMaps maps) {
     using Sh = BlocksShape<D, NT>;
-    constexpr int RW = Sh::RW, KS = D / 16, MT = D / 16, ST = Sh::ST;
+    constexpr int RW = Sh::RW, KS = D / 16, MT = D / 16, ST = Sh::ST, U = kBlocksStage / 16;  // U: halves of 16 tokens of a stage
     constexpr long long kBudget = 4000000000LL;  // ~2 s of clock cycles a wait
 
     extern __shared__ __align__(1024) uint8_t smem[];
@@ -90,15 +94,17 @@ __global__ void __launch_bounds__(kBlocksWarps * 32, 2) decode_blocks_kernel(con
     float* s_w = reinterpret_cast<float*>(smem + Sh::OFF_W);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + Sh::OFF_FLAG);
     float* s_in = reinterpret_cast<float*>(smem + Sh::OFF_IN);
+    volatile int* s_n = reinterpret_cast<volatile int*>(smem + Sh::OFF_N);  // tokens of a stage's halves (the second << 8); 0: the end
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nthreads = blockDim.x;
-    const int HT = p.head_warps, teams = (nthreads >> 5) / HT, team = warp / HT, wt = warp - team * HT;
+    const int HT = p.head_warps, teams = p.teams, workers = teams * HT, team = warp / HT, wt = warp - team * HT;
+    const bool loader = warp == workers;
     const int rank = blockIdx.x & (p.parts - 1), cl = blockIdx.x >> (__ffs(p.parts) - 1);  // (parts: a power of two)
     const int pair = cl % p.pairs, shard = cl / p.pairs;
     const int h = pair % p.Hkv, bt = pair / p.Hkv, t = bt % p.T, b = bt / p.T;
-    const int R = Sh::SLOTS / teams, slot0 = team * R;  // this team's ring
-    auto full = [&](int s) { return bars + 8u * (slot0 + s); };
-    auto empty = [&](int s) { return bars + 8u * (Sh::SLOTS + slot0 + s); };
+    const int R = Sh::SLOTS / teams;  // stages of a team's ring
+    auto full = [&](int s) { return bars + 8u * s; };
+    auto empty = [&](int s) { return bars + 8u * (Sh::SLOTS + s); };
 
     // ---- set-up that reads no input ----
     if (tid == 0) {
@@ -118,252 +124,257 @@ __global__ void __launch_bounds__(kBlocksWarps * 32, 2) decode_blocks_kernel(con
     pdl_wait();
     pdl_launch_dependents();
 
-    // ---- q: column tile n's rows wt * RW + 8 n + lane / 4 as B fragments ----
-    uint32_t qf[NT][KS][2];
-    {
-        const uint32_t* q32 = reinterpret_cast<const uint32_t*>(p.q);
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            const int r = wt * RW + 8 * n + (lane >> 2);
-            const uint32_t* qr = q32 + ((size_t)pair * p.G + r) * (D / 2) + (lane & 3);
-#pragma unroll
-            for (int kk = 0; kk < KS; ++kk) {
-                qf[n][kk][0] = r < p.G ? __ldg(qr + kk * 8) : 0u;
-                qf[n][kk][1] = r < p.G ? __ldg(qr + kk * 8 + 4) : 0u;
+    float o[MT][NT][4], m[NT][2], l[NT][2], lr[F32OUT ? 1 : NT][2];
+    bool dead = false;
+    if (loader) {
+        // ---- the tokens this query token sees, and the units of this CTA ----
+        const int us = p.unit_log2;
+        const bool T16 = us == 4;  // a stage takes two units
+        const int raw = __ldg(p.seq_lens + b), L = raw < 0 ? 0 : raw > p.S_max ? p.S_max : raw;
+        const int32_t* list = p.blocks + (size_t)pair * p.K;
+        const int units = p.K << (p.block_log2 - us), submask = (1 << (p.block_log2 - us)) - 1;
+        const int W = p.shards * p.parts, last_block = (p.S_max - 1) >> p.block_log2;  // of the cache's
+        const uint64_t policy = l2_evict_first_policy();
+        if (raw != L && lane == 0 && p.status) atomicOr(p.status, KVD_STATUS_SEQ_LEN_CLAMPED);
+        const int seen = L - p.T + 1 + t;  // <= 0: none
+        int issued = 0, to_team = 0, slot = 0, phase = 1;  // phase: parity of the last release of the slots in turn
+        auto next_stage = [&]() {  // the next stage's slot, or -1
+            const int s = to_team * R + slot;
+            if (issued >= teams * R && !__all_sync(0xffffffffu, tc::mbar_wait(empty(s), phase, abort_flag, kBudget))) return -1;
+            ++issued;
+            if (++to_team == teams) {
+                to_team = 0;
+                if (++slot == R) slot = 0, phase ^= 1;
             }
-        }
-    }
-
-    // ---- the tokens this query token sees, and the units of this team ----
-    const int raw = __ldg(p.seq_lens + b), L = raw < 0 ? 0 : raw > p.S_max ? p.S_max : raw;
-    if (raw != L && tid == 0 && p.status) atomicOr(p.status, KVD_STATUS_SEQ_LEN_CLAMPED);
-    const int seen = L - p.T + 1 + t;  // <= 0: none
-    const int32_t* list = p.blocks + (size_t)pair * p.K;
-    const int units = p.K << p.unit_shift, submask = (1 << p.unit_shift) - 1;
-    const int W = p.shards * p.parts * teams, wid = (shard * p.parts + rank) * teams + team;
-    const int last_block = (p.S_max - 1) >> (p.unit_shift + 4);  // of the cache's
-
-    // Units are looked up 32 at a time, one a lane: how many of its tokens count, and its cache row. Those of entries
-    // that name no block the token sees have none and are passed over. (List and table are read beside the length, not behind it.)
-    struct Cursor {
-        int u;          // the next look-up's first unit of this team
-        uint32_t mask;  // lanes whose unit is still to come
-        int row, n;
-    };
-    auto look_up = [&](Cursor& c, bool rows) {
-        do {
-            const long long u = c.u + (long long)lane * W;
-            const int blk = u < units ? __ldg(list + ((int)u >> p.unit_shift)) : -1;
+            return s;
+        };
+        auto issue = [&](int row0, int n0, int row1, int n1) {
+            const int s = next_stage();
+            if (s < 0) {
+                dead = true;
+                return;
+            }
+            if (lane == 0) {
+                const uint32_t dst = ring + (uint32_t)s * 2 * Sh::ELEM, bar = full(s);
+                s_n[s] = n0 | (n1 << 8);
+                tc::mbar_arrive_expect_tx(bar, T16 && n1 == 0 ? Sh::ELEM : 2 * Sh::ELEM);
+#pragma unroll
+                for (int c = 0; c < D / 64; ++c) {
+                    tc::tma_load_3d(dst + c * (Sh::ROWS_S * 128), &maps.k, c * 64, h, row0, bar, policy);
+                    tc::tma_load_3d(dst + Sh::ELEM + c * (Sh::ROWS_S * 128), &maps.v, c * 64, h, row0, bar, policy);
+                }
+                if (T16 && n1 > 0) {
+#pragma unroll
+                    for (int c = 0; c < D / 64; ++c) {
+                        tc::tma_load_3d(dst + c * (Sh::ROWS_S * 128) + 2048, &maps.k, c * 64, h, row1, bar, policy);
+                        tc::tma_load_3d(dst + Sh::ELEM + c * (Sh::ROWS_S * 128) + 2048, &maps.v, c * 64, h, row1, bar, policy);
+                    }
+                }
+            }
+        };
+        // Units are looked up 32 at a time, one a lane: how many of its tokens count, and its cache row. Those of entries that
+        // name no block the token sees have none and are passed over.
+        int row0 = 0, n0 = 0;  // a unit that waits for a second one
+        for (long long u0 = shard * p.parts + rank; u0 < units && !dead; u0 += 32LL * W) {
+            const long long u = u0 + (long long)lane * W;
+            const int blk = u < units ? __ldg(list + ((int)u >> (p.block_log2 - us))) : -1;
             const bool named = blk >= 0 && blk <= last_block;
-            const int tok = named ? ((blk << p.unit_shift) + ((int)u & submask)) << 4 : 0;
+            const int tok = named ? (blk << p.block_log2) + (((int)u & submask) << us) : 0;
             const bool held = named && tok < p.S_max;
+            int row = 0;
             bool bad = false;
-            if (rows && held) {
+            if (held) {
                 if (p.pg.block_table) {
                     const int page = __ldg(p.pg.block_table + (size_t)b * p.pg.max_blocks + (tok >> p.pg.page_shift));
                     bad = (unsigned)page >= (unsigned)p.pg.num_pages;  // reads as zero rows: past the pool's end
-                    c.row = bad ? p.pg.num_pages << p.pg.page_shift : (page << p.pg.page_shift) + (tok & ((1 << p.pg.page_shift) - 1));
+                    row = bad ? p.pg.num_pages << p.pg.page_shift : (page << p.pg.page_shift) + (tok & ((1 << p.pg.page_shift) - 1));
                 } else {
-                    c.row = b * p.S_max + tok;
+                    row = b * p.S_max + tok;
                 }
             }
-            c.n = held ? min(16, seen - tok) : 0;
-            if (bad && c.n > 0 && p.status) atomicOr(p.status, KVD_STATUS_BAD_PAGE);
-            c.mask = __ballot_sync(0xffffffffu, c.n > 0);
-            const long long next = c.u + 32LL * W;
-            c.u = next < units ? (int)next : units;
-        } while (c.mask == 0 && c.u < units);
-    };
-
-    // ---- loads: K and V of each unit in turn, into the ring's slots in turn ----
-    Cursor lc{min(wid, units), 0, 0, 0}, cc = lc;
-    int issued = 0, islot = 0, iphase = 1, irow = 0;  // iphase: parity of the last release of slot islot
-    bool more = true;
-    const uint64_t policy = l2_evict_first_policy();
-    bool dead = false;
-    auto issue = [&]() {  // whole leading warps call this
-        if (!(issued & 1)) {
-            if (lc.mask == 0 && lc.u < units) look_up(lc, true);
-            if (lc.mask == 0) {
-                more = false;
-                return;
+            const int n = held ? min(1 << us, seen - tok) : 0;
+            if (bad && n > 0 && p.status) atomicOr(p.status, KVD_STATUS_BAD_PAGE);
+            for (uint32_t mask = __ballot_sync(0xffffffffu, n > 0); mask && !dead; mask &= mask - 1) {
+                const int src = __ffs(mask) - 1, ru = __shfl_sync(0xffffffffu, row, src), nu = __shfl_sync(0xffffffffu, n, src);
+                if (!T16) {
+                    issue(ru, min(nu, 16), 0, max(nu - 16, 0));
+                } else if (n0 == 0) {
+                    row0 = ru, n0 = nu;
+                } else {
+                    issue(row0, n0, ru, nu);
+                    n0 = 0;
+                }
             }
-            const int i = __ffs(lc.mask) - 1;
-            lc.mask &= lc.mask - 1;
-            irow = __shfl_sync(0xffffffffu, lc.row, i);
         }
-        if (HT > 1 && issued >= R && !dead && !tc::mbar_wait(empty(islot), iphase, abort_flag, kBudget)) dead = true;
-        if (lane == 0 && !dead) {
-            const CUtensorMap* map = (issued & 1) ? &maps.v : &maps.k;
-            const uint32_t dst = ring + (uint32_t)(slot0 + islot) * Sh::ELEM, bar = full(islot);
-            tc::mbar_arrive_expect_tx(bar, Sh::ELEM);
-#pragma unroll
-            for (int c = 0; c < D / 64; ++c) tc::tma_load_3d(dst + c * 2048, map, c * 64, h, irow, bar, policy);
+        if (n0 > 0 && !dead) issue(row0, n0, 0, 0);
+        for (int j = 0; j < teams && !dead; ++j) {  // the end, for every team
+            const int s = next_stage();
+            if (s < 0) {
+                dead = true;
+            } else if (lane == 0) {
+                s_n[s] = 0;
+                tc::mbar_arrive(full(s));
+            }
         }
-        ++issued;
-        if (++islot == R) islot = 0, iphase ^= 1;
-    };
-    const bool lead = wt == 0;
-    if (lead) {
-        look_up(lc, true);
-        for (int i = 0; i < R && more; ++i) issue();
-    }
-
-    // l: the weights' sum, for lse. lr: of the weights as V meets them, so that the output is a convex combination of V
-    // rows (the same where float32 output carries both parts).
-    float o[MT][NT][4], m[NT][2], l[NT][2], lr[F32OUT ? 1 : NT][2];
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-        m[n][0] = m[n][1] = -FLT_MAX;
-        l[n][0] = l[n][1] = 0.f;
-        if constexpr (!F32OUT) lr[n][0] = lr[n][1] = 0.f;
-#pragma unroll
-        for (int i = 0; i < MT; ++i) o[i][n][0] = o[i][n][1] = o[i][n][2] = o[i][n][3] = 0.f;
-    }
-
-    // ---- the units ----
-    // A slot given back is filled again at once by a warp alone; a team's leader fills the slot of two elements before, so
-    // that it seldom waits for the others.
-    int done = 0, cslot = 0, cphase = 0;
-    auto release = [&]() {
-        __syncwarp();
-        if (HT > 1) {
-            if (lane == 0) tc::mbar_arrive(empty(cslot));
-            if (lead && done >= 2 && more) issue();
-        } else if (more) {
-            issue();
+        if (dead) {  // copies still on their way are waited for (again with a limit), since the ring's place is used below
+            for (int s = 0; s < teams * R; ++s) {
+                // the stages issued to this slot: its last one's phase
+                const int at = (s % R) * teams + s / R, uses = issued > at ? (issued - at + teams * R - 1) / (teams * R) : 0;
+                if (uses > 0)
+                    for (long long t0 = clock64(); !tc::mbar_test(full(s), (uses - 1) & 1) && clock64() - t0 < kBudget;) {
+                    }
+            }
         }
-        ++done;
-        if (++cslot == R) cslot = 0, cphase ^= 1;
-    };
-    auto chunk = [&](uint32_t base, int row, int c) {  // 16-byte chunk c of a swizzled row
-        return base + (uint32_t)((c >> 3) * 2048 + row * 128 + (((c & 7) ^ (row & 7)) << 4));
-    };
-    look_up(cc, false);
-    while (cc.mask) {
-        const int src = __ffs(cc.mask) - 1;
-        const int n_tok = __shfl_sync(0xffffffffu, cc.n, src);
-        cc.mask &= cc.mask - 1;
-        if (cc.mask == 0 && cc.u < units) look_up(cc, false);
-
-        if (!tc::mbar_wait(full(cslot), cphase, abort_flag, kBudget)) {
-            dead = true;
-            break;
-        }
-        float s[NT][4];
+    } else {
+        // ---- q: column tile n's rows wt * RW + 8 n + lane / 4 as B fragments ----
+        uint32_t qf[NT][KS][2];
         {
-            const uint32_t kb = ring + (uint32_t)(slot0 + cslot) * Sh::ELEM;
-            const int row = lane & 15, half = lane >> 4;
-            float s2[NT][4];
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) s[n][e] = s2[n][e] = 0.f;
-#pragma unroll
-            for (int kk = 0; kk < KS; ++kk) {
-                uint32_t a[4];
-                ldmatrix_x4(chunk(kb, row, 2 * kk + half), a[0], a[1], a[2], a[3]);
-#pragma unroll
-                for (int n = 0; n < NT; ++n) mma_bf16_free((kk & 1) ? s2[n] : s[n], a, qf[n][kk][0], qf[n][kk][1]);
-            }
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) s[n][e] = (s[n][e] + s2[n][e]) * p.scale_log2;
-        }
-        release();
-        // Tokens lane / 4 (s[n][0..1]) and lane / 4 + 8 (s[n][2..3]), query rows 8 n + 2 (lane % 4) + 0..1.
-        if (n_tok < 16) {
+            const uint32_t* q32 = reinterpret_cast<const uint32_t*>(p.q);
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
-                if ((lane >> 2) >= n_tok) s[n][0] = s[n][1] = -CUDART_INF_F;
-                if ((lane >> 2) + 8 >= n_tok) s[n][2] = s[n][3] = -CUDART_INF_F;
+                const int r = wt * RW + 8 * n + (lane >> 2);
+                const uint32_t* qr = q32 + ((size_t)pair * p.G + r) * (D / 2) + (lane & 3);
+#pragma unroll
+                for (int kk = 0; kk < KS; ++kk) {
+                    qf[n][kk][0] = r < p.G ? __ldg(qr + kk * 8) : 0u;
+                    qf[n][kk][1] = r < p.G ? __ldg(qr + kk * 8 + 4) : 0u;
+                }
             }
         }
-        bool raise = false;
+        // l: the weights' sum, for lse. lr: of the weights as V meets them, so that the output is a convex combination of V
+        // rows (the same where float32 output carries both parts).
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-            raise |= fmaxf(s[n][0], s[n][2]) > m[n][0] + 8.f;
-            raise |= fmaxf(s[n][1], s[n][3]) > m[n][1] + 8.f;
+            m[n][0] = m[n][1] = -FLT_MAX;
+            l[n][0] = l[n][1] = 0.f;
+            if constexpr (!F32OUT) lr[n][0] = lr[n][1] = 0.f;
+#pragma unroll
+            for (int i = 0; i < MT; ++i) o[i][n][0] = o[i][n][1] = o[i][n][2] = o[i][n][3] = 0.f;
         }
-        if (__any_sync(0xffffffffu, raise)) {
+        auto chunk = [&](uint32_t base, int row, int c) {  // 16-byte chunk c of a swizzled row
+            return base + (uint32_t)((c >> 3) * (Sh::ROWS_S * 128) + row * 128 + (((c & 7) ^ (row & 7)) << 4));
+        };
+        int slot = 0, phase = 0;
+        while (true) {
+            const int st = team * R + slot;
+            if (!__all_sync(0xffffffffu, tc::mbar_wait(full(st), phase, abort_flag, kBudget))) {
+                dead = true;
+                break;
+            }
+            const int counts = s_n[st];
+            if (counts == 0) break;
+            const int n_tok[2] = {counts & 0xff, counts >> 8};
+            const uint32_t kb = ring + (uint32_t)st * 2 * Sh::ELEM, vb = kb + Sh::ELEM;
+            // ---- scores: tokens 16 u + lane / 4 (s[u][n][0..1]) and + 8 (s[u][n][2..3]), query rows 8 n + 2 (lane % 4) + 0..1 ----
+            float s[U][NT][4];
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
+            for (int u = 0; u < U; ++u)
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    float x = fmaxf(s[n][e], s[n][e + 2]);
+                for (int n = 0; n < NT; ++n) s[u][n][0] = s[u][n][1] = s[u][n][2] = s[u][n][3] = 0.f;
 #pragma unroll
-                    for (int off = 4; off <= 16; off <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, off));
-                    const float up = fmaxf(m[n][e], x), f = exp2f(m[n][e] - up);
-                    m[n][e] = up;
-                    l[n][e] *= f;
-                    if constexpr (!F32OUT) lr[n][e] *= f;
+            for (int kk = 0; kk < KS; ++kk)
 #pragma unroll
-                    for (int i = 0; i < MT; ++i) {
-                        o[i][n][e] *= f;
-                        o[i][n][e + 2] *= f;
+                for (int u = 0; u < U; ++u) {
+                    uint32_t a[4];
+                    ldmatrix_x4(chunk(kb, 16 * u + (lane & 15), 2 * kk + (lane >> 4)), a[0], a[1], a[2], a[3]);
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) mma_bf16_free(s[u][n], a, qf[n][kk][0], qf[n][kk][1]);
+                }
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) s[u][n][e] *= p.scale_log2;
+            bool raise = false;
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                if (n_tok[u] < 16) {
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) {
+                        if ((lane >> 2) >= n_tok[u]) s[u][n][0] = s[u][n][1] = -CUDART_INF_F;
+                        if ((lane >> 2) + 8 >= n_tok[u]) s[u][n][2] = s[u][n][3] = -CUDART_INF_F;
                     }
                 }
-        }
-        uint32_t ph[NT][2], pl[F32OUT ? NT : 1][2];  // the weights as B fragments
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int y = 0; y < 2; ++y) {
-                const float e0 = tc::ex2_approx(s[n][2 * y] - m[n][0]), e1 = tc::ex2_approx(s[n][2 * y + 1] - m[n][1]);
-                const uint32_t hi = pack_bf16x2(e0, e1);
-                ph[n][y] = movmatrix_trans(hi);
-                l[n][0] += e0;
-                l[n][1] += e1;
-                if constexpr (F32OUT) {
-                    pl[n][y] = movmatrix_trans(pack_bf16x2(e0 - bf16_lo(hi), e1 - bf16_hi(hi)));
-                } else {
-                    lr[n][0] += bf16_lo(hi);
-                    lr[n][1] += bf16_hi(hi);
-                }
-            }
-
-        if (!tc::mbar_wait(full(cslot), cphase, abort_flag, kBudget)) {
-            dead = true;
-            break;
-        }
-        {
-            const uint32_t vb = ring + (uint32_t)(slot0 + cslot) * Sh::ELEM;
-            if (n_tok < 16) {  // rows past the last token hold anything: zero, since 0 * NaN is not 0
-                for (int i = lane + n_tok * 8; i < 16 * 8; i += 32)
-#pragma unroll
-                    for (int c = 0; c < D / 64; ++c)
-                        *reinterpret_cast<uint4*>(smem + (vb - ring) + c * 2048 + i * 16) = make_uint4(0u, 0u, 0u, 0u);
-                __syncwarp();
-            }
-            const int row = (lane & 7) + ((lane >> 4) << 3), odd = (lane >> 3) & 1;
-#pragma unroll
-            for (int i = 0; i < MT; ++i) {
-                uint32_t a[4];
-                ldmatrix_x4_trans(chunk(vb, row, 2 * i + odd), a[0], a[1], a[2], a[3]);
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
-                    mma_bf16_free(o[i][n], a, ph[n][0], ph[n][1]);
-                    if constexpr (F32OUT) mma_bf16_free(o[i][n], a, pl[n][0], pl[n][1]);
+                    raise |= fmaxf(s[u][n][0], s[u][n][2]) > m[n][0] + 8.f;
+                    raise |= fmaxf(s[u][n][1], s[u][n][3]) > m[n][1] + 8.f;
                 }
             }
-            if (n_tok < 16) tc::fence_proxy_async_smem();  // the zeros come before the next load
+            if (__any_sync(0xffffffffu, raise)) {
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        float x = fmaxf(fmaxf(s[0][n][e], s[0][n][e + 2]), fmaxf(s[1][n][e], s[1][n][e + 2]));
+#pragma unroll
+                        for (int off = 4; off <= 16; off <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, off));
+                        const float up = fmaxf(m[n][e], x), f = exp2f(m[n][e] - up);
+                        m[n][e] = up;
+                        l[n][e] *= f;
+                        if constexpr (!F32OUT) lr[n][e] *= f;
+#pragma unroll
+                        for (int i = 0; i < MT; ++i) {
+                            o[i][n][e] *= f;
+                            o[i][n][e + 2] *= f;
+                        }
+                    }
+            }
+            // ---- the weights as B fragments ----
+            uint32_t ph[U][NT][2], pl[F32OUT ? U : 1][F32OUT ? NT : 1][2];
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int y = 0; y < 2; ++y) {
+                        const float e0 = tc::ex2_approx(s[u][n][2 * y] - m[n][0]), e1 = tc::ex2_approx(s[u][n][2 * y + 1] - m[n][1]);
+                        const uint32_t hi = pack_bf16x2(e0, e1);
+                        ph[u][n][y] = movmatrix_trans(hi);
+                        l[n][0] += e0;
+                        l[n][1] += e1;
+                        if constexpr (F32OUT) {
+                            pl[u][n][y] = movmatrix_trans(pack_bf16x2(e0 - bf16_lo(hi), e1 - bf16_hi(hi)));
+                        } else {
+                            lr[n][0] += bf16_lo(hi);
+                            lr[n][1] += bf16_hi(hi);
+                        }
+                    }
+            // ---- V rows past the last token hold anything: zero, since 0 * NaN is not 0 ----
+            const bool part = n_tok[0] < 16 || n_tok[1] < 16;
+            if (part) {
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+                    for (int i = lane + n_tok[u] * 8; i < 16 * 8; i += 32)
+#pragma unroll
+                        for (int c = 0; c < D / 64; ++c)
+                            *reinterpret_cast<uint4*>(smem + (vb - ring) + c * (Sh::ROWS_S * 128) + u * 2048 + i * 16) = make_uint4(0u, 0u, 0u, 0u);
+                __syncwarp();
+            }
+#pragma unroll
+            for (int i = 0; i < MT; ++i)
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    uint32_t a[4];
+                    ldmatrix_x4_trans(chunk(vb, 16 * u + (lane & 7) + ((lane >> 4) << 3), 2 * i + ((lane >> 3) & 1)), a[0], a[1], a[2], a[3]);
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) {
+                        mma_bf16_free(o[i][n], a, ph[u][n][0], ph[u][n][1]);
+                        if constexpr (F32OUT) mma_bf16_free(o[i][n], a, pl[u][n][0], pl[u][n][1]);
+                    }
+                }
+            if (part) tc::fence_proxy_async_smem();  // the zeros come before the next load
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(empty(st));
+            if (++slot == R) slot = 0, phase ^= 1;
         }
-        release();
     }
-    if (dead) {
-        if (lane == 0 && p.status) atomicOr(p.status, KVD_STATUS_TIMEOUT);
-        // Copies still on their way are waited for (again with a limit), since the ring's place is used below.
-        if (lead)
-            for (; done < issued; ++done) {
-                for (long long t0 = clock64(); !tc::mbar_test(full(cslot), cphase) && clock64() - t0 < kBudget;) {
-                }
-                if (++cslot == R) cslot = 0, cphase ^= 1;
-            }
-    }
+    if (dead && lane == 0 && p.status) atomicOr(p.status, KVD_STATUS_TIMEOUT);
 
     // ---- the states to shared memory, in the ring's place ----
     __syncthreads();
+    if (!loader) {
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -389,6 +400,7 @@ __global__ void __launch_bounds__(kBlocksWarps * 32, 2) decode_blocks_kernel(con
                 states[r * ST + 16 * i + (lane >> 2) + 8] = o[i][n][e + 2];
             }
         }
+    }
     __syncthreads();
 
     // ---- joined over the CTA's teams, then over the cluster ----
@@ -499,7 +511,7 @@ cudaError_t launch_decode_blocks(const BlocksParams& p, cudaStream_t stream) {
     const cuuint64_t rows = p.pg.block_table ? (cuuint64_t)p.pg.num_pages << p.pg.page_shift : (cuuint64_t)p.B * p.S_max;
     const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)p.Hkv, rows};
     const cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)p.Hkv * D * 2};
-    const cuuint32_t box[3] = {64, 1, 16};
+    const cuuint32_t box[3] = {64, 1, (cuuint32_t)1 << p.unit_log2};
     if (!tc_encode_map(&maps.k, p.k, 3, dims, strides, box, false) || !tc_encode_map(&maps.v, p.v, 3, dims, strides, box, false))
         return cudaErrorInvalidValue;
     auto kern = decode_blocks_kernel<D, NT, F32OUT>;
@@ -508,7 +520,7 @@ cudaError_t launch_decode_blocks(const BlocksParams& p, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)p.shards * p.pairs * p.parts, 1, 1);
-    cfg.blockDim = dim3((unsigned)(kBlocksWarps / p.head_warps * p.head_warps) * 32, 1, 1);
+    cfg.blockDim = dim3((unsigned)(p.teams * p.head_warps + 1) * 32, 1, 1);
     cfg.dynamicSmemBytes = Sh::SMEM;
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
@@ -524,8 +536,9 @@ cudaError_t launch_decode_blocks(const BlocksParams& p, cudaStream_t stream) {
 
 #define KVD_BLOCKS_LAUNCH(DD)                                                                             \
     cudaError_t launch_decode_blocks_d##DD(const BlocksParams& p, bool f32_out, cudaStream_t stream) {    \
-        if (p.G <= 8) return f32_out ? launch_decode_blocks<DD, 1, true>(p, stream) : launch_decode_blocks<DD, 1, false>(p, stream); \
-        return f32_out ? launch_decode_blocks<DD, 2, true>(p, stream) : launch_decode_blocks<DD, 2, false>(p, stream);               \
+        if (p.head_rows == 8) return f32_out ? launch_decode_blocks<DD, 1, true>(p, stream) : launch_decode_blocks<DD, 1, false>(p, stream); \
+        if constexpr (DD < 256) return f32_out ? launch_decode_blocks<DD, 2, true>(p, stream) : launch_decode_blocks<DD, 2, false>(p, stream); \
+        return cudaErrorInvalidValue;                                                                     \
     }
 
 }  // namespace kvd
