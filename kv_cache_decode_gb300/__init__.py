@@ -1508,6 +1508,7 @@ class RopeAxes:
                  factor: float = 1.0, original_len: float = 0.0, slow: Optional[float] = None, fast: Optional[float] = None,
                  attn_factor: float = 0.0, interleaved: bool = False, device="cuda"):
         import torch
+        sections = tuple(sections)
         turns, axes, self.factor = rope_axes_table(sections, base, order, per_axis, scaling, factor, original_len, slow, fast,
                                                    attn_factor)
         self.n_axes, self.rotary_dim, self.interleaved = len(sections), 2 * len(axes), bool(interleaved)
@@ -1629,7 +1630,7 @@ def kv_append_axes(rope: RopeAxes, k, v, k_new, v_new, slots, positions, *, q=No
     if positions.dim() > 2 or slots.dim() > 1 or k_new.dim() > 3 or v_new.dim() > 3 or (q is not None and (q.dim() > 3 or q_out.dim() > 3)):
         _same_batch(what, positions.shape[1:], slots.shape, k_new.shape[:-2], v_new.shape[:-2],
                     *(() if q is None else (q.shape[:-2], q_out.shape[:-2])))
-    if N == 0 or n == 0:
+    if N == 0:
         return
     c = (_pack_cache(k.data_ptr(), v.data_ptr(), ksp, vsp, 0, 0, 0, cap, n, fp8) if paged else
          _pack_cache(k.data_ptr(), v.data_ptr(), ksp, vsp, 0, cap, 0, 0, 0, fp8))

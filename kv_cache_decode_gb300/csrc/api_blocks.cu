@@ -146,13 +146,14 @@ kvd_status kvd_pages_update(int32_t* block_table, int32_t* free_pages, int32_t* 
     if (batch < 0 || n_rows < 0 || n_rows > 0x7fffffffLL) return KVD_ERR_INVALID_ARG;
     PagedCache pg;
     int cap = 0;
-    const kvd_status st = check_paged(block_table, max_blocks, page_size, num_pages, &pg, &cap);
+    // (Without sequences there may be no table and no lengths; slots and positions are filled all the same.)
+    const kvd_status st = check_paged(batch > 0 ? block_table : free_pages, max_blocks, page_size, num_pages, &pg, &cap);
     if (st != KVD_OK) return st;
     if ((long long)batch * max_blocks > 0x7fffffffLL) return KVD_ERR_INVALID_ARG;
     if (batch > kPagesMaxBatch) return KVD_ERR_UNSUPPORTED;
-    const void* all[10] = {block_table, free_pages, free_count, seq_lens, new_lens, pos, row_offsets, slots, positions, status_word};
+    const void* all[10] = {free_pages, free_count, block_table, seq_lens, new_lens, pos, row_offsets, slots, positions, status_word};
     for (int i = 0; i < 10; ++i)
-        if ((i < 5 && !all[i]) || (all[i] && !aligned(all[i], 4))) return KVD_ERR_INVALID_ARG;
+        if ((i < (batch > 0 ? 5 : 2) && !all[i]) || (all[i] && !aligned(all[i], 4))) return KVD_ERR_INVALID_ARG;
     const size_t b4 = (size_t)batch * 4;
     const ByteRange r[9] = {{block_table, b4 * max_blocks}, {free_pages, (size_t)num_pages * 4}, {free_count, 4}, {seq_lens, b4},
                             {pos, pos ? b4 : 0}, {row_offsets, row_offsets ? b4 + 4 : 0}, {slots, slots ? (size_t)n_rows * 4 : 0},
@@ -246,7 +247,7 @@ kvd_status kvd_kv_append_axes(const kvd_cache* cache, const kvd_rope_axes* rope,
     } else if (cache->s_max <= 0) {
         return KVD_ERR_INVALID_ARG;
     }
-    if (rows > 0x7fffffffLL) return KVD_ERR_INVALID_ARG;
+    if (rows > 0x7fffffffLL || (rows == 0 && n_rows > 0)) return KVD_ERR_INVALID_ARG;
     if ((q != nullptr) != (q_out != nullptr) || n_heads_kv > (1 << 20) || (q && (n_heads_q < 1 || n_heads_q > (1 << 20))))
         return KVD_ERR_INVALID_ARG;
     if (!slots || !aligned(slots, 4)) return KVD_ERR_INVALID_ARG;
@@ -260,7 +261,7 @@ kvd_status kvd_kv_append_axes(const kvd_cache* cache, const kvd_rope_axes* rope,
         if ((st = check_strided(q, q_stride, qw, 2)) != KVD_OK) return st;
         if ((st = check_strided(q_out, q_out_stride, qw, 2)) != KVD_OK) return st;
     }
-    if (n_rows == 0 || rows == 0) return KVD_OK;
+    if (n_rows == 0) return KVD_OK;
     const Rows rk{k_new, k_stride, kw, n_rows, 2}, rv{v_new, v_stride, kw, n_rows, 2}, rq{q, q_stride, qw, n_rows, 2},
         ro{q_out, q_out_stride, qw, n_rows, 2};
     const ByteRange none{nullptr, 0}, rp{positions, positions_bytes(r, n_rows)}, rs{slots, (size_t)n_rows * 4};

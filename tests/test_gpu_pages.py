@@ -110,6 +110,19 @@ def test_pages_rollback_restores():
         assert torch.equal(x, y)
 
 
+def test_pages_without_sequences():
+    import torch
+    import kv_cache_decode_gb300 as kvd
+    dev = cuda_or_skip()
+    i32 = dict(dtype=torch.int32, device=dev)
+    free, count = torch.arange(5, **i32), torch.tensor([5], **i32)
+    none, off, slots, positions = torch.empty(0, **i32), torch.full((1,), 9, **i32), torch.full((7,), 9, **i32), torch.full((7,), 9, **i32)
+    kvd.pages_update(torch.empty(0, 3, **i32), free, count, none, none.clone(), 16, pos=none.clone(), row_offsets=off, slots=slots,
+                     positions=positions)
+    assert off.tolist() == [0] and slots.tolist() == [-1] * 7 and positions.tolist() == [-1] * 7
+    assert free.tolist() == list(range(5)) and count.tolist() == [5]
+
+
 def test_pages_bad_state():
     """Counts and lengths out of range, entries and stack places that name no page: flagged, in bounds, the rest served."""
     import torch
@@ -273,6 +286,74 @@ def test_append(form, N, Hq, Hkv, D):
     (k2, v2), (ks2, vs2) = empty()
     kvd.kv_append_axes(rope, k2, v2, k, v, torch.from_numpy(slots).to(dev), pos, k_scales=ks2, v_scales=vs2, paged=False)
     assert torch.equal(k2, kw) and torch.equal(v2, vw)
+
+
+def test_turn_negative_turns_back():
+    """The rotation by minus the positions undoes it (fp32: two roundings of each, 4e-7 of a pair's length together with the
+    cosines' and sines')."""
+    import torch
+    import kv_cache_decode_gb300 as kvd
+    dev = cuda_or_skip()
+    x = torch.randn(333, 4, 128, device=dev)
+    p = torch.randint(0, 1 << 20, (3, 333), device=dev).int()
+    rope = kvd.RopeAxes((16, 24, 24), device=dev)
+    y, z = torch.empty_like(x), torch.empty_like(x)
+    kvd.rope_apply_axes(rope, x, p, y)
+    kvd.rope_apply_axes(rope, y, -p, z)
+    assert float((z - x).abs().max()) <= 6e-7 * float(x.abs().max()) * 2 ** 0.5
+
+
+@pytest.mark.parametrize("what", ["turn", "append", "pages", "bounds", "select", "decode"])
+def test_other_stream(what):
+    """Each call on a stream of its own, whose inputs that stream makes, gives what it gives on the current one."""
+    import torch
+    import kv_cache_decode_gb300 as kvd
+    dev = cuda_or_skip()
+    g = torch.Generator(device=dev)
+    g.manual_seed(1)
+    i32 = dict(dtype=torch.int32, device=dev)
+    q, k = torch.randn(4, 8, 64, generator=g, device=dev).bfloat16(), torch.randn(4, 512, 2, 64, generator=g, device=dev).bfloat16()
+    lens, rope = torch.tensor([512, 77, 300, 16], **i32), kvd.RopeAxes((8, 24), device=dev)
+    p = torch.randint(0, 1000, (2, 4), generator=g, device=dev).int()
+    side = torch.cuda.Stream()
+
+    def run(stream):
+        on = stream or torch.cuda.current_stream()
+        with torch.cuda.stream(on):
+            torch.cuda._sleep(200000)
+            qq, kk, ll, pp = q * 1, k * 1, lens * 1, p * 1
+            codes, scales = kvd.alloc_block_bounds(kk, 16)
+            if what == "turn":
+                res = torch.empty_like(qq)
+            elif what == "append":
+                res = kk.clone()
+                new, slots = qq[:, :2].contiguous(), torch.tensor([3, 600, -1, 2047], **i32)
+            elif what == "pages":
+                table, free, count = torch.full((4, 40), -1, **i32), torch.arange(150, **i32), torch.tensor([150], **i32)
+                old, res = torch.zeros(4, **i32), torch.empty(905, **i32)
+            elif what == "decode":
+                res, blocks = torch.empty_like(qq), (torch.arange(4 * 2 * 5, **i32) % 32).view(4, 2, 5)
+            elif what == "select":
+                codes.copy_(torch.arange(codes.numel(), device=dev).view_as(codes) % 127)
+                scales.fill_(0.5)
+                res, ws = torch.empty(4, 2, 5, **i32), torch.empty(1 << 16, dtype=torch.uint8, device=dev)
+        if what == "turn":
+            kvd.rope_apply_axes(rope, qq, pp, res, stream=stream)
+        elif what == "append":
+            kvd.kv_append_axes(rope, res, kk, new, new.clone(), slots, pp, paged=False, stream=stream)
+        elif what == "pages":
+            kvd.pages_update(table, free, count, old, ll, 16, slots=res, stream=stream)
+        elif what == "bounds":
+            kvd.kv_block_bounds(kk, codes, scales, ll, 512, 16, stream=stream)
+            res = codes
+        elif what == "select":
+            kvd.block_select(qq, codes, scales, ll, 512, 16, res, workspace=ws, stream=stream)
+        else:
+            kvd.decode_blocks(qq, kk, kk, blocks, ll, 16, 0.125, res, stream=stream)
+        torch.cuda.synchronize()
+        return res
+    torch.cuda.synchronize()
+    assert torch.equal(run(None), run(side))
 
 
 # ---------------------------------------------------------------------------
