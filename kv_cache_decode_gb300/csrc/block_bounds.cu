@@ -62,35 +62,23 @@ __global__ void __launch_bounds__(kBoundsThreads) block_bounds_kernel(const Boun
     const uint4* k = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.k) + ((size_t)row * p.Hkv + h) * D) + c;
     const size_t step = (size_t)p.Hkv * TPR;  // 16-byte vectors between tokens
     uint32_t hi[4], lo[4];
-    int t = tid / TPR;
-    {
-        const uint4 v = __ldg(k + min(t, n_tok - 1) * step);  // (a thread past a short block's tokens repeats its last)
-        hi[0] = lo[0] = v.x, hi[1] = lo[1] = v.y, hi[2] = lo[2] = v.z, hi[3] = lo[3] = v.w;
-        t += RPP;
-    }
-    auto take = [&](const uint4& v) {
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    const int t0 = tid / TPR;
+    for (int t = t0; t < n_tok || t == t0; t += 8 * RPP) {  // eight loads in flight; a thread past the tokens repeats the last
+        uint4 v[8];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            hi[e] = max_bf16x2_nan(hi[e], w[e]);
-            lo[e] = min_bf16x2(lo[e], w[e]);
+        for (int e = 0; e < 8; ++e) v[e] = __ldg(k + (size_t)min(t + e * RPP, n_tok - 1) * step);
+        if (t == t0) {
+            hi[0] = lo[0] = v[0].x, hi[1] = lo[1] = v[0].y, hi[2] = lo[2] = v[0].z, hi[3] = lo[3] = v[0].w;
         }
-    };
-    for (; t + 3 * RPP < n_tok; t += 4 * RPP) {  // four loads in flight
-        uint4 v[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] = __ldg(k + (size_t)(t + e * RPP) * step);
+        for (int e = 0; e < 8; ++e) {
+            const uint32_t w[4] = {v[e].x, v[e].y, v[e].z, v[e].w};
 #pragma unroll
-        for (int e = 0; e < 4; ++e) take(v[e]);
-    }
-    {  // up to three more, at once
-        uint4 v[3];
-#pragma unroll
-        for (int e = 0; e < 3; ++e)
-            if (t + e * RPP < n_tok) v[e] = __ldg(k + (size_t)(t + e * RPP) * step);
-#pragma unroll
-        for (int e = 0; e < 3; ++e)
-            if (t + e * RPP < n_tok) take(v[e]);
+            for (int c4 = 0; c4 < 4; ++c4) {
+                hi[c4] = max_bf16x2_nan(hi[c4], w[c4]);
+                lo[c4] = min_bf16x2(lo[c4], w[c4]);
+            }
+        }
     }
 #pragma unroll
     for (int off = TPR; off < 32; off <<= 1)
