@@ -648,7 +648,7 @@ kvd_status kvd_pages_update(int32_t* block_table, int32_t* free_pages, int32_t* 
  * Rotary positions of several axes, as for the tokens of images and video (time, height, width): pair i of a
  * head's first rotary_dim columns turns by positions[axes[i]] * w_i, otherwise as kvd_rope.
  *   turns   : device uint64 [rotary_dim / 2], as kvd_rope's
- *   axes    : device uint8 [rotary_dim / 2], each below n_axes
+ *   axes    : device uint8 [rotary_dim / 2], 8-byte aligned, each below n_axes
  *   n_axes  : 1 .. KVD_MAX_AXES
  * kvd_rope_axes_table fills HOST arrays of rotary_dim / 2 entries (rotary_dim = twice the sum of sections, a multiple of
  * 16 up to 256) and the factor: axis a takes sections[a] >= 1 pairs, which are neighbours (dealt 0: the first

@@ -43,7 +43,7 @@ bool apart(const ByteRange* r, int n_written, int n) {
 
 kvd_status check_axes(const kvd_rope_axes* rope, const int32_t* positions, long long axis_stride, long long rows, int head_dim,
                       RopeAxes* out) {
-    if (!rope || !rope->turns || !aligned(rope->turns, 8) || !rope->axes) return KVD_ERR_INVALID_ARG;
+    if (!rope || !rope->turns || !aligned(rope->turns, 8) || !rope->axes || !aligned(rope->axes, 8)) return KVD_ERR_INVALID_ARG;
     if (rope->rotary_dim < 16 || rope->rotary_dim > 256 || rope->rotary_dim % 16 != 0 || rope->rotary_dim > head_dim)
         return KVD_ERR_INVALID_ARG;
     if (!std::isfinite(rope->factor) || rope->n_axes < 1 || rope->n_axes > KVD_MAX_AXES) return KVD_ERR_INVALID_ARG;

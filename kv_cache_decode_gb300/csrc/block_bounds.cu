@@ -5,9 +5,10 @@
 // every token of the block (up to float32's rounding): what block_select.cu scores blocks by. A block with a key that is not
 // finite gets the scale NaN and codes 0.
 //
-// A CTA takes one KV head of one block: 2 * block * D bytes read once, 2 D + 4 written; bound by memory for prompts, by latency for
-// the few blocks that a step fills. Thread i of a row's D / 8 holds 8 columns' running maxima and minima of every
-// (128 * 8 / D)-th token as bf16 pairs (exact).
+// A CTA of four warps takes one KV head of one block, or, of blocks of up to 4,096 values, a warp each: 2 * block * D bytes read
+// once, 2 D + 4 written; bound by memory for prompts (82 us for 537 MB, 6.6 TB/s), by latency for the few blocks that a step fills. A
+// thread holds 8 columns' running maxima and minima of its tokens as bf16 pairs (exact), eight loads in flight. (32 x 8,192 tokens, 8 KV
+// heads of 128, blocks of 16: a warp a block 106 us, a CTA 210; of 32: 91 and 109.)
 #include "../../include/kvdecode.h"
 #include "blocks.h"
 #include "common.cuh"
@@ -25,16 +26,18 @@ __device__ __forceinline__ uint32_t min_bf16x2(uint32_t a, uint32_t b) {
     return *reinterpret_cast<const uint32_t*>(&r);
 }
 
-template <int D>
-__global__ void __launch_bounds__(kBoundsThreads) block_bounds_kernel(const BoundsParams p, int per_seq) {
-    constexpr int TPR = D / 8, RPP = kBoundsThreads / TPR;  // threads of a row, rows of a pass
+// WPI: warps of an item, a (block, KV head).
+template <int D, int WPI>
+__global__ void __launch_bounds__(kBoundsThreads) block_bounds_kernel(const BoundsParams p, unsigned per_seq, unsigned items) {
+    constexpr int TPR = D / 8, RPP = 32 * WPI / TPR, IPC = 4 / WPI;  // threads of a row, rows of a pass, items of a CTA
     __shared__ uint4 s_hi[4][TPR], s_lo[4][TPR];
     pdl_wait();
     pdl_launch_dependents();
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int h = blockIdx.x % p.Hkv;
-    const long long rest = blockIdx.x / p.Hkv;
-    const int i = (int)(rest % per_seq), b = (int)(rest / per_seq);
+    const int tid = threadIdx.x % (32 * WPI), lane = tid & 31, warp = tid >> 5;  // of the item's
+    const unsigned item = blockIdx.x * IPC + threadIdx.x / (32 * WPI);  // (items: below 2^31)
+    if (item >= items) return;
+    const unsigned rest = item / (unsigned)p.Hkv;
+    const int h = (int)(item - rest * p.Hkv), b = (int)(rest / per_seq), i = (int)(rest - b * per_seq);
     const int raw = __ldg(p.seq_lens + b), len = raw < 0 ? 0 : raw > p.S_max ? p.S_max : raw;
     const int raw0 = p.from_lens ? __ldg(p.from_lens + b) : 0, from = raw0 < 0 ? 0 : raw0;
     const int bs = p.block_shift, n_tok = 1 << bs;
@@ -87,18 +90,20 @@ __global__ void __launch_bounds__(kBoundsThreads) block_bounds_kernel(const Boun
             hi[e] = max_bf16x2_nan(hi[e], __shfl_xor_sync(0xffffffffu, hi[e], off));
             lo[e] = min_bf16x2(lo[e], __shfl_xor_sync(0xffffffffu, lo[e], off));
         }
-    if (lane < TPR) {
-        s_hi[warp][lane] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-        s_lo[warp][lane] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+    if constexpr (WPI > 1) {
+        if (lane < TPR) {
+            s_hi[warp][lane] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+            s_lo[warp][lane] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        }
+        __syncthreads();
+        if (warp != 0) return;
     }
-    __syncthreads();
-    if (warp != 0) return;
     // ---- the scale and the codes ----
     float fh[8], fl[8], a = 0.f;
     bool bad = false;
     if (lane < TPR) {
 #pragma unroll
-        for (int w = 1; w < 4; ++w) {
+        for (int w = 1; w < WPI; ++w) {
             const uint4 x = s_hi[w][lane], y = s_lo[w][lane];
             const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
@@ -144,7 +149,9 @@ __global__ void __launch_bounds__(kBoundsThreads) block_bounds_kernel(const Boun
 cudaError_t launch_block_bounds(const BoundsParams& p, cudaStream_t stream) {
     const int per_seq = (int)(((long long)p.max_new + (1 << p.block_shift) - 1) >> p.block_shift);  // blocks max_new tokens can fill
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)((long long)p.B * per_seq * p.Hkv), 1, 1);
+    const long long items = (long long)p.B * per_seq * p.Hkv;
+    const bool small = (p.D << p.block_shift) <= 4096;
+    cfg.gridDim = dim3((unsigned)(small ? (items + 3) / 4 : items), 1, 1);
     cfg.blockDim = dim3(kBoundsThreads, 1, 1);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
@@ -153,9 +160,9 @@ cudaError_t launch_block_bounds(const BoundsParams& p, cudaStream_t stream) {
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     switch (p.D) {
-        case 64: return cudaLaunchKernelEx(&cfg, block_bounds_kernel<64>, p, per_seq);
-        case 128: return cudaLaunchKernelEx(&cfg, block_bounds_kernel<128>, p, per_seq);
-        case 256: return cudaLaunchKernelEx(&cfg, block_bounds_kernel<256>, p, per_seq);
+        case 64: return cudaLaunchKernelEx(&cfg, small ? block_bounds_kernel<64, 1> : block_bounds_kernel<64, 4>, p, (unsigned)per_seq, (unsigned)items);
+        case 128: return cudaLaunchKernelEx(&cfg, small ? block_bounds_kernel<128, 1> : block_bounds_kernel<128, 4>, p, (unsigned)per_seq, (unsigned)items);
+        case 256: return cudaLaunchKernelEx(&cfg, small ? block_bounds_kernel<256, 1> : block_bounds_kernel<256, 4>, p, (unsigned)per_seq, (unsigned)items);
         default: return cudaErrorInvalidValue;
     }
 }

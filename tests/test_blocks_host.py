@@ -91,7 +91,7 @@ TURN = dict(rope=None, x=FAKE + 0x10000, xs=1024, xd=0, y=FAKE + 0x900000, ys=10
 
 
 @pytest.mark.parametrize("rope,kw,want", [
-    (None, {}, INV), (dict(turns=None), {}, INV), (dict(turns=FAKE + 4), {}, INV), (dict(axes=None), {}, INV), (dict(rotary_dim=24), {}, INV),
+    (None, {}, INV), (dict(turns=None), {}, INV), (dict(turns=FAKE + 4), {}, INV), (dict(axes=None), {}, INV), (dict(axes=FAKE + 4), {}, INV), (dict(rotary_dim=24), {}, INV),
     (dict(rotary_dim=144), {}, INV), (dict(n_axes=0), {}, INV), (dict(n_axes=5), {}, INV), (dict(factor=float("nan")), {}, INV),
     ({}, dict(pos=None), INV), ({}, dict(pos=FAKE + 2), INV), ({}, dict(axis=9), INV), ({}, dict(axis=-1), INV), ({}, dict(rows=-1), INV),
     ({}, dict(rows=1 << 31), INV), ({}, dict(H=0), INV), ({}, dict(D=100), INV), ({}, dict(D=2048), UNS), ({}, dict(xs=1000), INV),
