@@ -530,7 +530,7 @@ cudaError_t launch_decode_blocks(const BlocksParams& p, cudaStream_t stream) {
     attr[1].val.clusterDim.x = (unsigned)p.parts;
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 2;
+    cfg.numAttrs = p.parts > 1 ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, kern, p, maps);
 }
 

@@ -264,7 +264,7 @@ cudaError_t launch_pages(const PagesParams& p, cudaStream_t stream) {
     attr[0].val.clusterDim.x = (unsigned)parts;
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = parts > 1 ? 1 : 0;
     return cudaLaunchKernelEx(&cfg, pages_kernel, p, parts);
 }
 
