@@ -74,14 +74,22 @@ kvd_status check_place(const int32_t* block_table, int s_max, int max_blocks, in
     return KVD_OK;
 }
 
-// CTAs of a pair: enough that all together fill the multiprocessors' places, as far as every team keeps two
-// stages; joined in a cluster up to 16, beyond that (few pairs of long lists) in several clusters of which each team keeps four.
-void split_blocks(long long pairs, long long stages, int teams, long long places, int* parts, int* shards) {
-    int n = 1;
-    while (n < 16 && pairs * n * 2 <= places && stages >= 4LL * n * teams) n *= 2;
-    *parts = n;
-    *shards = 1;
-    if (n == 16) *shards = (int)std::max(1LL, std::min(places / (pairs * 16), stages / (64LL * teams)));
+// CTAs of a pair (a cluster of n) and clusters of a pair. Clusters run in waves, as many at once as the
+// multiprocessors' groups hold: of 152 multiprocessors 76 clusters on two of them, 36 on four, 14 on eight, 7 on sixteen
+// (two CTAs a multiprocessor halve what a cluster takes). A CTA costs about what 18 stages cost one CTA (start, list, join), so
+// that n is the one with the least waves * (18 + stages / n). 16 pairs of 4,096 tokens, 8 heads: clusters of 4 / 8 / 16 take
+// 17.6 / 11.8 / 17.7 us (two waves of 16); 360 pairs of 2,048: one CTA 64, two 58, four 67. Pairs of which clusters of 16 leave
+// places free get several clusters of 128 stages and more, joined by a second launch (4 us; one pair of 16,384 tokens: 17.4 -> 12).
+void split_blocks(long long pairs, long long stages, int ctas, int sms, int* parts, int* shards) {
+    constexpr int kTenths[5] = {10, 20, 42, 108, 200};  // multiprocessors that a cluster on 1, 2, 4, 8, 16 of them takes, in tenths
+    long long best = 0, room = 0;
+    *parts = *shards = 1;
+    for (int i = 0; i < 5 && (i == 0 || stages >= 1 << i); ++i) {
+        const long long at_once = std::max(1LL, i == 0 ? (long long)sms * ctas : 10LL * sms / kTenths[i - (ctas > 1)]);
+        const long long cost = (pairs + at_once - 1) / at_once * (18 * 16 + (stages * 16 >> i));
+        if (i == 0 || cost < best) best = cost, *parts = 1 << i, room = at_once / pairs;
+    }
+    if (*parts == 16) *shards = (int)std::max(1LL, std::min(room, stages / 128));
 }
 
 kvd_status plan_blocks(int batch, int T, int Hq, int Hkv, int D, int K, int block_tokens, int num_sms, BlocksParams* p, size_t* ws) {
@@ -109,7 +117,7 @@ kvd_status plan_blocks(int batch, int T, int Hq, int Hkv, int D, int K, int bloc
     *ws = 0;
     p->parts = p->shards = 1;
     if (pairs == 0) return KVD_OK;
-    split_blocks(pairs, (long long)K * block_tokens / kBlocksStage, p->teams, (D == 256 ? 1LL : 2LL) * sms, &p->parts, &p->shards);
+    split_blocks(pairs, std::max(1LL, (long long)K * block_tokens / kBlocksStage), D == 256 ? 1 : 2, sms, &p->parts, &p->shards);
     if (p->shards > 1) {
         const size_t rows = (size_t)pairs * p->G;
         *ws = align256(p->shards * rows * D * sizeof(float)) + align256(p->shards * rows * sizeof(float));
