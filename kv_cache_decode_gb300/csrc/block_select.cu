@@ -7,8 +7,10 @@
 // the list ascends. Since I is a whole number, exact in float32 in whatever order it is summed, the selection is a
 // matter of definition and not of the order of additions.
 //
-// Reads 2 D + 4 bytes a (block, KV head) once for all query tokens; bound by memory for batches, by latency for one
-// sequence. The first launch scores, some CTAs a (sequence, KV head), a warp tiles of 16 blocks: f16 MMAs
+// Reads 2 D + 4 bytes a (block, KV head) once for all query tokens. 32 sequences of 16,384 to 131,072 tokens in blocks of 32, 32 heads
+// on 8 of 128: 41 us, 31 scoring (153 MB at 4.9 TB/s: latency between loads and scores, 10 cycles an instruction of a warp) and 10 selecting;
+// one of 131,072 in blocks of 64: 7.9, latency throughout. (Both in one launch of clusters: 53 and 9.9, since the cluster waits for its
+// slowest part and the selection holds the scorers' places.) The first launch scores, some CTAs a (sequence, KV head), a warp tiles of 16 blocks: f16 MMAs
 // m16n8k16 with the blocks as rows and the query rows as columns, I = [hi lo] [max(c, 0) min(c, 0)]^T. A code enters as code + 128
 // in the low bits of an f16, a subnormal; products and sums of these are whole numbers below 2^24 (times 2^-24), so exact. A lane's 16-byte
 // copy is 16 consecutive codes of a row; the MMA's k order is the permutation of columns that fits, the same for both operands, so codes

@@ -2,7 +2,9 @@
 // head), the softmax over the tokens of the blocks that its list names,
 //   s_t = scale * q . k_t,  out = sum_t 2^(s_t - m) v_t / sum_t 2^(s_t - m)   (base 2, log2(e) in the scale).
 // It reads K * block rows of K and V a pair where the attention over all tokens reads the sequence;
-// bound by memory for batches, by latency for one sequence.
+// bound by memory for batches (64 sequences, 32 heads on 8 of 128, 4,096 tokens each: 159 us for 1.07 GB, the copy rate), by latency for
+// one sequence (2,048 tokens: 6.6 to 7 us), by shared-memory reads for wide groups at head_dim 256, whose 6 or 8 warps each read
+// every K and V row (64 sequences, 48 heads on one, 4,096 tokens: 72 us, 3.8 TB/s; 32 heads 50.5).
 //
 // A stage is 32 tokens, K rows and V rows, brought by TMA into a ring (128-byte swizzle): as one box
 // where blocks and pages have 32 tokens, else two units of 16 of any listed blocks. A loading warp looks the list up, 32 units at a

