@@ -359,10 +359,13 @@ __global__ void __launch_bounds__(kPickThreads) block_pick_kernel(const SelectPa
 #pragma unroll 1
     for (int round = 0; round < 3; ++round) {
         const int shift = max(0, 21 - __clz(hi - lo));  // (hi - lo) >> shift is below 2,048
-#pragma unroll 4
-        for (int i = lo_j + tid; i < hi_j; i += kPickThreads) {
-            const uint32_t k = key[i];
-            if (k >= lo && k <= hi) atomicAdd(&s_hist[(k - lo) >> shift], 1u);
+        for (int i0 = lo_j + tid; i0 < hi_j; i0 += 8 * kPickThreads) {  // (loads first: none is moved ahead of an atomic)
+            uint32_t k[8];
+#pragma unroll
+            for (int u = 0; u < 8; ++u) k[u] = i0 + u * kPickThreads < hi_j ? key[i0 + u * kPickThreads] : 0u;  // 0: below every lo
+#pragma unroll
+            for (int u = 0; u < 8; ++u)
+                if (k[u] >= lo && k[u] <= hi) atomicAdd(&s_hist[(k[u] - lo) >> shift], 1u);
         }
         __syncthreads();
         // Thread i adds up 4 parts, from the top, and leaves zeros; the one in which the running sum reaches `need` has the border.
@@ -404,16 +407,23 @@ __global__ void __launch_bounds__(kPickThreads) block_pick_kernel(const SelectPa
 #pragma unroll 1
     for (int c0 = lo_j; c0 < hi_j; c0 += CHUNK) {
         const int words = (min(CHUNK, hi_j - c0) + 31) / 32;
-#pragma unroll 4
-        for (int w = warp; w < words; w += WARPS) {
-            const int i = c0 + 32 * w + lane;
-            const uint32_t k = i < hi_j ? key[i] : 0u;
-            const bool border = k >= lo && k <= hi;
-            const uint32_t keep = __ballot_sync(0xffffffffu, k > hi || (border && !value && !ranked));
-            const uint32_t same = __ballot_sync(0xffffffffu, border);
-            if (lane == 0) s_keep[w] = keep;
-            if (lane == 1) s_same[w] = same;
-            if (ranked && one_chunk && border) tie(k, i);
+        for (int w0 = warp; w0 < words; w0 += 4 * WARPS) {
+            uint32_t k[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const int i = c0 + 32 * (w0 + u * WARPS) + lane;
+                k[u] = i < hi_j ? key[i] : 0u;
+            }
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const int w = w0 + u * WARPS;
+                const bool border = k[u] >= lo && k[u] <= hi;
+                const uint32_t keep = __ballot_sync(0xffffffffu, k[u] > hi || (border && !value && !ranked));
+                const uint32_t same = __ballot_sync(0xffffffffu, border);
+                if (w < words && lane == 0) s_keep[w] = keep;
+                if (w < words && lane == 1) s_same[w] = same;
+                if (ranked && one_chunk && border && w < words) tie(k[u], c0 + 32 * w + lane);
+            }
         }
         __syncthreads();
         if (ranked) {
