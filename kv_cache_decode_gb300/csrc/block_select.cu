@@ -8,8 +8,8 @@
 // matter of definition and not of the order of additions.
 //
 // Reads 2 D + 4 bytes a (block, KV head) once for all query tokens. 32 sequences of 16,384 to 131,072 tokens in blocks of 32, 32 heads
-// on 8 of 128: 41 us, 31 scoring (153 MB at 4.9 TB/s: latency between loads and scores, 10 cycles an instruction of a warp) and 10 selecting;
-// one of 131,072 in blocks of 64: 7.9, latency throughout. (Both in one launch of clusters: 53 and 9.9, since the cluster waits for its
+// on 8 of 128: 41 us, 33 scoring (153 MB at 4.6 TB/s: some 500 instructions a tile of 16 blocks, a third of them the rows' fragments) and 8 selecting;
+// one of 131,072 in blocks of 64: 7.4, latency throughout; 65,536 keys a CTA, which it reads from L2, 44 to select. (Both in one launch of clusters: 53 and 9.9, since the cluster waits for its
 // slowest part and the selection holds the scorers' places.) The first launch scores, some CTAs a (sequence, KV head), a warp tiles of 16 blocks: f16 MMAs
 // m16n8k16 with the blocks as rows and the query rows as columns, I = [hi lo] [max(c, 0) min(c, 0)]^T. A code enters as code + 128
 // in the low bits of an f16, a subnormal; products and sums of these are whole numbers below 2^24 (times 2^-24), so exact. A lane's 16-byte
@@ -320,18 +320,26 @@ __global__ void __launch_bounds__(kPickThreads) block_pick_kernel(const SelectPa
     const bool fits = (long long)vecs * 16 + kSelBins * 4 + kSelTies * 8 <= room;
     const uint32_t* key = fits ? s_key : src;
     uint32_t mn = 0xffffffffu, mx = 0u;
-#pragma unroll 2
-    for (int v = tid; v < vecs; v += kPickThreads) {
-        const uint4 x = __ldcg(reinterpret_cast<const uint4*>(src) + v);
-        uint32_t k[4] = {x.x, x.y, x.z, x.w};
+    for (int v0 = tid; v0 < vecs; v0 += 4 * kPickThreads) {
+        uint4 x[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const bool in = 4 * v + e >= lo_j && 4 * v + e < hi_j;
-            if (!in) k[e] = 0u;
-            mn = min(mn, in ? k[e] : 0xffffffffu);
-            mx = max(mx, k[e]);
+        for (int u = 0; u < 4; ++u) {
+            const int v = v0 + u * kPickThreads;
+            x[u] = v < vecs ? __ldcg(reinterpret_cast<const uint4*>(src) + v) : make_uint4(0u, 0u, 0u, 0u);
         }
-        if (fits) reinterpret_cast<uint4*>(s_key)[v] = make_uint4(k[0], k[1], k[2], k[3]);
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const int v = v0 + u * kPickThreads;
+            uint32_t k[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const bool in = 4 * v + e >= lo_j && 4 * v + e < hi_j;
+                if (!in) k[e] = 0u;
+                mn = min(mn, in ? k[e] : 0xffffffffu);
+                mx = max(mx, k[e]);
+            }
+            if (fits && v < vecs) reinterpret_cast<uint4*>(s_key)[v] = make_uint4(k[0], k[1], k[2], k[3]);
+        }
     }
     mn = __reduce_min_sync(0xffffffffu, mn);
     mx = __reduce_max_sync(0xffffffffu, mx);
@@ -400,8 +408,14 @@ __global__ void __launch_bounds__(kPickThreads) block_pick_kernel(const SelectPa
     auto tie = [&](uint32_t k, int i) { s_tie[atomicAdd(&s_ties, 1u) & (kSelTies - 1)] = make_uint2(k, (uint32_t)i); };
     const bool one_chunk = hi_j - lo_j <= CHUNK;
     if (ranked && !one_chunk) {
-        for (int i = lo_j + tid; i < hi_j; i += kPickThreads)
-            if (key[i] >= lo && key[i] <= hi) tie(key[i], i);
+        for (int i0 = lo_j + tid; i0 < hi_j; i0 += 8 * kPickThreads) {
+            uint32_t k[8];
+#pragma unroll
+            for (int u = 0; u < 8; ++u) k[u] = i0 + u * kPickThreads < hi_j ? key[i0 + u * kPickThreads] : 0u;
+#pragma unroll
+            for (int u = 0; u < 8; ++u)
+                if (k[u] >= lo && k[u] <= hi) tie(k[u], i0 + u * kPickThreads);
+        }
     }
     uint32_t base = 0;  // kept before this chunk
 #pragma unroll 1
