@@ -166,6 +166,23 @@ def test_attention_long_and_many(Hq, Hkv, D, block, K, lens):
         assert np.array_equal(got[0], again[0]) and np.array_equal(got[1], again[1])
 
 
+@pytest.mark.parametrize("Hq,D", [(8, 64), (48, 64), (3, 128), (48, 128), (8, 256), (20, 256)])
+@pytest.mark.parametrize("B", [400, 100, 50, 12, 4])
+def test_attention_by_how_many_pairs_there_are(Hq, D, B):
+    """From one CTA a pair to clusters of 16, joined by sent and by fetched states."""
+    dev = cuda_or_skip()
+    r = np.random.default_rng(B + D)
+    lens = r.integers(0, 180, B)
+    c = Cache(r, lens, 1, D, 16, dev)
+    q = _normal(r, (B, 1, Hq, D))
+    for K in (9, 33):
+        x = _lists(r, c, 1, K, 16)
+        for dtype in ("f32", "bf16"):
+            got = _run(c, q, x, 16, dev, dtype)
+            assert got[2] == 0
+            _close(got[:2], _want(c, q, x, 16), dtype)
+
+
 def test_attention_scores():
     """Scores that rise along the list raise the maxima again and again; one that towers; equal ones."""
     dev = cuda_or_skip()
