@@ -6,9 +6,10 @@
 // finite gets the scale NaN and codes 0.
 //
 // A CTA of four warps takes one KV head of one block, or, of blocks of up to 4,096 values, a warp each: 2 * block * D bytes read
-// once, 2 D + 4 written; bound by memory for prompts (82 us for 537 MB, 6.6 TB/s), by latency for the few blocks that a step fills. A
-// thread holds 8 columns' running maxima and minima of its tokens as bf16 pairs (exact), eight loads in flight. (32 x 8,192 tokens, 8 KV
-// heads of 128, blocks of 16: a warp a block 106 us, a CTA 210; of 32: 91 and 109.)
+// once, 2 D + 4 written; bound by memory for prompts (80.5 us for 537 MB in blocks of 64, the copy rate; in blocks of 16 87, at 64 columns
+// 115), by latency for the few blocks that a step fills (3.3 us). A thread holds 8 columns' running maxima and minima of its tokens as
+// bf16 pairs (exact), eight loads in flight; the divisions are shared out to the lanes that hold the same columns (all of them in each: 83, 106
+// and 175 us). Blocks of 16 of 128 columns by whole CTAs: 210.
 #include "../../include/kvdecode.h"
 #include "blocks.h"
 #include "common.cuh"
@@ -61,8 +62,7 @@ __global__ void __launch_bounds__(kBoundsThreads) block_bounds_kernel(const Boun
         block = (long long)b * (p.S_max >> bs) + j;
     }
     // ---- maxima and minima of this thread's columns ----
-    const int c = tid % TPR;
-    const uint4* k = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.k) + ((size_t)row * p.Hkv + h) * D) + c;
+    const uint4* k = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.k) + ((size_t)row * p.Hkv + h) * D) + tid % TPR;
     const size_t step = (size_t)p.Hkv * TPR;  // 16-byte vectors between tokens
     uint32_t hi[4], lo[4];
     const int t0 = tid / TPR;
@@ -98,13 +98,13 @@ __global__ void __launch_bounds__(kBoundsThreads) block_bounds_kernel(const Boun
         __syncthreads();
         if (warp != 0) return;
     }
-    // ---- the scale and the codes ----
-    float fh[8], fl[8], a = 0.f;
-    bool bad = false;
-    if (lane < TPR) {
+    // ---- the scale and the codes: a lane takes a share of its 8 columns, since all that hold them have the same result ----
+    constexpr int SHARES = 32 / TPR, PAIRS = 4 / SHARES;  // lanes of the same columns; pairs of columns of each
+    const int share = lane / TPR, c = lane % TPR;
+    if constexpr (WPI > 1) {
 #pragma unroll
         for (int w = 1; w < WPI; ++w) {
-            const uint4 x = s_hi[w][lane], y = s_lo[w][lane];
+            const uint4 x = s_hi[w][c], y = s_lo[w][c];
             const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
@@ -112,37 +112,48 @@ __global__ void __launch_bounds__(kBoundsThreads) block_bounds_kernel(const Boun
                 lo[e] = min_bf16x2(lo[e], ys[e]);
             }
         }
+    }
+    float fh[2 * PAIRS], fl[2 * PAIRS], a = 0.f;
+    bool bad = false;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            fh[2 * e] = bf16_lo(hi[e]), fh[2 * e + 1] = bf16_hi(hi[e]);
-            fl[2 * e] = bf16_lo(lo[e]), fl[2 * e + 1] = bf16_hi(lo[e]);
-        }
+    for (int e = 0; e < PAIRS; ++e) {
+        uint32_t x = hi[e], y = lo[e];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            bad |= !isfinite(fh[e]) || !isfinite(fl[e]);  // a NaN shows in the maximum, infinities in either
-            a = fmaxf(a, fmaxf(fabsf(fh[e]), fabsf(fl[e])));
-        }
+        for (int g = 1; g < SHARES; ++g)
+            if (share == g) x = hi[g * PAIRS + e], y = lo[g * PAIRS + e];
+        fh[2 * e] = bf16_lo(x), fh[2 * e + 1] = bf16_hi(x);
+        fl[2 * e] = bf16_lo(y), fl[2 * e + 1] = bf16_hi(y);
     }
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, off));
+    for (int e = 0; e < 2 * PAIRS; ++e) {
+        bad |= !isfinite(fh[e]) || !isfinite(fl[e]);  // a NaN shows in the maximum, infinities in either
+        a = fmaxf(a, fmaxf(fabsf(fh[e]), fabsf(fl[e])));
+    }
+    a = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(a)));  // (not negative: their bits are in order)
     bad = __any_sync(0xffffffffu, bad);
     const float s = bad ? __uint_as_float(0x7fffffffu) : __fdiv_rn(a, 127.f);
     const size_t at = (size_t)block * p.Hkv + h;
     if (lane == 0) p.scales[at] = s;
-    if (lane < TPR) {
-        uint32_t up[2] = {0u, 0u}, down[2] = {0u, 0u};
-        if (!bad && s > 0.f) {
+    uint32_t up[(PAIRS + 1) / 2] = {}, down[(PAIRS + 1) / 2] = {};
+    if (!bad && s > 0.f) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const int x = max(-127, min(127, __float2int_ru(__fdiv_rn(fh[e], s))));
-                const int y = max(-127, min(127, __float2int_rd(__fdiv_rn(fl[e], s))));
-                up[e >> 2] |= (uint32_t)(x & 0xff) << (8 * (e & 3));
-                down[e >> 2] |= (uint32_t)(y & 0xff) << (8 * (e & 3));
-            }
+        for (int e = 0; e < 2 * PAIRS; ++e) {
+            const int x = max(-127, min(127, __float2int_ru(__fdiv_rn(fh[e], s))));
+            const int y = max(-127, min(127, __float2int_rd(__fdiv_rn(fl[e], s))));
+            up[e >> 2] |= (uint32_t)(x & 0xff) << (8 * (e & 3));
+            down[e >> 2] |= (uint32_t)(y & 0xff) << (8 * (e & 3));
         }
-        uint2* dst = reinterpret_cast<uint2*>(p.codes + at * 2 * D);
-        dst[lane] = make_uint2(up[0], up[1]);
-        dst[TPR + lane] = make_uint2(down[0], down[1]);
+    }
+    int8_t* dst = p.codes + at * 2 * D + 8 * c + 2 * PAIRS * share;
+    if constexpr (PAIRS == 1) {
+        *reinterpret_cast<uint16_t*>(dst) = (uint16_t)up[0];
+        *reinterpret_cast<uint16_t*>(dst + D) = (uint16_t)down[0];
+    } else if constexpr (PAIRS == 2) {
+        *reinterpret_cast<uint32_t*>(dst) = up[0];
+        *reinterpret_cast<uint32_t*>(dst + D) = down[0];
+    } else {
+        *reinterpret_cast<uint2*>(dst) = make_uint2(up[0], up[1]);
+        *reinterpret_cast<uint2*>(dst + D) = make_uint2(down[0], down[1]);
     }
 }
 
