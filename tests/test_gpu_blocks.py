@@ -424,6 +424,32 @@ def test_select(Hq, Hkv, D, T, block, page):
         assert np.array_equal(got, _select_want(q, codes, scales, lens, block, K, first, last, bt, page)), (K, first, last)
 
 
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("G,T", [(1, 1), (8, 2), (8, 3), (8, 6), (8, 11), (3, 9), (12, 1), (12, 2), (12, 3), (12, 5), (2, 25), (64, 2)])
+def test_select_widths(D, G, T):
+    """Every number of query rows scored at once, in one round and several, for sequences of no block to many."""
+    dev = cuda_or_skip()
+    r = np.random.default_rng(D + G + T)
+    Hkv, block = 2, 16
+    for page in (0, 32):
+        lens = [16 * 300 + 3, 0, 16 * 33, 16 * 8 - 1, 16 * 150, 31]
+        nb, B = 301, len(lens)
+        bt, n, per = None, B, nb
+        if page:
+            per = page // block
+            n = B * 151 + 2
+            bt = r.permutation(n)[:B * 151].reshape(B, 151).astype(np.int32)
+            for b, L in enumerate(lens):
+                bt[b, -(-L // page):] = -1
+        codes = _codes(r, (n, per, Hkv, D))
+        scales = r.uniform(0.01, 0.03, (n, per, Hkv)).astype(np.float32)
+        q = _normal(r, (B, T, G * Hkv, D))
+        for K, first, last in ((8, 1, 2), (100, 0, 1)):
+            got, st = _select(dev, q, codes, scales, lens, nb * block, block, K, first, last, bt)
+            assert st == 0
+            assert np.array_equal(got, _select_want(q, codes, scales, lens, block, K, first, last, bt, page)), (K, page)
+
+
 def test_select_whole_numbers_are_exact():
     """The largest sums there are, and neighbours one apart; many ties; scales that order blocks by their last bit."""
     dev = cuda_or_skip()
