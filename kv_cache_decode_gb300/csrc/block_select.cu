@@ -268,7 +268,7 @@ __global__ void __launch_bounds__(SelectShape<D>::THREADS, D == 256 ? 1 : NT == 
                         if (width > 4) v0 = fmaxf(v0, __shfl_xor_sync(0xffffffffu, v0, 2));
                         const int j = j0 + g8 + 8 * e;
                         if (j >= full) continue;
-                        const int t = G > 8 ? n / per_tok : (8 * n + 2 * j4) / cols;  // of this round
+                        const int t = G > 8 ? n / per_tok : (8 * n + 2 * j4) / cols;  // among those scored at once
                         const uint32_t k0 = ok[e] ? score_key(__fmul_rn(v0, sc[e])) : kSelNoPage;
                         if (width == 1) {
                             if (t < nt) keys[(size_t)(t0 + t) * p.key_stride + j] = k0;
