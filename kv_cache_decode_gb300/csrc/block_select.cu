@@ -91,7 +91,8 @@ __global__ void __launch_bounds__(SelectShape<D>::THREADS, D == 256 ? 1 : NT == 
         const int per_tok = (G + 7) / 8;                 // tiles of a token (G > 8: several)
         const int toks = G > 8 ? NT / per_tok : NT * (8 / cols);  // tokens of a round
         uint8_t* ring = smem + NT * Sh::FRAG + warp * STAGES * Sh::TILE;
-        // A tile's rows of this lane: blocks j0 + g8 and j0 + g8 + 8, by their place among all bounds (-1: none).
+        // A tile's rows of this lane: blocks j0 + g8 and j0 + g8 + 8, by their place among all bounds (-1: none). Lanes
+        // go different ways here; the warp comes together again at the end.
         auto look_up = [&](int j0, long long (&at)[2]) {
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
@@ -113,6 +114,7 @@ __global__ void __launch_bounds__(SelectShape<D>::THREADS, D == 256 ? 1 : NT == 
                     if (blk >= 0) at[e] = blk * p.Hkv + h;
                 }
             }
+            __syncwarp();
         };
         // Their codes and scales on the way to the lane's own places of a stage; `have` keeps which rows are there.
         uint32_t have = 0;
@@ -185,7 +187,7 @@ __global__ void __launch_bounds__(SelectShape<D>::THREADS, D == 256 ? 1 : NT == 
                             c[e] = rintf(x);
                             near |= fabsf(fabsf(x - c[e]) - 0.5f) < 1e-4f;
                         }
-                        if (near) {
+                        if (near) {  // (by lane; the warp meets again before the sum)
 #pragma unroll
                             for (int e = 0; e < 2; ++e) c[e] = rintf(__fdiv_rn(e ? bf16_hi(qw[i]) : bf16_lo(qw[i]), s));
                         }
@@ -198,9 +200,11 @@ __global__ void __launch_bounds__(SelectShape<D>::THREADS, D == 256 ? 1 : NT == 
                     f[KS / 2 * 64] = pack_f16x2(fminf(c[0], 0.f), fminf(c[1], 0.f));
                     sum += (int)c[0] + (int)c[1];
                 }
+                __syncwarp();
                 sum = __reduce_add_sync(0xffffffffu, sum);
                 if (lane == 0) s_sc[x] = s, s_bias[x] = (float)sum * -0x1p-17f;  // -128 of them, in units of 2^-24
             }
+            __syncwarp();
             __syncthreads();
             int stage = 0;
             for (int j0 = first; j0 < full; j0 += step) {
@@ -210,7 +214,9 @@ __global__ void __launch_bounds__(SelectShape<D>::THREADS, D == 256 ? 1 : NT == 
                 cp_async_commit();
                 look_up(j0 + STAGES * step, at);
                 cp_async_wait<STAGES - 1>();
-                asm volatile("" ::: "memory");
+                // The MMAs are .aligned: a warp's threads have to execute each of them together. What came before (look-ups, the
+                // last tile's stores) let lanes go different ways, and only this makes sure that they have met again.
+                __syncwarp();
                 const uint8_t* mine = ring + stage * Sh::TILE + lane * 16;
                 // Codes enter the MMAs as code + 128 in the low bits of an f16, a subnormal of that many 2^-24; the sums start
                 // from what that adds. Products and sums are whole numbers below 2^24 in these units: exact.
@@ -267,15 +273,16 @@ __global__ void __launch_bounds__(SelectShape<D>::THREADS, D == 256 ? 1 : NT == 
                         if (width > 2) v0 = fmaxf(v0, __shfl_xor_sync(0xffffffffu, v0, 1));
                         if (width > 4) v0 = fmaxf(v0, __shfl_xor_sync(0xffffffffu, v0, 2));
                         const int j = j0 + g8 + 8 * e;
-                        if (j >= full) continue;
+                        const bool here = j < full;
                         const int t = G > 8 ? n / per_tok : (8 * n + 2 * j4) / cols;  // among those scored at once
                         const uint32_t k0 = ok[e] ? score_key(__fmul_rn(v0, sc[e])) : kSelNoPage;
                         if (width == 1) {
-                            if (t < nt) keys[(size_t)(t0 + t) * p.key_stride + j] = k0;
-                            if (t + 1 < nt) keys[(size_t)(t0 + t + 1) * p.key_stride + j] = ok[e] ? score_key(__fmul_rn(v1, sc[e])) : kSelNoPage;
-                        } else if ((2 * j4) % width == 0 && t < nt) {
+                            if (here && t < nt) keys[(size_t)(t0 + t) * p.key_stride + j] = k0;
+                            if (here && t + 1 < nt) keys[(size_t)(t0 + t + 1) * p.key_stride + j] = ok[e] ? score_key(__fmul_rn(v1, sc[e])) : kSelNoPage;
+                        } else if (here && (2 * j4) % width == 0 && t < nt) {
                             keys[(size_t)(t0 + t) * p.key_stride + j] = k0;
                         }
+                        __syncwarp();
                     }
                 }
             }

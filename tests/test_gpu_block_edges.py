@@ -1,0 +1,34 @@
+"""Edges of the page tables, the appends by slots and the attention over selected blocks on the GPU: what parts a warp's
+threads, states that do not hold together, caches shorter than a block, steps in which not every sequence grows."""
+import numpy as np
+import pytest
+
+import blocks_ref as ref
+from gpu_helpers import cuda_or_skip
+from test_gpu_blocks import _codes, _normal, _select, _select_want
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("G,T", [(1, 1), (2, 1), (1, 9), (8, 2), (8, 4), (8, 6), (8, 11), (12, 5)])
+def test_select_pages_missing_anywhere(D, G, T):
+    """Lanes of one tile of 16 blocks that go different ways: entries without a page here and there, sequences that end
+    inside a tile, every number of query rows scored at once, in one round and several."""
+    import kv_cache_decode_gb300 as kvd
+    dev = cuda_or_skip()
+    r = np.random.default_rng(1000 + D + G + T)
+    Hkv, block, page, nb = 2, 16, 32, 150
+    lens = [16 * 300 - 5, 16 * 257 + 3, 16 * 130, 16 * 9 + 1, 40]
+    B = len(lens)
+    n = B * nb + 2
+    bt = r.permutation(n)[:B * nb].reshape(B, nb).astype(np.int32)
+    bt[r.random(bt.shape) < 0.2] = -1
+    bt[r.random(bt.shape) < 0.1] = 2 ** 31 - 1
+    codes = _codes(r, (n, page // block, Hkv, D))
+    scales = r.uniform(0.01, 0.03, (n, page // block, Hkv)).astype(np.float32)
+    q = _normal(r, (B, T, G * Hkv, D))
+    for K, first, last in ((8, 1, 2), (100, 0, 1)):
+        got, st = _select(dev, q, codes, scales, lens, nb * page, block, K, first, last, bt)
+        assert st == kvd.STATUS_BAD_PAGE
+        assert np.array_equal(got, _select_want(q, codes, scales, lens, block, K, first, last, bt, page)), K
