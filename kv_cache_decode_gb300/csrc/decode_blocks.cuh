@@ -263,6 +263,7 @@ __global__ void __launch_bounds__((BlocksShape<D, NT>::WARPS + 1) * 32, BlocksSh
                 dead = true;
                 break;
             }
+            __syncwarp();  // (lanes leave the wait one by one; what follows is .aligned and wants them together)
             const int counts = s_n[st];
             if (counts == 0) break;
             const int n_tok[2] = {counts & 0xff, counts >> 8};
@@ -297,6 +298,7 @@ __global__ void __launch_bounds__((BlocksShape<D, NT>::WARPS + 1) * 32, BlocksSh
                         if ((lane >> 2) >= n_tok[u]) s[u][n][0] = s[u][n][1] = -CUDART_INF_F;
                         if ((lane >> 2) + 8 >= n_tok[u]) s[u][n][2] = s[u][n][3] = -CUDART_INF_F;
                     }
+                    __syncwarp();
                 }
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {

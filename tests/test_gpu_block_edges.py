@@ -5,7 +5,7 @@ import pytest
 
 import blocks_ref as ref
 from gpu_helpers import cuda_or_skip
-from test_gpu_blocks import _codes, _normal, _select, _select_want
+from test_gpu_blocks import Cache, _close, _codes, _normal, _run, _select, _select_want, _want
 
 pytestmark = pytest.mark.gpu
 
@@ -32,3 +32,18 @@ def test_select_pages_missing_anywhere(D, G, T):
         got, st = _select(dev, q, codes, scales, lens, nb * page, block, K, first, last, bt)
         assert st == kvd.STATUS_BAD_PAGE
         assert np.array_equal(got, _select_want(q, codes, scales, lens, block, K, first, last, bt, page)), K
+
+
+@pytest.mark.parametrize("block,page", [(16, 16), (32, 32), (64, 0)])
+@pytest.mark.parametrize("Hq,D", [(4, 64), (16, 128), (48, 64), (40, 256)])
+def test_attention_every_tail(Hq, D, block, page):
+    """Stages that end at every token, for teams of one warp and of several: the scores past the end are masked by lane."""
+    dev = cuda_or_skip()
+    r = np.random.default_rng(Hq + D + block)
+    c = Cache(r, list(range(1, 70)), 1, D, page, dev)
+    q = _normal(r, (c.B, 1, Hq, D))
+    x = np.tile(r.permutation(-(-c.S // block)).astype(np.int32), (c.B, 1, 1, 1))
+    for dtype in ("bf16", "f32"):
+        got = _run(c, q, x, block, dev, dtype)
+        assert got[2] == 0
+        _close(got[:2], _want(c, q, x, block), dtype)
