@@ -70,6 +70,23 @@ struct BlocksShape {
     static_assert(CTAS * (SMEM + 1024) <= 227 * 1024, "shared memory of an SM");
 };
 
+// How often slot s (stage s % R of team s / R) is filled by `issued` stages, dealt to the teams' rings of R in turn.
+__host__ __device__ constexpr int blocks_slot_uses(int issued, int s, int teams, int R) {
+    return issued > s % R * teams + s / R ? (issued - (s % R * teams + s / R) - 1) / (teams * R) + 1 : 0;
+}
+// ... as counting them one by one gives it.
+constexpr bool blocks_slot_uses_hold(int teams, int R) {
+    int uses[64] = {};
+    for (int issued = 0; issued < 5 * teams * R; ++issued) {
+        for (int s = 0; s < teams * R; ++s)
+            if (uses[s] != blocks_slot_uses(issued, s, teams, R)) return false;
+        ++uses[issued % teams * R + issued / teams % R];
+    }
+    return true;
+}
+static_assert(blocks_slot_uses_hold(1, 12) && blocks_slot_uses_hold(4, 3) && blocks_slot_uses_hold(2, 5) && blocks_slot_uses_hold(3, 4),
+              "the last phase of each slot");
+
 // The bf16 MMA of common.cuh without its ordering against other instructions.
 __device__ __forceinline__ void mma_bf16_free(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
     asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
@@ -128,6 +145,7 @@ __global__ void __launch_bounds__((BlocksShape<D, NT>::WARPS + 1) * 32, BlocksSh
 
     float o[MT][NT][4], m[NT][2], l[NT][2], lr[F32OUT ? 1 : NT][2];
     bool dead = false;
+    int issued = 0;  // stages the loading warp has issued
     if (loader) {
         // ---- the tokens this query token sees, and the units of this CTA ----
         const int us = p.unit_log2;
@@ -139,7 +157,7 @@ __global__ void __launch_bounds__((BlocksShape<D, NT>::WARPS + 1) * 32, BlocksSh
         const uint64_t policy = l2_evict_first_policy();
         if (raw != L && lane == 0 && p.status) atomicOr(p.status, KVD_STATUS_SEQ_LEN_CLAMPED);
         const int seen = L - p.T + 1 + t;  // <= 0: none
-        int issued = 0, to_team = 0, slot = 0, phase = 1;  // phase: parity of the last release of the slots in turn
+        int to_team = 0, slot = 0, phase = 1;  // phase: parity of the last release of the slots in turn
         auto next_stage = [&]() {  // the next stage's slot, or -1
             const int s = to_team * R + slot;
             if (issued >= teams * R && !__all_sync(0xffffffffu, tc::mbar_wait(empty(s), phase, abort_flag, kBudget))) return -1;
@@ -216,15 +234,6 @@ __global__ void __launch_bounds__((BlocksShape<D, NT>::WARPS + 1) * 32, BlocksSh
             } else if (lane == 0) {
                 s_n[s] = 0;
                 tc::mbar_arrive(full(s));
-            }
-        }
-        if (dead) {  // copies still on their way are waited for (again with a limit), since the ring's place is used below
-            for (int s = 0; s < teams * R; ++s) {
-                // the stages issued to this slot: its last one's phase
-                const int at = (s % R) * teams + s / R, uses = issued > at ? (issued - at + teams * R - 1) / (teams * R) : 0;
-                if (uses > 0)
-                    for (long long t0 = clock64(); !tc::mbar_test(full(s), (uses - 1) & 1) && clock64() - t0 < kBudget;) {
-                    }
             }
         }
     } else {
@@ -376,8 +385,21 @@ __global__ void __launch_bounds__((BlocksShape<D, NT>::WARPS + 1) * 32, BlocksSh
     }
     if (dead && lane == 0 && p.status) atomicOr(p.status, KVD_STATUS_TIMEOUT);
 
-    // ---- the states to shared memory, in the ring's place ----
+    // ---- where a wait of any warp gave up, copies may still be on their way: they are waited for (again with a limit), ----
+    // ---- since the ring's place is used below and the CTA must not leave before them ----
     __syncthreads();
+    if (*abort_flag) {  // (set before the barrier: every thread reads the same)
+        if (loader)
+            for (int s = 0; s < teams * R; ++s) {
+                const int uses = blocks_slot_uses(issued, s, teams, R);
+                if (uses > 0)
+                    for (long long t0 = clock64(); !tc::mbar_test(full(s), (uses - 1) & 1) && clock64() - t0 < kBudget;) {
+                    }
+            }
+        __syncthreads();
+    }
+
+    // ---- the states to shared memory, in the ring's place ----
     if (!loader) {
 #pragma unroll
     for (int n = 0; n < NT; ++n)
