@@ -104,15 +104,18 @@ __global__ void __launch_bounds__(kPagesThreads, 1) pages_kernel(const PagesPara
     }
     const int R = (int)released;
     // ---- a sequence grows when all that is needed up to it fits; one that needs no page always ----
+    // (Where lengths claim more pages than the pool has, the stack ends with the pool: never more than num_pages are given
+    // out, so that the tokens of those, below 2^31, and of every sequence's last page before are below 2^32.)
     const long long have = (long long)F + R;
-    uint32_t taken_u = 0, rows_u = 0;  // (the tokens of all pages, and of every sequence's last one, are below 2^32)
+    const int top = (int)min(have, (long long)p.num_pages);
+    uint32_t taken_u = 0, rows_u = 0;
     for (int b0 = 0; b0 < p.B; b0 += kPagesThreads) {
         const int b = b0 + tid;
         int old = 0, want = 0, need = 0;
         if (b < p.B) {  // (this thread's own entries)
             old = s_old[b], want = s_row[b];
             need = max(pages_of(want) - pages_of(old), 0);
-            if (need > 0 && (long long)s_need[b] + need > have) {
+            if (need > 0 && (long long)s_need[b] + need > top) {
                 need = 0;
                 want = old;
                 flags |= KVD_STATUS_NO_PAGES;
@@ -154,18 +157,17 @@ __global__ void __launch_bounds__(kPagesThreads, 1) pages_kernel(const PagesPara
         else
             flags |= KVD_STATUS_BAD_PAGE;  // more pages come back than the pool has
     }
-    const int top = (int)min(have, (long long)p.num_pages);
     sync();
-    // ---- pages taken: the i-th from place top - 1 - i ----
+    // ---- pages taken: the i-th from place top - 1 - i (taken <= top) ----
 #pragma unroll 4
     for (int i = gtid; i < taken; i += gthreads) {
         const int b = owner_of(s_need, p.B, i), held = pages_of(s_old[b]);
-        const int at = top - 1 - i, page = at >= 0 ? __ldcg(p.free_pages + at) : -1;
+        const int page = __ldcg(p.free_pages + (top - 1 - i));
         if ((unsigned)page >= (unsigned)p.num_pages) flags |= KVD_STATUS_BAD_PAGE;
         p.table[(size_t)b * p.max_blocks + held + (i - s_need[b])] = page;
     }
     if (rank == 0) {
-        if (tid == 0) *p.free_count = max(top - taken, 0);
+        if (tid == 0) *p.free_count = top - taken;
         for (int b = tid; b < p.B; b += kPagesThreads) {
             const int old = s_old[b], grown = s_row[b + 1] - s_row[b];
             int len = old + grown;

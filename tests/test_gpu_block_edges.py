@@ -47,3 +47,49 @@ def test_attention_every_tail(Hq, D, block, page):
         got = _run(c, q, x, block, dev, dtype)
         assert got[2] == 0
         _close(got[:2], _want(c, q, x, block), dtype)
+
+
+# ---------------------------------------------------------------------------
+# page tables
+# ---------------------------------------------------------------------------
+
+def _pages(dev, table, free, count, lens, new, page, rows):
+    import torch
+    import kv_cache_decode_gb300 as kvd
+    i32 = dict(dtype=torch.int32, device=dev)
+    t = [x if torch.is_tensor(x) else torch.tensor(x, **i32) for x in (table, free, count, lens, new)]
+    off, slots, st = torch.full((len(new) + 1,), 99, **i32), torch.full((rows,), 99, **i32), torch.zeros(1, **i32)
+    kvd.pages_update(*t, page, row_offsets=off, slots=slots, status=st)
+    torch.cuda.synchronize()
+    return t[:4] + [off.tolist(), slots.tolist()], int(st.item())
+
+
+def test_pages_no_more_than_the_pool_has():
+    """Lengths that claim more pages than there are: what comes back fills the stack, and no more is given out than it holds."""
+    import kv_cache_decode_gb300 as kvd
+    dev = cuda_or_skip()
+    none = [-1] * 4
+    held = [[0, 1, -1, -1], [1, 2, -1, -1]]
+    # 1 free and 4 that come back are taken for 3: four pages are not there
+    (table, free, count, lens, off, slots), st = _pages(dev, held + [none], [0, 1, 2], [1], [32, 32, 0], [0, 0, 64], 16, 5)
+    assert st == kvd.STATUS_BAD_PAGE | kvd.STATUS_NO_PAGES
+    assert table.tolist() == [none] * 3 and count.tolist() == [3] and lens.tolist() == [0, 0, 0]
+    assert off == [0] * 4 and slots == [-1] * 5
+    # three are
+    (table, free, count, lens, off, slots), st = _pages(dev, held + [none], [0, 1, 2], [1], [32, 32, 0], [0, 0, 48], 16, 49)
+    assert st == kvd.STATUS_BAD_PAGE and count.tolist() == [0] and lens.tolist() == [0, 0, 48] and off == [0, 0, 0, 48]
+    want = free.tolist()[::-1]
+    assert table.tolist() == [none] * 2 + [want + [-1]] and slots == [p * 16 + t for p in want for t in range(16)] + [-1]
+
+
+def test_pages_sums_past_32_bits():
+    """Tokens that lengths of this size would add up to pass 2^32: refused, since the pool cannot hold them."""
+    import torch
+    import kv_cache_decode_gb300 as kvd
+    dev = cuda_or_skip()
+    i32 = dict(dtype=torch.int32, device=dev)
+    table = torch.full((10, 1 << 18), -1, **i32)
+    (table, free, count, lens, off, slots), st = _pages(dev, table, torch.zeros(1, **i32), [1], [1 << 30] * 5 + [0] * 5, [0] * 5 + [1 << 30] * 5, 4096,
+                                                        1000)
+    assert st == kvd.STATUS_BAD_PAGE | kvd.STATUS_NO_PAGES
+    assert lens.tolist() == [0] * 10 and off == [0] * 11 and slots == [-1] * 1000 and bool((table == -1).all())
