@@ -632,6 +632,8 @@ kvd_status kvd_decode_fp4(const kvd_cache_fp4* cache, const void* q, const int32
  *   pos         : device int32 [batch], the lengths before: kvd_kv_append_rope's pos
  *   row_offsets : device int32 [batch + 1], running sums of the tokens that each sequence grew by
  *   slots       : device int32 [n_rows]: for the new tokens packed end to end, the cache row of each: page * page_size + place in it
+ *                 (a sequence that does not grow has none: row i of a step of one token each is not sequence i's then; sequence
+ *                 b's are those from row_offsets[b] to row_offsets[b + 1])
  *   positions   : device int32 [n_rows]: their positions in their sequences
  * Rows of slots and positions behind the last token are -1; tokens past n_rows get none (KVD_STATUS_POS_OUT_OF_RANGE). A table
  * entry or place of the stack that names no page is handed on as it is, its slots are -1 (KVD_STATUS_BAD_PAGE). Lengths before that hold more

@@ -1,5 +1,8 @@
 """Edges of the page tables, the appends by slots and the attention over selected blocks on the GPU: what parts a warp's
 threads, states that do not hold together, caches shorter than a block, steps in which not every sequence grows."""
+import os
+import re
+
 import numpy as np
 import pytest
 
@@ -93,3 +96,88 @@ def test_pages_sums_past_32_bits():
                                                         1000)
     assert st == kvd.STATUS_BAD_PAGE | kvd.STATUS_NO_PAGES
     assert lens.tolist() == [0] * 10 and off == [0] * 11 and slots == [-1] * 1000 and bool((table == -1).all())
+
+
+# ---------------------------------------------------------------------------
+# steps in which not every sequence grows
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("graph", [False, True])
+def test_readme_step(graph):
+    """The README's step as it stands there, for sequences that grow, pause, finish and find no page: every key and value in
+    its own sequence, and the answers of those that grew against the definitions."""
+    import torch
+    import kv_cache_decode_gb300 as kvd
+    dev = cuda_or_skip()
+    readme = open(os.path.join(os.path.dirname(os.path.abspath(__file__)), "..", "README.md")).read()
+    code, = [x for x in re.findall(r"```python\n(.*?)```", readme, re.S) if "RopeAxes" in x]
+    at = code.index("kvd.pages_update")
+    g = torch.Generator(device=dev)
+    g.manual_seed(11)
+    B, Hq, Hkv, D, max_blocks, pages = 6, 8, 2, 128, 4, 9
+    i32 = dict(dtype=torch.int32, device=dev)
+
+    def rows(*shape):
+        return torch.randn(*shape, generator=g, device=dev).bfloat16()
+    env = dict(torch=torch, kvd=kvd, B=B, Hq=Hq, Hkv=Hkv, D=D, max_len=64 * max_blocks, seq_lens=torch.zeros(B, **i32),
+               new_lens=torch.zeros(B, **i32), old=torch.zeros(B, **i32), slots=torch.zeros(B, **i32), offsets=torch.zeros(B + 1, **i32),
+               table=torch.full((B, max_blocks), -1, **i32), free=torch.arange(pages, **i32), count=torch.tensor([pages], **i32),
+               positions=torch.zeros(3, B, **i32), blocks=torch.zeros(B, Hkv, 64, **i32), status=torch.zeros(1, **i32),
+               out=torch.zeros(B, Hq, D, device=dev), q=rows(B, Hq, D), k_new=rows(B, Hkv, D), v_new=rows(B, Hkv, D),
+               k_pool=rows(pages, 64, Hkv, D), v_pool=rows(pages, 64, Hkv, D))
+    exec(code[:at], env)
+    step = compile(code[at:], "README.md", "exec")
+    # lengths before: pages 2 + 1 + 1 + 2 + 1 + 1 = 8 of 9
+    lens = [65, 1, 63, 128, 30, 64]
+    kvd.pages_update(env["table"], env["free"], env["count"], env["seq_lens"], torch.tensor(lens, **i32), 64)
+    assert int(env["count"]) == 1
+    keep = {n: x.clone() for n, x in env.items() if torch.is_tensor(x)}
+    if graph:
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            exec(step, env)
+        torch.cuda.current_stream().wait_stream(side)
+        G = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(G):
+            exec(step, env)
+        for n, x in keep.items():
+            env[n].copy_(x)
+    # sequence 3 takes the last page, 5 finds none; 1 pauses, 4 finishes (its page comes back first: 5 gets it in the next step)
+    steps = [([66, 1, 64, 129, 30, 65], [66, 1, 64, 129, 30, 64], True), ([67, 2, 64, 130, 0, 65], [67, 2, 64, 130, 0, 65], False),
+             ([67, 3, 65, 131, 1, 66], [67, 3, 64, 131, 0, 66], True)]
+    have = [dict() for _ in range(B)]  # what each sequence's tokens hold, by position: those of these steps
+    for want, got, refused in steps:
+        env["new_lens"].copy_(torch.tensor(want, **i32))
+        for n in ("q", "k_new", "v_new"):
+            env[n].copy_(rows(*env[n].shape))
+        env["positions"].copy_(torch.randint(0, 5000, (3, B), generator=g, device=dev))
+        env["status"].zero_()
+        kt, qt = torch.empty_like(env["k_new"]), torch.empty_like(env["q"])
+        kvd.rope_apply_axes(env["rope"], env["k_new"], env["positions"], kt)
+        kvd.rope_apply_axes(env["rope"], env["q"], env["positions"], qt)
+        vt = env["v_new"].clone()
+        G.replay() if graph else exec(step, env)
+        torch.cuda.synchronize()
+        assert env["seq_lens"].tolist() == got and int(env["status"]) == (kvd.STATUS_NO_PAGES if refused else 0)
+        grown = [b for b in range(B) if got[b] > lens[b]]
+        for b in range(B):
+            have[b] = {t: x for t, x in have[b].items() if t < got[b]}
+            if b in grown:
+                have[b][got[b] - 1] = kt[b].clone(), vt[b].clone()
+        table = env["table"].tolist()
+        kf, vf = env["k_pool"].view(-1, Hkv, D), env["v_pool"].view(-1, Hkv, D)
+        for b in range(B):
+            for t, (k, v) in have[b].items():
+                row = table[b][t // 64] * 64 + t % 64
+                assert torch.equal(kf[row], k) and torch.equal(vf[row], v), (b, t)
+        assert torch.equal(env["q"], qt)
+        for b in grown:  # (fewer blocks than 64: all of them)
+            at_rows = [table[b][t // 64] * 64 + t % 64 for t in range(got[b])]
+            k, v = (x[at_rows].double().cpu().numpy() for x in (kf, vf))
+            for h in range(Hkv):
+                o, _, spread = ref.attend(qt[b, 4 * h:4 * h + 4].double().cpu().numpy(), k[:, h], v[:, h], list(range(4)), got[b], 64,
+                                          D ** -0.5)
+                tol = 1e-4 * np.maximum(1, spread) + 2 * 2.0 ** -16 / (1 - 2.0 ** -16) * spread  # (test_gpu_blocks.py's, float32)
+                assert (np.abs(env["out"][b, 4 * h:4 * h + 4].double().cpu().numpy() - o) <= tol).all()
+        lens = got
