@@ -1446,7 +1446,8 @@ def pages_update(block_table, free_pages, free_count, seq_lens, new_lens, page_s
     (kvd_pages_update). int32 on one device: block_table [B, max_blocks], free_pages [num_pages] and free_count [1], and
     seq_lens [B] are updated; new_lens [B]. Written where given: pos [B] (the lengths before), row_offsets [B + 1],
     and for the new tokens packed end to end slots [N] and positions [N], -1 behind the last
-    (empty ones are as none)."""
+    (empty ones are as none). Sequence b's are those from row_offsets[b] to row_offsets[b + 1]: none where it does
+    not grow. Every page belongs to one sequence."""
     torch = _torch or _import_torch()
     what, i32 = "pages_update", torch.int32
     try:
