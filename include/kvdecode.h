@@ -657,7 +657,8 @@ kvd_status kvd_pages_update(int32_t* block_table, int32_t* free_pages, int32_t* 
  * 16 up to 256) and the factor: axis a takes sections[a] >= 1 pairs, which are neighbours (dealt 0: the first
  * sections[0] pairs turn by axis 0, the next by axis 1, ...) or dealt out in turn (dealt 1: 0, 1, 2, 0, 1, 2, ..., passing over
  * axes that have theirs). A pair's frequency goes by its index among all pairs (per_axis 0), or by its index among
- * its axis' pairs, as in a table of 2 * sections[a] columns (per_axis 1: sections are multiples of 8). Base and scaling as kvd_rope_table.
+ * its axis' pairs, as in a table of 2 * sections[a] columns (per_axis 1: sections[a] >= 8, of any size). Base and scaling as
+ * kvd_rope_table. (All pairs together are a multiple of 8: of a head of 72 columns 64 can be turned, not 72.)
  */
 #define KVD_MAX_AXES 4
 typedef struct kvd_rope_axes {

@@ -1483,7 +1483,8 @@ def rope_axes_table(sections, base: float = 10000.0, order: str = "blocks", per_
                     attn_factor: float = 0.0):
     """(turns, axes, factor) of pairs shared out to axes, sections[a] to axis a (kvd_rope_axes_table): frequencies
     as rope_table's and the axis of each pair, uint8, both [sum of sections] (numpy, on the host). order "blocks": an
-    axis' pairs are neighbours; "dealt": dealt out in turn. per_axis: frequencies by a pair's index among its axis' own."""
+    axis' pairs are neighbours; "dealt": dealt out in turn. per_axis: frequencies by a pair's index among its axis' own,
+    8 at least."""
     if scaling not in ROPE_SCALINGS:
         raise ValueError(f"scaling must be one of {sorted(ROPE_SCALINGS)}, got {scaling!r}")
     if order not in ("blocks", "dealt"):

@@ -179,7 +179,7 @@ kvd_status kvd_rope_axes_table(const int* sections, int n_axes, int dealt, int p
     if (!sections || !turns_host || !axes_host || !factor_out || n_axes < 1 || n_axes > KVD_MAX_AXES) return KVD_ERR_INVALID_ARG;
     int half = 0;
     for (int a = 0; a < n_axes; ++a) {
-        if (sections[a] < 1 || sections[a] > 128 || (per_axis && sections[a] % 8 != 0)) return KVD_ERR_INVALID_ARG;
+        if (sections[a] < (per_axis ? 8 : 1) || sections[a] > 128) return KVD_ERR_INVALID_ARG;
         half += sections[a];
     }
     if (half > 128 || half % 8 != 0) return KVD_ERR_INVALID_ARG;
@@ -195,8 +195,8 @@ kvd_status kvd_rope_axes_table(const int* sections, int n_axes, int dealt, int p
     float factor = 1.f;
     for (int a = 0; a < (per_axis ? n_axes : 1); ++a) {
         uint64_t own[128];
-        const kvd_status st = kvd_rope_table(2 * (per_axis ? sections[a] : half), base, scaling, scale, original_len, slow, fast,
-                                             attn_factor, own, &factor);
+        const kvd_status st = rope_turns(per_axis ? sections[a] : half, base, scaling, scale, original_len, slow, fast, attn_factor,
+                                         own, &factor);
         if (st != KVD_OK) return st;
         for (int i = 0; i < half; ++i)
             if (!per_axis || axis[i] == a) turns[i] = own[per_axis ? number[i] : i];

@@ -61,6 +61,9 @@ kvd_status check_paged(const int32_t* block_table, int max_blocks, int page_size
 kvd_status check_append(void* k_cache, void* v_cache, const void* k_new, const void* v_new, const int32_t* pos,
                         int batch, int s_max, int Hkv, int D, const int32_t* status);
 kvd_status device_sms(int* sms);
+// The frequencies of 8 to 128 pairs that share a table (api_fp4.cu).
+kvd_status rope_turns(int pairs, double base, kvd_rope_scaling scaling, double scale, double original_len, double slow, double fast,
+                      double attn_factor, uint64_t* turns_host, float* factor_out);
 size_t workspace_for(int n_split, int batch, int Hq, int Hkv, int D);
 
 }  // namespace kvd

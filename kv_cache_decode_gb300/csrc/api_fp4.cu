@@ -142,23 +142,18 @@ kvd_status plan_fp4(int batch, int T, int Hq, int Hkv, int D, int max_len, int n
 }
 
 }  // namespace
-}  // namespace kvd
 
-using namespace kvd;
-
-extern "C" {
-
-kvd_status kvd_rope_table(int rotary_dim, double base, kvd_rope_scaling scaling, double scale, double original_len,
-                          double slow, double fast, double attn_factor, uint64_t* turns_host, float* factor_out) {
-    if (!turns_host || !factor_out) return KVD_ERR_INVALID_ARG;
-    if (rotary_dim < 16 || rotary_dim > 256 || rotary_dim % 16 != 0) return KVD_ERR_INVALID_ARG;
+// The frequencies of pairs that share a table of 2 * pairs columns.
+kvd_status rope_turns(int pairs, double base, kvd_rope_scaling scaling, double scale, double original_len, double slow, double fast,
+                      double attn_factor, uint64_t* turns_host, float* factor_out) {
+    if (!turns_host || !factor_out || pairs < 8 || pairs > 128) return KVD_ERR_INVALID_ARG;
     if (!std::isfinite(base) || base <= 1.0 || !std::isfinite(attn_factor) || attn_factor < 0) return KVD_ERR_INVALID_ARG;
     const bool ramp = scaling == KVD_ROPE_PARTS || scaling == KVD_ROPE_WAVELENGTH;
     if (scaling < KVD_ROPE_NONE || scaling > KVD_ROPE_WAVELENGTH) return KVD_ERR_INVALID_ARG;
     if (scaling != KVD_ROPE_NONE && !(std::isfinite(scale) && scale >= 1.0)) return KVD_ERR_INVALID_ARG;
     if (ramp && !(std::isfinite(original_len) && original_len > 0 && slow > 0 && std::isfinite(fast) && fast > slow))
         return KVD_ERR_INVALID_ARG;
-    const double R = rotary_dim, two_pi = 6.283185307179586476925;
+    const double R = 2.0 * pairs, two_pi = 6.283185307179586476925;
     if (scaling == KVD_ROPE_BASE) base *= std::pow(scale, R / (R - 2.0));
     if (!std::isfinite(base)) return KVD_ERR_INVALID_ARG;
     double lo = 0, hi = 0;
@@ -168,7 +163,7 @@ kvd_status kvd_rope_table(int rotary_dim, double base, kvd_rope_scaling scaling,
         hi = std::min(std::ceil(index(slow)), R - 1.0);
         if (hi <= lo) hi = lo + 0.001;  // a step
     }
-    for (int i = 0; i < rotary_dim / 2; ++i) {
+    for (int i = 0; i < pairs; ++i) {
         double w = std::pow(base, -2.0 * i / R);
         double keep = 1.0;
         if (scaling == KVD_ROPE_LINEAR) keep = 0.0;
@@ -180,6 +175,18 @@ kvd_status kvd_rope_table(int rotary_dim, double base, kvd_rope_scaling scaling,
     }
     *factor_out = (float)(attn_factor > 0 ? attn_factor : scaling == KVD_ROPE_PARTS ? 0.1 * std::log(scale) + 1.0 : 1.0);
     return KVD_OK;
+}
+
+}  // namespace kvd
+
+using namespace kvd;
+
+extern "C" {
+
+kvd_status kvd_rope_table(int rotary_dim, double base, kvd_rope_scaling scaling, double scale, double original_len,
+                          double slow, double fast, double attn_factor, uint64_t* turns_host, float* factor_out) {
+    if (rotary_dim % 16 != 0) return KVD_ERR_INVALID_ARG;
+    return rope_turns(rotary_dim / 2, base, scaling, scale, original_len, slow, fast, attn_factor, turns_host, factor_out);
 }
 
 kvd_status kvd_rope_apply(const kvd_rope* rope, const void* x, long long x_stride, kvd_out_dtype in_dtype, void* y,

@@ -7,8 +7,10 @@ import numpy as np
 import pytest
 
 import blocks_ref as ref
-from gpu_helpers import cuda_or_skip
+from gpu_helpers import bf16_tensor_bits, cuda_or_skip, to_dev_bf16
 from test_gpu_blocks import Cache, _close, _codes, _normal, _run, _select, _select_want, _want
+from test_gpu_pages import _check_turn, _positions, _rope
+from workloads import bf16_bits_to_f32, f32_to_bf16_bits
 
 pytestmark = pytest.mark.gpu
 
@@ -96,6 +98,30 @@ def test_pages_sums_past_32_bits():
                                                         1000)
     assert st == kvd.STATUS_BAD_PAGE | kvd.STATUS_NO_PAGES
     assert lens.tolist() == [0] * 10 and off == [0] * 11 and slots == [-1] * 1000 and bool((table == -1).all())
+
+
+# ---------------------------------------------------------------------------
+# rotary positions of several axes
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("order,interleaved", [("blocks", False), ("dealt", False), ("blocks", True)])
+@pytest.mark.parametrize("sections,N,H,D", [((20, 20), 300, 16, 80), ((22, 21, 21), 77, 8, 128), ((8, 28, 28), 20000, 1, 128),
+                                            ((9, 15), 9, 3, 64), ((31, 33), 30000, 2, 256)])
+def test_turn_by_tables_of_each_axis(sections, N, H, D, order, interleaved):
+    """Sections that end inside a thread's eight pairs, each with frequencies of its own table."""
+    import torch
+    import kv_cache_decode_gb300 as kvd
+    dev = cuda_or_skip()
+    r = np.random.default_rng(sum(sections))
+    rope, turns, axes, factor = _rope(kvd, dev, sections, per_axis=True, order=order, interleaved=interleaved)
+    pos = _positions(r, len(sections), N)
+    x = r.standard_normal((N, H, D)).astype(np.float32)
+    bits = f32_to_bf16_bits(x)
+    xd, xb, pd = torch.from_numpy(x).to(dev), to_dev_bf16(bits, dev), torch.from_numpy(pos).to(dev)
+    kvd.rope_apply_axes(rope, xd, pd, xd)
+    _check_turn(xd.cpu().numpy().astype(np.float64), x, pos, turns, axes, factor, interleaved, False)
+    kvd.rope_apply_axes(rope, xb, pd, xb)
+    _check_turn(bf16_bits_to_f32(bf16_tensor_bits(xb)).astype(np.float64), bf16_bits_to_f32(bits), pos, turns, axes, factor, interleaved, True)
 
 
 # ---------------------------------------------------------------------------
