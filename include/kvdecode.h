@@ -707,6 +707,7 @@ kvd_status kvd_kv_append_axes(const kvd_cache* cache, const kvd_rope_axes* rope,
  *   codes  : int8 [batch, s_max / block_tokens, n_heads_kv, 2, head_dim] (hi, then lo), 16-byte aligned; for pools
  *            [num_pages, page_size / block_tokens, n_heads_kv, 2, head_dim], block_tokens at most page_size
  *   scales : float32 [batch, s_max / block_tokens, n_heads_kv] (pools likewise)
+ * A contiguous cache shorter than a block has no bounds: codes and scales may be NULL then.
  * kvd_kv_block_bounds writes the bounds of the blocks of a bf16 cache (K; contiguous [batch, s_max, ...] or pool) that are full at seq_lens[b]
  * and were not at from_lens[b] (NULL: 0), other entries left as they are; max_new is the largest seq_lens[b] - from_lens[b] the call may see (blocks past
  * it are left, KVD_STATUS_SEQ_LEN_CLAMPED). A table entry that names no page: nothing is written, KVD_STATUS_BAD_PAGE.

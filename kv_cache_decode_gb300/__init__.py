@@ -1673,7 +1673,8 @@ def _bounds(what, codes, scales, block_tokens, B, block_table, torch):
                 per * table, dev)
     if n != B:
         raise ValueError(f"{what}: inconsistent shapes")
-    return _pack_bounds(codes.data_ptr(), scales.data_ptr(), 0, per * blk, 0, 0, 0, blk), Hkv, D, per, dev
+    # (The bounds of a cache shorter than a block are empty; any capacity below a block says so.)
+    return _pack_bounds(codes.data_ptr(), scales.data_ptr(), 0, per * blk or blk - 1, 0, 0, 0, blk), Hkv, D, per, dev
 
 
 def kv_block_bounds(k, codes, scales, seq_lens, max_new: int, block_tokens: int, *, from_lens=None, block_table=None, status=None,

@@ -135,8 +135,8 @@ kvd_status check_bounds(const kvd_block_bounds* b, int batch, int Hkv, int D, Pa
     const kvd_status st = check_place(b->block_table, b->s_max, b->max_blocks, b->page_size, b->num_pages, batch, pg, cap, &rows);
     if (st != KVD_OK) return st;
     if (b->block_table && b->block_tokens > b->page_size) return KVD_ERR_INVALID_ARG;
-    if (!b->codes || !b->scales || !aligned(b->codes, 16) || !aligned(b->scales, 4)) return KVD_ERR_INVALID_ARG;
     *blocks = b->block_table ? (size_t)(rows / b->block_tokens) : (size_t)batch * (size_t)(b->s_max / b->block_tokens);
+    if ((*blocks > 0 && (!b->codes || !b->scales)) || !aligned(b->codes, 16) || !aligned(b->scales, 4)) return KVD_ERR_INVALID_ARG;
     return KVD_OK;
 }
 

@@ -54,6 +54,27 @@ def test_attention_every_tail(Hq, D, block, page):
         _close(got[:2], _want(c, q, x, block), dtype)
 
 
+@pytest.mark.parametrize("S,block", [(20, 32), (1, 16), (40, 4096)])
+def test_caches_shorter_than_a_block(S, block):
+    """No bounds, one block that every token sees: bounds, selection and attention as over any cache."""
+    import torch
+    import kv_cache_decode_gb300 as kvd
+    dev = cuda_or_skip()
+    r = np.random.default_rng(S)
+    c = Cache(r, [S, 0, 1, (S + 1) // 2], 2, 64, 0, dev, S=S)
+    codes, scales = kvd.alloc_block_bounds(c.kd, block)
+    assert codes.numel() == 0
+    status = torch.zeros(1, dtype=torch.int32, device=dev)
+    kvd.kv_block_bounds(c.kd, codes, scales, c.lens_d, S, block, status=status)
+    q = _normal(r, (4, 1, 8, 64))
+    got, st = _select(dev, q, codes.cpu().numpy(), scales.cpu().numpy(), c.lens.tolist(), S, block, 3, 1, 2)
+    assert st == 0 and int(status.item()) == 0
+    assert got.tolist() == [[[[0 if L else -1, -1, -1]] * 2] for L in c.lens.tolist()]
+    o, l, st = _run(c, q, got, block, dev, "f32")
+    assert st == 0
+    _close((o, l), _want(c, q, got, block), "f32")
+
+
 # ---------------------------------------------------------------------------
 # page tables
 # ---------------------------------------------------------------------------
