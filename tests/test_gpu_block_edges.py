@@ -9,7 +9,7 @@ import pytest
 import blocks_ref as ref
 from gpu_helpers import bf16_tensor_bits, cuda_or_skip, to_dev_bf16
 from test_gpu_blocks import Cache, _close, _codes, _normal, _run, _select, _select_want, _want
-from test_gpu_pages import _check_turn, _positions, _rope
+from test_gpu_pages import _check_turn, _positions, _rope, test_append as _append
 from workloads import bf16_bits_to_f32, f32_to_bf16_bits
 
 pytestmark = pytest.mark.gpu
@@ -49,6 +49,20 @@ def test_attention_every_tail(Hq, D, block, page):
     q = _normal(r, (c.B, 1, Hq, D))
     x = np.tile(r.permutation(-(-c.S // block)).astype(np.int32), (c.B, 1, 1, 1))
     for dtype in ("bf16", "f32"):
+        got = _run(c, q, x, block, dev, dtype)
+        assert got[2] == 0
+        _close(got[:2], _want(c, q, x, block), dtype)
+
+
+@pytest.mark.parametrize("Hq,Hkv,D,block,K,lens", [(8, 1, 128, 128, 256, [32768]), (1, 1, 64, 16, 700, [11111]),
+                                                   (48, 1, 256, 64, 128, [9000, 4097])])
+def test_attention_of_several_clusters_flags_nothing(Hq, Hkv, D, block, K, lens):
+    dev = cuda_or_skip()
+    r = np.random.default_rng(K)
+    c = Cache(r, lens, Hkv, D, 16, dev)
+    q = _normal(r, (c.B, 1, Hq, D))
+    x = r.integers(0, -(-c.S // block), (c.B, 1, Hkv, K)).astype(np.int32)
+    for dtype in ("f32", "bf16"):
         got = _run(c, q, x, block, dev, dtype)
         assert got[2] == 0
         _close(got[:2], _want(c, q, x, block), dtype)
@@ -143,6 +157,15 @@ def test_turn_by_tables_of_each_axis(sections, N, H, D, order, interleaved):
     _check_turn(xd.cpu().numpy().astype(np.float64), x, pos, turns, axes, factor, interleaved, False)
     kvd.rope_apply_axes(rope, xb, pd, xb)
     _check_turn(bf16_bits_to_f32(bf16_tensor_bits(xb)).astype(np.float64), bf16_bits_to_f32(bits), pos, turns, axes, factor, interleaved, True)
+
+
+@pytest.mark.parametrize("form,N,Hq,Hkv,D", [
+    ("bf16", 5, 4, 2, 80), ("bf16", 30000, 2, 1, 80), ("bf16", 7, 2, 1, 264), ("bf16", 30000, 2, 1, 264), ("bf16", 30000, 2, 1, 128),
+    ("bf16", 30000, 1, 1, 256), ("int8", 30000, 2, 1, 128), ("int8", 30000, 1, 1, 256), ("fp8", 30000, 2, 1, 128),
+    ("fp8", 30000, 1, 1, 256)])
+def test_append_every_width(form, N, Hq, Hkv, D):
+    """Heads of any width, and tokens of few heads, several to a warp, of every width: as test_gpu_pages.py's appends."""
+    _append(form, N, Hq, Hkv, D)
 
 
 # ---------------------------------------------------------------------------
