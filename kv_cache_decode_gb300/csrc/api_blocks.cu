@@ -22,6 +22,40 @@ cudaError_t allow_clusters(const void* kernel, int smem_bytes, std::atomic<uint6
     return e;
 }
 
+cudaError_t clusters_at_once(const void* kernel, int threads, int smem_bytes, std::atomic<uint64_t>* ready, std::atomic<uint64_t>* known,
+                             int (&n)[5]) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
+    uint64_t all = known[dev].load(std::memory_order_acquire);  // 12 bits a size, and a bit that says so
+    if (!all) {
+        if ((e = allow_clusters(kernel, smem_bytes, ready)) != cudaSuccess) return e;
+        all = 1ull << 63;
+        for (int i = 0; i < 5; ++i) {
+            cudaLaunchConfig_t cfg = {};
+            cfg.gridDim = dim3(16, 1, 1);
+            cfg.blockDim = dim3((unsigned)threads, 1, 1);
+            cfg.dynamicSmemBytes = (size_t)smem_bytes;
+            cudaLaunchAttribute attr[1];
+            attr[0].id = cudaLaunchAttributeClusterDimension;
+            attr[0].val.clusterDim.x = 1u << i;
+            attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+            cfg.attrs = attr;
+            cfg.numAttrs = 1;
+            int count = 0;
+            if (cudaOccupancyMaxActiveClusters(&count, kernel, &cfg) != cudaSuccess) {
+                (void)cudaGetLastError();
+                count = 0;  // none of this size
+            }
+            all |= (uint64_t)std::min(std::max(count, i == 0 ? 1 : 0), 0xfff) << (12 * i);
+        }
+        known[dev].store(all, std::memory_order_release);
+    }
+    for (int i = 0; i < 5; ++i) n[i] = (int)(all >> (12 * i)) & 0xfff;
+    return cudaSuccess;
+}
+
 namespace {
 
 constexpr int kMaxKept = 1 << 20;  // entries of a list
@@ -74,31 +108,39 @@ kvd_status check_place(const int32_t* block_table, int s_max, int max_blocks, in
     return KVD_OK;
 }
 
-// CTAs of a pair (a cluster of n) and clusters of a pair. Clusters run in waves, as many at once as the
-// multiprocessors' groups hold: of 152 multiprocessors 76 clusters on two of them, 36 on four, 14 on eight, 7 on sixteen
-// (two CTAs a multiprocessor halve what a cluster takes). A CTA costs about what 18 stages cost one CTA (start, list, join), so
-// that n is the one with the least waves * (18 + stages / n). 16 pairs of 4,096 tokens, 8 heads: clusters of 4 / 8 / 16 take
-// 17.6 / 11.8 / 17.7 us (two waves of 16); 360 pairs of 2,048: one CTA 64, two 58, four 67. Pairs of which clusters of 16 leave
-// places free get several clusters of 128 stages and more, joined by a second launch (4 us; one pair of 16,384 tokens: 17.4 -> 12).
-void split_blocks(long long pairs, long long stages, int ctas, int sms, int* parts, int* shards) {
-    constexpr int kTenths[5] = {10, 20, 42, 108, 200};  // multiprocessors that a cluster on 1, 2, 4, 8, 16 of them takes, in tenths
+// CTAs of a pair (a cluster of n) and clusters of a pair. Clusters run in waves, as many at once as the multiprocessors'
+// groups hold (at_once, by log2 n; 0: none of that size). A CTA costs about what 18 stages cost one CTA (start, list, join), so that n is
+// the one with the least waves * (18 + stages / n). 16 pairs of 4,096 tokens, 8 heads: clusters of 4 / 8 / 16 take 17.6 / 11.8 /
+// 17.7 us (two waves of 16); 360 pairs of 2,048: one CTA 64, two 58, four 67. Pairs of which clusters of 16 leave places free get
+// several clusters of 128 stages and more, joined by a second launch (4 us; one pair of 16,384 tokens: 17.4 -> 12).
+void split_blocks(long long pairs, long long stages, const int (&at_once)[5], int* parts, int* shards) {
     long long best = 0, room = 0;
     *parts = *shards = 1;
     for (int i = 0; i < 5 && (i == 0 || stages >= 1 << i); ++i) {
-        const long long at_once = std::max(1LL, i == 0 ? (long long)sms * ctas : 10LL * sms / kTenths[i - (ctas > 1)]);
-        const long long cost = (pairs + at_once - 1) / at_once * (18 * 16 + (stages * 16 >> i));
-        if (i == 0 || cost < best) best = cost, *parts = 1 << i, room = at_once / pairs;
+        if (at_once[i] == 0) continue;
+        const long long cost = (pairs + at_once[i] - 1) / at_once[i] * (18 * 16 + (stages * 16 >> i));
+        if (best == 0 || cost < best) best = cost, *parts = 1 << i, room = at_once[i] / pairs;
     }
     if (*parts == 16) *shards = (int)std::max(1LL, std::min(room, stages / 128));
 }
+
+// Of 152 multiprocessors with room for one CTA or two, as the device has it: for plans made for a number of multiprocessors.
+constexpr int kAtOnce[2][5] = {{152, 76, 36, 15, 7}, {304, 152, 74, 36, 14}};
 
 kvd_status plan_blocks(int batch, int T, int Hq, int Hkv, int D, int K, int block_tokens, int num_sms, BlocksParams* p, size_t* ws) {
     kvd_status st = check_shape(batch, Hq, Hkv, D, KVD_OUT_BF16);
     if (st != KVD_OK) return st;
     if (T < 1 || K < 1 || num_sms < 0 || !power_of_two(block_tokens, 16, 4096)) return KVD_ERR_INVALID_ARG;
     if (T > KVD_MAX_TOKENS || K > kMaxKept || (long long)K * block_tokens > 0x3fffffffLL) return KVD_ERR_UNSUPPORTED;
-    int sms = num_sms;
-    if (sms == 0 && (st = device_sms(&sms)) != KVD_OK) return st;
+    int at_once[5];
+    for (int i = 0; i < 5; ++i) at_once[i] = (int)((long long)kAtOnce[D != 256][i] * num_sms / 152);
+    at_once[0] = std::max(at_once[0], 1);
+    if (num_sms == 0) {
+        const cudaError_t e = D == 64    ? blocks_at_once_d64(at_once)
+                              : D == 128 ? blocks_at_once_d128(at_once)
+                                         : blocks_at_once_d256(at_once);
+        if (e != cudaSuccess) return KVD_ERR_CUDA;
+    }
     p->B = batch;
     p->T = T;
     p->Hq = Hq;
@@ -117,7 +159,7 @@ kvd_status plan_blocks(int batch, int T, int Hq, int Hkv, int D, int K, int bloc
     *ws = 0;
     p->parts = p->shards = 1;
     if (pairs == 0) return KVD_OK;
-    split_blocks(pairs, std::max(1LL, (long long)K * block_tokens / kBlocksStage), D == 256 ? 1 : 2, sms, &p->parts, &p->shards);
+    split_blocks(pairs, std::max(1LL, (long long)K * block_tokens / kBlocksStage), at_once, &p->parts, &p->shards);
     if (p->shards > 1) {
         const size_t rows = (size_t)pairs * p->G;
         *ws = align256(p->shards * rows * D * sizeof(float)) + align256(p->shards * rows * sizeof(float));

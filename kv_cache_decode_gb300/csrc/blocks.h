@@ -32,6 +32,13 @@ struct BlocksParams {
 };
 // Lets a kernel use so much shared memory and clusters of 16, once a device (a bit of *ready each).
 cudaError_t allow_clusters(const void* kernel, int smem_bytes, std::atomic<uint64_t>* ready);
+// Clusters of 1, 2, 4, 8 and 16 such CTAs that the current device runs at once (0: it cannot place one of that size), asked once
+// a device (known: kMaxDevices of them).
+cudaError_t clusters_at_once(const void* kernel, int threads, int smem_bytes, std::atomic<uint64_t>* ready, std::atomic<uint64_t>* known,
+                             int (&n)[5]);
+cudaError_t blocks_at_once_d64(int (&n)[5]);
+cudaError_t blocks_at_once_d128(int (&n)[5]);
+cudaError_t blocks_at_once_d256(int (&n)[5]);
 cudaError_t launch_decode_blocks_d64(const BlocksParams& p, bool f32_out, cudaStream_t stream);
 cudaError_t launch_decode_blocks_d128(const BlocksParams& p, bool f32_out, cudaStream_t stream);
 cudaError_t launch_decode_blocks_d256(const BlocksParams& p, bool f32_out, cudaStream_t stream);

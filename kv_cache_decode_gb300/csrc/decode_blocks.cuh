@@ -30,6 +30,7 @@
 #include <atomic>
 
 #include "../../include/kvdecode.h"
+#include "api_common.h"
 #include "blocks.h"
 #include "cluster.cuh"
 #include "common.cuh"
@@ -530,6 +531,15 @@ __global__ void __launch_bounds__((BlocksShape<D, NT>::WARPS + 1) * 32, BlocksSh
     cluster_sync();  // no CTA leaves while another reads its states
 }
 
+// Of the CTAs at D columns, whichever instance: their shared memory decides.
+template <int D>
+cudaError_t blocks_at_once(int (&n)[5]) {
+    constexpr int NT = D < 256 ? 2 : 1;
+    static std::atomic<uint64_t> ready{0}, known[kMaxDevices];
+    return clusters_at_once(reinterpret_cast<const void*>(decode_blocks_kernel<D, NT, true>), (BlocksShape<D, NT>::WARPS + 1) * 32,
+                            BlocksShape<D, NT>::SMEM, &ready, known, n);
+}
+
 template <int D, int NT, bool F32OUT>
 cudaError_t launch_decode_blocks(const BlocksParams& p, cudaStream_t stream) {
     using Sh = BlocksShape<D, NT>;
@@ -561,6 +571,7 @@ cudaError_t launch_decode_blocks(const BlocksParams& p, cudaStream_t stream) {
 }
 
 #define KVD_BLOCKS_LAUNCH(DD)                                                                             \
+    cudaError_t blocks_at_once_d##DD(int (&n)[5]) { return blocks_at_once<DD>(n); }                       \
     cudaError_t launch_decode_blocks_d##DD(const BlocksParams& p, bool f32_out, cudaStream_t stream) {    \
         if (p.head_rows == 8) return f32_out ? launch_decode_blocks<DD, 1, true>(p, stream) : launch_decode_blocks<DD, 1, false>(p, stream); \
         if constexpr (DD < 256) return f32_out ? launch_decode_blocks<DD, 2, true>(p, stream) : launch_decode_blocks<DD, 2, false>(p, stream); \

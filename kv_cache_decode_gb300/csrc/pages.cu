@@ -249,14 +249,18 @@ __global__ void __launch_bounds__(kPagesThreads, 1) pages_kernel(const PagesPara
 }
 
 cudaError_t launch_pages(const PagesParams& p, cudaStream_t stream) {
-    static std::atomic<uint64_t> ready{0};
+    static std::atomic<uint64_t> ready{0}, known[kMaxDevices];
     const int smem = 4 * (p.B + 1) * (int)sizeof(int);
-    const cudaError_t e = allow_clusters(reinterpret_cast<const void*>(pages_kernel), 4 * (kPagesMaxBatch + 1) * (int)sizeof(int), &ready);
+    int at_once[5];
+    cudaError_t e = allow_clusters(reinterpret_cast<const void*>(pages_kernel), 4 * (kPagesMaxBatch + 1) * (int)sizeof(int), &ready);
+    if (e == cudaSuccess)
+        e = clusters_at_once(reinterpret_cast<const void*>(pages_kernel), kPagesThreads, 4 * (kPagesMaxBatch + 1) * (int)sizeof(int), &ready,
+                             known, at_once);
     if (e != cudaSuccess) return e;
     // A CTA for 8,192 rows, two steps of its threads, and for 16,384 table entries (few of which change in a call).
     const long long rows = p.slots || p.positions ? p.rows : 0, entries = (long long)p.B * p.max_blocks;
     int parts = 1;
-    while (parts < 16 && (parts * 8192LL < rows || parts * 16384LL < entries)) parts *= 2;
+    for (int i = 1; i < 5 && at_once[i] > 0 && (parts * 8192LL < rows || parts * 16384LL < entries); ++i) parts *= 2;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)parts, 1, 1);
     cfg.blockDim = dim3(kPagesThreads, 1, 1);

@@ -68,6 +68,37 @@ def test_attention_of_several_clusters_flags_nothing(Hq, Hkv, D, block, K, lens)
         _close(got[:2], _want(c, q, x, block), dtype)
 
 
+@pytest.mark.parametrize("D", [64, 256])
+@pytest.mark.parametrize("B", [7, 8, 14, 15, 16, 36, 37, 74, 75, 76, 77])
+def test_attention_where_waves_end(B, D):
+    """Numbers of pairs at which clusters of one size fill the machine, and one more."""
+    dev = cuda_or_skip()
+    r = np.random.default_rng(B + D)
+    c = Cache(r, r.integers(0, 700, B), 1, D, 32, dev)
+    q = _normal(r, (B, 1, 8, D))
+    x = r.integers(0, -(-c.S // 32), (B, 1, 1, 40)).astype(np.int32)
+    got = _run(c, q, x, 32, dev, "f32")
+    assert got[2] == 0
+    _close(got[:2], _want(c, q, x, 32), "f32")
+
+
+def test_plans_for_this_device():
+    """A plan for 152 multiprocessors is what a device of 152 says of itself."""
+    import torch
+    import kv_cache_decode_gb300 as kvd
+    cuda_or_skip()
+    if torch.cuda.get_device_properties(0).multi_processor_count != 152:
+        pytest.skip("another number of multiprocessors")
+    some = 0
+    for D in (64, 128, 256):
+        for B in (1, 2, 3, 5, 7, 8, 14, 15, 16):
+            for K in (1, 16, 128, 1024):
+                n = kvd.decode_blocks_plan(B, 1, 8, 1, D, K, 64, num_sms=152)
+                assert kvd.decode_blocks_plan(B, 1, 8, 1, D, K, 64) == n
+                some += n > 0
+    assert some > 10
+
+
 @pytest.mark.parametrize("S,block", [(20, 32), (1, 16), (40, 4096)])
 def test_caches_shorter_than_a_block(S, block):
     """No bounds, one block that every token sees: bounds, selection and attention as over any cache."""
