@@ -612,35 +612,40 @@ kvd_status kvd_decode_fp4(const kvd_cache_fp4* cache, const void* q, const int32
                           int32_t* status_word, kvd_stream_t stream);
 
 /*
- * Page tables from request lengths. Every paged call takes a block table; this one keeps it on the device: sequence
- * b of a batch goes from seq_lens[b] tokens to new_lens[b] (longer, shorter, or 0), its pages coming from
- * a stack of free ones and going back there.
- *   block_table : device int32 [batch, max_blocks], as for the paged calls; entries of blocks that hold tokens name pages
- *                 (each held once: pages that sequences share are not counted)
- *   free_pages  : device int32 [num_pages], the stack: places [0, *free_count) are free pages, those above hold anything
+ * Page tables from request lengths. Every paged call takes a block table; this one keeps it on the
+ * device: sequence b of a batch goes from seq_lens[b] tokens to new_lens[b] (longer, shorter, or
+ * 0), its pages coming from a stack of free ones and going back there.
+ *   block_table : device int32 [batch, max_blocks], as for the paged calls; entries of blocks that
+ *                 hold tokens name pages (each held once: pages that sequences share are not
+ *                 counted)
+ *   free_pages  : device int32 [num_pages], the stack: places [0, *free_count) are free pages,
+ *                 those above hold anything
  *   free_count  : device int32 [1]
  *   seq_lens    : device int32 [batch], in: the lengths before, out: those after
- *   new_lens    : device int32 [batch]; one outside [0, max_blocks * page_size] leaves its sequence as it is
- *                 (KVD_STATUS_POS_OUT_OF_RANGE)
- * In this order: the pages of blocks past ceil(new / page_size) go back and their entries become -1, the r-th of R of them, counted by sequence
- * and block, to place F + R - 1 - r of the stack (F the count before); then the i-th page that is needed, counted
- * likewise, comes from place F + R - 1 - i. A sequence that needs pages grows when all
- * that is needed up to it, of it and the sequences before it, is there; otherwise it keeps its length and gets no page (KVD_STATUS_NO_PAGES), and so
- * do later ones that need pages. One that needs none always grows. A shrink right behind a growth leaves table and
- * stack as they were before both.
+ *   new_lens    : device int32 [batch]; one outside [0, max_blocks * page_size] leaves its sequence
+ *                 as it is (KVD_STATUS_POS_OUT_OF_RANGE)
+ * In this order: the pages of blocks past ceil(new / page_size) go back and their entries become
+ * -1, the r-th of R of them, counted by sequence and block, to place F + R - 1 - r of the stack (F
+ * the count before); then the i-th page that is needed, counted likewise, comes from place F + R -
+ * 1 - i. A sequence that needs pages grows when all that is needed up to it, of it and the
+ * sequences before it, is there; otherwise it keeps its length and gets no page
+ * (KVD_STATUS_NO_PAGES), and so do later ones that need pages. One that needs none always grows. A
+ * shrink right behind a growth leaves table and stack as they were before both.
  * What it writes besides, each optional (NULL); none may overlap another array of the call:
  *   pos         : device int32 [batch], the lengths before: kvd_kv_append_rope's pos
  *   row_offsets : device int32 [batch + 1], running sums of the tokens that each sequence grew by
- *   slots       : device int32 [n_rows]: for the new tokens packed end to end, the cache row of each: page * page_size + place in it
- *                 (a sequence that does not grow has none: row i of a step of one token each is not sequence i's then; sequence
- *                 b's are those from row_offsets[b] to row_offsets[b + 1])
+ *   slots       : device int32 [n_rows]: for the new tokens packed end to end, the cache row of
+ *                 each: page * page_size + place in it (a sequence that does not grow has none: row
+ *                 i of a step of one token each is not sequence i's then; sequence b's are those
+ *                 from row_offsets[b] to row_offsets[b + 1])
  *   positions   : device int32 [n_rows]: their positions in their sequences
- * Rows of slots and positions behind the last token are -1; tokens past n_rows get none (KVD_STATUS_POS_OUT_OF_RANGE). A table
- * entry or place of the stack that names no page is handed on as it is, its slots are -1 (KVD_STATUS_BAD_PAGE). Lengths before that hold more
- * pages than the pool leaves room for on the stack: it is full then, what is left over is dropped (KVD_STATUS_BAD_PAGE). seq_lens outside [0, capacity] are clamped
- * (KVD_STATUS_SEQ_LEN_CLAMPED).
- * Errors: KVD_ERR_INVALID_ARG for null or misaligned pointers, bad sizes (page_size, max_blocks, num_pages as the paged calls;
- * batch * max_blocks and n_rows at most 2^31 - 1) or overlaps; KVD_ERR_UNSUPPORTED for batch > 8192; KVD_ERR_CUDA.
+ * Rows of slots and positions behind the last token are -1; tokens past n_rows get none
+ * (KVD_STATUS_POS_OUT_OF_RANGE). A table entry or place of the stack that names no page is handed
+ * on as it is, its slots are -1 (KVD_STATUS_BAD_PAGE). Where the lengths before claim more pages than
+ * the pool has, those that come back and find the stack full are dropped (KVD_STATUS_BAD_PAGE). seq_lens outside [0, capacity] are clamped (KVD_STATUS_SEQ_LEN_CLAMPED).
+ * Errors: KVD_ERR_INVALID_ARG for null or misaligned pointers, bad sizes (page_size, max_blocks,
+ * num_pages as the paged calls; batch * max_blocks and n_rows at most 2^31 - 1) or overlaps;
+ * KVD_ERR_UNSUPPORTED for batch > 8192; KVD_ERR_CUDA.
  */
 kvd_status kvd_pages_update(int32_t* block_table, int32_t* free_pages, int32_t* free_count, int32_t* seq_lens,
                             const int32_t* new_lens, int batch, int max_blocks, int page_size, int num_pages, int32_t* pos,
@@ -648,17 +653,20 @@ kvd_status kvd_pages_update(int32_t* block_table, int32_t* free_pages, int32_t* 
                             kvd_stream_t stream);
 
 /*
- * Rotary positions of several axes, as for the tokens of images and video (time, height, width): pair i of a
- * head's first rotary_dim columns turns by positions[axes[i]] * w_i, otherwise as kvd_rope.
+ * Rotary positions of several axes, as for the tokens of images and video (time, height, width):
+ * pair i of a head's first rotary_dim columns turns by positions[axes[i]] * w_i, otherwise as
+ * kvd_rope.
  *   turns   : device uint64 [rotary_dim / 2], as kvd_rope's
  *   axes    : device uint8 [rotary_dim / 2], 8-byte aligned, each below n_axes
  *   n_axes  : 1 .. KVD_MAX_AXES
- * kvd_rope_axes_table fills HOST arrays of rotary_dim / 2 entries (rotary_dim = twice the sum of sections, a multiple of
- * 16 up to 256) and the factor: axis a takes sections[a] >= 1 pairs, which are neighbours (dealt 0: the first
- * sections[0] pairs turn by axis 0, the next by axis 1, ...) or dealt out in turn (dealt 1: 0, 1, 2, 0, 1, 2, ..., passing over
- * axes that have theirs). A pair's frequency goes by its index among all pairs (per_axis 0), or by its index among
- * its axis' pairs, as in a table of 2 * sections[a] columns (per_axis 1: sections[a] >= 8, of any size). Base and scaling as
- * kvd_rope_table. (All pairs together are a multiple of 8: of a head of 72 columns 64 can be turned, not 72.)
+ * kvd_rope_axes_table fills HOST arrays of rotary_dim / 2 entries (rotary_dim = twice the sum of
+ * sections, a multiple of 16 up to 256) and the factor: axis a takes sections[a] >= 1 pairs, which
+ * are neighbours (dealt 0: the first sections[0] pairs turn by axis 0, the next by axis 1, ...) or
+ * dealt out in turn (dealt 1: 0, 1, 2, 0, 1, 2, ..., passing over axes that have theirs). A pair's
+ * frequency goes by its index among all pairs (per_axis 0), or by its index among its axis' pairs,
+ * as in a table of 2 * sections[a] columns (per_axis 1: sections[a] >= 8, of any size). Base and
+ * scaling as kvd_rope_table. (All pairs together are a multiple of 8: of a head of 72 columns 64
+ * can be turned, not 72.)
  */
 #define KVD_MAX_AXES 4
 typedef struct kvd_rope_axes {
@@ -676,15 +684,19 @@ kvd_status kvd_rope_axes_table(const int* sections, int n_axes, int dealt, int p
 
 /*
  * kvd_rope_apply_axes: kvd_rope_apply by positions of several axes.
- *   positions : device int32, axis a of row n at a * axis_stride + n (axis_stride >= rows where n_axes > 1), any values
- * kvd_kv_append_axes: kvd_kv_append_rope for tokens whose rotary positions do not say where they go: row n's key (turned)
- * and value are stored in the cache row slots[n] of a cache of kvd_decode_ex's description: page * page_size + place in
- * the page for pools (page_size and num_pages set; no table is read), b * s_max + t for a contiguous cache of `batch` sequences (page_size and num_pages 0).
- *   slots     : device int32 [n_rows] (kvd_pages_update makes them). A negative one stores nothing; one past the cache
- *               stores nothing and sets KVD_STATUS_POS_OUT_OF_RANGE. The row's query is turned all the same. What a slot named twice
- *               holds afterwards is not defined.
- * Other arguments, results and errors as kvd_rope_apply and kvd_kv_append_rope; an fp4 cache takes rows turned by
- * kvd_rope_apply_axes through kvd_kv_append_fp4.
+ *   positions : device int32, axis a of row n at a * axis_stride + n (axis_stride >= rows where
+ *               n_axes > 1), any values
+ * kvd_kv_append_axes: kvd_kv_append_rope for tokens whose rotary positions do not say where they
+ * go: row n's key (turned) and value are stored in the cache row slots[n] of a cache of
+ * kvd_decode_ex's description: page * page_size + place in the page for pools (page_size and
+ * num_pages set; no table is read), b * s_max + t for a contiguous cache of `batch` sequences
+ * (page_size and num_pages 0).
+ *   slots     : device int32 [n_rows] (kvd_pages_update makes them). A negative one stores nothing;
+ *               one past the cache stores nothing and sets KVD_STATUS_POS_OUT_OF_RANGE. The row's
+ *               query is turned all the same. What a slot named twice holds afterwards is not
+ *               defined.
+ * Other arguments, results and errors as kvd_rope_apply and kvd_kv_append_rope; an fp4 cache takes
+ * rows turned by kvd_rope_apply_axes through kvd_kv_append_fp4.
  */
 kvd_status kvd_rope_apply_axes(const kvd_rope_axes* rope, const void* x, long long x_stride, kvd_out_dtype in_dtype, void* y,
                                long long y_stride, kvd_out_dtype out_dtype, const int32_t* positions, long long axis_stride,
@@ -695,22 +707,27 @@ kvd_status kvd_kv_append_axes(const kvd_cache* cache, const kvd_rope_axes* rope,
                               int n_heads_q, int n_heads_kv, int head_dim, int32_t* status_word, kvd_stream_t stream);
 
 /*
- * Attention over selected blocks: for long contexts, a query attends to the blocks of tokens that a cheap score ranks
- * first, and reads those alone. Three calls: kvd_kv_block_bounds after an append, kvd_block_select and kvd_decode_blocks for a
- * step's queries. A block is block_tokens tokens (a power of two in [16, 4096]) of a sequence: block j is tokens
- * [j * block_tokens, (j + 1) * block_tokens).
+ * Attention over selected blocks: for long contexts, a query attends to the blocks of tokens that a
+ * cheap score ranks first, and reads those alone. Three calls: kvd_kv_block_bounds after an append,
+ * kvd_block_select and kvd_decode_blocks for a step's queries. A block is block_tokens tokens (a
+ * power of two in [16, 4096]) of a sequence: block j is tokens [j * block_tokens, (j + 1) *
+ * block_tokens).
  *
- * Bounds: of every full block and KV head, in 8 bits, what its keys reach at most and at least in each column:
+ * Bounds: of every full block and KV head, in 8 bits, what its keys reach at most and at least in
+ * each column:
  *   a = max |k| over the block, scale = a / 127, hi_d = ceil(max_t k_td / scale), lo_d = floor(min_t k_td / scale),
  *   clamped to [-127, 127], divisions IEEE float32 (a = 0: scale 0 and codes 0). A block with a key that is not finite has
- *   scale NaN and codes 0.
- *   codes  : int8 [batch, s_max / block_tokens, n_heads_kv, 2, head_dim] (hi, then lo), 16-byte aligned; for pools
- *            [num_pages, page_size / block_tokens, n_heads_kv, 2, head_dim], block_tokens at most page_size
+ * scale NaN and codes 0.
+ *   codes  : int8 [batch, s_max / block_tokens, n_heads_kv, 2, head_dim] (hi, then lo), 16-byte
+ *            aligned; for pools [num_pages, page_size / block_tokens, n_heads_kv, 2, head_dim],
+ *            block_tokens at most page_size
  *   scales : float32 [batch, s_max / block_tokens, n_heads_kv] (pools likewise)
  * A contiguous cache shorter than a block has no bounds: codes and scales may be NULL then.
- * kvd_kv_block_bounds writes the bounds of the blocks of a bf16 cache (K; contiguous [batch, s_max, ...] or pool) that are full at seq_lens[b]
- * and were not at from_lens[b] (NULL: 0), other entries left as they are; max_new is the largest seq_lens[b] - from_lens[b] the call may see (blocks past
- * it are left, KVD_STATUS_SEQ_LEN_CLAMPED). A table entry that names no page: nothing is written, KVD_STATUS_BAD_PAGE.
+ * kvd_kv_block_bounds writes the bounds of the blocks of a bf16 cache (K; contiguous [batch, s_max,
+ * ...] or pool) that are full at seq_lens[b] and were not at from_lens[b] (NULL: 0), other entries
+ * left as they are; max_new is the largest seq_lens[b] - from_lens[b] the call may see (blocks past
+ * it are left, KVD_STATUS_SEQ_LEN_CLAMPED). A table entry that names no page: nothing is written,
+ * KVD_STATUS_BAD_PAGE.
  */
 typedef struct kvd_block_bounds {
     int8_t* codes;
@@ -726,18 +743,21 @@ kvd_status kvd_kv_block_bounds(const void* k_cache, const kvd_block_bounds* boun
 
 /*
  * kvd_block_select: the n_keep blocks of the highest scores, for every query token and KV head.
- *   q          : bf16 [batch, n_tokens, n_heads_q, head_dim], 16-byte aligned; token i sees the first
- *                seq_lens[b] - n_tokens + 1 + i tokens (seq_lens clamped to max_seq_len)
- *   blocks_out : device int32 [batch, n_tokens, n_heads_kv, n_keep], ascending, -1 behind the last where the token sees
- *                fewer blocks (it then keeps them all)
- * Score of block j for KV head g: with c = round-half-even(q / s), s = max |q| / 127 (IEEE float32) for each of the group's
- * query rows, I = sum_d (c_d > 0 ? c_d hi_d : c_d lo_d) in whole numbers, the largest of fl(I * s) over the rows times the block's
- * scale, rounded to float32; a NaN counts as +infinity. A row that is not finite takes no part. The first n_first (>= 0) and the last n_last (>= 1, the block being filled among
- * them) blocks that the token sees are always kept (n_first + n_last <= n_keep); ties go to the lower index. So the result is
- * defined bit for bit. A block whose table entry names no page ranks last (KVD_STATUS_BAD_PAGE).
- *   workspace  : kvd_block_select_plan's bytes, 256-byte aligned; needs no initialisation and is not preserved
- * Errors: as the decode calls; KVD_ERR_INVALID_ARG also for max_seq_len past the bounds' blocks, n_keep < 1 or overlaps;
- * KVD_ERR_UNSUPPORTED for n_keep > 2^20.
+ *   q          : bf16 [batch, n_tokens, n_heads_q, head_dim], 16-byte aligned; token i sees the
+ *                first seq_lens[b] - n_tokens + 1 + i tokens (seq_lens clamped to max_seq_len)
+ *   blocks_out : device int32 [batch, n_tokens, n_heads_kv, n_keep], ascending, -1 behind the last
+ *                where the token sees fewer blocks (it then keeps them all)
+ * Score of block j for KV head g: with c = round-half-even(q / s), s = max |q| / 127 (IEEE float32)
+ * for each of the group's query rows, I = sum_d (c_d > 0 ? c_d hi_d : c_d lo_d) in whole numbers,
+ * the largest of fl(I * s) over the rows times the block's scale, rounded to float32; a NaN counts
+ * as +infinity. A row that is not finite takes no part. The first n_first (>= 0) and the last
+ * n_last (>= 1, the block being filled among them) blocks that the token sees are always kept
+ * (n_first + n_last <= n_keep); ties go to the lower index. So the result is defined bit for bit. A
+ * block whose table entry names no page ranks last (KVD_STATUS_BAD_PAGE).
+ *   workspace  : kvd_block_select_plan's bytes, 256-byte aligned; needs no initialisation and is
+ *                not preserved
+ * Errors: as the decode calls; KVD_ERR_INVALID_ARG also for max_seq_len past the bounds' blocks,
+ * n_keep < 1 or overlaps; KVD_ERR_UNSUPPORTED for n_keep > 2^20.
  */
 kvd_status kvd_block_select_plan(int batch, int n_tokens, int n_heads_kv, int max_seq_len, int block_tokens,
                                  size_t* workspace_bytes_out);
@@ -746,16 +766,19 @@ kvd_status kvd_block_select(const kvd_block_bounds* bounds, const void* q, const
                             void* workspace, size_t workspace_bytes, int32_t* blocks_out, int32_t* status_word, kvd_stream_t stream);
 
 /*
- * kvd_decode_blocks: kvd_decode_attention_multi over the listed blocks only, of a bf16 cache (contiguous, or paged with any page size;
- * 8-bit caches: KVD_ERR_UNSUPPORTED).
- *   blocks : device int32 [batch, n_tokens, n_heads_kv, n_blocks], kvd_block_select's or a caller's own: in any order;
- *            entries that are negative or past the last block the token sees are passed over, of its last block the tokens it sees
- *            count, and a block named twice counts twice
- * A token whose list names no block it sees gets a zero row and lse -inf. Rows past a sequence's length may hold anything.
+ * kvd_decode_blocks: kvd_decode_attention_multi over the listed blocks only, of a bf16 cache
+ * (contiguous, or paged with any page size; 8-bit caches: KVD_ERR_UNSUPPORTED).
+ *   blocks : device int32 [batch, n_tokens, n_heads_kv, n_blocks], kvd_block_select's or a caller's
+ *            own: in any order; entries that are negative or past the last block the token sees are
+ *            passed over, of its last block the tokens it sees count, and a block named twice
+ *            counts twice
+ * A token whose list names no block it sees gets a zero row and lse -inf. Rows past a sequence's
+ * length may hold anything.
  *   workspace : kvd_decode_blocks_plan's bytes (often 0: then NULL is taken), 256-byte aligned
- * Results: softmax weights are bf16 where the output is (off by 2^-8 of themselves at most, as kvd_decode_attention's), by 2^-16 for float32 output;
- * lse is of the weights before that rounding. Other arguments, status and errors as kvd_decode_ex without an append;
- * KVD_ERR_UNSUPPORTED for caches of 2^31 - 16 token rows and more.
+ * Results: softmax weights are bf16 where the output is (off by 2^-8 of themselves at most, as
+ * kvd_decode_attention's), by 2^-16 for float32 output; lse is of the weights before that rounding.
+ * Other arguments, status and errors as kvd_decode_ex without an append; KVD_ERR_UNSUPPORTED for
+ * caches of 2^31 - 16 token rows and more.
  */
 kvd_status kvd_decode_blocks_plan(int batch, int n_tokens, int n_heads_q, int n_heads_kv, int head_dim, int n_blocks,
                                   int block_tokens, int num_sms, size_t* workspace_bytes_out);

@@ -108,11 +108,12 @@ kvd_status check_place(const int32_t* block_table, int s_max, int max_blocks, in
     return KVD_OK;
 }
 
-// CTAs of a pair (a cluster of n) and clusters of a pair. Clusters run in waves, as many at once as the multiprocessors'
-// groups hold (at_once, by log2 n; 0: none of that size). A CTA costs about what 18 stages cost one CTA (start, list, join), so that n is
-// the one with the least waves * (18 + stages / n). 16 pairs of 4,096 tokens, 8 heads: clusters of 4 / 8 / 16 take 17.6 / 11.8 /
-// 17.7 us (two waves of 16); 360 pairs of 2,048: one CTA 64, two 58, four 67. Pairs of which clusters of 16 leave places free get
-// several clusters of 128 stages and more, joined by a second launch (4 us; one pair of 16,384 tokens: 17.4 -> 12).
+// CTAs of a pair (a cluster of n) and clusters of a pair. Clusters run in waves, as many at once as the
+// multiprocessors' groups hold (at_once, by log2 n; 0: none of that size). A CTA costs about what 18 stages
+// cost one CTA (start, list, join), so that n is the one with the least waves * (18 + stages / n). 16 pairs of
+// 4,096 tokens, 8 heads: clusters of 4 / 8 / 16 take 17.6 / 11.8 / 17.7 us (two waves of 16); 360 pairs of
+// 2,048: one CTA 64, two 58, four 67. Pairs of which clusters of 16 leave places free get several clusters of
+// 128 stages and more, joined by a second launch (4 us; one pair of 16,384 tokens: 17.4 -> 12).
 void split_blocks(long long pairs, long long stages, const int (&at_once)[5], int* parts, int* shards) {
     long long best = 0, room = 0;
     *parts = *shards = 1;
@@ -124,7 +125,8 @@ void split_blocks(long long pairs, long long stages, const int (&at_once)[5], in
     if (*parts == 16) *shards = (int)std::max(1LL, std::min(room, stages / 128));
 }
 
-// Of 152 multiprocessors with room for one CTA or two, as the device has it: for plans made for a number of multiprocessors.
+// Of 152 multiprocessors with room for one CTA or two, as the device has it: for plans made for a number of
+// multiprocessors.
 constexpr int kAtOnce[2][5] = {{152, 76, 36, 15, 7}, {304, 152, 74, 36, 14}};
 
 kvd_status plan_blocks(int batch, int T, int Hq, int Hkv, int D, int K, int block_tokens, int num_sms, BlocksParams* p, size_t* ws) {
@@ -149,8 +151,8 @@ kvd_status plan_blocks(int batch, int T, int Hq, int Hkv, int D, int K, int bloc
     p->K = K;
     p->block_log2 = log2_of(block_tokens);
     const long long pairs = (long long)batch * T * Hkv;
-    // Query rows to warps: 16 each (two column tiles), at head_dim 256, whose accumulators take the registers of one, 8. As many teams as
-    // the warps give, with three stages each at least.
+    // Query rows to warps: 16 each (two column tiles), at head_dim 256, whose accumulators take the registers
+    // of one, 8. As many teams as the warps give, with three stages each at least.
     p->head_rows = p->G <= 8 || D == 256 ? 8 : 16;
     p->head_warps = (p->G + p->head_rows - 1) / p->head_rows;
     p->teams = std::max(1, std::min(blocks_warps(D) / p->head_warps, blocks_slots(D) / 3));
@@ -266,7 +268,8 @@ kvd_status kvd_rope_apply_axes(const kvd_rope_axes* rope, const void* x, long lo
     if ((st = check_strided(y, y_stride, width, oes)) != KVD_OK) return st;
     const Rows rx{x, x_stride, width, rows, ies}, ry{y, y_stride, width, rows, oes};
     const bool in_place = x == y && x_stride == y_stride && in_dtype == out_dtype;
-    if ((!in_place && rows_meet(rx, ry)) || ry.range().overlaps(ByteRange{positions, positions_bytes(r, rows)})) return KVD_ERR_INVALID_ARG;
+    if ((!in_place && rows_meet(rx, ry)) || ry.range().overlaps(ByteRange{positions, positions_bytes(r, rows)}))
+        return KVD_ERR_INVALID_ARG;
     if (rows == 0) return KVD_OK;
     int sms = 0;
     if ((st = device_sms(&sms)) != KVD_OK) return st;
@@ -317,20 +320,23 @@ kvd_status kvd_kv_append_axes(const kvd_cache* cache, const kvd_rope_axes* rope,
     const ByteRange none{nullptr, 0}, rp{positions, positions_bytes(r, n_rows)}, rs{slots, (size_t)n_rows * 4};
     const bool in_place = q && q == q_out;
     if (in_place && q_stride != q_out_stride) return KVD_ERR_INVALID_ARG;
-    if (q && ((!in_place && rows_meet(ro, rq)) || rows_meet(ro, rk) || rows_meet(ro, rv) || ro.range().overlaps(rp) || ro.range().overlaps(rs)))
+    if (q && ((!in_place && rows_meet(ro, rq)) || rows_meet(ro, rk) || rows_meet(ro, rv) || ro.range().overlaps(rp) ||
+              ro.range().overlaps(rs)))
         return KVD_ERR_INVALID_ARG;
     const size_t cbytes = (size_t)rows * kw * (quant ? 1 : 2), sbytes = quant ? (size_t)rows * n_heads_kv * 4 : 0;
-    const ByteRange ranges[10] = {{cache->k, cbytes}, {cache->v, cbytes}, {cache->k_scales, sbytes}, {cache->v_scales, sbytes}, rk.range(),
-                                  rv.range(), q ? rq.range() : none, q ? ro.range() : none, rp, rs};
+    const ByteRange ranges[10] = {{cache->k, cbytes}, {cache->v, cbytes}, {cache->k_scales, sbytes}, {cache->v_scales, sbytes},
+                                  rk.range(), rv.range(), q ? rq.range() : none, q ? ro.range() : none, rp, rs};
     if (!apart(ranges, 4, 10)) return KVD_ERR_INVALID_ARG;
     int sms = 0;
     if ((st = device_sms(&sms)) != KVD_OK) return st;
     const AppendTarget to{cache->k, cache->v, cache->k_scales, cache->v_scales,
-                          quant ? (cache->fp8 ? CacheForm::kFp8 : CacheForm::kInt8) : CacheForm::kBf16, 0, PagedCache{nullptr, 0, 0, 0}};
+                          quant ? (cache->fp8 ? CacheForm::kFp8 : CacheForm::kInt8) : CacheForm::kBf16, 0,
+                          PagedCache{nullptr, 0, 0, 0}};
     const NewRows in{q, q_out, k_new, v_new, q_stride, q_out_stride, k_stride, v_stride, nullptr, nullptr, 0, 0, q ? n_heads_q : 0,
                      n_heads_kv, head_dim, n_rows};
-    return launch_append_axes(to, r, in, slots, rows, status_word, sms, static_cast<cudaStream_t>(stream)) == cudaSuccess ? KVD_OK
-                                                                                                                        : KVD_ERR_CUDA;
+    return launch_append_axes(to, r, in, slots, rows, status_word, sms, static_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? KVD_OK
+               : KVD_ERR_CUDA;
 }
 
 kvd_status kvd_kv_block_bounds(const void* k_cache, const kvd_block_bounds* bounds, const int32_t* from_lens, const int32_t* seq_lens,
@@ -340,10 +346,11 @@ kvd_status kvd_kv_block_bounds(const void* k_cache, const kvd_block_bounds* boun
     size_t blocks = 0;
     const kvd_status st = check_bounds(bounds, batch, n_heads_kv, head_dim, &pg, &cap, &blocks);
     if (st != KVD_OK) return st;
-    if (max_new < 0 || !k_cache || !seq_lens || !aligned(k_cache, 16) || !aligned(seq_lens, 4) || (from_lens && !aligned(from_lens, 4)) ||
-        (status_word && !aligned(status_word, 4)))
+    if (max_new < 0 || !k_cache || !seq_lens || !aligned(k_cache, 16) || !aligned(seq_lens, 4) ||
+        (from_lens && !aligned(from_lens, 4)) || (status_word && !aligned(status_word, 4)))
         return KVD_ERR_INVALID_ARG;
-    const long long rows = bounds->block_table ? (long long)bounds->num_pages * bounds->page_size : (long long)batch * bounds->s_max;
+    const long long rows =
+        bounds->block_table ? (long long)bounds->num_pages * bounds->page_size : (long long)batch * bounds->s_max;
     const size_t heads = blocks * n_heads_kv;
     const ByteRange r[5] = {{bounds->codes, heads * 2 * head_dim}, {bounds->scales, heads * 4},
                             {k_cache, (size_t)rows * n_heads_kv * head_dim * 2}, {seq_lens, (size_t)batch * 4},
@@ -360,7 +367,8 @@ kvd_status kvd_kv_block_bounds(const void* k_cache, const kvd_block_bounds* boun
 
 kvd_status kvd_block_select_plan(int batch, int n_tokens, int n_heads_kv, int max_seq_len, int block_tokens,
                                  size_t* workspace_bytes_out) {
-    if (!workspace_bytes_out || batch < 0 || n_tokens < 1 || n_heads_kv <= 0 || max_seq_len < 0 || !power_of_two(block_tokens, 16, 4096))
+    if (!workspace_bytes_out || batch < 0 || n_tokens < 1 || n_heads_kv <= 0 || max_seq_len < 0 ||
+        !power_of_two(block_tokens, 16, 4096))
         return KVD_ERR_INVALID_ARG;
     if (n_tokens > KVD_MAX_TOKENS) return KVD_ERR_UNSUPPORTED;
     *workspace_bytes_out = align256((size_t)batch * n_tokens * n_heads_kv * select_key_stride(max_seq_len, block_tokens) * 4);
@@ -423,11 +431,13 @@ kvd_status kvd_block_select(const kvd_block_bounds* bounds, const void* q, const
     p.n_last = n_last;
     p.key_stride = select_key_stride(max_seq_len, bounds->block_tokens);
     p.pg = pg;
-    // CTAs of a pair: for about three rounds of those that are resident, as far as every warp has a tile of 16 blocks (32 sequences of
-    // 16,384 to 131,072 tokens in blocks of 32, 8 KV heads: one round 47.0 us, two 42.3, three 41.0, six 42.7).
+    // CTAs of a pair: for about three rounds of those that are resident, as far as every warp has a tile of 16
+    // blocks (32 sequences of 16,384 to 131,072 tokens in blocks of 32, 8 KV heads: one round 47.0 us, two
+    // 42.3, three 41.0, six 42.7).
     const int tiles_cta = head_dim == 256 ? 16 : 8;
     const long long tiles = (p.key_stride + 15LL) / 16;
-    const int parts = (int)std::max(1LL, std::min((3LL * select_ctas(head_dim, p.G, n_tokens) * sms + pairs - 1) / pairs, (tiles + tiles_cta - 1) / tiles_cta));
+    const long long three = (3LL * select_ctas(head_dim, p.G, n_tokens) * sms + pairs - 1) / pairs;
+    const int parts = (int)std::max(1LL, std::min(three, (tiles + tiles_cta - 1) / tiles_cta));
     if (pairs * parts > 0x7fffffffLL) return KVD_ERR_UNSUPPORTED;
     p.parts = parts;
     return launch_block_select(p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? KVD_OK : KVD_ERR_CUDA;
@@ -452,12 +462,13 @@ kvd_status kvd_decode_blocks(const kvd_cache* cache, const void* q, const int32_
     std::memset(&p, 0, sizeof p);
     int cap = 0;
     long long rows = 0;
-    st = check_place(cache->block_table, cache->s_max, cache->max_blocks, cache->page_size, cache->num_pages, batch, &p.pg, &cap, &rows);
+    st = check_place(cache->block_table, cache->s_max, cache->max_blocks, cache->page_size, cache->num_pages, batch, &p.pg, &cap,
+                     &rows);
     if (st != KVD_OK) return st;
     if (rows > 0x7fffffffLL - 16) return KVD_ERR_UNSUPPORTED;  // TMA coordinates are 32-bit
     if (!std::isfinite(scale)) return KVD_ERR_INVALID_ARG;
-    if (!cache->k || !cache->v || !q || !blocks || !seq_lens || !out || !aligned(cache->k, 16) || !aligned(cache->v, 16) || !aligned(q, 16) ||
-        !aligned(blocks, 4) || !aligned(seq_lens, 4) || !aligned(out, 16) || (lse_out && !aligned(lse_out, 4)) ||
+    if (!cache->k || !cache->v || !q || !blocks || !seq_lens || !out || !aligned(cache->k, 16) || !aligned(cache->v, 16) ||
+        !aligned(q, 16) || !aligned(blocks, 4) || !aligned(seq_lens, 4) || !aligned(out, 16) || (lse_out && !aligned(lse_out, 4)) ||
         (status_word && !aligned(status_word, 4)))
         return KVD_ERR_INVALID_ARG;
     size_t need = 0;
@@ -492,7 +503,8 @@ kvd_status kvd_decode_blocks(const kvd_cache* cache, const void* q, const int32_
                           : head_dim == 128 ? launch_decode_blocks_d128(p, run_f32, s)
                                             : launch_decode_blocks_d256(p, run_f32, s);
     if (e != cudaSuccess) return KVD_ERR_CUDA;
-    if (p.shards > 1 && launch_merge_shards(p.out, p.lse, p.shards, (long long)out_rows, head_dim, true, out, f32, lse_out, s) != cudaSuccess)
+    if (p.shards > 1 &&
+        launch_merge_shards(p.out, p.lse, p.shards, (long long)out_rows, head_dim, true, out, f32, lse_out, s) != cudaSuccess)
         return KVD_ERR_CUDA;
     return KVD_OK;
 }

@@ -1,4 +1,5 @@
-// A unit of a new key or value row on its way into the cache, turned and, where the cache is quantized, encoded in registers.
+// A unit of a new key or value row on its way into the cache, turned and, where the cache is quantized, encoded
+// in registers.
 #pragma once
 
 #include "../../include/kvdecode.h"
@@ -7,9 +8,9 @@
 
 namespace kvd {
 
-// One unit (two vectors of 8 columns) of a key or value row, turned, into the cache: unit u of head h at cache row (fp4:
-// block of head 0) dst. R: the row's rotary columns (0 for values); turn: the rotation of its pairs. Whole warps call this,
-// a row's threads side by side; live: this thread has a unit.
+// One unit (two vectors of 8 columns) of a key or value row, turned, into the cache: unit u of head h at cache
+// row (fp4: block of head 0) dst. R: the row's rotary columns (0 for values); turn: the rotation of its pairs.
+// Whole warps call this, a row's threads side by side; live: this thread has a unit.
 template <CacheForm FORM, int DD, class F>
 __device__ __forceinline__ void put_unit(const AppendTarget& to, const NewRows& in, bool interleaved, const RopeRaw<false>& raw,
                                          const RopeUnit& ru, int R, bool value, int h, int u, int D, long long dst, int slot,

@@ -2,13 +2,14 @@
 // tokens, in 8 bits rounded outwards, with one float32 scale a (block, KV head):
 //   a = max |k|, scale = a / 127, hi_d = ceil(max_t k_td / scale), lo_d = floor(min_t k_td / scale), in [-127, 127],
 // the divisions IEEE float32. For any query, sum_d max(q_d hi_d, q_d lo_d) * scale is then at least q . k_t for
-// every token of the block (up to float32's rounding): what block_select.cu scores blocks by. A block with a key that is not
-// finite gets the scale NaN and codes 0.
+// every token of the block (up to float32's rounding): what block_select.cu scores blocks by. A block with a
+// key that is not finite gets the scale NaN and codes 0.
 //
-// A CTA of four warps takes one KV head of one block, or, of blocks of up to 4,096 values, a warp each: 2 * block * D bytes read
-// once, 2 D + 4 written; bound by memory for prompts (80.5 us for 537 MB in blocks of 64, the copy rate; in blocks of 16 87, at 64 columns
-// 115), by latency for the few blocks that a step fills (3.3 us). A thread holds 8 columns' running maxima and minima of its tokens as
-// bf16 pairs (exact), eight loads in flight; the divisions are shared out to the lanes that hold the same columns (all of them in each: 83, 106
+// A CTA of four warps takes one KV head of one block, or, of blocks of up to 4,096 values, a warp each: 2 *
+// block * D bytes read once, 2 D + 4 written; bound by memory for prompts (80.5 us for 537 MB in blocks of 64,
+// the copy rate; in blocks of 16 87, at 64 columns 115), by latency for the few blocks that a step fills (3.3
+// us). A thread holds 8 columns' running maxima and minima of its tokens as bf16 pairs (exact), eight loads in
+// flight; the divisions are shared out to the lanes that hold the same columns (all of them in each: 83, 106
 // and 175 us). Blocks of 16 of 128 columns by whole CTAs: 210.
 #include "../../include/kvdecode.h"
 #include "blocks.h"
@@ -62,7 +63,8 @@ __global__ void __launch_bounds__(kBoundsThreads) block_bounds_kernel(const Boun
         block = (long long)b * (p.S_max >> bs) + j;
     }
     // ---- maxima and minima of this thread's columns ----
-    const uint4* k = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.k) + ((size_t)row * p.Hkv + h) * D) + tid % TPR;
+    const __nv_bfloat16* rows = static_cast<const __nv_bfloat16*>(p.k) + ((size_t)row * p.Hkv + h) * D;
+    const uint4* k = reinterpret_cast<const uint4*>(rows) + tid % TPR;
     const size_t step = (size_t)p.Hkv * TPR;  // 16-byte vectors between tokens
     uint32_t hi[4], lo[4];
     const int t0 = tid / TPR;
@@ -170,10 +172,11 @@ cudaError_t launch_block_bounds(const BoundsParams& p, cudaStream_t stream) {
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
+    auto launch = [&](auto kernel) { return cudaLaunchKernelEx(&cfg, kernel, p, (unsigned)per_seq, (unsigned)items); };
     switch (p.D) {
-        case 64: return cudaLaunchKernelEx(&cfg, small ? block_bounds_kernel<64, 1> : block_bounds_kernel<64, 4>, p, (unsigned)per_seq, (unsigned)items);
-        case 128: return cudaLaunchKernelEx(&cfg, small ? block_bounds_kernel<128, 1> : block_bounds_kernel<128, 4>, p, (unsigned)per_seq, (unsigned)items);
-        case 256: return cudaLaunchKernelEx(&cfg, small ? block_bounds_kernel<256, 1> : block_bounds_kernel<256, 4>, p, (unsigned)per_seq, (unsigned)items);
+        case 64: return launch(small ? block_bounds_kernel<64, 1> : block_bounds_kernel<64, 4>);
+        case 128: return launch(small ? block_bounds_kernel<128, 1> : block_bounds_kernel<128, 4>);
+        case 256: return launch(small ? block_bounds_kernel<256, 1> : block_bounds_kernel<256, 4>);
         default: return cudaErrorInvalidValue;
     }
 }

@@ -3,21 +3,24 @@
 // of KV head g:
 //   I = sum_d (c_d > 0 ? c_d * hi_d : c_d * lo_d)   in whole numbers, below 2^23
 //   score = fl(max over the group's rows of fl(I * s_r) * scale_j); NaN counts as +inf
-// The first n_first and the last n_last blocks that the query token sees are always kept; ties go to the lowest index;
-// the list ascends. Since I is a whole number, exact in float32 in whatever order it is summed, the selection is a
-// matter of definition and not of the order of additions.
+// The first n_first and the last n_last blocks that the query token sees are always kept; ties go to the lowest
+// index; the list ascends. Since I is a whole number, exact in float32 in whatever order it is summed, the
+// selection is a matter of definition and not of the order of additions.
 //
-// Reads 2 D + 4 bytes a (block, KV head) once for all query tokens. 32 sequences of 16,384 to 131,072 tokens in blocks of 32, 32 heads
-// on 8 of 128: 41 us, 33 scoring (153 MB at 4.6 TB/s: some 500 instructions a tile of 16 blocks, a third of them the rows' fragments) and 8 selecting;
-// one of 131,072 in blocks of 64: 7.4, latency throughout; 65,536 keys a CTA, which it reads from L2, 44 to select. (Both in one launch of clusters: 53 and 9.9, since the cluster waits for its
-// slowest part and the selection holds the scorers' places.) The first launch scores, some CTAs a (sequence, KV head), a warp tiles of 16 blocks: f16 MMAs
-// m16n8k16 with the blocks as rows and the query rows as columns, I = [hi lo] [max(c, 0) min(c, 0)]^T. A code enters as code + 128
-// in the low bits of an f16, a subnormal; products and sums of these are whole numbers below 2^24 (times 2^-24), so exact. A lane's 16-byte
-// copy is 16 consecutive codes of a row; the MMA's k order is the permutation of columns that fits, the same for both operands, so codes
-// go from the lane's own place in shared memory to fragments without a shuffle, and a warp waits for its own copies alone. Keys
-// (scores as ordered integers) go to the workspace. A second launch selects, a CTA a (sequence, query token, KV head): a
-// histogram over 2,048 equal parts of the range [smallest, largest] of the keys, then (seldom) over the part that holds the border, until
-// that part has few keys, which are ranked one by one; the kept ones become bits, the bits the list.
+// Reads 2 D + 4 bytes a (block, KV head) once for all query tokens. 32 sequences of 16,384 to 131,072 tokens in
+// blocks of 32, 32 heads on 8 of 128: 41.5 us, 33 scoring (153 MB at 4.6 TB/s: some 500 instructions a tile of 16
+// blocks, a third of them the rows' fragments) and 8 selecting; one of 131,072 in blocks of 64: 7.7, latency
+// throughout; 65,536 keys a CTA, which it reads from L2, 44 to select. (Both in one launch of clusters: 53 and
+// 9.9, since the cluster waits for its slowest part and the selection holds the scorers' places.) The first
+// launch scores, some CTAs a (sequence, KV head), a warp tiles of 16 blocks: f16 MMAs m16n8k16 with the blocks
+// as rows and the query rows as columns, I = [hi lo] [max(c, 0) min(c, 0)]^T. A code enters as code + 128 in
+// the low bits of an f16, a subnormal; products and sums of these are whole numbers below 2^24 (times 2^-24),
+// so exact. A lane's 16-byte copy is 16 consecutive codes of a row; the MMA's k order is the permutation of
+// columns that fits, the same for both operands, so codes go from the lane's own place in shared memory to
+// fragments without a shuffle, and a warp waits for its own copies alone. Keys (scores as ordered integers) go
+// to the workspace. A second launch selects, a CTA a (sequence, query token, KV head): a histogram over 2,048
+// equal parts of the range [smallest, largest] of the keys, then (seldom) over the part that holds the border,
+// until that part has few keys, which are ranked one by one; the kept ones become bits, the bits the list.
 #include <math_constants.h>
 
 #include <algorithm>
@@ -34,13 +37,14 @@ constexpr int kPickThreads = 512;
 constexpr int kSelTiles = 8;        // column tiles of 8 query rows scored at once
 constexpr int kSelTies = 64;        // keys around the border that are ranked one by one
 
-// Shared memory of the scoring: the query rows' fragments, then a ring of tiles a warp, in which every lane has its own
-// 16 bytes of each load and its two rows' scales. The selection puts the keys in its place.
+// Shared memory of the scoring: the query rows' fragments, then a ring of tiles a warp, in which every lane has
+// its own 16 bytes of each load and its two rows' scales. The selection puts the keys in its place.
 template <int D>
 struct SelectShape {
     static constexpr int KS = 2 * D / 16, LOADS = 2 * D / 64;  // k-steps; 16-byte loads of a lane and row
     static constexpr int WARPS = D == 256 ? 16 : 8, THREADS = 32 * WARPS;
-    static constexpr int STAGES = D == 256 ? 1 : D == 128 ? 2 : 3;  // three CTAs an SM, at head_dim 256 one of twice the warps
+    static constexpr int STAGES = D == 256 ? 1 : D == 128 ? 2 : 3;  // three CTAs an SM with one column tile, two
+                                                                    // with more; at head_dim 256 one of twice the warps
     static constexpr int TILE = 2 * LOADS * 512 + 2 * 128;     // 16 blocks' codes, and scales
     static constexpr int RING = WARPS * STAGES * TILE;
     static constexpr int FRAG = KS * 32 * 8;                   // a column tile's fragments
@@ -91,8 +95,8 @@ __global__ void __launch_bounds__(SelectShape<D>::THREADS, D == 256 ? 1 : NT == 
         const int per_tok = (G + 7) / 8;                 // tiles of a token (G > 8: several)
         const int toks = G > 8 ? NT / per_tok : NT * (8 / cols);  // tokens of a round
         uint8_t* ring = smem + NT * Sh::FRAG + warp * STAGES * Sh::TILE;
-        // A tile's rows of this lane: blocks j0 + g8 and j0 + g8 + 8, by their place among all bounds (-1: none). Lanes
-        // go different ways here; the warp comes together again at the end.
+        // A tile's rows of this lane: blocks j0 + g8 and j0 + g8 + 8, by their place among all bounds (-1:
+        // none). Lanes go different ways here; the warp comes together again at the end.
         auto look_up = [&](int j0, long long (&at)[2]) {
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
@@ -135,7 +139,8 @@ __global__ void __launch_bounds__(SelectShape<D>::THREADS, D == 256 ? 1 : NT == 
         };
         for (int t0 = 0; t0 < p.T; t0 += toks) {
             const int nt = min(toks, p.T - t0);
-            // Column x of a round: token x / (8 per_tok) row x % (8 per_tok) for wide groups, else token x / cols, row x % cols.
+            // Column x of a round: token x / (8 per_tok) row x % (8 per_tok) for wide groups, else token x /
+            // cols, row x % cols.
             auto column = [&](int x, int& t, int& r) {
                 const int w = G > 8 ? 8 * per_tok : cols;
                 t = x / w;
@@ -148,8 +153,8 @@ __global__ void __launch_bounds__(SelectShape<D>::THREADS, D == 256 ? 1 : NT == 
             auto load_row = [&](int x) {
                 int t, r;
                 const bool live = column(x, t, r);
-                const uint32_t* q = reinterpret_cast<const uint32_t*>(static_cast<const __nv_bfloat16*>(p.q) +
-                                                                      (((size_t)b * p.T + t0 + (live ? t : 0)) * p.Hq + (size_t)h * G + (live ? r : 0)) * D);
+                const size_t row = ((size_t)b * p.T + t0 + (live ? t : 0)) * p.Hq + (size_t)h * G + (live ? r : 0);
+                const uint32_t* q = reinterpret_cast<const uint32_t*>(static_cast<const __nv_bfloat16*>(p.q) + row * D);
 #pragma unroll
                 for (int i = 0; i < WORDS; ++i) qw[i] = live ? __ldg(q + lane + 32 * i) : 0x7fc07fc0u;  // no row: NaN
             };
@@ -173,7 +178,8 @@ __global__ void __launch_bounds__(SelectShape<D>::THREADS, D == 256 ? 1 : NT == 
                 // A row that is not finite takes no part, as a column without a row: codes 0, scale NaN.
                 const float s = a < 0x7f80u ? __fdiv_rn(__uint_as_float(a << 16), 127.f) : __uint_as_float(0x7fffffffu);
                 int sum = 0;  // of the row's codes
-                // round(q / s): by the reciprocal, but where that may lie on the other side of a half by the quotient itself.
+                // round(q / s): by the reciprocal, but where that may lie on the other side of a half by the
+                // quotient itself.
                 const float inv = s > 1e-30f ? __frcp_rn(s) : 0.f;
 #pragma unroll
                 for (int i = 0; i < WORDS; ++i) {
@@ -214,12 +220,14 @@ __global__ void __launch_bounds__(SelectShape<D>::THREADS, D == 256 ? 1 : NT == 
                 cp_async_commit();
                 look_up(j0 + STAGES * step, at);
                 cp_async_wait<STAGES - 1>();
-                // The MMAs are .aligned: a warp's threads have to execute each of them together. What came before (look-ups, the
-                // last tile's stores) let lanes go different ways, and only this makes sure that they have met again.
+                // The MMAs are .aligned: a warp's threads have to execute each of them together. What came
+                // before (look-ups, the last tile's stores) let lanes go different ways, and only this makes
+                // sure that they have met again.
                 __syncwarp();
                 const uint8_t* mine = ring + stage * Sh::TILE + lane * 16;
-                // Codes enter the MMAs as code + 128 in the low bits of an f16, a subnormal of that many 2^-24; the sums start
-                // from what that adds. Products and sums are whole numbers below 2^24 in these units: exact.
+                // Codes enter the MMAs as code + 128 in the low bits of an f16, a subnormal of that many 2^-24;
+                // the sums start from what that adds. Products and sums are whole numbers below 2^24 in these
+                // units: exact.
                 float acc[NT][4], acc2[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
@@ -228,7 +236,8 @@ __global__ void __launch_bounds__(SelectShape<D>::THREADS, D == 256 ? 1 : NT == 
                 }
 #pragma unroll
                 for (int c = 0; c < LOADS; ++c) {
-                    const uint4 wx = *reinterpret_cast<const uint4*>(mine + c * 512), wy = *reinterpret_cast<const uint4*>(mine + (LOADS + c) * 512);
+                    const uint4 wx = *reinterpret_cast<const uint4*>(mine + c * 512);
+                    const uint4 wy = *reinterpret_cast<const uint4*>(mine + (LOADS + c) * 512);
                     const uint32_t x[4] = {wx.x, wx.y, wx.z, wx.w}, y[4] = {wy.x, wy.y, wy.z, wy.w};
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
@@ -278,7 +287,8 @@ __global__ void __launch_bounds__(SelectShape<D>::THREADS, D == 256 ? 1 : NT == 
                         const uint32_t k0 = ok[e] ? score_key(__fmul_rn(v0, sc[e])) : kSelNoPage;
                         if (width == 1) {
                             if (here && t < nt) keys[(size_t)(t0 + t) * p.key_stride + j] = k0;
-                            if (here && t + 1 < nt) keys[(size_t)(t0 + t + 1) * p.key_stride + j] = ok[e] ? score_key(__fmul_rn(v1, sc[e])) : kSelNoPage;
+                            if (here && t + 1 < nt)
+                                keys[(size_t)(t0 + t + 1) * p.key_stride + j] = ok[e] ? score_key(__fmul_rn(v1, sc[e])) : kSelNoPage;
                         } else if (here && (2 * j4) % width == 0 && t < nt) {
                             keys[(size_t)(t0 + t) * p.key_stride + j] = k0;
                         }
@@ -321,8 +331,8 @@ __global__ void __launch_bounds__(kPickThreads) block_pick_kernel(const SelectPa
     for (int i = tid; i < p.n_first; i += kPickThreads) out[i] = i;
     for (int i = tid; i < p.n_last; i += kPickThreads) out[p.K - p.n_last + i] = hi_j + i;
     if (want == 0) return;
-    // Keys in shared memory where they fit (0 for those of the first and last vector that do not compete), else where they
-    // lie (the workspace, in L2).
+    // Keys in shared memory where they fit (0 for those of the first and last vector that do not compete), else
+    // where they lie (the workspace, in L2).
     const int vecs = (hi_j + 3) / 4;
     const bool fits = (long long)vecs * 16 + kSelBins * 4 + kSelTies * 8 <= room;
     const uint32_t* key = fits ? s_key : src;
@@ -368,9 +378,9 @@ __global__ void __launch_bounds__(kPickThreads) block_pick_kernel(const SelectPa
         }
         return x;
     };
-    // Keys above hi are kept, `need` of those in [lo, hi] too: rounds of a histogram over 2,048 equal parts of that range,
-    // until few keys are left in the part that has the border, or all of them are kept, or it is one value.
-    // (A round takes 11 bits off the range: three at most.)
+    // Keys above hi are kept, `need` of those in [lo, hi] too: rounds of a histogram over 2,048 equal parts of
+    // that range, until few keys are left in the part that has the border, or all of them are kept, or it is
+    // one value. (A round takes 11 bits off the range: three at most.)
 #pragma unroll 1
     for (int round = 0; round < 3; ++round) {
         const int shift = max(0, 21 - __clz(hi - lo));  // (hi - lo) >> shift is below 2,048
@@ -383,7 +393,8 @@ __global__ void __launch_bounds__(kPickThreads) block_pick_kernel(const SelectPa
                 if (k[u] >= lo && k[u] <= hi) atomicAdd(&s_hist[(k[u] - lo) >> shift], 1u);
         }
         __syncthreads();
-        // Thread i adds up 4 parts, from the top, and leaves zeros; the one in which the running sum reaches `need` has the border.
+        // Thread i adds up 4 parts, from the top, and leaves zeros; the one in which the running sum reaches
+        // `need` has the border.
         static_assert(kSelBins == 4 * kPickThreads, "a vector of parts a thread");
         uint4* hp = reinterpret_cast<uint4*>(s_hist) + kPickThreads - 1 - tid;
         const uint4 x = *hp;

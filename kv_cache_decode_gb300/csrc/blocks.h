@@ -9,7 +9,8 @@
 
 namespace kvd {
 
-// Tokens of a stage of the attention over listed blocks, working warps of a CTA at most, stages of a CTA's ring (see BlocksShape).
+// Tokens of a stage of the attention over listed blocks, working warps of a CTA at most, stages of a CTA's ring
+// (see BlocksShape).
 constexpr int kBlocksStage = 32;
 constexpr int blocks_warps(int D) { return D == 256 ? 8 : 4; }
 constexpr int blocks_slots(int D) { return (D == 256 ? 192 : 96) * 1024 / (4 * D * kBlocksStage); }
@@ -32,8 +33,8 @@ struct BlocksParams {
 };
 // Lets a kernel use so much shared memory and clusters of 16, once a device (a bit of *ready each).
 cudaError_t allow_clusters(const void* kernel, int smem_bytes, std::atomic<uint64_t>* ready);
-// Clusters of 1, 2, 4, 8 and 16 such CTAs that the current device runs at once (0: it cannot place one of that size), asked once
-// a device (known: kMaxDevices of them).
+// Clusters of 1, 2, 4, 8 and 16 such CTAs that the current device runs at once (0: it cannot place one of that
+// size), asked once a device (known: kMaxDevices of them).
 cudaError_t clusters_at_once(const void* kernel, int threads, int smem_bytes, std::atomic<uint64_t>* ready, std::atomic<uint64_t>* known,
                              int (&n)[5]);
 cudaError_t blocks_at_once_d64(int (&n)[5]);

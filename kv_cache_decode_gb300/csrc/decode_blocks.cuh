@@ -1,26 +1,30 @@
 // Attention over listed blocks of tokens: for every (sequence, query token, KV
 // head), the softmax over the tokens of the blocks that its list names,
 //   s_t = scale * q . k_t,  out = sum_t 2^(s_t - m) v_t / sum_t 2^(s_t - m)   (base 2, log2(e) in the scale).
-// It reads K * block rows of K and V a pair where the attention over all tokens reads the sequence;
-// bound by memory for batches (64 sequences, 32 heads on 8 of 128, 4,096 tokens each: 159 us for 1.07 GB, the copy rate), by latency for
-// one sequence (2,048 tokens: 6.6 to 7 us), by shared-memory reads for wide groups at head_dim 256, whose 6 or 8 warps each read
-// every K and V row (64 sequences, 48 heads on one, 4,096 tokens: 72 us, 3.8 TB/s; 32 heads 50.5).
+// It reads K * block rows of K and V a pair where the attention over all tokens reads the sequence; bound by
+// memory for batches (64 sequences, 32 heads on 8 of 128, 4,096 tokens each: 159 us for 1.07 GB, the copy
+// rate), by latency for one sequence (2,048 tokens: 6.6 to 7 us). Wide groups: 64 sequences, 48 heads on one,
+// 4,096 tokens take 72 us at head_dim 256 (3.8 TB/s; 32 heads 50.8), 39 at 128 and 28.6 at 64. Their 3 to 8 warps
+// a team each read every K and V row: at 256 the shared-memory pipe is at 61 % of its peak over the whole time
+// and 78 % where an SM works, tensor cores 29 %; at 128 and 64 it is at 32 and 24 %, and a warp mostly waits for
+// its own last result (2 of 6 to 7 cycles an instruction) and its stages: latency of few warps.
 //
-// A stage is 32 tokens, K rows and V rows, brought by TMA into a ring (128-byte swizzle): as one box
-// where blocks and pages have 32 tokens, else two units of 16 of any listed blocks. A loading warp looks the list up, 32 units at a
-// time, and deals the stages to the CTA's teams in turn; a team works on its stages alone, so that nothing but its own
-// loads holds it up. (Loads issued by the working warps themselves took 950 of a 16-token step's 2,200 cycles.) The
-// products are turned round so that tokens fill the 16 rows of m16n8k16 MMAs and query rows
-// their 8 columns (a group of 4 to 8 query heads is one column tile): S^T = K q^T, O^T = V^T w, the weights
-// transposed by movmatrix. The running maximum of a column is raised only where a score passes it by 2^8
-// (a vote a stage otherwise): weights stay below 2^8 and keep their relative precision, bf16's 2^-8, the same
-// rounding as the other attention kernels' of this library; for float32 output a second bf16 carries the rest to 2^-16.
-// Teams are single warps for groups of up to 16 query heads (head_dim 256: 8); wider ones are shared out to the head_warps warps of a team.
+// A stage is 32 tokens, K rows and V rows, brought by TMA into a ring (128-byte swizzle): as one box where
+// blocks and pages have 32 tokens, else two units of 16 of any listed blocks. A loading warp looks the list up,
+// 32 units at a time, and deals the stages to the CTA's teams in turn; a team works on its stages alone, so
+// that nothing but its own loads holds it up. (Loads issued by the working warps themselves took 950 of a
+// 16-token step's 2,200 cycles.) The products are turned round so that tokens fill the 16 rows of m16n8k16 MMAs
+// and query rows their 8 columns (a group of 4 to 8 query heads is one column tile): S^T = K q^T, O^T = V^T w,
+// the weights transposed by movmatrix. The running maximum of a column is raised only where a score passes it
+// by 2^8 (a vote a stage otherwise): weights stay below 2^8 and keep their relative precision, bf16's 2^-8, the
+// same rounding as the other attention kernels' of this library; for float32 output a second bf16 carries the
+// rest to 2^-16. Teams are single warps for groups of up to 16 query heads (head_dim 256: 8); wider ones are
+// shared out to the head_warps warps of a team.
 //
-// A pair's CTAs (parts, up to 16) are a cluster: their states are joined over
-// distributed shared memory, each CTA writing a share of the output, without a second launch or a workspace. Where even
-// 16 CTAs a pair leave SMs idle, `shards` such clusters a pair write normalised float32 results, which the
-// shard merge of split_kv_merge.cu joins.
+// A pair's CTAs (parts, up to 16) are a cluster: their states are joined over distributed shared memory, each
+// CTA writing a share of the output, without a second launch or a workspace. Where even 16 CTAs a pair leave
+// SMs idle, `shards` such clusters a pair write normalised float32 results, which the shard merge of
+// split_kv_merge.cu joins.
 #pragma once
 
 #include <cuda.h>
@@ -85,7 +89,8 @@ constexpr bool blocks_slot_uses_hold(int teams, int R) {
     }
     return true;
 }
-static_assert(blocks_slot_uses_hold(1, 12) && blocks_slot_uses_hold(4, 3) && blocks_slot_uses_hold(2, 5) && blocks_slot_uses_hold(3, 4),
+static_assert(blocks_slot_uses_hold(1, 12) && blocks_slot_uses_hold(4, 3) && blocks_slot_uses_hold(2, 5) &&
+                  blocks_slot_uses_hold(3, 4),
               "the last phase of each slot");
 
 // The bf16 MMA of common.cuh without its ordering against other instructions.
@@ -193,8 +198,8 @@ __global__ void __launch_bounds__((BlocksShape<D, NT>::WARPS + 1) * 32, BlocksSh
                 }
             }
         };
-        // Units are looked up 32 at a time, one a lane: how many of its tokens count, and its cache row. Those of entries that
-        // name no block the token sees have none and are passed over.
+        // Units are looked up 32 at a time, one a lane: how many of its tokens count, and its cache row. Those
+        // of entries that name no block the token sees have none and are passed over.
         int row0 = 0, n0 = 0;  // a unit that waits for a second one
         for (long long u0 = shard * p.parts + rank; u0 < units && !dead; u0 += 32LL * W) {
             const long long u = u0 + (long long)lane * W;
@@ -208,7 +213,8 @@ __global__ void __launch_bounds__((BlocksShape<D, NT>::WARPS + 1) * 32, BlocksSh
                 if (p.pg.block_table) {
                     const int page = __ldg(p.pg.block_table + (size_t)b * p.pg.max_blocks + (tok >> p.pg.page_shift));
                     bad = (unsigned)page >= (unsigned)p.pg.num_pages;  // reads as zero rows: past the pool's end
-                    row = bad ? p.pg.num_pages << p.pg.page_shift : (page << p.pg.page_shift) + (tok & ((1 << p.pg.page_shift) - 1));
+                    row = bad ? p.pg.num_pages << p.pg.page_shift
+                              : (page << p.pg.page_shift) + (tok & ((1 << p.pg.page_shift) - 1));
                 } else {
                     row = b * p.S_max + tok;
                 }
@@ -253,8 +259,8 @@ __global__ void __launch_bounds__((BlocksShape<D, NT>::WARPS + 1) * 32, BlocksSh
                 }
             }
         }
-        // l: the weights' sum, for lse. lr: of the weights as V meets them, so that the output is a convex combination of V
-        // rows (the same where float32 output carries both parts).
+        // l: the weights' sum, for lse. lr: of the weights as V meets them, so that the output is a convex
+        // combination of V rows (the same where float32 output carries both parts).
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
             m[n][0] = m[n][1] = -FLT_MAX;
@@ -363,7 +369,8 @@ __global__ void __launch_bounds__((BlocksShape<D, NT>::WARPS + 1) * 32, BlocksSh
                     for (int i = lane + n_tok[u] * 8; i < 16 * 8; i += 32)
 #pragma unroll
                         for (int c = 0; c < D / 64; ++c)
-                            *reinterpret_cast<uint4*>(smem + (vb - ring) + c * (Sh::ROWS_S * 128) + u * 2048 + i * 16) = make_uint4(0u, 0u, 0u, 0u);
+                            *reinterpret_cast<uint4*>(smem + (vb - ring) + c * (Sh::ROWS_S * 128) + u * 2048 + i * 16) =
+                                make_uint4(0u, 0u, 0u, 0u);
                 __syncwarp();
             }
 #pragma unroll
@@ -371,7 +378,8 @@ __global__ void __launch_bounds__((BlocksShape<D, NT>::WARPS + 1) * 32, BlocksSh
 #pragma unroll
                 for (int u = 0; u < U; ++u) {
                     uint32_t a[4];
-                    ldmatrix_x4_trans(chunk(vb, 16 * u + (lane & 7) + ((lane >> 4) << 3), 2 * i + ((lane >> 3) & 1)), a[0], a[1], a[2], a[3]);
+                    ldmatrix_x4_trans(chunk(vb, 16 * u + (lane & 7) + ((lane >> 4) << 3), 2 * i + ((lane >> 3) & 1)), a[0], a[1],
+                                      a[2], a[3]);
 #pragma unroll
                     for (int n = 0; n < NT; ++n) {
                         mma_bf16_free(o[i][n], a, ph[u][n][0], ph[u][n][1]);
@@ -386,8 +394,8 @@ __global__ void __launch_bounds__((BlocksShape<D, NT>::WARPS + 1) * 32, BlocksSh
     }
     if (dead && lane == 0 && p.status) atomicOr(p.status, KVD_STATUS_TIMEOUT);
 
-    // ---- where a wait of any warp gave up, copies may still be on their way: they are waited for (again with a limit), ----
-    // ---- since the ring's place is used below and the CTA must not leave before them ----
+    // ---- where a wait of any warp gave up, copies may still be on their way: they are waited for (again with a ----
+    // ---- limit), since the ring's place is used below and the CTA must not leave before them ----
     __syncthreads();
     if (*abort_flag) {  // (set before the barrier: every thread reads the same)
         if (loader)
@@ -573,8 +581,10 @@ cudaError_t launch_decode_blocks(const BlocksParams& p, cudaStream_t stream) {
 #define KVD_BLOCKS_LAUNCH(DD)                                                                             \
     cudaError_t blocks_at_once_d##DD(int (&n)[5]) { return blocks_at_once<DD>(n); }                       \
     cudaError_t launch_decode_blocks_d##DD(const BlocksParams& p, bool f32_out, cudaStream_t stream) {    \
-        if (p.head_rows == 8) return f32_out ? launch_decode_blocks<DD, 1, true>(p, stream) : launch_decode_blocks<DD, 1, false>(p, stream); \
-        if constexpr (DD < 256) return f32_out ? launch_decode_blocks<DD, 2, true>(p, stream) : launch_decode_blocks<DD, 2, false>(p, stream); \
+        if (p.head_rows == 8)                                                                             \
+            return f32_out ? launch_decode_blocks<DD, 1, true>(p, stream) : launch_decode_blocks<DD, 1, false>(p, stream); \
+        if constexpr (DD < 256)                                                                           \
+            return f32_out ? launch_decode_blocks<DD, 2, true>(p, stream) : launch_decode_blocks<DD, 2, false>(p, stream); \
         return cudaErrorInvalidValue;                                                                     \
     }
 

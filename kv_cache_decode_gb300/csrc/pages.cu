@@ -1,13 +1,15 @@
-// Page tables, slots and positions from request lengths. Sequence b goes from seq_lens[b] tokens to new_lens[b]: the pages
-// it gives up go back on the stack of free ones, then pages that it needs come from its top, in order of sequence and
-// block, as long as the running sum of what is needed fits. With prefix sums over the
-// sequences every page's place on the stack is a matter of arithmetic, so nothing is counted by atomics and the
-// same call always gives the same table. Released pages are laid down in reverse, so that a shrink right behind a growth leaves
-// the stack as it was.
+// Page tables, slots and positions from request lengths. Sequence b goes from seq_lens[b] tokens to
+// new_lens[b]: the pages it gives up go back on the stack of free ones, then pages that it needs come from its
+// top, in order of sequence and block, as long as the running sum of what is needed fits. With prefix sums over
+// the sequences every page's place on the stack is a matter of arithmetic, so nothing is counted by atomics and
+// the same call always gives the same table. Released pages are laid down in reverse, so that a shrink right
+// behind a growth leaves the stack as it was.
 //
-// One launch: a CTA, or a cluster of up to 16 where many slots are written; every CTA forms the prefix sums for itself in
-// shared memory (a few thousand integers at most), and barriers part the release, the growth and the slots. Bound by latency (a growth and the shrink
-// back of 64 sequences by up to 8 tokens: 9.4 us for the two; 24 prompts of up to 4,096 tokens with their slots and positions: 29).
+// One launch: a CTA, or a cluster of up to 16 where many slots are written; every CTA forms the prefix sums for
+// itself in shared memory (16 bytes a sequence: up to 131 KB for 8,192 of them), and barriers part the release,
+// the growth and the slots. Bound by latency (a growth by 5 tokens of 64 sequences and the shrink back: 9.6 us
+// for the two), for prompts by the slots' stores from 16 multiprocessors (up to 4,096 tokens each with slots and
+// positions, and back: 24 prompts 12 us, 256 30).
 #include <algorithm>
 
 #include "../../include/kvdecode.h"
@@ -29,7 +31,8 @@ __device__ __forceinline__ int owner_of(const int* a, int n, int x) {
     return lo;
 }
 
-// Exclusive prefix sums of two numbers over the block; tot receives their sums. s_warp: not used by the call before this one.
+// Exclusive prefix sums of two numbers over the block; tot receives their sums. s_warp: not used by the call
+// before this one.
 __device__ __forceinline__ void block_scan2(uint32_t (&v)[2], uint32_t (&tot)[2], uint32_t (*s_warp)[2]) {
     static_assert(kPagesThreads == 1024, "a lane a warp");
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -91,7 +94,8 @@ __global__ void __launch_bounds__(kPagesThreads, 1) pages_kernel(const PagesPara
         const int b = b0 + tid;
         int old = 0, want = 0;
         if (b < p.B) lengths(b, old, want);
-        uint32_t v[2] = {(uint32_t)max(pages_of(old) - pages_of(want), 0), (uint32_t)max(pages_of(want) - pages_of(old), 0)};
+        const int more = pages_of(want) - pages_of(old);
+        uint32_t v[2] = {(uint32_t)max(-more, 0), (uint32_t)max(more, 0)};
         block_scan2(v, tot, s_warp[turn ^= 1]);
         if (b < p.B) {
             s_old[b] = old;
@@ -104,8 +108,9 @@ __global__ void __launch_bounds__(kPagesThreads, 1) pages_kernel(const PagesPara
     }
     const int R = (int)released;
     // ---- a sequence grows when all that is needed up to it fits; one that needs no page always ----
-    // (Where lengths claim more pages than the pool has, the stack ends with the pool: never more than num_pages are given
-    // out, so that the tokens of those, below 2^31, and of every sequence's last page before are below 2^32.)
+    // (Where lengths claim more pages than the pool has, the stack ends with the pool: never more than
+    // num_pages are given out, so that the tokens of those, below 2^31, and of every sequence's last page
+    // before are below 2^32.)
     const long long have = (long long)F + R;
     const int top = (int)min(have, (long long)p.num_pages);
     uint32_t taken_u = 0, rows_u = 0;
@@ -181,8 +186,8 @@ __global__ void __launch_bounds__(kPagesThreads, 1) pages_kernel(const PagesPara
     if (p.slots || p.positions) {
         sync();
         const long long total = min((long long)rows, p.rows);
-        // A warp takes a stretch of rows, 128 at a time, four neighbours a lane: the sequence is searched for once, then
-        // followed; two steps' table entries are on the way at once.
+        // A warp takes a stretch of rows, 128 at a time, four neighbours a lane: the sequence is searched for
+        // once, then followed; two steps' table entries are on the way at once.
         const bool wide = ((reinterpret_cast<uintptr_t>(p.slots) | reinterpret_cast<uintptr_t>(p.positions)) & 15) == 0;
         auto put = [&](long long n, long long end, const int (&slot)[4], const int (&at)[4]) {
             if (wide && n + 4 <= end) {
@@ -250,12 +255,11 @@ __global__ void __launch_bounds__(kPagesThreads, 1) pages_kernel(const PagesPara
 
 cudaError_t launch_pages(const PagesParams& p, cudaStream_t stream) {
     static std::atomic<uint64_t> ready{0}, known[kMaxDevices];
-    const int smem = 4 * (p.B + 1) * (int)sizeof(int);
+    const void* kernel = reinterpret_cast<const void*>(pages_kernel);
+    const int smem = 4 * (p.B + 1) * (int)sizeof(int), most = 4 * (kPagesMaxBatch + 1) * (int)sizeof(int);
     int at_once[5];
-    cudaError_t e = allow_clusters(reinterpret_cast<const void*>(pages_kernel), 4 * (kPagesMaxBatch + 1) * (int)sizeof(int), &ready);
-    if (e == cudaSuccess)
-        e = clusters_at_once(reinterpret_cast<const void*>(pages_kernel), kPagesThreads, 4 * (kPagesMaxBatch + 1) * (int)sizeof(int), &ready,
-                             known, at_once);
+    cudaError_t e = allow_clusters(kernel, most, &ready);
+    if (e == cudaSuccess) e = clusters_at_once(kernel, kPagesThreads, most, &ready, known, at_once);
     if (e != cudaSuccess) return e;
     // A CTA for 8,192 rows, two steps of its threads, and for 16,384 table entries (few of which change in a call).
     const long long rows = p.slots || p.positions ? p.rows : 0, entries = (long long)p.B * p.max_blocks;

@@ -1,11 +1,10 @@
-// Rotary positions of several axes (time, height and width of an image's or a
-// video's tokens): pair i of a row turns by position[axes[i]] * w_i, the phases as in rope.cuh. Rows are turned as rope.cu
-// turns them, and appended as kv_append_rope.cu appends them, but to cache rows
-// that a slot map names, since a token's positions no longer say where it lies. One read of q, k and v
-// and one write of each; bound by memory for prompts (turning 1.07 GB 156 us, appending 1.19 GB 177: the copy rate) and by latency for
-// single tokens (3.5 us). A warp takes a row, a share of
-// its heads where there are few rows, or several rows where rows are short; a row's positions (4 at most) are loaded once and picked
-// from registers.
+// Rotary positions of several axes (time, height and width of an image's or a video's tokens): pair i of a row
+// turns by position[axes[i]] * w_i, the phases as in rope.cuh. Rows are turned as rope.cu turns them, and
+// appended as kv_append_rope.cu appends them, but to cache rows that a slot map names, since a token's
+// positions no longer say where it lies. One read of q, k and v and one write of each; bound by memory for
+// prompts (turning 1.07 GB 156 us, appending 1.19 GB 177: the copy rate) and by latency for single tokens (3.5
+// us). A warp takes a row, a share of its heads where there are few rows, or several rows where rows are short;
+// a row's positions (4 at most) are loaded once and picked from registers.
 #include <algorithm>
 
 #include "append_unit.cuh"
@@ -37,7 +36,8 @@ __device__ __forceinline__ void axes_table(const RopeAxes& rope, const AxisPos& 
 #pragma unroll
         for (int a = 0; a < 4; ++a) at.p[a] = a < rope.n_axes ? __shfl_sync(0xffffffffu, mine.p[a], tok & 31) : 0;
         if (tok < n)
-            rope_table_put(buf, tok * half + i, rope_cos_sin(at.on(__ldg(rope.axes + i)), __ldg(rope.table.turns + i), rope.table.factor));
+            rope_table_put(buf, tok * half + i,
+                           rope_cos_sin(at.on(__ldg(rope.axes + i)), __ldg(rope.table.turns + i), rope.table.factor));
         i += 32;
     }
     __syncwarp();
@@ -75,9 +75,10 @@ __global__ void __launch_bounds__(kAxesWarps * 32) rope_axes_rows_kernel(const R
                                  [&]() { axes_table(rope, at, n, rt.s_cs); });
 }
 
-// Short rows of one head, where no thread shares a pair's cosine and sine with another: two units of 16 columns a thread, which forms
-// its own. Rows of up to 128 columns: 134 MB of bf16 rows of 64 columns (all turned) take 38 us, 64 by the warps above; of 80 41 and 57, of
-// 128 (half turned) 40.5 and 42; of 256, which stay with the warps, 40.5 and 32.
+// Short rows of one head, where no thread shares a pair's cosine and sine with another: two units of 16 columns
+// a thread, which forms its own. Rows of up to 128 columns: 134 MB of bf16 rows of 64 columns (all turned) take
+// 38 us, 64 by the warps above; of 80 41 and 57, of 128 (half turned) 40.5 and 42; of 256, which stay with the
+// warps, 40.5 and 32.
 template <bool IN32, bool OUT32>
 __global__ void __launch_bounds__(kAxesWarps * 32) rope_axes_one_kernel(const RopeAxes rope, const void* x, long long xs, void* y,
                                                                         long long ys, unsigned total, int D) {
@@ -275,10 +276,14 @@ cudaError_t launch_append_axes(const AppendTarget& to, const RopeAxes& rope, con
     (per_warp > 1 ? cudaLaunchKernelEx(&cfg, append_axes_rows_kernel<CacheForm::F, DD>, to, rope, in, slots, cache_rows,       \
                                        per_warp, status)                                                                       \
                   : cudaLaunchKernelEx(&cfg, append_axes_kernel<CacheForm::F, DD>, to, rope, in, slots, cache_rows, parts, status))
-#define KVD_APP_D(F) (in.D == 64 ? KVD_APP(F, 64) : in.D == 128 ? KVD_APP(F, 128) : in.D == 256 ? KVD_APP(F, 256) : cudaErrorInvalidValue)
+#define KVD_APP_D(F) \
+    (in.D == 64 ? KVD_APP(F, 64) : in.D == 128 ? KVD_APP(F, 128) : in.D == 256 ? KVD_APP(F, 256) : cudaErrorInvalidValue)
     switch (to.form) {
         case CacheForm::kBf16:
-            return in.D == 64 ? KVD_APP(kBf16, 64) : in.D == 128 ? KVD_APP(kBf16, 128) : in.D == 256 ? KVD_APP(kBf16, 256) : KVD_APP(kBf16, 0);
+            return in.D == 64    ? KVD_APP(kBf16, 64)
+                   : in.D == 128 ? KVD_APP(kBf16, 128)
+                   : in.D == 256 ? KVD_APP(kBf16, 256)
+                                 : KVD_APP(kBf16, 0);
         case CacheForm::kInt8: return KVD_APP_D(kInt8);
         case CacheForm::kFp8: return KVD_APP_D(kFp8);
         case CacheForm::kFp4: break;
