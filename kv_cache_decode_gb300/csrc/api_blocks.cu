@@ -432,8 +432,10 @@ kvd_status kvd_block_select(const kvd_block_bounds* bounds, const void* q, const
     p.key_stride = select_key_stride(max_seq_len, bounds->block_tokens);
     p.pg = pg;
     // CTAs of a pair: for about three rounds of those that are resident, as far as every warp has a tile of 16
-    // blocks (32 sequences of 16,384 to 131,072 tokens in blocks of 32, 8 KV heads: one round 47.0 us, two
-    // 42.3, three 41.0, six 42.7).
+    // blocks. One / two / three / four / six rounds, us: 32 sequences of 16,384 to 131,072 tokens in blocks of
+    // 32, 32 heads on 8 of 128, 46.5 / 42.2 / 41.3 / 42.1 / 43.4; of 64 columns 40.6 / 36.3 / 35.6 / 36.4 / 37.6;
+    // 4 query tokens 71 / 67.2 / 66.8 / 67.2 / 70.4; 64 sequences, 48 heads on one of 256, 60.2 / 57.1 / 56.5 /
+    // 58.8 / 56.9. One sequence of 65,536 blocks alone would have one round: 70 against 74.
     const int tiles_cta = head_dim == 256 ? 16 : 8;
     const long long tiles = (p.key_stride + 15LL) / 16;
     const long long three = (3LL * select_ctas(head_dim, p.G, n_tokens) * sms + pairs - 1) / pairs;
