@@ -642,7 +642,8 @@ kvd_status kvd_decode_fp4(const kvd_cache_fp4* cache, const void* q, const int32
  * Rows of slots and positions behind the last token are -1; tokens past n_rows get none
  * (KVD_STATUS_POS_OUT_OF_RANGE). A table entry or place of the stack that names no page is handed
  * on as it is, its slots are -1 (KVD_STATUS_BAD_PAGE). Where the lengths before claim more pages than
- * the pool has, those that come back and find the stack full are dropped (KVD_STATUS_BAD_PAGE). seq_lens outside [0, capacity] are clamped (KVD_STATUS_SEQ_LEN_CLAMPED).
+ * the pool has, those that come back and find the stack full are dropped (KVD_STATUS_BAD_PAGE).
+ * seq_lens outside [0, capacity] are clamped (KVD_STATUS_SEQ_LEN_CLAMPED).
  * Errors: KVD_ERR_INVALID_ARG for null or misaligned pointers, bad sizes (page_size, max_blocks,
  * num_pages as the paged calls; batch * max_blocks and n_rows at most 2^31 - 1) or overlaps;
  * KVD_ERR_UNSUPPORTED for batch > 8192; KVD_ERR_CUDA.
